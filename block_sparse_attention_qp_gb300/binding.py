@@ -11,6 +11,13 @@ And the autograd pair mirroring the package API of Flash-MSA (``flash_msa_func``
 ``flash_msa_warmup_func``, PyPI page "Usage"): ``msa_func`` and ``msa_warmup_func`` return
 ``(attn_out, kl_loss)`` where kl_loss is a zero placeholder whose gradient drives the proxy
 heads in the backward.
+
+What stands around sparse attention in a model:
+  msa_norm_rope_forward, msa_norm_rope_backward, msa_norm_rope_append (norm and rotation of the
+  heads, the last one into the decode caches), with the autograd functions msa_norm_rope_func and
+  msa_norm_rope_packed_func;
+  msa_window_forward, msa_window_backward, msa_window_decode (causal attention over a sliding window
+  and the first tokens), with the autograd function msa_window_func.
 """
 from __future__ import annotations
 
@@ -25,12 +32,18 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmsa.so")
 
 OP_FORWARD, OP_BACKWARD, OP_WARMUP_FORWARD, OP_WARMUP_BACKWARD, OP_DECODE = 0, 1, 2, 3, 4
+OP_WINDOW_FORWARD, OP_WINDOW_BACKWARD, OP_WINDOW_DECODE = 5, 6, 7
+OP_NORM_ROPE_BACKWARD, OP_NORM_ROPE_APPEND = 8, 9
+ROPE_ROTATE, ROPE_CACHE, ROPE_PARTS = 1, 2, 8
 STATUS_BITS = {1: "bad block index", 2: "work list overflow", 4: "device wait timeout",
                8: "internal layout check"}
 _SYMBOLS = ("msa_workspace_size", "msa_forward", "msa_backward", "msa_warmup_forward",
             "msa_warmup_backward", "msa_device_status", "msa_status_string", "msa_last_error",
             "msa_profile_begin", "msa_profile_end", "msa_launch_count", "msa_forward_noalloc",
-            "msa_forward_noalloc_status", "msa_selftest_wait_timeout", "msa_decode")
+            "msa_forward_noalloc_status", "msa_selftest_wait_timeout", "msa_decode",
+            "msa_window_workspace_size", "msa_window_forward", "msa_window_backward",
+            "msa_window_decode", "msa_norm_rope_forward", "msa_norm_rope_append",
+            "msa_norm_rope_backward", "msa_norm_rope_workspace_size")
 
 
 class MSAError(RuntimeError):
@@ -41,6 +54,26 @@ class Shape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("S", ctypes.c_int32), ("Hq", ctypes.c_int32),
                 ("Hkv", ctypes.c_int32), ("Hp", ctypes.c_int32), ("D", ctypes.c_int32),
                 ("top_k", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class WindowShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("S", ctypes.c_int32), ("Hq", ctypes.c_int32),
+                ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("sinks", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class RopePart(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("x_batch", ctypes.c_int64), ("x_token", ctypes.c_int64),
+                ("y", ctypes.c_void_p), ("y_batch", ctypes.c_int64), ("y_token", ctypes.c_int64),
+                ("dx", ctypes.c_void_p), ("dx_batch", ctypes.c_int64),
+                ("dx_token", ctypes.c_int64), ("weight", ctypes.c_void_p),
+                ("dweight", ctypes.c_void_p), ("heads", ctypes.c_int32), ("flags", ctypes.c_int32)]
+
+
+class RopeShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("N", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("rotary", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("capacity", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
 _lib = None
@@ -69,6 +102,20 @@ def load_library(path: str = LIB_PATH):
         lib.msa_device_status.argtypes = [P, ctypes.POINTER(ctypes.c_uint), P]
         lib.msa_decode.argtypes = [SP, P, P, P, P, P, P, P, P, P, P, Z, P]
         lib.msa_decode.restype = I
+        WP, RP, RS = (ctypes.POINTER(x) for x in (WindowShape, RopePart, RopeShape))
+        lib.msa_window_workspace_size.argtypes = [WP, I]
+        lib.msa_window_workspace_size.restype = Z
+        lib.msa_window_forward.argtypes = [WP, P, P, P, P, P, P, Z, P]
+        lib.msa_window_backward.argtypes = [WP, P, P, P, P, P, P, P, P, P, P, Z, P]
+        lib.msa_window_decode.argtypes = [WP, P, P, P, P, P, P, P, Z, P]
+        lib.msa_norm_rope_forward.argtypes = [RS, RP, I, P, P, P]
+        lib.msa_norm_rope_append.argtypes = [RS, RP, I, P, P, P, Z, P]
+        lib.msa_norm_rope_backward.argtypes = [RS, RP, I, P, P, P, Z, P]
+        lib.msa_norm_rope_workspace_size.argtypes = [I, I]
+        lib.msa_norm_rope_workspace_size.restype = Z
+        for name in ("msa_window_forward", "msa_window_backward", "msa_window_decode",
+                     "msa_norm_rope_forward", "msa_norm_rope_append", "msa_norm_rope_backward"):
+            getattr(lib, name).restype = I
         lib.msa_status_string.argtypes = [I]
         lib.msa_status_string.restype = ctypes.c_char_p
         lib.msa_last_error.restype = ctypes.c_char_p
@@ -421,3 +468,373 @@ def msa_func(Q_proxy, K_proxy, Q, K, V, top_k: int, scale: float):
 def msa_warmup_func(Q_proxy, K_proxy, Q, K, V, top_k: int, scale: float):
     """Warmup mode: dense main attention, proxy trained over the full causal prefix."""
     return _MSAFunction.apply(Q_proxy, K_proxy, Q, K, V, int(top_k), float(scale), True)
+
+
+# ---------------------------------------------------------------- sliding-window attention
+def make_window_shape(q, k, window, sinks, scale) -> WindowShape:
+    """Shape of a window op: q [B, S, Hq, D] (decode: [B, Hq, D]), k [B, S, Hkv, D]."""
+    B, S, Hkv = k.shape[:3]
+    return WindowShape(B, S, q.shape[-2], Hkv, q.shape[-1], _int32(window, "window"),
+                       _int32(sinks, "sinks"), float(scale))
+
+
+def _int32(x, name) -> int:
+    """x as an int32; larger values (a window of "everything") saturate."""
+    x = int(x)
+    if x < -2 ** 31:
+        raise MSAError(f"{name} is out of range: {x}")
+    return min(x, 2 ** 31 - 1)
+
+
+def msa_window_workspace_size(shape: WindowShape, op: int) -> int:
+    n = load_library().msa_window_workspace_size(ctypes.byref(shape), op)
+    if n == 0:
+        raise MSAError(f"unsupported shape for op {op}: "
+                       f"{load_library().msa_last_error().decode()}")
+    return int(n)
+
+
+def window_workspace(shape: WindowShape, op: int, device) -> torch.Tensor:
+    """Fresh workspace of a window op (uint8 tensor)."""
+    return torch.empty(msa_window_workspace_size(shape, op), dtype=torch.uint8, device=device)
+
+
+def _req_ws(ws, device):
+    _req(ws, "ws", torch.uint8)
+    if ws.device != device:
+        raise MSAError(f"ws is on {ws.device}, the inputs on {device}")
+
+
+def _dims(t, name, n):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dim() != n:
+        raise MSAError(f"{name} has shape {tuple(t.shape)}, expected {n} dimensions")
+
+
+@_on_tensor_device
+def msa_window_forward(q, k, v, window: int, sinks: int, scale: float, ws=None):
+    """Causal GQA attention of every query over the last ``window`` tokens (itself included) and the
+    first ``sinks`` tokens.  q [B, S, Hq, 128], k, v [B, S, Hkv, 128], any S.  Returns (o, lse)."""
+    _dims(q, "q", 4)
+    _dims(k, "k", 4)
+    B, S, Hq, D = q.shape
+    Hkv = k.shape[2]
+    for t, n, h in ((q, "q", Hq), (k, "k", Hkv), (v, "v", Hkv)):
+        _req(t, n, shape=(B, S, h, D))
+    shape = make_window_shape(q, k, window, sinks, scale)
+    if ws is None:
+        ws = window_workspace(shape, OP_WINDOW_FORWARD, q.device)
+    _req_ws(ws, q.device)
+    o = torch.empty_like(q)
+    lse = torch.empty((B, Hq, S), dtype=torch.float32, device=q.device)
+    _check(load_library().msa_window_forward(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v),
+                                             _ptr(o), _ptr(lse), _ptr(ws), ws.numel(),
+                                             _stream(q.device)), "msa_window_forward")
+    return o, lse
+
+
+@_on_tensor_device
+def msa_window_backward(q, k, v, o, lse, dout, window: int, sinks: int, scale: float, ws=None):
+    """Gradients (dq, dk, dv) of sum(o * dout); o, lse from msa_window_forward on the same inputs."""
+    _dims(q, "q", 4)
+    _dims(k, "k", 4)
+    B, S, Hq, D = q.shape
+    Hkv = k.shape[2]
+    for t, n, h in ((q, "q", Hq), (k, "k", Hkv), (v, "v", Hkv), (o, "o", Hq), (dout, "dout", Hq)):
+        _req(t, n, shape=(B, S, h, D))
+    _req(lse, "lse", torch.float32, (B, Hq, S))
+    shape = make_window_shape(q, k, window, sinks, scale)
+    if ws is None:
+        ws = window_workspace(shape, OP_WINDOW_BACKWARD, q.device)
+    _req_ws(ws, q.device)
+    dq, dk, dv = (torch.empty_like(x) for x in (q, k, v))
+    _check(load_library().msa_window_backward(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v),
+                                              _ptr(o), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk),
+                                              _ptr(dv), _ptr(ws), ws.numel(), _stream(q.device)),
+           "msa_window_backward")
+    return dq, dk, dv
+
+
+@_on_tensor_device
+def msa_window_decode(q, k_cache, v_cache, seq_len, window: int, sinks: int, scale: float, ws=None):
+    """Decode step: q [B, Hq, 128] against caches [B, S, Hkv, 128] that already hold the new tokens at
+    seq_len - 1 (seq_len [B] int32 on the device).  Returns (o [B, Hq, 128], lse [B, Hq]); the rows of
+    a sequence whose length is not in 1 .. S are not written (msa_device_status tells)."""
+    _dims(q, "q", 3)
+    _dims(k_cache, "k_cache", 4)
+    B, Hq, D = q.shape
+    S, Hkv = k_cache.shape[1:3]
+    _req(q, "q")
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _req(t, n, shape=(B, S, Hkv, D))
+    _req(seq_len, "seq_len", torch.int32, (B,))
+    shape = make_window_shape(q, k_cache, window, sinks, scale)
+    if ws is None:
+        ws = window_workspace(shape, OP_WINDOW_DECODE, q.device)
+    _req_ws(ws, q.device)
+    o = torch.empty_like(q)
+    lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    _check(load_library().msa_window_decode(ctypes.byref(shape), _ptr(q), _ptr(k_cache),
+                                            _ptr(v_cache), _ptr(seq_len), _ptr(o), _ptr(lse),
+                                            _ptr(ws), ws.numel(), _stream(q.device)),
+           "msa_window_decode")
+    return o, lse
+
+
+class _WindowFunction(torch.autograd.Function):
+    # Workspaces are allocated per call: the caching allocator hands a captured graph memory of its
+    # own, so graphs captured on one stream never share one.
+    @staticmethod
+    def forward(ctx, q, k, v, window, sinks, scale):
+        q, k, v = (x.contiguous() for x in (q, k, v))
+        o, lse = msa_window_forward(q, k, v, window, sinks, scale)
+        ctx.save_for_backward(q, k, v, o, lse)
+        ctx.how = (window, sinks, scale)
+        return o
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, do):
+        q, k, v, o, lse = ctx.saved_tensors
+        return msa_window_backward(q, k, v, o, lse, do.contiguous(), *ctx.how) + (None,) * 3
+
+
+def msa_window_func(Q, K, V, window: int, sinks: int, scale: float):
+    """Sliding-window attention with autograd (msa_window_forward / msa_window_backward); returns
+    attn_out."""
+    return _WindowFunction.apply(Q, K, V, int(window), int(sinks), float(scale))
+
+
+# ---------------------------------------------------------------- norm and rotation of the heads
+def _rows(t, name, B=None, N=None, H=None, write=False):
+    """Checks a part tensor [B, N, H, 128]: rows contiguous, heads 128 apart, batch and token strides
+    free.  Returns its (pointer, batch stride, token stride)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if not t.is_cuda:
+        raise MSAError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise MSAError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 4 or t.shape[3] != 128 or 0 in t.shape:
+        raise MSAError(f"{name} has shape {tuple(t.shape)}, expected [B, N, heads, 128]")
+    want = (B, N, H)
+    if any(w is not None and w != g for w, g in zip(want, t.shape)):
+        raise MSAError(f"{name} has shape {tuple(t.shape)}, expected {want + (128,)}")
+    sb, st, sh, sd = t.stride()
+    if sd != 1 or (t.shape[2] > 1 and sh != 128):
+        raise MSAError(f"{name}: rows must be contiguous and heads 128 elements apart "
+                       f"(strides {t.stride()})")
+    sb, st = sb if t.shape[0] > 1 else 0, st if t.shape[1] > 1 else 0
+    if sb % 8 or st % 8 or t.data_ptr() % 16:
+        raise MSAError(f"{name} must be 16-byte aligned, batch and token strides multiples of 8")
+    if write:
+        row = t.shape[2] * 128  # a token's rows; no two tokens may share memory
+        need = row
+        for stride, n in sorted(x for x in ((sb, t.shape[0]), (st, t.shape[1])) if x[1] > 1):
+            if stride < need:
+                raise MSAError(f"{name} overlaps itself (strides {t.stride()})")
+            need += stride * (n - 1)
+    return t.data_ptr(), sb, st
+
+
+def _rope_parts(xs, weights, rotate, inv_freq, interleaved, eps, positions):
+    """Checks what the norm and rotation entry points share; returns (shape, parts, B, N)."""
+    xs = list(xs)
+    if not 1 <= len(xs) <= ROPE_PARTS:
+        raise MSAError(f"between 1 and {ROPE_PARTS} tensors, got {len(xs)}")
+    weights = [None] * len(xs) if weights is None else list(weights)
+    rotate = [inv_freq is not None] * len(xs) if rotate is None else list(rotate)
+    if len(weights) != len(xs) or len(rotate) != len(xs):
+        raise MSAError(f"{len(xs)} tensors, {len(weights)} weights, {len(rotate)} rotate flags")
+    B, N = (xs[0].shape[0], xs[0].shape[1]) if isinstance(xs[0], torch.Tensor) and xs[0].dim() == 4 else (None, None)
+    parts = (RopePart * len(xs))()
+    for i, (p, x, w, r) in enumerate(zip(parts, xs, weights, rotate)):
+        p.x, p.x_batch, p.x_token = _rows(x, f"xs[{i}]", B, N)
+        if x.device != xs[0].device:
+            raise MSAError(f"xs[{i}] is on {x.device}, xs[0] on {xs[0].device}")
+        if w is not None:
+            _req(w, f"weights[{i}]", torch.float32, (128,))
+            _same(w, f"weights[{i}]", xs[0])
+            p.weight = w.data_ptr()
+        p.heads = x.shape[2]
+        p.flags = ROPE_ROTATE if r else 0
+    rotary = 0
+    if inv_freq is not None:
+        _dims(inv_freq, "inv_freq", 1)
+        _req(inv_freq, "inv_freq", torch.float32)
+        _same(inv_freq, "inv_freq", xs[0])
+        rotary = 2 * inv_freq.numel()
+    elif any(rotate):
+        raise MSAError("inv_freq is needed to rotate")
+    if positions is not None:
+        _req(positions, "positions", torch.int32, (B, N))
+        _same(positions, "positions", xs[0])
+    return RopeShape(B, N, 128, rotary, int(bool(interleaved)), 0, float(eps)), parts, B, N
+
+
+def _same(t, name, x):
+    if t.device != x.device:
+        raise MSAError(f"{name} is on {t.device}, the inputs on {x.device}")
+
+
+def _rope_ws(nparts, op, device, ws):
+    if ws is None:
+        n = int(load_library().msa_norm_rope_workspace_size(nparts, op))
+        return torch.empty(n, dtype=torch.uint8, device=device)
+    _req_ws(ws, device)
+    return ws
+
+
+def _rope_device(xs):
+    if not xs or not isinstance(xs[0], torch.Tensor):
+        raise TypeError("xs must be a sequence of tensors")
+    if not xs[0].is_cuda:
+        raise MSAError("xs[0] must be a CUDA tensor")
+    return torch.cuda.device(xs[0].device)
+
+
+def msa_norm_rope_forward(xs, weights, inv_freq, positions=None, eps: float = 1e-6, rotate=None,
+                          interleaved: bool = False):
+    """RMS norm of every head's row and the position rotation, in one pass over several tensors.
+
+    xs: up to 8 tensors [B, N, heads, 128] bf16 -- q, k, the proxy heads -- usually the slices of one
+    packed projection (``packed.split(heads, 2)``; only rows and heads have to be dense).
+    weights: one fp32 [128] or None (not normed) per tensor.  inv_freq: fp32 [rotary / 2], the first
+    ``rotary`` (a multiple of 16) elements of a row turn by position * inv_freq; None: no rotation.
+    rotate: one truth value per tensor (default: all).  positions: int32 [B, N], default 0 .. N - 1.
+    A tensor without weight and rotation is copied.  Returns contiguous tensors [B, N, heads, 128]."""
+    with _rope_device(xs):
+        shape, parts, B, N = _rope_parts(xs, weights, rotate, inv_freq, interleaved, eps, positions)
+        ys = []
+        for p, x in zip(parts, xs):
+            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            p.y, p.y_batch, p.y_token = y.data_ptr(), y.stride(0), y.stride(1)
+            ys.append(y)
+        _check(load_library().msa_norm_rope_forward(
+            ctypes.byref(shape), parts, len(ys), _ptr(positions), _ptr(inv_freq),
+            _stream(xs[0].device)), "msa_norm_rope_forward")
+        return tuple(ys)
+
+
+def msa_norm_rope_backward(xs, weights, dys, inv_freq, positions=None, eps: float = 1e-6,
+                           rotate=None, interleaved: bool = False, dxs=None, ws=None):
+    """Gradients of msa_norm_rope_forward: (dxs, dweights), dweights fp32 [128] or None per tensor.
+    dxs: where to write them (e.g. the slices of one packed gradient), default new tensors."""
+    with _rope_device(xs):
+        shape, parts, B, N = _rope_parts(xs, weights, rotate, inv_freq, interleaved, eps, positions)
+        if len(dys) != len(xs) or (dxs is not None and len(dxs) != len(xs)):
+            raise MSAError("one dy (and dx, where given) per tensor")
+        dev = xs[0].device
+        dxs = [torch.empty(x.shape, dtype=x.dtype, device=dev) for x in xs] if dxs is None else list(dxs)
+        dws = []
+        for i, (p, x, dy, dx) in enumerate(zip(parts, xs, dys, dxs)):
+            p.y, p.y_batch, p.y_token = _rows(dy, f"dys[{i}]", B, N, x.shape[2])
+            p.dx, p.dx_batch, p.dx_token = _rows(dx, f"dxs[{i}]", B, N, x.shape[2], write=True)
+            _same(dy, f"dys[{i}]", x)
+            _same(dx, f"dxs[{i}]", x)
+            dw = torch.empty(128, dtype=torch.float32, device=dev) if p.weight else None
+            p.dweight = dw.data_ptr() if dw is not None else None
+            dws.append(dw)
+        ws = _rope_ws(len(dxs), OP_NORM_ROPE_BACKWARD, dev, ws)
+        _check(load_library().msa_norm_rope_backward(
+            ctypes.byref(shape), parts, len(dxs), _ptr(positions), _ptr(inv_freq), _ptr(ws),
+            ws.numel(), _stream(dev)), "msa_norm_rope_backward")
+        return tuple(dxs), tuple(dws)
+
+
+def msa_norm_rope_append(xs, weights, inv_freq, seq_len, caches, eps: float = 1e-6, rotate=None,
+                         interleaved: bool = False, ws=None):
+    """Norm and rotation of the newest tokens of sequences of lengths seq_len [B] (int32 on the device),
+    those with a cache written to their rows of it.
+
+    xs: tensors [B, N, heads, 128] (or [B, heads, 128]: one token), token i at position
+    seq_len - N + i.  caches: per tensor a cache [B, S, heads, 128] (one head: also [B, S, 128]) or
+    None.  Returns per tensor its cache, or a new tensor of the shape of x: for (q, k, v, qp, kp) with
+    caches (None, k_cache, v_cache, None, kp_cache) the arguments of msa_decode and
+    msa_window_decode.  Sequences with a length outside N .. S are skipped (msa_device_status of ws
+    tells)."""
+    with _rope_device(xs):
+        flat = [isinstance(x, torch.Tensor) and x.dim() == 3 for x in xs]
+        x4 = [x.unsqueeze(1) if f else x for x, f in zip(xs, flat)]
+        shape, parts, B, N = _rope_parts(x4, weights, rotate, inv_freq, interleaved, eps, None)
+        _req(seq_len, "seq_len", torch.int32, (B,))
+        _same(seq_len, "seq_len", x4[0])
+        if len(caches) != len(xs):
+            raise MSAError("one cache (or None) per tensor")
+        caps = {c.shape[1] for c in caches if isinstance(c, torch.Tensor) and c.dim() >= 3}
+        if len(caps) > 1:
+            raise MSAError(f"caches of different capacities: {sorted(caps)}")
+        shape.capacity = caps.pop() if caps else 2 ** 31 - 1
+        outs = []
+        for i, (p, x, c, f) in enumerate(zip(parts, x4, caches, flat)):
+            if c is None:
+                y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+                p.y, p.y_batch, p.y_token = y.data_ptr(), y.stride(0), y.stride(1)
+                outs.append(y.squeeze(1) if f else y)
+                continue
+            c4 = c.unsqueeze(2) if isinstance(c, torch.Tensor) and c.dim() == 3 else c
+            p.y, p.y_batch, p.y_token = _rows(c4, f"caches[{i}]", B, None, x.shape[2], write=True)
+            _same(c4, f"caches[{i}]", x)
+            p.flags |= ROPE_CACHE
+            outs.append(c)
+        ws = _rope_ws(len(outs), OP_NORM_ROPE_APPEND, x4[0].device, ws)
+        _check(load_library().msa_norm_rope_append(
+            ctypes.byref(shape), parts, len(outs), _ptr(seq_len), _ptr(inv_freq), _ptr(ws),
+            ws.numel(), _stream(x4[0].device)), "msa_norm_rope_append")
+        return tuple(outs)
+
+
+class _NormRopeFunction(torch.autograd.Function):
+    """tensors: the weights that are there, then either one packed x (heads given) or the xs."""
+    @staticmethod
+    def forward(ctx, heads, has_w, inv_freq, positions, eps, rotate, interleaved, *tensors):
+        nw = sum(has_w)
+        given, xs = list(tensors[:nw]), tensors[nw:]
+        weights = [given.pop(0).detach().float().contiguous() if h else None for h in has_w]
+        parts = xs[0].split(heads, 2) if heads is not None else xs
+        ys = msa_norm_rope_forward(parts, weights, inv_freq, positions, eps, rotate, interleaved)
+        ctx.save_for_backward(inv_freq, positions, *xs, *(w for w in weights if w is not None))
+        ctx.how = (heads, has_w, eps, rotate, interleaved, len(xs), [t.dtype for t in tensors[:nw]])
+        return ys
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, *dys):
+        heads, has_w, eps, rotate, interleaved, nx, dtypes = ctx.how
+        inv_freq, positions = ctx.saved_tensors[:2]
+        xs, saved = ctx.saved_tensors[2:2 + nx], list(ctx.saved_tensors[2 + nx:])
+        weights = [saved.pop(0) if h else None for h in has_w]
+        if heads is not None:
+            dx = torch.empty(xs[0].shape, dtype=xs[0].dtype, device=xs[0].device)
+            parts, out = xs[0].split(heads, 2), dx.split(heads, 2)
+        else:
+            parts, out = xs, None
+        dxs, dws = msa_norm_rope_backward(parts, weights, [d.contiguous() for d in dys], inv_freq,
+                                          positions, eps, rotate, interleaved, dxs=out)
+        grads = tuple(w.to(t) for w, t in zip((w for w in dws if w is not None), dtypes))
+        return (None,) * 7 + grads + ((dx,) if heads is not None else dxs)
+
+
+def _norm_rope_apply(heads, xs, weights, inv_freq, positions, eps, rotate, interleaved):
+    n = len(xs) if heads is None else len(heads)
+    weights = [None] * n if weights is None else list(weights)
+    rotate = None if rotate is None else [bool(r) for r in rotate]
+    return _NormRopeFunction.apply(heads, [w is not None for w in weights], inv_freq, positions,
+                                   float(eps), rotate, bool(interleaved),
+                                   *(w for w in weights if w is not None), *xs)
+
+
+def msa_norm_rope_func(xs, weights, inv_freq, positions=None, eps: float = 1e-6, rotate=None,
+                       interleaved: bool = False):
+    """msa_norm_rope_forward with autograd: gradients of the xs and of the weights (any floating dtype;
+    used in fp32)."""
+    return _norm_rope_apply(None, tuple(xs), weights, inv_freq, positions, eps, rotate, interleaved)
+
+
+def msa_norm_rope_packed_func(x, heads, weights, inv_freq, positions=None, eps: float = 1e-6,
+                              rotate=None, interleaved: bool = False):
+    """The same on one packed projection x [B, N, sum(heads), 128]: returns one contiguous tensor per
+    entry of heads; the gradient of x is written packed, without a copy."""
+    return _norm_rope_apply([int(h) for h in heads], (x,), weights, inv_freq, positions, eps, rotate,
+                            interleaved)

@@ -564,6 +564,196 @@ void emit_proxy_grads(const Dims& d, const Plan& p, void* ws, void* dqp, void* d
   timed("grad_convert", st, [&] { launch_convert(at<float>(ws, p.dkp), dkp, (long long)d.B * d.S * kD, st); });
 }
 
+// ---- sliding-window attention
+struct WinPlan {
+  size_t rowm = 0, part = 0, opart = 0, lpart = 0, bytes = 0;
+};
+WinPlan win_plan(const WinDims& d, int op) {
+  WinPlan p;
+  Carver c;
+  c.take(256);  // status word and work counters
+  const size_t rows = (size_t)d.B * d.S * d.Hq;
+  if (op == MSA_OP_WINDOW_BACKWARD) {
+    p.rowm = c.take(rows * sizeof(float2));
+    p.part = c.take((size_t)win_items(d).partials * 2 * kBlock * kD * sizeof(float));
+  }
+  if (op == MSA_OP_WINDOW_DECODE) {
+    const WinSplit w = win_decode_split(d);
+    const size_t n = w.nsplit > 1 ? (size_t)w.nsplit * d.B * d.Hq : 0;
+    p.opart = c.take(n * kD * sizeof(float));
+    p.lpart = c.take(n * sizeof(float));
+  }
+  p.bytes = c.off;
+  return p;
+}
+
+int check_window(const msa_window_shape_t* s, int op, WinDims* out) {
+  if (!s) {
+    set_err("shape is null");
+    return MSA_ERR_INVALID_ARG;
+  }
+  if (s->B < 1 || s->S < 1 || s->Hq < 1 || s->Hkv < 1) {
+    set_err("B, S, Hq and Hkv must be positive");
+    return MSA_ERR_INVALID_ARG;
+  }
+  if (s->window < 1 || s->sinks < 0) {
+    set_err("window must be at least 1 and sinks at least 0");
+    return MSA_ERR_INVALID_ARG;
+  }
+  if (!(s->scale > 0.f) || s->scale > 3e38f) {
+    set_err("scale must be positive and finite");
+    return MSA_ERR_INVALID_ARG;
+  }
+  if (s->D != kD) {
+    set_err("only head dim 128 is supported");
+    return MSA_ERR_UNSUPPORTED;
+  }
+  if (s->S > (1 << 23)) {
+    set_err("S must be at most 2^23");
+    return MSA_ERR_UNSUPPORTED;
+  }
+  const int G = s->Hq % s->Hkv == 0 ? s->Hq / s->Hkv : 0;
+  if (!(G == 1 || G == 2 || G == 4 || G == 8 || G == 16)) {
+    set_err("Hq / Hkv must be 1, 2, 4, 8 or 16");
+    return MSA_ERR_UNSUPPORTED;
+  }
+  // TMA strides are below 2^40 bytes; grids and item numbers are 32-bit
+  if ((long long)s->S * s->Hq >= (1ll << 32) || (long long)s->B * s->Hq >= (1ll << 22) ||
+      (op != MSA_OP_WINDOW_DECODE && (long long)s->B * s->S * s->Hq >= (1ll << 31))) {
+    set_err("S*Hq must stay below 2^32, B*Hq below 2^22 and (not in decode) B*S*Hq below 2^31");
+    return MSA_ERR_UNSUPPORTED;
+  }
+  WinDims d;
+  d.B = s->B;
+  d.S = s->S;
+  d.Hq = s->Hq;
+  d.Hkv = s->Hkv;
+  d.G = G;
+  d.W = s->window < s->S ? s->window : s->S;
+  d.ns = d.W == s->S ? 0 : s->sinks < s->S ? s->sinks : s->S;  // (a full window holds the sinks)
+  d.nsp = (d.ns + 7) / 8 * 8;
+  d.scale = s->scale;
+  *out = d;
+  return MSA_OK;
+}
+
+int check_ws_bytes(size_t need, void* ws, size_t bytes) {
+  Plan p;
+  p.bytes = need;
+  return check_ws(p, ws, bytes);
+}
+
+// ---- norm and rotation
+constexpr size_t kRopeStatus = 256;
+size_t rope_ws(int nparts, int op) {
+  if (nparts < 1 || nparts > kRopeParts) return 0;
+  if (op == MSA_OP_NORM_ROPE_APPEND) return kRopeStatus;
+  if (op == MSA_OP_NORM_ROPE_BACKWARD)
+    return kRopeStatus + up((size_t)rope_partials() * nparts * kD * sizeof(float));
+  return 0;
+}
+
+// op: MSA_OP_NORM_ROPE_BACKWARD, MSA_OP_NORM_ROPE_APPEND, or -1 for the forward
+int check_rope(const msa_rope_shape_t* s, const msa_rope_part_t* parts, int nparts, const int32_t* pos,
+               const float* inv_freq, int op, RopeArgs* out) {
+  if (!s || !parts) {
+    set_err("shape or parts is null");
+    return MSA_ERR_INVALID_ARG;
+  }
+  if (s->B < 1 || s->N < 1 || nparts < 1) {
+    set_err("B, N and the number of parts must be positive");
+    return MSA_ERR_INVALID_ARG;
+  }
+  if (!(s->eps >= 0.f) || s->eps > 3e38f) {
+    set_err("eps must be finite and not negative");
+    return MSA_ERR_INVALID_ARG;
+  }
+  if (nparts > kRopeParts) {
+    set_err("at most 8 parts");
+    return MSA_ERR_UNSUPPORTED;
+  }
+  if (s->D != kD) {
+    set_err("only head dim 128 is supported");
+    return MSA_ERR_UNSUPPORTED;
+  }
+  if (s->rotary < 0 || s->rotary > kD || s->rotary % 16 != 0) {
+    set_err("rotary must be a multiple of 16 in 0 .. 128");
+    return MSA_ERR_UNSUPPORTED;
+  }
+  if ((long long)s->B * s->N >= (1ll << 31)) {
+    set_err("B*N must stay below 2^31");
+    return MSA_ERR_UNSUPPORTED;
+  }
+  RopeArgs a;
+  memset(&a, 0, sizeof(a));
+  a.B = s->B;
+  a.N = s->N;
+  a.rot = s->rotary;
+  a.inter = s->interleaved != 0;
+  a.nparts = nparts;
+  a.eps = s->eps;
+  int rc;
+  if (op == MSA_OP_NORM_ROPE_APPEND) {
+    if ((rc = check_ptrs({pos}))) return rc;
+    if (s->capacity < s->N) {
+      set_err("capacity must be at least N");
+      return MSA_ERR_INVALID_ARG;
+    }
+    a.cap = s->capacity;
+    a.seq_len = pos;
+  } else {
+    if (pos && (rc = check_ptrs({pos}))) return rc;
+    a.positions = pos;
+  }
+  if (a.rot > 0 && (rc = check_ptrs({inv_freq}))) return rc;
+  a.inv_freq = inv_freq;
+  for (int i = 0; i < nparts; ++i) {
+    const msa_rope_part_t& p = parts[i];
+    RopePart& o = a.p[i];
+    const bool bwd = op == MSA_OP_NORM_ROPE_BACKWARD;
+    if ((rc = check_ptrs({p.x, p.y})) || (bwd && (rc = check_ptrs({p.dx}))) ||
+        (p.weight && (rc = check_ptrs({p.weight}))) || (bwd && p.dweight && (rc = check_ptrs({p.dweight}))))
+      return rc;
+    if (p.heads < 1 || p.heads > 1024) {
+      set_err("a part has 1 .. 1024 heads");
+      return MSA_ERR_UNSUPPORTED;
+    }
+    if ((p.flags & ~(MSA_ROPE_ROTATE | MSA_ROPE_CACHE)) ||
+        ((p.flags & MSA_ROPE_CACHE) && op != MSA_OP_NORM_ROPE_APPEND)) {
+      set_err("unknown part flag, or MSA_ROPE_CACHE outside msa_norm_rope_append");
+      return MSA_ERR_INVALID_ARG;
+    }
+    if (bwd && p.dweight && !p.weight) {
+      set_err("dweight of a part without a weight");
+      return MSA_ERR_INVALID_ARG;
+    }
+    if (p.x_batch % 8 || p.x_token % 8 || p.y_batch % 8 || p.y_token % 8 ||
+        (bwd && (p.dx_batch % 8 || p.dx_token % 8))) {
+      set_err("strides must be multiples of 8 elements");
+      return MSA_ERR_INVALID_ARG;
+    }
+    o.x = static_cast<const bf16*>(p.x);
+    o.xb = p.x_batch;
+    o.xt = p.x_token;
+    o.y = static_cast<bf16*>(p.y);
+    o.yb = p.y_batch;
+    o.yt = p.y_token;
+    if (bwd) {
+      o.dx = static_cast<bf16*>(p.dx);
+      o.dxb = p.dx_batch;
+      o.dxt = p.dx_token;
+      o.dw = p.dweight;
+    }
+    o.w = p.weight;
+    o.H = p.heads;
+    o.flags = ((p.flags & MSA_ROPE_ROTATE) && a.rot > 0 ? kRopeRotate : 0) |
+              (p.flags & MSA_ROPE_CACHE ? kRopeCache : 0);
+    a.rows += p.heads;
+  }
+  *out = a;
+  return MSA_OK;
+}
+
 }  // namespace
 
 // Sets the text msa_last_error() returns on this thread (used by entry points in other files).
@@ -875,6 +1065,133 @@ int msa_decode(const msa_shape_t* shape, const void* q, const void* qp, const vo
     return MSA_ERR_CUDA;
   }
   return cuda_fail("msa_decode");
+}
+
+size_t msa_window_workspace_size(const msa_window_shape_t* shape, int op) {
+  WinDims d;
+  if (op < MSA_OP_WINDOW_FORWARD || op > MSA_OP_WINDOW_DECODE) {
+    set_err("not a window op");
+    return 0;
+  }
+  if (check_window(shape, op, &d) != MSA_OK) return 0;
+  return win_plan(d, op).bytes;
+}
+
+int msa_window_forward(const msa_window_shape_t* shape, const void* q, const void* k, const void* v,
+                       void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  WinDims d;
+  int rc = check_window(shape, MSA_OP_WINDOW_FORWARD, &d);
+  if (rc) return rc;
+  if ((rc = check_ptrs({q, k, v, o, lse}))) return rc;
+  if ((rc = check_ws_bytes(win_plan(d, MSA_OP_WINDOW_FORWARD).bytes, workspace, workspace_bytes))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaGetLastError();
+  unsigned* status = at<unsigned>(workspace, 0);
+  cudaMemsetAsync(status, 0, 32 * sizeof(unsigned), st);  // status, counters, wait place
+  bool ok = true;
+  timed("win_fwd", st, [&] { ok = launch_win_fwd(d, q, k, v, o, lse, status, st); });
+  if (!ok) {
+    set_err("msa_window_forward: could not create TMA tensor maps (cuTensorMapEncodeTiled)");
+    return MSA_ERR_CUDA;
+  }
+  return cuda_fail("msa_window_forward");
+}
+
+int msa_window_backward(const msa_window_shape_t* shape, const void* q, const void* k, const void* v,
+                        const void* o, const float* lse, const void* dout, void* dq, void* dk,
+                        void* dv, void* workspace, size_t workspace_bytes, void* stream) {
+  WinDims d;
+  int rc = check_window(shape, MSA_OP_WINDOW_BACKWARD, &d);
+  if (rc) return rc;
+  if ((rc = check_ptrs({q, k, v, o, lse, dout, dq, dk, dv}))) return rc;
+  const WinPlan p = win_plan(d, MSA_OP_WINDOW_BACKWARD);
+  if ((rc = check_ws_bytes(p.bytes, workspace, workspace_bytes))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaGetLastError();
+  unsigned* status = at<unsigned>(workspace, 0);
+  cudaMemsetAsync(status, 0, 32 * sizeof(unsigned), st);  // status, counters, wait place
+  Dims rows{};
+  rows.B = d.B;
+  rows.S = d.S;
+  rows.Hq = d.Hq;
+  timed("bwd_rowdot", st, [&] { launch_bwd_rowdot(rows, o, dout, lse, at<float2>(workspace, p.rowm), st); });
+  bool ok = true;
+  timed("win_bwd", st, [&] {
+    ok = launch_win_bwd(d, q, k, v, dout, at<float2>(workspace, p.rowm), dq, dk, dv,
+                        at<float>(workspace, p.part), status, st);
+  }, win_items(d).join_blocks ? 3 : 2);
+  if (!ok) {
+    set_err("msa_window_backward: could not create TMA tensor maps (cuTensorMapEncodeTiled)");
+    return MSA_ERR_CUDA;
+  }
+  return cuda_fail("msa_window_backward");
+}
+
+int msa_window_decode(const msa_window_shape_t* shape, const void* q, const void* k_cache,
+                      const void* v_cache, const int32_t* seq_len, void* o, float* lse,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+  WinDims d;
+  int rc = check_window(shape, MSA_OP_WINDOW_DECODE, &d);
+  if (rc) return rc;
+  if ((rc = check_ptrs({q, k_cache, v_cache, seq_len, o, lse}))) return rc;
+  const WinPlan p = win_plan(d, MSA_OP_WINDOW_DECODE);
+  if ((rc = check_ws_bytes(p.bytes, workspace, workspace_bytes))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaGetLastError();
+  unsigned* status = at<unsigned>(workspace, 0);
+  cudaMemsetAsync(status, 0, 32 * sizeof(unsigned), st);  // status, counters, wait place
+  bool ok = true;
+  timed("win_decode", st, [&] {
+    ok = launch_win_decode(d, q, k_cache, v_cache, seq_len, o, lse, at<float>(workspace, p.opart),
+                           at<float>(workspace, p.lpart), status, st);
+  }, win_decode_split(d).nsplit > 1 ? 2 : 1);
+  if (!ok) {
+    set_err("msa_window_decode: could not create TMA tensor maps (cuTensorMapEncodeTiled)");
+    return MSA_ERR_CUDA;
+  }
+  return cuda_fail("msa_window_decode");
+}
+
+size_t msa_norm_rope_workspace_size(int nparts, int op) { return rope_ws(nparts, op); }
+
+int msa_norm_rope_forward(const msa_rope_shape_t* shape, const msa_rope_part_t* parts, int nparts,
+                          const int32_t* positions, const float* inv_freq, void* stream) {
+  RopeArgs a;
+  const int rc = check_rope(shape, parts, nparts, positions, inv_freq, -1, &a);
+  if (rc) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaGetLastError();
+  timed("norm_rope_fwd", st, [&] { launch_norm_rope_fwd(a, st); });
+  return cuda_fail("msa_norm_rope_forward");
+}
+
+int msa_norm_rope_append(const msa_rope_shape_t* shape, const msa_rope_part_t* parts, int nparts,
+                         const int32_t* seq_len, const float* inv_freq, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  RopeArgs a;
+  int rc = check_rope(shape, parts, nparts, seq_len, inv_freq, MSA_OP_NORM_ROPE_APPEND, &a);
+  if (rc) return rc;
+  if ((rc = check_ws_bytes(kRopeStatus, workspace, workspace_bytes))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaGetLastError();
+  a.status = at<unsigned>(workspace, 0);  // written whole by the kernel
+  timed("norm_rope_append", st, [&] { launch_norm_rope_fwd(a, st); });
+  return cuda_fail("msa_norm_rope_append");
+}
+
+int msa_norm_rope_backward(const msa_rope_shape_t* shape, const msa_rope_part_t* parts, int nparts,
+                           const int32_t* positions, const float* inv_freq, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  RopeArgs a;
+  int rc = check_rope(shape, parts, nparts, positions, inv_freq, MSA_OP_NORM_ROPE_BACKWARD, &a);
+  if (rc) return rc;
+  if ((rc = check_ws_bytes(rope_ws(nparts, MSA_OP_NORM_ROPE_BACKWARD), workspace, workspace_bytes))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaGetLastError();
+  a.status = at<unsigned>(workspace, 0);
+  a.partial = at<float>(workspace, kRopeStatus);
+  timed("norm_rope_bwd", st, [&] { launch_norm_rope_bwd(a, st); }, 2);
+  return cuda_fail("msa_norm_rope_backward");
 }
 
 int msa_device_status(void* workspace, unsigned* flags, void* stream) {

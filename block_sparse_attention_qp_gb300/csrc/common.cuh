@@ -25,6 +25,7 @@ constexpr int kSchedProxyBwd = 9;
 constexpr int kSchedAttnFwd = 10;
 constexpr int kSchedProxyLse = 11;
 constexpr int kSchedDenseFwd = 12;
+constexpr int kSchedWinDkv = 13;
 // Word 16: the id of the first bounded wait that gave up, in kernels that record it (0: none).
 constexpr int kStatusWhere = 16;
 

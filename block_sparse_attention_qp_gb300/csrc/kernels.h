@@ -1,5 +1,6 @@
 // Internal interface between the C-ABI layer (api.cu) and the kernel files.
 #pragma once
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -150,6 +151,70 @@ void launch_decode_select(const Dims& d, const float* scores, const int32_t* seq
 bool launch_decode_attn(const Dims& d, const void* q, const void* k_cache, const void* v_cache,
                         const int32_t* seq_len, const int32_t* block_idx, void* o, float* lse,
                         unsigned* status, cudaStream_t st);  // false: no tensor map
+
+// ------------------------------------------- norm and rotation of the heads (norm_rope.cu)
+constexpr int kRopeRotate = 1, kRopeCache = 2;  // RopePart::flags
+constexpr int kRopeParts = 8;                   // parts of one call at most
+// One part: H consecutive heads (128 elements apart) of every token, with its own norm weight.
+struct RopePart {
+  const __nv_bfloat16* x;  // [B][N][H][128], batch and token strides in elements
+  long long xb, xt;
+  __nv_bfloat16* y;  // forward: the output (kRopeCache: its rows by position); backward: dy (read)
+  long long yb, yt;
+  __nv_bfloat16* dx;
+  long long dxb, dxt;
+  const float* w;  // [128], NULL: not normed
+  float* dw;       // [128] or NULL
+  int H, flags;
+};
+struct RopeArgs {
+  int B, N, rot, inter, nparts, rows;  // rows: heads of all parts
+  int cap;                             // append: rows of a cache
+  float eps;
+  const int32_t* positions;  // [B][N] or NULL: 0 .. N - 1
+  const int32_t* seq_len;    // append: [B], the new tokens are the last N of it
+  const float* inv_freq;     // [rot / 2]
+  unsigned* status;          // append, backward: written whole by the call
+  float* partial;            // backward: [rope_partials()][nparts][128]
+  int rows_chunk, chunks;    // set by the launch
+  RopePart p[kRopeParts];
+};
+int rope_partials();
+void launch_norm_rope_fwd(RopeArgs a, cudaStream_t st);
+void launch_norm_rope_bwd(RopeArgs a, cudaStream_t st);  // two kernels
+
+// ------------------------------------------- sliding-window attention (window.cuh, win_*.cu)
+struct WinDims {
+  int B, S, Hq, Hkv, G;
+  int W, ns, nsp;  // window and sinks, at most S; nsp: the sinks rounded up to a multiple of 8
+  float scale;
+};
+// Causal attention over the window and the sinks; q, o [B, S, Hq, 128], k, v [B, S, Hkv, 128], lse
+// [B, Hq, S].  The launches return false if a tensor map could not be made.
+bool launch_win_fwd(const WinDims& d, const void* q, const void* k, const void* v, void* o,
+                    float* lse, unsigned* status, cudaStream_t st);
+
+// Work items of the key-outer backward: first the sink blocks' chunks, then the window blocks'.
+struct WinItems {
+  int sink_blocks, sink_chunk, sink_items;  // key blocks that hold sinks; query tiles per item
+  int win_chunk, win_split;                 // window blocks: tiles per item, items per block
+  int items, partials, join_blocks;         // partial slots (2 x 128 x 128 fp32); blocks to join
+};
+WinItems win_items(const WinDims& d);
+// dq, dk, dv from rowm (launch_bwd_rowdot) and `part`, win_items(d).partials slots.
+bool launch_win_bwd(const WinDims& d, const void* q, const void* k, const void* v, const void* dout,
+                    const float2* rowm, void* dq, void* dk, void* dv, float* part, unsigned* status,
+                    cudaStream_t st);
+
+// Decode step over caches of capacity d.S: key tiles per split and splits; opart [nsplit][B][Hq][128],
+// lpart [nsplit][B][Hq] (used when nsplit > 1).
+struct WinSplit {
+  int nsplit, tiles;
+};
+WinSplit win_decode_split(const WinDims& d);
+bool launch_win_decode(const WinDims& d, const void* q, const void* k_cache, const void* v_cache,
+                       const int32_t* seq_len, void* o, float* lse, float* opart, float* lpart,
+                       unsigned* status, cudaStream_t st);
 
 int num_sms();
 void set_api_error(const char* what);

@@ -36,6 +36,21 @@ inline bool make_tmap_bf16(CUtensorMap* m, const void* base, int rank, const uin
   return r == CUDA_SUCCESS;
 }
 
+// bf16 rows [B][S][H][128] (contiguous): box of 64 columns x `heads` x `rows` tokens of one sequence,
+// landing as rows * heads rows of 128 bytes, 128-byte swizzled.  Tokens past S read as zero and are
+// not written.
+inline bool make_tmap_rows(CUtensorMap* m, const void* base, int B, int S, int H, int heads, int rows) {
+  auto enc = tmap_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[4] = {128, (cuuint64_t)H, (cuuint64_t)S, (cuuint64_t)B};
+  const cuuint64_t str[3] = {256, (cuuint64_t)H * 256, (cuuint64_t)S * H * 256};
+  const cuuint32_t box[4] = {64, (cuuint32_t)heads, (cuuint32_t)rows, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, str, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Tensor of fp32 rows of 128 elements, unswizzled (for TMA reductions from row-major staging):
 // dims (128, d1, d2) with byte strides s1, s2; box (b0, b1, b2).
 inline bool make_tmap_f32(CUtensorMap* m, const void* base, const uint64_t* dims,

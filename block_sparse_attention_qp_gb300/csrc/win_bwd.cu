@@ -1,0 +1,900 @@
+// Backward of causal attention over a sliding window and the first tokens (geometry: window.cuh), on
+// the tcgen05 tensor cores.  With P = exp(scale QK^T - LSE) over the visible pairs, dP = dO V^T and
+// D = rowsum(dO O) (rowdot_kernel in bwd.cu):
+//   dS = scale P (dP - D),  dV = P^T dO,  dK = dS^T Q,  dQ = dS K.
+//
+// Two kernels, each with its sums in tensor memory and no atomics, so a gradient has the same bits
+// every time and nothing is accumulated in memory; the price is S and dP computed twice (7 products
+// a tile pair instead of 5):
+//   win_dkv_kernel  key-outer: an item is one 128-key block and up to `chunk` of the 128-row query
+//                   tiles that see it (a tile: 128/G consecutive tokens x G heads).  A block with one
+//                   chunk writes its dK and dV rows; the chunks of a longer list (a sink block is
+//                   seen by the whole sequence) write fp32 partials that win_join_kernel adds in order.
+//   win_dq_kernel   query-outer over the key tiles of the forward's virtual walk.
+// Both split the softmax of a tile in two phases, so that the tensor core works through each of them:
+//   A  P from S alone, as soon as S is there (kept in fp32 registers for phase B)
+//   B  dS from P and dP.
+// win_dkv: ... dV(i) S(i+1) | dK(i) dP(i+1) ...: the first pair runs behind phase B of tile i, the
+// second behind phase A of tile i+1, and each phase waits for the pair before it only.  P^T and dS^T
+// (bf16) overwrite S^T and dP^T in tensor memory and are the products' A operands from there.
+// win_dq:  ... S(n+1) | dQ(n) dP(n+1) ...: S(n+1) runs behind phase B of tile n (P is in registers by
+// then), the pair behind phase A of n+1; dS overwrites dP, dQ has two buffers for two units.
+// P and dS are rounded to bf16 for their products (2^-9 relative each), the softmax scale is folded
+// into dS, everything else is fp32.  Bound by the tensor core: 32 (dkv) and 24 (dq) instructions of
+// 128 x 128 x 16 a tile pair, about 83 cycles each.
+//
+// Roles of both (384 threads): warp 0 TMA loads, warp 1 MMA issue, warp 2 the tile's row data (dkv)
+// or the TMA stores of dQ (dq), warps 4-11 softmax and epilogue: two per tensor-memory lane quarter,
+// one per half of the tile's columns.  Every wait is bounded.
+#include <math.h>
+
+#include "tmap.h"
+#include "window.cuh"
+
+namespace msa {
+namespace {
+
+constexpr int kTile = 128 * 128 * 2;  // 128 rows x 128 bf16, two SW128 panels
+constexpr int kItemRing = 4, kMetaRing = 4, kSoft = 8;
+
+struct DkvArgs {
+  WinDims d;
+  CUtensorMap q, dout, k, v;
+  const float2* rowm;  // {LSE log2 e, D} per query row [B, S, Hq]
+  bf16 *dk, *dv;
+  float* part;  // [slot][2: dV, dK][128 keys][128]
+  unsigned* status;
+  int* sched;
+  WinItems it;
+};
+struct DkvShared {
+  float nlse2[kMetaRing][128], ndrow[kMetaRing][128];  // -(LSE log2 e), -(D scale) per tile row
+  int it_ring[kItemRing];
+  uint64_t k_full, v_full, kv_empty, q_full[2], q_empty[2], do_full[2], do_empty[2], m_full[kMetaRing],
+      m_empty[kMetaRing], s_full, dp_full, pa, pb, acc_full, acc_free, it_full[kItemRing],
+      it_empty[kItemRing], mma_done;
+  uint32_t tmem;
+};
+
+// Item number -> key block n of (b, g) and its query tiles [i0, i1) (empty: i0 >= i1); slot: where its
+// partial goes, -1 when the block has no other item.
+struct DkvItem {
+  int b, g, n, i0, i1, slot;
+};
+template <int G>
+__device__ __forceinline__ int block_tiles(const WinDims& d, int n) {  // query tiles that see block n
+  const int k0 = n * kBlock;
+  long long last = (long long)k0 + kBlock - 1 + d.W - 1;  // the last query of the block's last key
+  if (k0 < d.ns || last >= d.S) last = d.S - 1;
+  return (int)((last - k0) / (128 / G)) + 1;
+}
+template <int G>
+__device__ __forceinline__ DkvItem dkv_item(const WinDims& d, const WinItems& w, int it) {
+  DkvItem x;
+  const int per = d.B * d.Hkv;
+  int c, chunk, bh;
+  if (it < w.sink_items) {  // chunk-major: concurrent items share query tiles
+    c = it / (w.sink_blocks * per);
+    const int rem = it % (w.sink_blocks * per);
+    x.n = rem / per;
+    bh = rem % per;
+    chunk = w.sink_chunk;
+  } else {
+    const int j = it - w.sink_items;
+    x.n = w.sink_blocks + j / (w.win_split * per);
+    c = j / per % w.win_split;
+    bh = j % per;
+    chunk = w.win_chunk;
+  }
+  x.b = bh / d.Hkv;
+  x.g = bh % d.Hkv;
+  const int nt = block_tiles<G>(d, x.n);
+  x.i0 = c * chunk;
+  x.i1 = x.i0 + chunk < nt ? x.i0 + chunk : nt;
+  x.slot = nt > chunk ? it : -1;
+  return x;
+}
+
+}  // namespace
+
+template <int G>
+__global__ void __launch_bounds__(384, 1) win_dkv_kernel(const __grid_constant__ DkvArgs A) {
+  using namespace sm100;
+  constexpr int TT = 128 / G;
+  const WinDims& d = A.d;
+  extern __shared__ uint8_t smem_raw[];
+  DkvShared* sh = reinterpret_cast<DkvShared*>(smem_raw);
+  uint8_t* sK = align1024(smem_raw + sizeof(DkvShared));
+  uint8_t* sV = sK + kTile;
+  uint8_t* sQ = sV + kTile;       // [2] query tiles
+  uint8_t* sD = sQ + 2 * kTile;   // [2] dO tiles
+  const uint32_t aK = smem_u32(sK), aV = smem_u32(sV), aQ = smem_u32(sQ), aD = smem_u32(sD);
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int total = A.it.items;
+
+  if (tid == 0) {
+    mbar_init(&sh->k_full, 1);
+    mbar_init(&sh->v_full, 1);
+    mbar_init(&sh->kv_empty, 1);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&sh->q_full[x], 1);
+      mbar_init(&sh->q_empty[x], 1);
+      mbar_init(&sh->do_full[x], 1);
+      mbar_init(&sh->do_empty[x], 1);
+    }
+    for (int x = 0; x < kMetaRing; ++x) {
+      mbar_init(&sh->m_full[x], 1);
+      mbar_init(&sh->m_empty[x], kSoft);
+    }
+    for (int x = 0; x < kItemRing; ++x) {
+      mbar_init(&sh->it_full[x], 1);
+      mbar_init(&sh->it_empty[x], 2 + kSoft);  // MMA, row data, softmax warps
+    }
+    mbar_init(&sh->s_full, 1);
+    mbar_init(&sh->dp_full, 1);
+    mbar_init(&sh->pa, kSoft);
+    mbar_init(&sh->pb, kSoft);
+    mbar_init(&sh->acc_full, 1);
+    mbar_init(&sh->acc_free, kSoft);
+    mbar_init(&sh->mma_done, 1);
+    mbar_fence_init();
+  }
+  if (warp == 0) {
+    __syncwarp();  // lane 0 initialised the barriers alone; the allocation is warp-collective
+    tmem_alloc(&sh->tmem, 512);
+    tmem_relinquish();
+  }
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t SB = sh->tmem, DB = SB + 128, RV = SB + 256, RK = SB + 384;
+  // item number k of this block (handed out in list order to whichever block asks next)
+  auto take1 = [&](long long k, int& v) -> bool {
+    const int x = (int)(k % kItemRing);
+    if (!mbar_wait(&sh->it_full[x], phase_of(k / kItemRing), A.status)) return false;
+    v = sh->it_ring[x];
+    mbar_arrive(&sh->it_empty[x]);
+    return true;
+  };
+  auto takew = [&](long long k, int& v) -> bool {
+    const int x = (int)(k % kItemRing);
+    if (!mbar_wait_warp(&sh->it_full[x], phase_of(k / kItemRing), A.status)) return false;
+    v = sh->it_ring[x];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh->it_empty[x]);
+    return true;
+  };
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- items + TMA loads
+    if (lane == 0) {
+      long long nk = 0, i = 0;  // items with tiles, tiles
+      bool ok = true;
+      for (long long k = 0; ok; ++k) {
+        const int x = (int)(k % kItemRing);
+        if (k >= kItemRing && !mbar_wait(&sh->it_empty[x], phase_of(k / kItemRing - 1), A.status)) break;
+        const int v = atomicAdd(A.sched, 1);
+        sh->it_ring[x] = v;
+        mbar_arrive(&sh->it_full[x]);
+        if (v >= total) break;
+        const DkvItem t = dkv_item<G>(d, A.it, v);
+        if (t.i0 >= t.i1) continue;
+        if (nk > 0 && !mbar_wait(&sh->kv_empty, phase_of(nk - 1), A.status)) break;
+        ++nk;
+        mbar_expect_tx(&sh->k_full, kTile);
+        mbar_expect_tx(&sh->v_full, kTile);
+        for (int c = 0; c < 2; ++c)
+          tma_load_rows(sK + c * (kTile / 2), &A.k, 64 * c, t.g, t.n * kBlock, t.b, &sh->k_full);
+        for (int c = 0; c < 2; ++c)
+          tma_load_rows(sV + c * (kTile / 2), &A.v, 64 * c, t.g, t.n * kBlock, t.b, &sh->v_full);
+        for (int tl = t.i0; tl < t.i1; ++tl, ++i) {
+          const int s = (int)(i & 1), tok = t.n * kBlock + tl * TT;
+          if (i >= 2 && !mbar_wait(&sh->q_empty[s], phase_of(i / 2 - 1), A.status)) { ok = false; break; }
+          mbar_expect_tx(&sh->q_full[s], kTile);
+          for (int c = 0; c < 2; ++c)
+            tma_load_rows(sQ + s * kTile + c * (kTile / 2), &A.q, 64 * c, t.g * G, tok, t.b, &sh->q_full[s]);
+          if (i >= 2 && !mbar_wait(&sh->do_empty[s], phase_of(i / 2 - 1), A.status)) { ok = false; break; }
+          mbar_expect_tx(&sh->do_full[s], kTile);
+          for (int c = 0; c < 2; ++c)
+            tma_load_rows(sD + s * kTile + c * (kTile / 2), &A.dout, 64 * c, t.g * G, tok, t.b, &sh->do_full[s]);
+        }
+      }
+      // no copy may still be landing in shared memory when the block exits
+      if (nk > 0) {
+        mbar_wait(&sh->k_full, phase_of(nk - 1), A.status);
+        mbar_wait(&sh->v_full, phase_of(nk - 1), A.status);
+      }
+      for (long long x = i >= 2 ? i - 2 : 0; x < i; ++x) {
+        mbar_wait(&sh->q_full[x & 1], phase_of(x >> 1), A.status);
+        mbar_wait(&sh->do_full[x & 1], phase_of(x >> 1), A.status);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issue
+    if (lane == 0) {
+      constexpr uint32_t id_s = idesc_bf16(128, 128, false, false);  // S^T = K Q^T, dP^T = V dO^T
+      constexpr uint32_t id_g = idesc_bf16(128, 128, false, true);   // dV = P^T dO, dK = dS^T Q
+      long long nk = 0, i = 0;
+      bool ok = true;
+      auto mma_s = [&](long long j) -> bool {
+        const int s = (int)(j & 1);
+        if (!mbar_wait(&sh->q_full[s], phase_of(j >> 1), A.status)) return false;
+        fence_after_sync();
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          mma_ss(SB, desc_kmajor(aK, 128, ks), desc_kmajor(aQ + s * kTile, 128, ks), id_s, ks > 0);
+        mma_commit(&sh->s_full);
+        return true;
+      };
+      auto mma_dp = [&](long long j) -> bool {
+        const int s = (int)(j & 1);
+        if (!mbar_wait(&sh->do_full[s], phase_of(j >> 1), A.status)) return false;
+        fence_after_sync();
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          mma_ss(DB, desc_kmajor(aV, 128, ks), desc_kmajor(aD + s * kTile, 128, ks), id_s, ks > 0);
+        mma_commit(&sh->dp_full);
+        return true;
+      };
+      for (long long k = 0; ok; ++k) {
+        int v;
+        if (!take1(k, v) || v >= total) break;
+        const DkvItem t = dkv_item<G>(d, A.it, v);
+        if (t.i0 >= t.i1) continue;
+        const int n = t.i1 - t.i0;
+        // P^T and dS^T of the previous item's last tile were read by products issued before these
+        ok = mbar_wait(&sh->k_full, phase_of(nk), A.status) && mma_s(i) &&
+             mbar_wait(&sh->v_full, phase_of(nk), A.status) && mma_dp(i);
+        for (int tl = 0; tl < n && ok; ++tl, ++i) {
+          const int s = (int)(i & 1);
+          // phase A has written P^T over S^T
+          if (!mbar_wait(&sh->pa, phase_of(i), A.status)) { ok = false; break; }
+          if (tl == 0 && nk > 0 && !mbar_wait(&sh->acc_free, phase_of(nk - 1), A.status)) { ok = false; break; }
+          fence_after_sync();
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)  // rows 0-63 in columns 0-31, rows 64-127 in 64-95
+            mma_ts(RV, SB + ks * 8 + (ks >= 4 ? 32 : 0), desc_mnmajor(aD + s * kTile, 128, ks), id_g,
+                   tl > 0 || ks > 0);
+          mma_commit(&sh->do_empty[s]);
+          if (tl + 1 < n && !mma_s(i + 1)) { ok = false; break; }
+          // phase B has written dS^T over dP^T
+          if (!mbar_wait(&sh->pb, phase_of(i), A.status)) { ok = false; break; }
+          fence_after_sync();
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            mma_ts(RK, DB + ks * 8 + (ks >= 4 ? 32 : 0), desc_mnmajor(aQ + s * kTile, 128, ks), id_g,
+                   tl > 0 || ks > 0);
+          mma_commit(&sh->q_empty[s]);
+          if (tl + 1 < n && !mma_dp(i + 1)) { ok = false; break; }
+        }
+        if (!ok) break;
+        mma_commit(&sh->acc_full);
+        mma_commit(&sh->kv_empty);
+        ++nk;
+      }
+      mma_commit(&sh->mma_done);
+      mbar_wait(&sh->mma_done, 0, A.status);  // no product may still write tensor memory
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ---------------------------------------------------------------- row data of the tiles
+    long long i = 0;
+    bool ok = true;
+    for (long long k = 0; ok; ++k) {
+      int v;
+      if (!takew(k, v) || v >= total) break;
+      const DkvItem t = dkv_item<G>(d, A.it, v);
+      for (int tl = t.i0; tl < t.i1; ++tl, ++i) {
+        const int s = (int)(i % kMetaRing), tok = t.n * kBlock + tl * TT;
+        float2 m[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = lane + 32 * e, q = tok + r / G;
+          m[e] = q < d.S ? __ldg(A.rowm + ((long long)t.b * d.S + q) * d.Hq + t.g * G + r % G)
+                         : make_float2(0.f, 0.f);
+        }
+        if (i >= kMetaRing && !mbar_wait_warp(&sh->m_empty[s], phase_of(i / kMetaRing - 1), A.status)) {
+          ok = false;
+          break;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sh->nlse2[s][lane + 32 * e] = -m[e].x;
+          sh->ndrow[s][lane + 32 * e] = -m[e].y * d.scale;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->m_full[s]);
+      }
+    }
+  } else if (warp >= 4) {
+    // ---------------------------------------------------------------- softmax (thread = key)
+    const int hf = (warp - 4) >> 2;  // rows 64 hf .. 64 hf + 63 of the tile
+    const int quad = warp & 3;
+    const int kr = quad * 32 + lane;  // key row = tensor-memory lane
+    const uint32_t lb = static_cast<uint32_t>(quad * 32) << 16;
+    const float sl2 = d.scale * kLog2e;
+    const float2 sl2x2 = make_float2(sl2, sl2), sc2 = make_float2(d.scale, d.scale);
+    long long nk = 0, i = 0;
+    bool ok = true;
+    for (long long k = 0; ok; ++k) {
+      int v;
+      if (!takew(k, v) || v >= total) break;
+      const DkvItem t = dkv_item<G>(d, A.it, v);
+      if (t.i0 >= t.i1) continue;
+      const int j = t.n * kBlock + kr;  // this thread's key
+      // queries that see it: j .. tmax
+      const int tmax = j >= d.S ? -1 : j < d.ns || j + d.W - 1 >= d.S ? d.S - 1 : j + d.W - 1;
+      for (int tl = t.i0; tl < t.i1; ++tl, ++i) {
+        const int s = (int)(i % kMetaRing), tok = t.n * kBlock + tl * TT;
+        // visible rows lo .. hi of this half, as a 64-bit mask (two words)
+        const int lo = (j - tok) * G - 64 * hf, hi = (tmax - tok + 1) * G - 1 - 64 * hf;
+        const uint32_t vis[2] = {bit_range(lo, hi, 0), bit_range(lo, hi, 1)};
+        const bool full = __all_sync(0xffffffffu, (vis[0] & vis[1]) == 0xffffffffu);
+        if (!mbar_wait_warp(&sh->m_full[s], phase_of(i / kMetaRing), A.status) ||
+            !mbar_wait_warp(&sh->s_full, phase_of(i), A.status)) {
+          ok = false;
+          break;
+        }
+        fence_after_sync();
+        // ---- phase A: P^T of this key and 64 rows; kept in fp32 for phase B
+        float p[64];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t rs[32], pw[16];
+          tmem_ld32(SB + lb + 64 * hf + 32 * c, rs);
+          tmem_wait_ld();
+          const float4* l4 = reinterpret_cast<const float4*>(sh->nlse2[s] + 64 * hf + 32 * c);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 nl = l4[e];
+            const float2 x0 = ffma2(make_float2(__uint_as_float(rs[4 * e]), __uint_as_float(rs[4 * e + 1])),
+                                    sl2x2, make_float2(nl.x, nl.y));
+            const float2 x1 = ffma2(make_float2(__uint_as_float(rs[4 * e + 2]), __uint_as_float(rs[4 * e + 3])),
+                                    sl2x2, make_float2(nl.z, nl.w));
+            float* pe = p + 32 * c + 4 * e;
+            pe[0] = exp2_ftz(x0.x);
+            pe[1] = exp2_ftz(x0.y);
+            pe[2] = exp2_ftz(x1.x);
+            pe[3] = exp2_ftz(x1.y);
+            if (!full) {
+#pragma unroll
+              for (int u = 0; u < 4; ++u) pe[u] = (vis[c] >> (4 * e + u)) & 1u ? pe[u] : 0.f;
+            }
+            pw[2 * e] = pack_bf16(pe[0], pe[1]);
+            pw[2 * e + 1] = pack_bf16(pe[2], pe[3]);
+          }
+          // over columns of S^T this half has read
+          tmem_st16(SB + lb + 64 * hf + 16 * c, pw);
+        }
+        tmem_wait_st();
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->pa);
+        // ---- phase B: dS^T = P^T (scale dP^T - scale D)
+        if (!mbar_wait_warp(&sh->dp_full, phase_of(i), A.status)) { ok = false; break; }
+        fence_after_sync();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t rp[32], dw[16];
+          tmem_ld32(DB + lb + 64 * hf + 32 * c, rp);
+          tmem_wait_ld();
+          const float4* d4 = reinterpret_cast<const float4*>(sh->ndrow[s] + 64 * hf + 32 * c);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 nd = d4[e];
+            const float* pe = p + 32 * c + 4 * e;
+            float2 y0 = ffma2(make_float2(__uint_as_float(rp[4 * e]), __uint_as_float(rp[4 * e + 1])), sc2,
+                              make_float2(nd.x, nd.y));
+            float2 y1 = ffma2(make_float2(__uint_as_float(rp[4 * e + 2]), __uint_as_float(rp[4 * e + 3])), sc2,
+                              make_float2(nd.z, nd.w));
+            y0 = fmul2(y0, make_float2(pe[0], pe[1]));
+            y1 = fmul2(y1, make_float2(pe[2], pe[3]));
+            dw[2 * e] = pack_bf16(y0.x, y0.y);
+            dw[2 * e + 1] = pack_bf16(y1.x, y1.y);
+          }
+          tmem_st16(DB + lb + 64 * hf + 16 * c, dw);
+        }
+        tmem_wait_st();
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sh->pb);
+          mbar_arrive(&sh->m_empty[s]);
+        }
+      }
+      if (!ok) break;
+      // ---- item end: the dV (rows-0-63 warps) or dK (rows-64-127 warps) row of this key
+      if (!mbar_wait_warp(&sh->acc_full, phase_of(nk), A.status)) break;
+      ++nk;
+      fence_after_sync();
+      const uint32_t acc = (hf == 0 ? RV : RK) + lb;
+      if (t.slot < 0) {
+        bf16* dst = (hf == 0 ? A.dv : A.dk) + (((long long)t.b * d.S + j) * d.Hkv + t.g) * kD;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t r[32];
+          tmem_ld32(acc + c * 32, r);
+          tmem_wait_ld();
+          if (j < d.S) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              uint4 w;
+              w.x = pack_bf16(__uint_as_float(r[8 * u]), __uint_as_float(r[8 * u + 1]));
+              w.y = pack_bf16(__uint_as_float(r[8 * u + 2]), __uint_as_float(r[8 * u + 3]));
+              w.z = pack_bf16(__uint_as_float(r[8 * u + 4]), __uint_as_float(r[8 * u + 5]));
+              w.w = pack_bf16(__uint_as_float(r[8 * u + 6]), __uint_as_float(r[8 * u + 7]));
+              reinterpret_cast<uint4*>(dst + c * 32)[u] = w;
+            }
+          }
+          __syncwarp();
+        }
+      } else {
+        float* dst = A.part + ((long long)t.slot * 2 + hf) * (kBlock * kD) + (long long)kr * kD;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t r[32];
+          tmem_ld32(acc + c * 32, r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            reinterpret_cast<uint4*>(dst + c * 32)[u] = make_uint4(r[4 * u], r[4 * u + 1], r[4 * u + 2], r[4 * u + 3]);
+        }
+      }
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->acc_free);
+    }
+  }
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  if (warp == 0) tmem_dealloc(sh->tmem, 512);
+}
+
+// dK and dV rows of the key blocks whose query tiles were split: their partials added in order.  One
+// block per 8 rows of (key block, b, g) and tensor; 32 threads a row, four values each.
+template <int G>
+__global__ void __launch_bounds__(256) win_join_kernel(WinDims d, WinItems w, const float* part, bf16* dk, bf16* dv) {
+  const int per = d.B * d.Hkv;
+  const int unit = blockIdx.x / 16, row = (blockIdx.x % 16) * 8 + threadIdx.x / 32, c = threadIdx.x % 32;
+  const int n = unit / per, bh = unit % per, b = bh / d.Hkv, g = bh % d.Hkv;
+  const int hf = blockIdx.y;  // 0: dV, 1: dK
+  const bool sink = n < w.sink_blocks;
+  const int chunk = sink ? w.sink_chunk : w.win_chunk;
+  const int nt = block_tiles<G>(d, n), nc = (nt + chunk - 1) / chunk, j = n * kBlock + row;
+  if (nc == 1 || j >= d.S) return;
+  const long long first = sink ? (long long)n * per + bh
+                               : w.sink_items + ((long long)(n - w.sink_blocks) * w.win_split) * per + bh;
+  const long long step = sink ? (long long)w.sink_blocks * per : per;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int x = 0; x < nc; ++x) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(
+        part + ((first + x * step) * 2 + hf) * (kBlock * kD) + (long long)row * kD + 4 * c));
+    s.x += v.x;
+    s.y += v.y;
+    s.z += v.z;
+    s.w += v.w;
+  }
+  bf16* dst = (hf == 0 ? dv : dk) + (((long long)b * d.S + j) * d.Hkv + g) * kD + 4 * c;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+}
+
+// ========================================================================================== dQ
+namespace {
+constexpr int kRingQ = 5;  // shared-memory tiles of win_dq_kernel beside Q and dO
+
+struct DqArgs {
+  WinDims d;
+  KeyMaps k, v;
+  CUtensorMap q, dout, dq;
+  const float2* rowm;
+  unsigned* status;
+  int nseg;
+  long long units;  // nseg B Hkv: one 128-row tile each
+};
+struct DqShared {
+  uint64_t q_full, q_empty, do_full, do_empty, kv_full[kRingQ], kv_empty[kRingQ], s_full, dp_full, pa, pb,
+      dq_full, dq_free[2], st_full, mma_done;
+  uint32_t tmem;
+};
+struct DqUnit {
+  int b, g, t0;
+  KeyRun run;
+};
+template <int G>
+__device__ __forceinline__ DqUnit dq_unit(const WinDims& d, long long u) {
+  constexpr int TT = 128 / G;
+  const int per = d.B * d.Hkv;
+  DqUnit x;
+  const int rem = (int)(u % per);
+  x.b = rem / d.Hkv;
+  x.g = rem % d.Hkv;
+  x.t0 = (int)(u / per) * TT;
+  x.run = key_run(d, x.t0, x.t0 + TT - 1 < d.S ? x.t0 + TT - 1 : d.S - 1);
+  return x;
+}
+}  // namespace
+
+// One unit is one 128-row query tile.  The ring holds, in this order, K_0 V_0 K_1 V_1 .. of a unit and
+// then one tile without a load, through which the unit's dQ leaves.  Q and dO have one buffer each:
+// the next unit's Q is loaded once the last S product has read it, its dO after the last dP product,
+// both a step before the unit ends.
+template <int G>
+__global__ void __launch_bounds__(384, 1) win_dq_kernel(const __grid_constant__ DqArgs A) {
+  using namespace sm100;
+  const WinDims& d = A.d;
+  extern __shared__ uint8_t smem_raw[];
+  DqShared* sh = reinterpret_cast<DqShared*>(smem_raw);
+  uint8_t* sQ = align1024(smem_raw + sizeof(DqShared));
+  uint8_t* sD = sQ + kTile;
+  uint8_t* sR = sD + kTile;
+  const uint32_t aQ = smem_u32(sQ), aD = smem_u32(sD), aR = smem_u32(sR);
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+
+  if (tid == 0) {
+    mbar_init(&sh->q_full, 1);
+    mbar_init(&sh->q_empty, 1);
+    mbar_init(&sh->do_full, 1);
+    mbar_init(&sh->do_empty, 1);
+    for (int x = 0; x < kRingQ; ++x) {
+      mbar_init(&sh->kv_full[x], 1);
+      mbar_init(&sh->kv_empty[x], 1);
+    }
+    mbar_init(&sh->s_full, 1);
+    mbar_init(&sh->dp_full, 1);
+    mbar_init(&sh->pa, kSoft);
+    mbar_init(&sh->pb, kSoft);
+    mbar_init(&sh->dq_full, 1);
+    mbar_init(&sh->dq_free[0], kSoft);
+    mbar_init(&sh->dq_free[1], kSoft);
+    mbar_init(&sh->st_full, kSoft);
+    mbar_init(&sh->mma_done, 1);
+    mbar_fence_init();
+  }
+  if (warp == 0) {
+    __syncwarp();  // lane 0 initialised the barriers alone; the allocation is warp-collective
+    tmem_alloc(&sh->tmem, 512);
+    tmem_relinquish();
+  }
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t SB = sh->tmem, DP = SB + 128, RQ0 = SB + 256;  // dQ of unit nu: RQ0 + 128 (nu & 1)
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- TMA loads
+    if (lane == 0) {
+      long long nl = 0, nu = 0;
+      // ring entry nl is free: true, its slot in `slot`
+      int slot = 0;
+      auto take = [&]() -> bool {
+        slot = (int)(nl % kRingQ);
+        return nl < kRingQ || mbar_wait(&sh->kv_empty[slot], phase_of(nl / kRingQ - 1), A.status);
+      };
+      bool ok = true;
+      for (long long u = blockIdx.x; u < A.units && ok; u += gridDim.x, ++nu) {
+        const DqUnit x = dq_unit<G>(d, u);
+        if (nu > 0 && !mbar_wait(&sh->q_empty, phase_of(nu - 1), A.status)) { ok = false; break; }
+        mbar_expect_tx(&sh->q_full, kTile);
+        for (int c = 0; c < 2; ++c)
+          tma_load_rows(sQ + c * (kTile / 2), &A.q, 64 * c, x.g * G, x.t0, x.b, &sh->q_full);
+        for (int n = 0; n < x.run.nb && ok; ++n) {
+          if (!(ok = take())) break;
+          mbar_expect_tx(&sh->kv_full[slot], kTile);
+          load_key_tile(sR + slot * kTile, A.k, x.run, n, x.g, x.b, &sh->kv_full[slot]);
+          ++nl;
+          if (n == 0) {
+            if (nu > 0 && !mbar_wait(&sh->do_empty, phase_of(nu - 1), A.status)) { ok = false; break; }
+            mbar_expect_tx(&sh->do_full, kTile);
+            for (int c = 0; c < 2; ++c)
+              tma_load_rows(sD + c * (kTile / 2), &A.dout, 64 * c, x.g * G, x.t0, x.b, &sh->do_full);
+          }
+          if (!(ok = take())) break;
+          mbar_expect_tx(&sh->kv_full[slot], kTile);
+          load_key_tile(sR + slot * kTile, A.v, x.run, n, x.g, x.b, &sh->kv_full[slot]);
+          ++nl;
+        }
+        if (!ok || !(ok = take())) break;
+        mbar_arrive(&sh->kv_full[slot]);  // the tile dQ leaves through: nothing to load
+        ++nl;
+      }
+      // no copy may still be landing in shared memory when the block exits (after a wait that gave
+      // up, the last loads of Q and dO are waited for by their own phase only as far as issued)
+      for (long long x = nl >= kRingQ ? nl - kRingQ : 0; x < nl; ++x)
+        mbar_wait(&sh->kv_full[x % kRingQ], phase_of(x / kRingQ), A.status);
+      if (ok && nu > 0) {
+        mbar_wait(&sh->q_full, phase_of(nu - 1), A.status);
+        mbar_wait(&sh->do_full, phase_of(nu - 1), A.status);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issue
+    if (lane == 0) {
+      constexpr uint32_t id_s = idesc_bf16(128, 128, false, false);  // S = Q K^T, dP = dO V^T
+      constexpr uint32_t id_q = idesc_bf16(128, 128, false, true);   // dQ += dS K
+      // a step: key tile n of unit nu; its K is ring entry nl, its V nl + 1
+      struct Step {
+        long long u, nu, nl;
+        int n, nb;
+      };
+      auto load_unit = [&](Step& t) { t.nb = t.u < A.units ? dq_unit<G>(d, t.u).run.nb : 0; };
+      auto next = [&](Step t) {
+        if (t.n + 1 < t.nb) {
+          ++t.n;
+          t.nl += 2;
+        } else {
+          t.u += gridDim.x;
+          ++t.nu;
+          t.n = 0;
+          t.nl += 3;  // the entry dQ leaves through
+          load_unit(t);
+        }
+        return t;
+      };
+      auto mma_s = [&](const Step& t) -> bool {
+        const int slot = (int)(t.nl % kRingQ);
+        if (t.n == 0 && !mbar_wait(&sh->q_full, phase_of(t.nu), A.status)) return false;
+        if (!mbar_wait(&sh->kv_full[slot], phase_of(t.nl / kRingQ), A.status)) return false;
+        fence_after_sync();
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          mma_ss(SB, desc_kmajor(aQ, 128, ks), desc_kmajor(aR + slot * kTile, 128, ks), id_s, ks > 0);
+        mma_commit(&sh->s_full);
+        if (t.n + 1 == t.nb) mma_commit(&sh->q_empty);
+        return true;
+      };
+      auto mma_dp = [&](const Step& t) -> bool {
+        const int slot = (int)((t.nl + 1) % kRingQ);
+        if (t.n == 0 && !mbar_wait(&sh->do_full, phase_of(t.nu), A.status)) return false;
+        if (!mbar_wait(&sh->kv_full[slot], phase_of((t.nl + 1) / kRingQ), A.status)) return false;
+        fence_after_sync();
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          mma_ss(DP, desc_kmajor(aD, 128, ks), desc_kmajor(aR + slot * kTile, 128, ks), id_s, ks > 0);
+        mma_commit(&sh->dp_full);
+        mma_commit(&sh->kv_empty[slot]);
+        if (t.n + 1 == t.nb) mma_commit(&sh->do_empty);
+        return true;
+      };
+      Step t{(long long)blockIdx.x, 0, 0, 0, 0};
+      load_unit(t);
+      bool ok = t.nb > 0 && mma_s(t) && mma_dp(t);
+      for (long long i = 0; ok; ++i) {
+        const Step nx = next(t);
+        const bool more = nx.nb > 0;
+        // phase A has read S
+        if (!mbar_wait(&sh->pa, phase_of(i), A.status)) break;
+        if (more && !mma_s(nx)) break;
+        // phase B has written dS over dP
+        if (!mbar_wait(&sh->pb, phase_of(i), A.status)) break;
+        if (t.n == 0 && t.nu >= 2 && !mbar_wait(&sh->dq_free[t.nu & 1], phase_of(t.nu / 2 - 1), A.status)) break;
+        fence_after_sync();
+        const int slot = (int)(t.nl % kRingQ);
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)  // keys 0-63 in columns 0-31, keys 64-127 in 64-95
+          mma_ts(RQ0 + 128 * (uint32_t)(t.nu & 1), DP + ks * 8 + (ks >= 4 ? 32 : 0),
+                 desc_mnmajor(aR + slot * kTile, 128, ks), id_q, t.n > 0 || ks > 0);
+        mma_commit(&sh->kv_empty[slot]);
+        if (t.n + 1 == t.nb) mma_commit(&sh->dq_full);
+        if (!more || !mma_dp(nx)) break;
+        t = nx;
+      }
+      mma_commit(&sh->mma_done);
+      mbar_wait(&sh->mma_done, 0, A.status);  // no product may still write tensor memory
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ---------------------------------------------------------------- TMA stores of dQ
+    if (lane == 0) {
+      long long nl = 0, nu = 0;
+      for (long long u = blockIdx.x; u < A.units; u += gridDim.x, ++nu, ++nl) {
+        const DqUnit x = dq_unit<G>(d, u);
+        nl += 2 * x.run.nb;  // the unit's last ring entry
+        const int slot = (int)(nl % kRingQ);
+        if (!mbar_wait(&sh->st_full, phase_of(nu), A.status)) break;
+        tma_store_rows(&A.dq, aR + slot * kTile, 0, x.g * G, x.t0, x.b);
+        tma_store_rows(&A.dq, aR + slot * kTile + kTile / 2, 64, x.g * G, x.t0, x.b);
+        bulk_store_commit();
+        bulk_store_wait_read();
+        mbar_arrive(&sh->kv_empty[slot]);
+      }
+      bulk_store_wait();
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ---------------------------------------------------------------- softmax (thread = row)
+    const int hf = (warp - 4) >> 2;  // keys 64 hf .. 64 hf + 63 of the tile
+    const int quad = warp & 3;
+    const int r = quad * 32 + lane;  // tile row = tensor-memory lane
+    const uint32_t lb = static_cast<uint32_t>(quad * 32) << 16;
+    const float sl2 = d.scale * kLog2e;
+    const float2 sl2x2 = make_float2(sl2, sl2), sc2 = make_float2(d.scale, d.scale);
+    auto row_data = [&](long long u) -> float2 {
+      if (u >= A.units) return make_float2(0.f, 0.f);
+      const DqUnit x = dq_unit<G>(d, u);
+      const int t = x.t0 + r / G;
+      return t < d.S ? __ldg(A.rowm + ((long long)x.b * d.S + t) * d.Hq + x.g * G + r % G)
+                     : make_float2(0.f, 0.f);
+    };
+    // dQ of unit number `nu` (its ring entry `nl`): tensor memory -> bf16 rows of the swizzled tile
+    auto epilogue = [&](long long nu, long long nl) -> bool {
+      const int slot = (int)(nl % kRingQ);
+      if (!mbar_wait_warp(&sh->dq_full, phase_of(nu), A.status) ||
+          !mbar_wait_warp(&sh->kv_full[slot], phase_of(nl / kRingQ), A.status))
+        return false;
+      fence_after_sync();
+      const uint32_t src = RQ0 + 128 * (uint32_t)(nu & 1) + lb + 64 * hf;
+      const uint32_t dst = aR + slot * kTile + hf * (kTile / 2);
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) {
+        uint32_t v[32];
+        tmem_ld32(src + 32 * c, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t w[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            w[y] = pack_bf16(__uint_as_float(v[8 * e + 2 * y]), __uint_as_float(v[8 * e + 2 * y + 1]));
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(dst + sw128_chunk(r, 4 * c + e)),
+                       "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                       : "memory");
+        }
+      }
+      fence_before_sync();
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sh->dq_free[nu & 1]);
+        mbar_arrive(&sh->st_full);
+      }
+      return true;
+    };
+    long long i = 0, nu = 0, nl = 0, pending = -1;  // pending: ring entry of the last unit's dQ
+    float2 m = row_data(blockIdx.x);
+    bool ok = true;
+    for (long long u = blockIdx.x; u < A.units && ok; u += gridDim.x, ++nu) {
+      const DqUnit x = dq_unit<G>(d, u);
+      const float2 mnext = row_data(u + gridDim.x);
+      const int t = x.t0 + r / G;
+      const float2 nl2 = make_float2(-m.x, -m.x), nd2 = make_float2(-m.y * d.scale, -m.y * d.scale);
+      for (int n = 0; n < x.run.nb; ++n, ++i) {
+        uint32_t vis[4];
+        visible_cols(d, x.run, n, t, vis);
+        const uint32_t vh[2] = {hf ? vis[2] : vis[0], hf ? vis[3] : vis[1]};
+        const bool full = __all_sync(0xffffffffu, (vh[0] & vh[1]) == 0xffffffffu);
+        if (!mbar_wait_warp(&sh->s_full, phase_of(i), A.status)) { ok = false; break; }
+        fence_after_sync();
+        // ---- phase A
+        float p[64];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t rs[32];
+          tmem_ld32(SB + lb + 64 * hf + 32 * c, rs);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 y = ffma2(make_float2(__uint_as_float(rs[2 * e]), __uint_as_float(rs[2 * e + 1])), sl2x2, nl2);
+            float* pe = p + 32 * c + 2 * e;
+            pe[0] = exp2_ftz(y.x);
+            pe[1] = exp2_ftz(y.y);
+            if (!full) {
+              pe[0] = (vh[c] >> (2 * e)) & 1u ? pe[0] : 0.f;
+              pe[1] = (vh[c] >> (2 * e + 1)) & 1u ? pe[1] : 0.f;
+            }
+          }
+        }
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->pa);
+        if (n == 0 && pending >= 0 && !epilogue(nu - 1, pending)) { ok = false; break; }
+        // ---- phase B
+        if (!mbar_wait_warp(&sh->dp_full, phase_of(i), A.status)) { ok = false; break; }
+        fence_after_sync();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t rp[32], dw[16];
+          tmem_ld32(DP + lb + 64 * hf + 32 * c, rp);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 y = fmul2(
+                ffma2(make_float2(__uint_as_float(rp[2 * e]), __uint_as_float(rp[2 * e + 1])), sc2, nd2),
+                make_float2(p[32 * c + 2 * e], p[32 * c + 2 * e + 1]));
+            dw[e] = pack_bf16(y.x, y.y);
+          }
+          tmem_st16(DP + lb + 64 * hf + 16 * c, dw);  // over columns of dP this half has read
+        }
+        tmem_wait_st();
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->pb);
+      }
+      if (!ok) break;
+      nl += 2 * x.run.nb;
+      pending = nl++;
+      m = mnext;
+    }
+    if (ok && pending >= 0) epilogue(nu - 1, pending);
+  }
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  if (warp == 0) tmem_dealloc(sh->tmem, 512);
+}
+
+// ========================================================================================== host
+// Key blocks and query tiles are cut so that the key-outer items number about eight per SM, in
+// chunks of at least four tiles; the window blocks are not split where they already have that many.
+WinItems win_items(const WinDims& d) {
+  WinItems w;
+  const int tt = kBlock / d.G, nblk = (d.S + kBlock - 1) / kBlock, per = d.B * d.Hkv;
+  w.sink_blocks = (d.ns + kBlock - 1) / kBlock;
+  const long long span = (long long)kBlock + d.W - 1 < d.S ? (long long)kBlock + d.W - 1 : d.S;
+  const long long win_tiles = (span + tt - 1) / tt, all_tiles = (d.S + tt - 1) / tt;
+  const long long total = (w.sink_blocks * all_tiles + (nblk - w.sink_blocks) * win_tiles) * per;
+  long long c = (total + 8ll * num_sms() - 1) / (8ll * num_sms());
+  if (c < 4) c = 4;
+  w.sink_chunk = (int)(c < all_tiles ? c : all_tiles);
+  w.win_chunk = (int)(c < win_tiles ? c : win_tiles);
+  w.win_split = (int)((win_tiles + w.win_chunk - 1) / w.win_chunk);
+  const int sink_split = (int)((all_tiles + w.sink_chunk - 1) / w.sink_chunk);
+  w.sink_items = w.sink_blocks * sink_split * per;
+  w.items = w.sink_items + (nblk - w.sink_blocks) * w.win_split * per;
+  // partials are indexed by item; without split window blocks only the sink items have any
+  w.partials = w.win_split > 1 ? w.items : sink_split > 1 ? w.sink_items : 0;
+  w.join_blocks = w.win_split > 1 ? nblk : sink_split > 1 ? w.sink_blocks : 0;
+  return w;
+}
+
+template <int G>
+static void win_bwd_g(const DkvArgs& a, const DqArgs& b, cudaStream_t st) {
+  const int n = num_sms();
+  const size_t s1 = sizeof(DkvShared) + 1024 + 6 * (size_t)kTile;
+  const size_t s2 = sizeof(DqShared) + 1024 + (2 + kRingQ) * (size_t)kTile;
+  cudaFuncSetAttribute(win_dkv_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s1);
+  cudaFuncSetAttribute(win_dq_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s2);
+  win_dkv_kernel<G><<<a.it.items < n ? a.it.items : n, 384, s1, st>>>(a);
+  win_dq_kernel<G><<<(int)(b.units < n ? b.units : n), 384, s2, st>>>(b);
+  if (a.it.join_blocks)
+    win_join_kernel<G><<<dim3(a.it.join_blocks * a.d.B * a.d.Hkv * 16, 2), 256, 0, st>>>(a.d, a.it, a.part, a.dk, a.dv);
+}
+
+bool launch_win_bwd(const WinDims& d, const void* q, const void* k, const void* v, const void* dout,
+                    const float2* rowm, void* dq, void* dk, void* dv, float* part, unsigned* status,
+                    cudaStream_t st) {
+  DkvArgs a;
+  DqArgs b;
+  const int tt = kBlock / d.G;
+  if (!make_tmap_rows(&a.q, q, d.B, d.S, d.Hq, d.G, tt) || !make_tmap_rows(&a.dout, dout, d.B, d.S, d.Hq, d.G, tt) ||
+      !make_tmap_rows(&a.k, k, d.B, d.S, d.Hkv, 1, kBlock) || !make_tmap_rows(&a.v, v, d.B, d.S, d.Hkv, 1, kBlock) ||
+      !make_key_maps(d, k, &b.k) || !make_key_maps(d, v, &b.v) ||
+      !make_tmap_rows(&b.dq, dq, d.B, d.S, d.Hq, d.G, tt))
+    return false;
+  a.d = b.d = d;
+  a.rowm = b.rowm = rowm;
+  a.status = b.status = status;
+  a.dk = (bf16*)dk;
+  a.dv = (bf16*)dv;
+  a.part = part;
+  a.sched = reinterpret_cast<int*>(status + kSchedWinDkv);
+  a.it = win_items(d);
+  b.q = a.q;
+  b.dout = a.dout;
+  b.nseg = (d.S + tt - 1) / tt;
+  b.units = (long long)b.nseg * d.B * d.Hkv;
+  switch (d.G) {
+    case 1: win_bwd_g<1>(a, b, st); break;
+    case 2: win_bwd_g<2>(a, b, st); break;
+    case 4: win_bwd_g<4>(a, b, st); break;
+    case 8: win_bwd_g<8>(a, b, st); break;
+    case 16: win_bwd_g<16>(a, b, st); break;
+    default: return false;
+  }
+  return true;
+}
+
+}  // namespace msa

@@ -1,0 +1,405 @@
+// Forward of causal attention over a sliding window and the first tokens (window.cuh has the
+// geometry): O = softmax(scale Q K^T) V over each query's visible keys, and the log-sum-exp of every
+// row, on the tcgen05 tensor cores.
+//
+// Query-outer: a unit is two 128-row tiles of one (b, KV head) -- a tile is 128/G consecutive tokens
+// x the G query heads of the group -- whose queries share every key tile of their joint run (one
+// tile per unit when pairs would leave SMs idle).  Per key tile n and query tile X:
+//   S_X = Q_X K_n^T                (tensor memory, 128 x 128 fp32)
+//   P = 2^(sl2 (S - mr)), l += row sum  (thread = row; P in bf16 over S in tensor memory); the
+//       running maximum mr moves only when the tile's maximum exceeds it by more than 8 / sl2, and
+//       then O_X and l are rescaled first (O_X's last product was issued before S_X, so it is done)
+//   O_X += P V_n
+// P is rounded to bf16 for its product: relative 2^-9 a key, which averages out to less than the
+// rounding of O itself; the row sum l is taken from the fp32 values.  Keys outside a row's window get
+// P = 0 exactly.  A row may see nothing of a tile (its maximum then stays -inf until it does).
+//
+// Bound by the tensor core: 4 x 128 flops a visible pair, and the tiles cost about
+// (W + 256/G + 128) / W of that; K and V come through L2.  The order of products is
+// O_A(n-1) S_A(n) O_B(n-1) S_B(n), so the softmax of one tile runs behind the products of the other.
+// Q has two buffers, so a unit's loads and first products overlap the previous unit's end; O leaves
+// through the unit's own Q buffer by TMA stores, which also drop the rows past the sequence.
+//
+// Roles (384 threads): warp 0 TMA loads, warp 1 MMA issue, warps 2 / 3 the TMA stores of tile A / B,
+// warps 4-7 / 8-11 softmax and epilogue of tile A / B.  Tensor memory: S_A, S_B, O_A, O_B (512
+// columns).  Units have equal cost but for the sequence's first window: they are dealt in turn,
+// tokens outermost, so that concurrent units share K and V.  Every wait is bounded.
+#include <math.h>
+
+#include "tmap.h"
+#include "window.cuh"
+
+namespace msa {
+namespace {
+
+constexpr int kTile = 128 * 128 * 2;  // 128 rows x 128 bf16, two SW128 panels
+constexpr int kRing = 3;              // K / V ring slots (loads alternate K, V)
+constexpr float kSlack = 8.f;         // log2 of the largest P kept without moving the row maximum
+
+struct FwdArgs {
+  WinDims d;
+  KeyMaps k, v;
+  CUtensorMap q, o;
+  float* lse;
+  unsigned* status;
+  int tiles;        // query tiles per unit, 1 or 2
+  int nseg;         // units along a sequence
+  long long units;  // nseg B Hkv
+};
+struct FwdShared {
+  uint64_t q_full[2], q_empty[2], kv_full[kRing], kv_empty[kRing], s_full[2], p_full[2], o_full[2],
+      o_free[2], st_full[2], mma_done;
+  uint32_t tmem;
+};
+struct FwdUnit {
+  int b, g, t0;
+  bool two;  // the second tile has a token
+  KeyRun run;
+};
+template <int G>
+__device__ __forceinline__ FwdUnit fwd_unit(const FwdArgs& A, long long u) {
+  constexpr int TT = 128 / G;
+  const WinDims& d = A.d;
+  FwdUnit x;
+  const int per = d.B * d.Hkv;
+  const int seg = (int)(u / per), rem = (int)(u % per);
+  x.b = rem / d.Hkv;
+  x.g = rem % d.Hkv;
+  x.t0 = seg * TT * A.tiles;
+  x.two = A.tiles == 2 && x.t0 + TT < d.S;
+  const int t1 = x.t0 + TT * A.tiles - 1;
+  x.run = key_run(d, x.t0, t1 < d.S ? t1 : d.S - 1);
+  return x;
+}
+
+}  // namespace
+
+template <int G>
+__global__ void __launch_bounds__(384, 1) win_fwd_kernel(const __grid_constant__ FwdArgs A) {
+  using namespace sm100;
+  constexpr int TT = 128 / G;
+  const WinDims& d = A.d;
+  extern __shared__ uint8_t smem_raw[];
+  FwdShared* sh = reinterpret_cast<FwdShared*>(smem_raw);
+  uint8_t* sQ = align1024(smem_raw + sizeof(FwdShared));  // [2 units][2 tiles][128 rows][128 d]
+  uint8_t* sR = sQ + 4 * kTile;                            // K / V ring
+  const uint32_t aQ = smem_u32(sQ), aR = smem_u32(sR);
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const float sl2 = d.scale * kLog2e;
+
+  if (tid == 0) {
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&sh->q_full[x], 1);
+      mbar_init(&sh->q_empty[x], 2);  // the store warps of both tiles
+      mbar_init(&sh->s_full[x], 1);
+      mbar_init(&sh->p_full[x], 4);
+      mbar_init(&sh->o_full[x], 1);
+      mbar_init(&sh->o_free[x], 4);
+      mbar_init(&sh->st_full[x], 4);
+    }
+    for (int x = 0; x < kRing; ++x) {
+      mbar_init(&sh->kv_full[x], 1);
+      mbar_init(&sh->kv_empty[x], 1);
+    }
+    mbar_init(&sh->mma_done, 1);
+    mbar_fence_init();
+  }
+  if (warp == 0) {
+    __syncwarp();  // lane 0 initialised the barriers alone; the allocation is warp-collective
+    tmem_alloc(&sh->tmem, 512);
+    tmem_relinquish();
+  }
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = sh->tmem;
+  const uint32_t S0 = tmem, O0 = tmem + 256;  // S_X = S0 + 128 X, O_X = O0 + 128 X
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- TMA loads
+    if (lane == 0) {
+      bool ok = true;
+      long long nl = 0, nu = 0;
+      for (long long u = blockIdx.x; u < A.units && ok; u += gridDim.x, ++nu) {
+        const FwdUnit x = fwd_unit<G>(A, u);
+        const int qs = (int)(nu & 1);
+        if (nu >= 2 && !mbar_wait(&sh->q_empty[qs], phase_of(nu / 2 - 1), A.status)) break;
+        uint8_t* dq = sQ + qs * 2 * kTile;
+        mbar_expect_tx(&sh->q_full[qs], (x.two ? 2 : 1) * kTile);
+        for (int X = 0; X < (x.two ? 2 : 1); ++X)
+          for (int c = 0; c < 2; ++c)
+            tma_load_rows(dq + X * kTile + c * (kTile / 2), &A.q, 64 * c, x.g * G, x.t0 + X * TT, x.b,
+                          &sh->q_full[qs]);
+        for (int n = 0; n < x.run.nb && ok; ++n)
+          for (int w = 0; w < 2; ++w, ++nl) {  // K_n, then V_n
+            const int slot = (int)(nl % kRing);
+            if (nl >= kRing && !mbar_wait(&sh->kv_empty[slot], phase_of(nl / kRing - 1), A.status)) {
+              ok = false;
+              break;
+            }
+            mbar_expect_tx(&sh->kv_full[slot], kTile);
+            load_key_tile(sR + slot * kTile, w ? A.v : A.k, x.run, n, x.g, x.b, &sh->kv_full[slot]);
+          }
+      }
+      // no copy may still be landing in shared memory when the block exits
+      for (long long x = nl >= kRing ? nl - kRing : 0; x < nl; ++x)
+        mbar_wait(&sh->kv_full[x % kRing], phase_of(x / kRing), A.status);
+      for (long long x = nu >= 2 ? nu - 2 : 0; x < nu; ++x)
+        mbar_wait(&sh->q_full[x & 1], phase_of(x >> 1), A.status);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issue
+    if (lane == 0) {
+      constexpr uint32_t id_s = idesc_bf16(128, 128, false, false);  // S = Q K^T
+      constexpr uint32_t id_o = idesc_bf16(128, 128, false, true);   // O += P V
+      long long nl = 0, nu = 0;
+      long long cs[2] = {0, 0};  // S products issued per tile
+      long long cu[2] = {0, 0};  // units begun per tile (o_free phases)
+      bool ok = true;
+      // O_X += P_X V for the last S product of tile X; V is load `lv` of the ring
+      auto mma_o = [&](int X, bool first, long long lv, bool last, bool free_v) -> bool {
+        if (!mbar_wait(&sh->p_full[X], phase_of(cs[X] - 1), A.status)) return false;
+        if (first) {
+          if (cu[X] > 0 && !mbar_wait(&sh->o_free[X], phase_of(cu[X] - 1), A.status)) return false;
+          ++cu[X];
+        }
+        const int slot = (int)(lv % kRing);
+        if (!mbar_wait(&sh->kv_full[slot], phase_of(lv / kRing), A.status)) return false;
+        fence_after_sync();
+        const uint32_t aV = aR + slot * kTile;
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          mma_ts(O0 + 128 * X, S0 + 128 * X + ks * 8, desc_mnmajor(aV, 128, ks), id_o, !first || ks > 0);
+        if (last) mma_commit(&sh->o_full[X]);
+        if (free_v) mma_commit(&sh->kv_empty[slot]);
+        return true;
+      };
+      auto mma_s = [&](int X, uint32_t q, int kslot, bool free_k) {
+        fence_after_sync();
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          mma_ss(S0 + 128 * X, desc_kmajor(q + X * kTile, 128, ks), desc_kmajor(aR + kslot * kTile, 128, ks),
+                 id_s, ks > 0);
+        mma_commit(&sh->s_full[X]);
+        if (free_k) mma_commit(&sh->kv_empty[kslot]);
+        ++cs[X];
+      };
+      for (long long u = blockIdx.x; u < A.units && ok; u += gridDim.x, ++nu) {
+        const FwdUnit x = fwd_unit<G>(A, u);
+        const int qs = (int)(nu & 1);
+        const uint32_t q = aQ + qs * 2 * kTile;
+        if (!mbar_wait(&sh->q_full[qs], phase_of(nu >> 1), A.status)) break;
+        for (int n = 0; n < x.run.nb; ++n, nl += 2) {
+          const int kslot = (int)(nl % kRing);
+          if (!mbar_wait(&sh->kv_full[kslot], phase_of(nl / kRing), A.status)) { ok = false; break; }
+          if (n > 0 && !mma_o(0, n == 1, nl - 1, false, !x.two)) { ok = false; break; }
+          mma_s(0, q, kslot, !x.two);
+          if (x.two) {
+            if (n > 0 && !mma_o(1, n == 1, nl - 1, false, true)) { ok = false; break; }
+            mma_s(1, q, kslot, true);
+          }
+        }
+        if (!ok) break;
+        ok = mma_o(0, x.run.nb == 1, nl - 1, true, !x.two) &&
+             (!x.two || mma_o(1, x.run.nb == 1, nl - 1, true, true));
+      }
+      mma_commit(&sh->mma_done);
+      mbar_wait(&sh->mma_done, 0, A.status);  // no product may still write tensor memory
+    }
+    __syncwarp();
+  } else if (warp < 4) {
+    // ---------------------------------------------------------------- TMA stores of O
+    if (lane == 0) {
+      const int X = warp - 2;
+      long long nu = 0, ns = 0;
+      for (long long u = blockIdx.x; u < A.units; u += gridDim.x, ++nu) {
+        const FwdUnit x = fwd_unit<G>(A, u);
+        const int qs = (int)(nu & 1);
+        if (X == 0 || x.two) {
+          if (!mbar_wait(&sh->st_full[X], phase_of(ns++), A.status)) break;
+          const uint32_t src = aQ + (qs * 2 + X) * kTile;
+          tma_store_rows(&A.o, src, 0, x.g * G, x.t0 + X * TT, x.b);
+          tma_store_rows(&A.o, src + kTile / 2, 64, x.g * G, x.t0 + X * TT, x.b);
+          bulk_store_commit();
+          bulk_store_wait_read();
+        } else if (!mbar_wait(&sh->q_full[qs], phase_of(nu >> 1), A.status)) {
+          break;  // (waited for only so that this arrival cannot run ahead into a later phase)
+        }
+        mbar_arrive(&sh->q_empty[qs]);
+      }
+      bulk_store_wait();
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- softmax + epilogue
+    const int X = (warp - 4) >> 2;  // tile A (warps 4-7) or B (warps 8-11)
+    const int w4 = warp % 4;
+    const int r = w4 * 32 + lane;  // tile row = tensor-memory lane
+    const uint32_t lb = static_cast<uint32_t>(w4 * 32) << 16;
+    const uint32_t Sx = S0 + 128 * X + lb, Ox = O0 + 128 * X + lb;
+    const float2 sl2x2 = make_float2(sl2, sl2);
+    long long cs = 0, nu = 0, nt = 0;  // S products, units, units with this tile
+    bool ok = true;
+    for (long long u = blockIdx.x; u < A.units && ok; u += gridDim.x, ++nu) {
+      const FwdUnit x = fwd_unit<G>(A, u);
+      if (X == 1 && !x.two) continue;
+      const int t = x.t0 + X * TT + r / G;  // this row's token
+      const int h = x.g * G + r % G;         // and query head
+      float mr = -INFINITY, l = 0.f;
+      for (int n = 0; n < x.run.nb; ++n, ++cs) {
+        uint32_t vis[4];
+        visible_cols(d, x.run, n, t, vis);
+        // tcgen05.ld / st are warp-collective: the masked path is chosen per warp
+        const bool full = __all_sync(0xffffffffu, (vis[0] & vis[1] & vis[2] & vis[3]) == 0xffffffffu);
+        if (!mbar_wait_warp(&sh->s_full[X], phase_of(cs), A.status)) { ok = false; break; }
+        fence_after_sync();
+        float mx = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t v[32];
+          tmem_ld32(Sx + q * 32, v);
+          tmem_wait_ld();
+          if (full) {
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) mx = fmax3(mx, __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
+          } else {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              mx = fmaxf(mx, (vis[q] >> c) & 1u ? __uint_as_float(v[c]) : -INFINITY);
+          }
+        }
+        if (n == 0) {
+          mr = mx;
+        } else {
+          const bool need = (mx - mr) * sl2 > kSlack;  // (both -inf: NaN, no)
+          if (__any_sync(0xffffffffu, need)) {          // rescale O and l of this warp's rows
+            const float alpha = need ? exp2_ftz((mr - mx) * sl2) : 1.f;
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+              uint32_t v[32];
+              tmem_ld32(Ox + q * 32, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * alpha);
+              tmem_st32(Ox + q * 32, v);
+            }
+            l *= alpha;
+            if (need) mr = mx;
+          }
+        }
+        const float mb = mr == -INFINITY ? 0.f : mr * sl2;
+        const float2 nmb = make_float2(-mb, -mb);
+        float2 la = make_float2(0.f, 0.f);
+#pragma unroll 1  // (a full unroll makes the compiler spill)
+        for (int q = 0; q < 4; ++q) {
+          uint32_t v[32];
+          tmem_ld32(Sx + q * 32, v);
+          tmem_wait_ld();
+          uint32_t pw[16];
+          const uint32_t vq = q == 0 ? vis[0] : q == 1 ? vis[1] : q == 2 ? vis[2] : vis[3];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const float2 e = ffma2(make_float2(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1])),
+                                   sl2x2, nmb);
+            float2 p = make_float2(exp2_ftz(e.x), exp2_ftz(e.y));
+            if (!full) {
+              p.x = (vq >> (2 * c)) & 1u ? p.x : 0.f;
+              p.y = (vq >> (2 * c + 1)) & 1u ? p.y : 0.f;
+            }
+            la = fadd2(la, p);
+            pw[c] = pack_bf16(p.x, p.y);
+          }
+          tmem_st16(Sx + q * 16, pw);
+        }
+        l += la.x + la.y;
+        tmem_wait_st();
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->p_full[X]);
+      }
+      if (!ok) break;
+      // ---- unit end: O / l into the tile's own Q rows (every S product has read them), as the
+      // swizzled tile its TMA store expects; then the LSE
+      if (!mbar_wait_warp(&sh->o_full[X], phase_of(nt), A.status)) break;
+      ++nt;
+      fence_after_sync();
+      const float sc = __fdividef(1.f, l);
+      const uint32_t dst = aQ + ((int)(nu & 1) * 2 + X) * kTile;
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        uint32_t v[32];
+        tmem_ld32(Ox + q * 32, v);
+        tmem_wait_ld();
+        if (q == 3) {  // O_X may now take the next unit's products
+          fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh->o_free[X]);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = pack_bf16(__uint_as_float(v[8 * c + 2 * e]) * sc, __uint_as_float(v[8 * c + 2 * e + 1]) * sc);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(
+                           dst + (q >> 1) * (kTile / 2) + sw128_chunk(r, (q & 1) * 4 + c)),
+                       "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                       : "memory");
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->st_full[X]);
+      if (t < d.S) A.lse[((long long)x.b * d.Hq + h) * d.S + t] = (mr * sl2 + __log2f(l)) * kLn2;
+    }
+  }
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// The three maps of K or V.  nsp mod 128 rows of the shared tile are sinks (0: no such tile).
+bool make_key_maps(const WinDims& d, const void* base, KeyMaps* m) {
+  const int a = d.nsp % kBlock;
+  return make_tmap_rows(&m->full, base, d.B, d.S, d.Hkv, 1, kBlock) &&
+         make_tmap_rows(&m->sink, base, d.B, d.S, d.Hkv, 1, a ? a : 8) &&
+         make_tmap_rows(&m->rest, base, d.B, d.S, d.Hkv, 1, a ? kBlock - a : 8);
+}
+
+template <int G>
+static void win_fwd_g(const FwdArgs& a, cudaStream_t st) {
+  const size_t smem = sizeof(FwdShared) + 1024 + (4 + kRing) * (size_t)kTile;
+  cudaFuncSetAttribute(win_fwd_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const int n = num_sms();
+  win_fwd_kernel<G><<<(int)(a.units < n ? a.units : n), 384, smem, st>>>(a);
+}
+
+bool launch_win_fwd(const WinDims& d, const void* q, const void* k, const void* v, void* o,
+                    float* lse, unsigned* status, cudaStream_t st) {
+  FwdArgs a;
+  if (!make_key_maps(d, k, &a.k) || !make_key_maps(d, v, &a.v) ||
+      !make_tmap_rows(&a.q, q, d.B, d.S, d.Hq, d.G, kBlock / d.G) ||
+      !make_tmap_rows(&a.o, o, d.B, d.S, d.Hq, d.G, kBlock / d.G))
+    return false;
+  a.d = d;
+  a.lse = lse;
+  a.status = status;
+  const int tt = kBlock / d.G;
+  const long long per = (long long)d.B * d.Hkv;
+  a.tiles = (d.S + 2 * tt - 1) / (2 * tt) * per < num_sms() ? 1 : 2;
+  a.nseg = (d.S + tt * a.tiles - 1) / (tt * a.tiles);
+  a.units = a.nseg * per;
+  switch (d.G) {
+    case 1: win_fwd_g<1>(a, st); break;
+    case 2: win_fwd_g<2>(a, st); break;
+    case 4: win_fwd_g<4>(a, st); break;
+    case 8: win_fwd_g<8>(a, st); break;
+    case 16: win_fwd_g<16>(a, st); break;
+    default: return false;
+  }
+  return true;
+}
+
+}  // namespace msa

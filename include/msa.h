@@ -84,7 +84,12 @@ enum msa_op {
   MSA_OP_BACKWARD = 1,
   MSA_OP_WARMUP_FORWARD = 2,
   MSA_OP_WARMUP_BACKWARD = 3,
-  MSA_OP_DECODE = 4
+  MSA_OP_DECODE = 4,
+  MSA_OP_WINDOW_FORWARD = 5, /* msa_window_workspace_size */
+  MSA_OP_WINDOW_BACKWARD = 6,
+  MSA_OP_WINDOW_DECODE = 7,
+  MSA_OP_NORM_ROPE_BACKWARD = 8, /* msa_norm_rope_workspace_size */
+  MSA_OP_NORM_ROPE_APPEND = 9
 };
 
 /* Bits of the device status word. */
@@ -194,6 +199,115 @@ MSA_API int msa_decode(const msa_shape_t* shape, const void* q, const void* qp,
                        const void* k_cache, const void* v_cache, const void* kp_cache,
                        const int32_t* seq_len, int32_t* block_idx, void* o, float* lse,
                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Causal GQA attention over a sliding window and the first tokens (sinks): the local layers that
+ * stand between sparse ones.  Query t sees key j iff j <= t and (t - j < window or j < sinks); a
+ * window of S or more is dense causal attention.  Layouts as above: q, o, dout, dq [B, S, Hq, 128],
+ * k, v, dk, dv [B, S, Hkv, 128], lse [B, Hq, S].  Supported: head dim 128, any 1 <= S <= 2^23,
+ * Hq / Hkv in {1, 2, 4, 8, 16}, window >= 1, sinks >= 0.  Inputs must be finite: an infinity or NaN
+ * in a K or V row reaches the queries whose tiles load it, also those whose window does not hold it
+ * (the decode step masks such rows exactly).
+ */
+typedef struct msa_window_shape {
+  int32_t B;       /* batch */
+  int32_t S;       /* sequence length; decode: capacity of the caches */
+  int32_t Hq;      /* query heads */
+  int32_t Hkv;     /* key/value heads */
+  int32_t D;       /* head dim, must be 128 */
+  int32_t window;  /* keys a query sees, itself included */
+  int32_t sinks;   /* first keys that stay visible */
+  float scale;     /* softmax scale, usually 128^-0.5 */
+} msa_window_shape_t;
+
+/* Bytes of workspace a window op needs (0 if the shape is unsupported). */
+MSA_API size_t msa_window_workspace_size(const msa_window_shape_t* shape, int op);
+
+/* Writes o and lse. */
+MSA_API int msa_window_forward(const msa_window_shape_t* shape, const void* q, const void* k,
+                       const void* v, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+/* Gradients of sum(o * dout); o and lse are the outputs of msa_window_forward for the same inputs.
+ * The same inputs give the same bits every time (no atomic sums). */
+MSA_API int msa_window_backward(const msa_window_shape_t* shape, const void* q, const void* k,
+                        const void* v, const void* o, const float* lse, const void* dout, void* dq,
+                        void* dk, void* dv, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Decode step: one new token per sequence at position t_b = seq_len[b] - 1 of its caches, which
+ * already hold it.  q, o [B, Hq, 128] bf16, lse [B, Hq] fp32, k_cache, v_cache [B, S, Hkv, 128],
+ * seq_len [B] int32 on the device, 1 <= seq_len[b] <= S (other values: the sequence's rows of o and
+ * lse are left as they were and MSA_DEVICE_BAD_INDEX is set).  Cache rows the token does not see --
+ * behind it, before its window, whatever they hold -- do not reach the result.
+ */
+MSA_API int msa_window_decode(const msa_window_shape_t* shape, const void* q, const void* k_cache,
+                      const void* v_cache, const int32_t* seq_len, void* o, float* lse,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * RMS norm of every head's row and the position rotation in one pass, for the inputs of the
+ * attention ops: q, k and the proxy heads, usually as slices of one packed projection.
+ * A call takes up to 8 parts.  A part is `heads` consecutive heads (128 elements apart) of every
+ * token; its tensors are bf16 [B, N, heads, 128] with batch and token strides in elements
+ * (multiples of 8) and 16-byte aligned bases.  Per row x (all in fp32, rounded once):
+ *     r = (mean(x^2) + eps)^-1/2,  u = weight x r   (weight NULL: u = x)
+ *     y = u with its first `rotary` elements turned in pairs (i, i + rotary/2) -- interleaved:
+ *         (2 i, 2 i + 1) -- by the angle position * inv_freq[i]   (without MSA_ROPE_ROTATE: y = u)
+ * rotary: a multiple of 16, 0 .. 128.  inv_freq: rotary / 2 floats on the device.  positions: int32
+ * [B, N] on the device, any value, or NULL for 0 .. N - 1.  Angles are exact to fp32 at every position.
+ */
+enum msa_rope_flags {
+  MSA_ROPE_ROTATE = 1, /* rotate this part */
+  MSA_ROPE_CACHE = 2   /* append only: y is a cache, its token index the token's position */
+};
+typedef struct msa_rope_part {
+  const void* x;
+  int64_t x_batch, x_token;
+  void* y; /* forward, append: output; backward: dy, read only */
+  int64_t y_batch, y_token;
+  void* dx; /* backward only */
+  int64_t dx_batch, dx_token;
+  const float* weight; /* [128] fp32, NULL: not normed */
+  float* dweight;      /* backward: [128] fp32, NULL: not wanted */
+  int32_t heads;
+  int32_t flags;
+} msa_rope_part_t;
+typedef struct msa_rope_shape {
+  int32_t B;           /* batch */
+  int32_t N;           /* tokens per sequence in x */
+  int32_t D;           /* head dim, must be 128 */
+  int32_t rotary;      /* rotated elements of a row */
+  int32_t interleaved; /* pairs (2 i, 2 i + 1) */
+  int32_t capacity;    /* append: tokens a cache holds */
+  float eps;           /* >= 0 */
+} msa_rope_shape_t;
+
+MSA_API int msa_norm_rope_forward(const msa_rope_shape_t* shape, const msa_rope_part_t* parts,
+                          int nparts, const int32_t* positions, const float* inv_freq,
+                          void* stream);
+
+/*
+ * Serving form: the N tokens of x are the last N of sequences of length seq_len[b] (device int32;
+ * N <= seq_len[b] <= capacity), so token i is at position seq_len[b] - N + i.  Parts with
+ * MSA_ROPE_CACHE go to that row of their cache (y: [B, capacity, heads, 128] with the part's
+ * strides), other rows of which are left as they were; other parts as in msa_norm_rope_forward.  A
+ * sequence whose length is out of range is skipped and MSA_DEVICE_BAD_INDEX set.  Then msa_decode
+ * or msa_window_decode run on the same caches and seq_len (N = 1).
+ */
+MSA_API int msa_norm_rope_append(const msa_rope_shape_t* shape, const msa_rope_part_t* parts,
+                         int nparts, const int32_t* seq_len, const float* inv_freq,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* dx of every part, and dweight summed over its rows, from x and dy (in `y`).  The same inputs give
+ * the same bits every time. */
+MSA_API int msa_norm_rope_backward(const msa_rope_shape_t* shape, const msa_rope_part_t* parts,
+                           int nparts, const int32_t* positions, const float* inv_freq,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace MSA_OP_NORM_ROPE_BACKWARD or MSA_OP_NORM_ROPE_APPEND needs for nparts parts (0:
+ * another op, or nparts out of range). */
+MSA_API size_t msa_norm_rope_workspace_size(int nparts, int op);
 
 /*
  * Reads (and clears) the device status word of `workspace` after the work queued on `stream`
