@@ -1116,10 +1116,12 @@ int msa_window_backward(const msa_window_shape_t* shape, const void* q, const vo
   rows.Hq = d.Hq;
   timed("bwd_rowdot", st, [&] { launch_bwd_rowdot(rows, o, dout, lse, at<float2>(workspace, p.rowm), st); });
   bool ok = true;
-  timed("win_bwd", st, [&] {
-    ok = launch_win_bwd(d, q, k, v, dout, at<float2>(workspace, p.rowm), dq, dk, dv,
-                        at<float>(workspace, p.part), status, st);
-  }, win_items(d).join_blocks ? 3 : 2);
+  const float2* rowm = at<float2>(workspace, p.rowm);
+  float* part = at<float>(workspace, p.part);
+  timed("win_dkv", st, [&] { ok = launch_win_dkv(d, q, k, v, dout, rowm, dk, dv, part, status, st); });
+  if (ok) timed("win_dq", st, [&] { ok = launch_win_dq(d, q, k, v, dout, rowm, dq, status, st); });
+  if (ok && win_items(d).join_blocks)
+    timed("win_join", st, [&] { ok = launch_win_join(d, part, dk, dv, st); });
   if (!ok) {
     set_err("msa_window_backward: could not create TMA tensor maps (cuTensorMapEncodeTiled)");
     return MSA_ERR_CUDA;

@@ -201,10 +201,13 @@ struct WinItems {
   int items, partials, join_blocks;         // partial slots (2 x 128 x 128 fp32); blocks to join
 };
 WinItems win_items(const WinDims& d);
-// dq, dk, dv from rowm (launch_bwd_rowdot) and `part`, win_items(d).partials slots.
-bool launch_win_bwd(const WinDims& d, const void* q, const void* k, const void* v, const void* dout,
-                    const float2* rowm, void* dq, void* dk, void* dv, float* part, unsigned* status,
-                    cudaStream_t st);
+// dk, dv and dq from rowm (launch_bwd_rowdot); dk, dv of split key blocks go to `part`
+// (win_items(d).partials slots) and are added by the join.
+bool launch_win_dkv(const WinDims& d, const void* q, const void* k, const void* v, const void* dout,
+                    const float2* rowm, void* dk, void* dv, float* part, unsigned* status, cudaStream_t st);
+bool launch_win_dq(const WinDims& d, const void* q, const void* k, const void* v, const void* dout,
+                   const float2* rowm, void* dq, unsigned* status, cudaStream_t st);
+bool launch_win_join(const WinDims& d, const float* part, void* dk, void* dv, cudaStream_t st);
 
 // Decode step over caches of capacity d.S: key tiles per split and splits; opart [nsplit][B][Hq][128],
 // lpart [nsplit][B][Hq] (used when nsplit > 1).

@@ -17,15 +17,18 @@
 // win_dkv: ... dV(i) S(i+1) | dK(i) dP(i+1) ...: the first pair runs behind phase B of tile i, the
 // second behind phase A of tile i+1, and each phase waits for the pair before it only.  P^T and dS^T
 // (bf16) overwrite S^T and dP^T in tensor memory and are the products' A operands from there.
-// win_dq:  ... S(n+1) | dQ(n) dP(n+1) ...: S(n+1) runs behind phase B of tile n (P is in registers by
-// then), the pair behind phase A of n+1; dS overwrites dP, dQ has two buffers for two units.
+// win_dq:  ... S(n+1) | dP(n+1) dQ(n) ...: S(n+1) is issued once S(n) is in registers, the pair after
+// phase B of tile n, which leaves dS in columns of its own (two buffers), so that dP(n+1) need not
+// wait for dQ(n).
 // P and dS are rounded to bf16 for their products (2^-9 relative each), the softmax scale is folded
 // into dS, everything else is fp32.  Bound by the tensor core: 32 (dkv) and 24 (dq) instructions of
 // 128 x 128 x 16 a tile pair, about 83 cycles each.
 //
-// Roles of both (384 threads): warp 0 TMA loads, warp 1 MMA issue, warp 2 the tile's row data (dkv)
-// or the TMA stores of dQ (dq), warps 4-11 softmax and epilogue: two per tensor-memory lane quarter,
-// one per half of the tile's columns.  Every wait is bounded.
+// Roles of both (640 threads): warp 0 TMA loads, warp 1 MMA issue, warp 2 the tile's row data (dkv)
+// or the TMA stores of dQ (dq), warps 4-19 softmax and epilogue: four per tensor-memory lane quarter,
+// one per 32 of the tile's columns (with two, a phase was bound by the latencies of a warp's loads and
+// exponentials: 2,400 cycles a tile of win_dkv against the 2,656 of its products).  Every wait is
+// bounded.
 #include <math.h>
 
 #include "tmap.h"
@@ -35,7 +38,9 @@ namespace msa {
 namespace {
 
 constexpr int kTile = 128 * 128 * 2;  // 128 rows x 128 bf16, two SW128 panels
-constexpr int kItemRing = 4, kMetaRing = 4, kSoft = 8;
+constexpr int kItemRing = 4, kMetaRing = 4;
+constexpr int kSoft = 16;        // softmax / epilogue warps
+constexpr int kBwdThreads = 640;  // 4 + kSoft warps
 
 struct DkvArgs {
   WinDims d;
@@ -98,7 +103,7 @@ __device__ __forceinline__ DkvItem dkv_item(const WinDims& d, const WinItems& w,
 }  // namespace
 
 template <int G>
-__global__ void __launch_bounds__(384, 1) win_dkv_kernel(const __grid_constant__ DkvArgs A) {
+__global__ void __launch_bounds__(kBwdThreads, 1) win_dkv_kernel(const __grid_constant__ DkvArgs A) {
   using namespace sm100;
   constexpr int TT = 128 / G;
   const WinDims& d = A.d;
@@ -109,7 +114,7 @@ __global__ void __launch_bounds__(384, 1) win_dkv_kernel(const __grid_constant__
   uint8_t* sQ = sV + kTile;       // [2] query tiles
   uint8_t* sD = sQ + 2 * kTile;   // [2] dO tiles
   const uint32_t aK = smem_u32(sK), aV = smem_u32(sV), aQ = smem_u32(sQ), aD = smem_u32(sD);
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int tid = threadIdx.x, lane = tid % 32, warp = warp_number();
   const int total = A.it.items;
 
   if (tid == 0) {
@@ -149,13 +154,6 @@ __global__ void __launch_bounds__(384, 1) win_dkv_kernel(const __grid_constant__
   fence_after_sync();
   const uint32_t SB = sh->tmem, DB = SB + 128, RV = SB + 256, RK = SB + 384;
   // item number k of this block (handed out in list order to whichever block asks next)
-  auto take1 = [&](long long k, int& v) -> bool {
-    const int x = (int)(k % kItemRing);
-    if (!mbar_wait(&sh->it_full[x], phase_of(k / kItemRing), A.status)) return false;
-    v = sh->it_ring[x];
-    mbar_arrive(&sh->it_empty[x]);
-    return true;
-  };
   auto takew = [&](long long k, int& v) -> bool {
     const int x = (int)(k % kItemRing);
     if (!mbar_wait_warp(&sh->it_full[x], phase_of(k / kItemRing), A.status)) return false;
@@ -212,81 +210,70 @@ __global__ void __launch_bounds__(384, 1) win_dkv_kernel(const __grid_constant__
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issue
-    if (lane == 0) {
-      constexpr uint32_t id_s = idesc_bf16(128, 128, false, false);  // S^T = K Q^T, dP^T = V dO^T
-      constexpr uint32_t id_g = idesc_bf16(128, 128, false, true);   // dV = P^T dO, dK = dS^T Q
+    {
       long long nk = 0, i = 0;
       bool ok = true;
       auto mma_s = [&](long long j) -> bool {
         const int s = (int)(j & 1);
-        if (!mbar_wait(&sh->q_full[s], phase_of(j >> 1), A.status)) return false;
+        if (!mbar_wait_warp(&sh->q_full[s], phase_of(j >> 1), A.status)) return false;
         fence_after_sync();
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          mma_ss(SB, desc_kmajor(aK, 128, ks), desc_kmajor(aQ + s * kTile, 128, ks), id_s, ks > 0);
-        mma_commit(&sh->s_full);
+        mma_kk(SB, aK, aQ + s * kTile, false);  // S^T = K Q^T
+        warp_mma_commit(&sh->s_full);
         return true;
       };
       auto mma_dp = [&](long long j) -> bool {
         const int s = (int)(j & 1);
-        if (!mbar_wait(&sh->do_full[s], phase_of(j >> 1), A.status)) return false;
+        if (!mbar_wait_warp(&sh->do_full[s], phase_of(j >> 1), A.status)) return false;
         fence_after_sync();
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          mma_ss(DB, desc_kmajor(aV, 128, ks), desc_kmajor(aD + s * kTile, 128, ks), id_s, ks > 0);
-        mma_commit(&sh->dp_full);
+        mma_kk(DB, aV, aD + s * kTile, false);  // dP^T = V dO^T
+        warp_mma_commit(&sh->dp_full);
         return true;
       };
       for (long long k = 0; ok; ++k) {
         int v;
-        if (!take1(k, v) || v >= total) break;
+        if (!takew(k, v) || v >= total) break;
         const DkvItem t = dkv_item<G>(d, A.it, v);
         if (t.i0 >= t.i1) continue;
         const int n = t.i1 - t.i0;
         // P^T and dS^T of the previous item's last tile were read by products issued before these
-        ok = mbar_wait(&sh->k_full, phase_of(nk), A.status) && mma_s(i) &&
-             mbar_wait(&sh->v_full, phase_of(nk), A.status) && mma_dp(i);
+        ok = mbar_wait_warp(&sh->k_full, phase_of(nk), A.status) && mma_s(i) &&
+             mbar_wait_warp(&sh->v_full, phase_of(nk), A.status) && mma_dp(i);
         for (int tl = 0; tl < n && ok; ++tl, ++i) {
           const int s = (int)(i & 1);
           // phase A has written P^T over S^T
-          if (!mbar_wait(&sh->pa, phase_of(i), A.status)) { ok = false; break; }
-          if (tl == 0 && nk > 0 && !mbar_wait(&sh->acc_free, phase_of(nk - 1), A.status)) { ok = false; break; }
+          if (!mbar_wait_warp(&sh->pa, phase_of(i), A.status)) { ok = false; break; }
+          if (tl == 0 && nk > 0 && !mbar_wait_warp(&sh->acc_free, phase_of(nk - 1), A.status)) { ok = false; break; }
           fence_after_sync();
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks)  // rows 0-63 in columns 0-31, rows 64-127 in 64-95
-            mma_ts(RV, SB + ks * 8 + (ks >= 4 ? 32 : 0), desc_mnmajor(aD + s * kTile, 128, ks), id_g,
-                   tl > 0 || ks > 0);
-          mma_commit(&sh->do_empty[s]);
+          // dV += P^T dO; P^T of rows 32 p .. 32 p + 31 in columns 32 p .. 32 p + 15
+          mma_tn<2, 32>(RV, SB, aD + s * kTile, tl > 0);
+          warp_mma_commit(&sh->do_empty[s]);
           if (tl + 1 < n && !mma_s(i + 1)) { ok = false; break; }
           // phase B has written dS^T over dP^T
-          if (!mbar_wait(&sh->pb, phase_of(i), A.status)) { ok = false; break; }
+          if (!mbar_wait_warp(&sh->pb, phase_of(i), A.status)) { ok = false; break; }
           fence_after_sync();
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            mma_ts(RK, DB + ks * 8 + (ks >= 4 ? 32 : 0), desc_mnmajor(aQ + s * kTile, 128, ks), id_g,
-                   tl > 0 || ks > 0);
-          mma_commit(&sh->q_empty[s]);
+          mma_tn<2, 32>(RK, DB, aQ + s * kTile, tl > 0);  // dK += dS^T Q
+          warp_mma_commit(&sh->q_empty[s]);
           if (tl + 1 < n && !mma_dp(i + 1)) { ok = false; break; }
         }
         if (!ok) break;
-        mma_commit(&sh->acc_full);
-        mma_commit(&sh->kv_empty);
+        warp_mma_commit(&sh->acc_full);
+        warp_mma_commit(&sh->kv_empty);
         ++nk;
       }
-      mma_commit(&sh->mma_done);
-      mbar_wait(&sh->mma_done, 0, A.status);  // no product may still write tensor memory
+      warp_mma_commit(&sh->mma_done);
+      mbar_wait_warp(&sh->mma_done, 0, A.status);  // no product may still write tensor memory
     }
     __syncwarp();
   } else if (warp == 2) {
     // ---------------------------------------------------------------- row data of the tiles
-    long long i = 0;
+    Ring<kMetaRing> meta;
     bool ok = true;
     for (long long k = 0; ok; ++k) {
       int v;
       if (!takew(k, v) || v >= total) break;
       const DkvItem t = dkv_item<G>(d, A.it, v);
-      for (int tl = t.i0; tl < t.i1; ++tl, ++i) {
-        const int s = (int)(i % kMetaRing), tok = t.n * kBlock + tl * TT;
+      for (int tl = t.i0; tl < t.i1; ++tl, meta.next()) {
+        const int s = meta.slot, tok = t.n * kBlock + tl * TT;
         float2 m[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -294,7 +281,7 @@ __global__ void __launch_bounds__(384, 1) win_dkv_kernel(const __grid_constant__
           m[e] = q < d.S ? __ldg(A.rowm + ((long long)t.b * d.S + q) * d.Hq + t.g * G + r % G)
                          : make_float2(0.f, 0.f);
         }
-        if (i >= kMetaRing && !mbar_wait_warp(&sh->m_empty[s], phase_of(i / kMetaRing - 1), A.status)) {
+        if (meta.wrapped && !mbar_wait_warp(&sh->m_empty[s], meta.phase ^ 1, A.status)) {
           ok = false;
           break;
         }
@@ -309,13 +296,15 @@ __global__ void __launch_bounds__(384, 1) win_dkv_kernel(const __grid_constant__
     }
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- softmax (thread = key)
-    const int hf = (warp - 4) >> 2;  // rows 64 hf .. 64 hf + 63 of the tile
+    const int part = (warp - 4) >> 2;  // rows 32 part .. 32 part + 31 of the tile
     const int quad = warp & 3;
     const int kr = quad * 32 + lane;  // key row = tensor-memory lane
     const uint32_t lb = static_cast<uint32_t>(quad * 32) << 16;
     const float sl2 = d.scale * kLog2e;
     const float2 sl2x2 = make_float2(sl2, sl2), sc2 = make_float2(d.scale, d.scale);
-    long long nk = 0, i = 0;
+    const uint32_t Sx = SB + lb + 32 * part, Dx = DB + lb + 32 * part;
+    int nk = 0, i = 0;
+    Ring<kMetaRing> meta;
     bool ok = true;
     for (long long k = 0; ok; ++k) {
       int v;
@@ -325,26 +314,27 @@ __global__ void __launch_bounds__(384, 1) win_dkv_kernel(const __grid_constant__
       const int j = t.n * kBlock + kr;  // this thread's key
       // queries that see it: j .. tmax
       const int tmax = j >= d.S ? -1 : j < d.ns || j + d.W - 1 >= d.S ? d.S - 1 : j + d.W - 1;
-      for (int tl = t.i0; tl < t.i1; ++tl, ++i) {
-        const int s = (int)(i % kMetaRing), tok = t.n * kBlock + tl * TT;
-        // visible rows lo .. hi of this half, as a 64-bit mask (two words)
-        const int lo = (j - tok) * G - 64 * hf, hi = (tmax - tok + 1) * G - 1 - 64 * hf;
-        const uint32_t vis[2] = {bit_range(lo, hi, 0), bit_range(lo, hi, 1)};
-        const bool full = __all_sync(0xffffffffu, (vis[0] & vis[1]) == 0xffffffffu);
-        if (!mbar_wait_warp(&sh->m_full[s], phase_of(i / kMetaRing), A.status) ||
+      const int k0 = t.n * kBlock;
+      const int tfull = k0 + kBlock <= d.ns || k0 + d.W >= d.S ? d.S : k0 + d.W;  // queries below it see key k0
+      for (int tl = t.i0; tl < t.i1; ++tl, ++i, meta.next()) {
+        const int s = meta.slot, tok = t.n * kBlock + tl * TT;
+        // the whole block behind every query of the tile, and inside its window?
+        const bool full = tok >= k0 + kBlock - 1 && tok + TT <= tfull;
+        uint32_t vis = 0xffffffffu;  // else the visible rows of this part, as a mask
+        if (!full) vis = bit_range((j - tok) * G - 32 * part, (tmax - tok + 1) * G - 1 - 32 * part, 0);
+        if (!mbar_wait_warp(&sh->m_full[s], meta.phase, A.status) ||
             !mbar_wait_warp(&sh->s_full, phase_of(i), A.status)) {
           ok = false;
           break;
         }
         fence_after_sync();
-        // ---- phase A: P^T of this key and 64 rows; kept in fp32 for phase B
-        float p[64];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        // ---- phase A: P^T of this key and 32 rows; kept in fp32 for phase B
+        float p[32];
+        {
           uint32_t rs[32], pw[16];
-          tmem_ld32(SB + lb + 64 * hf + 32 * c, rs);
+          tmem_ld32(Sx, rs);
           tmem_wait_ld();
-          const float4* l4 = reinterpret_cast<const float4*>(sh->nlse2[s] + 64 * hf + 32 * c);
+          const float4* l4 = reinterpret_cast<const float4*>(sh->nlse2[s] + 32 * part);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float4 nl = l4[e];
@@ -352,20 +342,19 @@ __global__ void __launch_bounds__(384, 1) win_dkv_kernel(const __grid_constant__
                                     sl2x2, make_float2(nl.x, nl.y));
             const float2 x1 = ffma2(make_float2(__uint_as_float(rs[4 * e + 2]), __uint_as_float(rs[4 * e + 3])),
                                     sl2x2, make_float2(nl.z, nl.w));
-            float* pe = p + 32 * c + 4 * e;
+            float* pe = p + 4 * e;
             pe[0] = exp2_ftz(x0.x);
             pe[1] = exp2_ftz(x0.y);
             pe[2] = exp2_ftz(x1.x);
             pe[3] = exp2_ftz(x1.y);
             if (!full) {
 #pragma unroll
-              for (int u = 0; u < 4; ++u) pe[u] = (vis[c] >> (4 * e + u)) & 1u ? pe[u] : 0.f;
+              for (int u = 0; u < 4; ++u) pe[u] = (vis >> (4 * e + u)) & 1u ? pe[u] : 0.f;
             }
             pw[2 * e] = pack_bf16(pe[0], pe[1]);
             pw[2 * e + 1] = pack_bf16(pe[2], pe[3]);
           }
-          // over columns of S^T this half has read
-          tmem_st16(SB + lb + 64 * hf + 16 * c, pw);
+          tmem_st16(Sx, pw);  // over columns of S^T this warp has read
         }
         tmem_wait_st();
         fence_before_sync();
@@ -374,26 +363,24 @@ __global__ void __launch_bounds__(384, 1) win_dkv_kernel(const __grid_constant__
         // ---- phase B: dS^T = P^T (scale dP^T - scale D)
         if (!mbar_wait_warp(&sh->dp_full, phase_of(i), A.status)) { ok = false; break; }
         fence_after_sync();
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        {
           uint32_t rp[32], dw[16];
-          tmem_ld32(DB + lb + 64 * hf + 32 * c, rp);
+          tmem_ld32(Dx, rp);
           tmem_wait_ld();
-          const float4* d4 = reinterpret_cast<const float4*>(sh->ndrow[s] + 64 * hf + 32 * c);
+          const float4* d4 = reinterpret_cast<const float4*>(sh->ndrow[s] + 32 * part);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float4 nd = d4[e];
-            const float* pe = p + 32 * c + 4 * e;
             float2 y0 = ffma2(make_float2(__uint_as_float(rp[4 * e]), __uint_as_float(rp[4 * e + 1])), sc2,
                               make_float2(nd.x, nd.y));
             float2 y1 = ffma2(make_float2(__uint_as_float(rp[4 * e + 2]), __uint_as_float(rp[4 * e + 3])), sc2,
                               make_float2(nd.z, nd.w));
-            y0 = fmul2(y0, make_float2(pe[0], pe[1]));
-            y1 = fmul2(y1, make_float2(pe[2], pe[3]));
+            y0 = fmul2(y0, make_float2(p[4 * e], p[4 * e + 1]));
+            y1 = fmul2(y1, make_float2(p[4 * e + 2], p[4 * e + 3]));
             dw[2 * e] = pack_bf16(y0.x, y0.y);
             dw[2 * e + 1] = pack_bf16(y1.x, y1.y);
           }
-          tmem_st16(DB + lb + 64 * hf + 16 * c, dw);
+          tmem_st16(Dx, dw);
         }
         tmem_wait_st();
         fence_before_sync();
@@ -404,42 +391,35 @@ __global__ void __launch_bounds__(384, 1) win_dkv_kernel(const __grid_constant__
         }
       }
       if (!ok) break;
-      // ---- item end: the dV (rows-0-63 warps) or dK (rows-64-127 warps) row of this key
+      // ---- item end: parts 0, 1 take the two halves of this key's dV row, parts 2, 3 of its dK row
       if (!mbar_wait_warp(&sh->acc_full, phase_of(nk), A.status)) break;
       ++nk;
       fence_after_sync();
-      const uint32_t acc = (hf == 0 ? RV : RK) + lb;
-      if (t.slot < 0) {
-        bf16* dst = (hf == 0 ? A.dv : A.dk) + (((long long)t.b * d.S + j) * d.Hkv + t.g) * kD;
+      const int which = part >> 1, col = 64 * (part & 1);
+      const uint32_t acc = (which == 0 ? RV : RK) + lb + col;
+      bf16* dst = (which == 0 ? A.dv : A.dk) + (((long long)t.b * d.S + j) * d.Hkv + t.g) * kD + col;
+      float* pdst = A.part + ((long long)t.slot * 2 + which) * (kBlock * kD) + (long long)kr * kD + col;
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t r[32];
-          tmem_ld32(acc + c * 32, r);
-          tmem_wait_ld();
-          if (j < d.S) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              uint4 w;
-              w.x = pack_bf16(__uint_as_float(r[8 * u]), __uint_as_float(r[8 * u + 1]));
-              w.y = pack_bf16(__uint_as_float(r[8 * u + 2]), __uint_as_float(r[8 * u + 3]));
-              w.z = pack_bf16(__uint_as_float(r[8 * u + 4]), __uint_as_float(r[8 * u + 5]));
-              w.w = pack_bf16(__uint_as_float(r[8 * u + 6]), __uint_as_float(r[8 * u + 7]));
-              reinterpret_cast<uint4*>(dst + c * 32)[u] = w;
-            }
-          }
-          __syncwarp();
-        }
-      } else {
-        float* dst = A.part + ((long long)t.slot * 2 + hf) * (kBlock * kD) + (long long)kr * kD;
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t r[32];
-          tmem_ld32(acc + c * 32, r);
-          tmem_wait_ld();
+      for (int c = 0; c < 2; ++c) {
+        uint32_t r[32];
+        tmem_ld32(acc + c * 32, r);
+        tmem_wait_ld();
+        if (t.slot >= 0) {
 #pragma unroll
           for (int u = 0; u < 8; ++u)
-            reinterpret_cast<uint4*>(dst + c * 32)[u] = make_uint4(r[4 * u], r[4 * u + 1], r[4 * u + 2], r[4 * u + 3]);
+            reinterpret_cast<uint4*>(pdst + c * 32)[u] = make_uint4(r[4 * u], r[4 * u + 1], r[4 * u + 2], r[4 * u + 3]);
+        } else if (j < d.S) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            uint4 w;
+            w.x = pack_bf16(__uint_as_float(r[8 * u]), __uint_as_float(r[8 * u + 1]));
+            w.y = pack_bf16(__uint_as_float(r[8 * u + 2]), __uint_as_float(r[8 * u + 3]));
+            w.z = pack_bf16(__uint_as_float(r[8 * u + 4]), __uint_as_float(r[8 * u + 5]));
+            w.w = pack_bf16(__uint_as_float(r[8 * u + 6]), __uint_as_float(r[8 * u + 7]));
+            reinterpret_cast<uint4*>(dst + c * 32)[u] = w;
+          }
         }
+        __syncwarp();
       }
       fence_before_sync();
       __syncwarp();
@@ -491,12 +471,11 @@ struct DqArgs {
   CUtensorMap q, dout, dq;
   const float2* rowm;
   unsigned* status;
-  int nseg;
-  long long units;  // nseg B Hkv: one 128-row tile each
+  long long units;  // one 128-row tile each
 };
 struct DqShared {
   uint64_t q_full, q_empty, do_full, do_empty, kv_full[kRingQ], kv_empty[kRingQ], s_full, dp_full, pa, pb,
-      dq_full, dq_free[2], st_full, mma_done;
+      dq_full, dq_free, st_full, mma_done;
   uint32_t tmem;
 };
 struct DqUnit {
@@ -522,7 +501,7 @@ __device__ __forceinline__ DqUnit dq_unit(const WinDims& d, long long u) {
 // the next unit's Q is loaded once the last S product has read it, its dO after the last dP product,
 // both a step before the unit ends.
 template <int G>
-__global__ void __launch_bounds__(384, 1) win_dq_kernel(const __grid_constant__ DqArgs A) {
+__global__ void __launch_bounds__(kBwdThreads, 1) win_dq_kernel(const __grid_constant__ DqArgs A) {
   using namespace sm100;
   const WinDims& d = A.d;
   extern __shared__ uint8_t smem_raw[];
@@ -531,7 +510,7 @@ __global__ void __launch_bounds__(384, 1) win_dq_kernel(const __grid_constant__ 
   uint8_t* sD = sQ + kTile;
   uint8_t* sR = sD + kTile;
   const uint32_t aQ = smem_u32(sQ), aD = smem_u32(sD), aR = smem_u32(sR);
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int tid = threadIdx.x, lane = tid % 32, warp = warp_number();
 
   if (tid == 0) {
     mbar_init(&sh->q_full, 1);
@@ -547,8 +526,7 @@ __global__ void __launch_bounds__(384, 1) win_dq_kernel(const __grid_constant__ 
     mbar_init(&sh->pa, kSoft);
     mbar_init(&sh->pb, kSoft);
     mbar_init(&sh->dq_full, 1);
-    mbar_init(&sh->dq_free[0], kSoft);
-    mbar_init(&sh->dq_free[1], kSoft);
+    mbar_init(&sh->dq_free, kSoft);
     mbar_init(&sh->st_full, kSoft);
     mbar_init(&sh->mma_done, 1);
     mbar_fence_init();
@@ -561,17 +539,24 @@ __global__ void __launch_bounds__(384, 1) win_dq_kernel(const __grid_constant__ 
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
-  const uint32_t SB = sh->tmem, DP = SB + 128, RQ0 = SB + 256;  // dQ of unit nu: RQ0 + 128 (nu & 1)
+  // dS of step i: DS + 64 (i & 1)
+  const uint32_t SB = sh->tmem, DP = SB + 128, DS = SB + 256, RQ = SB + 384;
 
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA loads
     if (lane == 0) {
       long long nl = 0, nu = 0;
-      // ring entry nl is free: true, its slot in `slot`
-      int slot = 0;
-      auto take = [&]() -> bool {
-        slot = (int)(nl % kRingQ);
-        return nl < kRingQ || mbar_wait(&sh->kv_empty[slot], phase_of(nl / kRingQ - 1), A.status);
+      Ring<kRingQ> ring;
+      auto taken = [&]() -> bool {  // the next ring slot is free
+        return !ring.wrapped || mbar_wait(&sh->kv_empty[ring.slot], ring.phase ^ 1, A.status);
+      };
+      auto load = [&](const KeyMaps& m, const DqUnit& x, int n) -> bool {
+        if (!taken()) return false;
+        mbar_expect_tx(&sh->kv_full[ring.slot], kTile);
+        load_key_tile(sR + ring.slot * kTile, m, x.run, n, x.g, x.b, &sh->kv_full[ring.slot]);
+        ring.next();
+        ++nl;
+        return true;
       };
       bool ok = true;
       for (long long u = blockIdx.x; u < A.units && ok; u += gridDim.x, ++nu) {
@@ -581,23 +566,18 @@ __global__ void __launch_bounds__(384, 1) win_dq_kernel(const __grid_constant__ 
         for (int c = 0; c < 2; ++c)
           tma_load_rows(sQ + c * (kTile / 2), &A.q, 64 * c, x.g * G, x.t0, x.b, &sh->q_full);
         for (int n = 0; n < x.run.nb && ok; ++n) {
-          if (!(ok = take())) break;
-          mbar_expect_tx(&sh->kv_full[slot], kTile);
-          load_key_tile(sR + slot * kTile, A.k, x.run, n, x.g, x.b, &sh->kv_full[slot]);
-          ++nl;
+          if (!(ok = load(A.k, x, n))) break;
           if (n == 0) {
             if (nu > 0 && !mbar_wait(&sh->do_empty, phase_of(nu - 1), A.status)) { ok = false; break; }
             mbar_expect_tx(&sh->do_full, kTile);
             for (int c = 0; c < 2; ++c)
               tma_load_rows(sD + c * (kTile / 2), &A.dout, 64 * c, x.g * G, x.t0, x.b, &sh->do_full);
           }
-          if (!(ok = take())) break;
-          mbar_expect_tx(&sh->kv_full[slot], kTile);
-          load_key_tile(sR + slot * kTile, A.v, x.run, n, x.g, x.b, &sh->kv_full[slot]);
-          ++nl;
+          ok = load(A.v, x, n);
         }
-        if (!ok || !(ok = take())) break;
-        mbar_arrive(&sh->kv_full[slot]);  // the tile dQ leaves through: nothing to load
+        if (!ok || !(ok = taken())) break;
+        mbar_arrive(&sh->kv_full[ring.slot]);  // the tile dQ leaves through: nothing to load
+        ring.next();
         ++nl;
       }
       // no copy may still be landing in shared memory when the block exits (after a wait that gave
@@ -612,88 +592,84 @@ __global__ void __launch_bounds__(384, 1) win_dq_kernel(const __grid_constant__ 
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issue
-    if (lane == 0) {
-      constexpr uint32_t id_s = idesc_bf16(128, 128, false, false);  // S = Q K^T, dP = dO V^T
-      constexpr uint32_t id_q = idesc_bf16(128, 128, false, true);   // dQ += dS K
-      // a step: key tile n of unit nu; its K is ring entry nl, its V nl + 1
+    {
+      // a step: key tile n of unit nu; its K and V in ring slots k and v
       struct Step {
-        long long u, nu, nl;
-        int n, nb;
+        long long u;
+        int nu, n, nb;
+        Ring<kRingQ> k, v;
       };
       auto load_unit = [&](Step& t) { t.nb = t.u < A.units ? dq_unit<G>(d, t.u).run.nb : 0; };
       auto next = [&](Step t) {
+        t.k = t.v;
+        t.k.next();
         if (t.n + 1 < t.nb) {
           ++t.n;
-          t.nl += 2;
         } else {
+          t.k.next();  // the tile dQ leaves through
           t.u += gridDim.x;
           ++t.nu;
           t.n = 0;
-          t.nl += 3;  // the entry dQ leaves through
           load_unit(t);
         }
+        t.v = t.k;
+        t.v.next();
         return t;
       };
       auto mma_s = [&](const Step& t) -> bool {
-        const int slot = (int)(t.nl % kRingQ);
-        if (t.n == 0 && !mbar_wait(&sh->q_full, phase_of(t.nu), A.status)) return false;
-        if (!mbar_wait(&sh->kv_full[slot], phase_of(t.nl / kRingQ), A.status)) return false;
+        if (t.n == 0 && !mbar_wait_warp(&sh->q_full, phase_of(t.nu), A.status)) return false;
+        if (!mbar_wait_warp(&sh->kv_full[t.k.slot], t.k.phase, A.status)) return false;
         fence_after_sync();
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          mma_ss(SB, desc_kmajor(aQ, 128, ks), desc_kmajor(aR + slot * kTile, 128, ks), id_s, ks > 0);
-        mma_commit(&sh->s_full);
-        if (t.n + 1 == t.nb) mma_commit(&sh->q_empty);
+        mma_kk(SB, aQ, aR + t.k.slot * kTile, false);  // S = Q K^T
+        warp_mma_commit(&sh->s_full);
+        if (t.n + 1 == t.nb) warp_mma_commit(&sh->q_empty);
         return true;
       };
       auto mma_dp = [&](const Step& t) -> bool {
-        const int slot = (int)((t.nl + 1) % kRingQ);
-        if (t.n == 0 && !mbar_wait(&sh->do_full, phase_of(t.nu), A.status)) return false;
-        if (!mbar_wait(&sh->kv_full[slot], phase_of((t.nl + 1) / kRingQ), A.status)) return false;
+        if (t.n == 0 && !mbar_wait_warp(&sh->do_full, phase_of(t.nu), A.status)) return false;
+        if (!mbar_wait_warp(&sh->kv_full[t.v.slot], t.v.phase, A.status)) return false;
         fence_after_sync();
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          mma_ss(DP, desc_kmajor(aD, 128, ks), desc_kmajor(aR + slot * kTile, 128, ks), id_s, ks > 0);
-        mma_commit(&sh->dp_full);
-        mma_commit(&sh->kv_empty[slot]);
-        if (t.n + 1 == t.nb) mma_commit(&sh->do_empty);
+        mma_kk(DP, aD, aR + t.v.slot * kTile, false);  // dP = dO V^T
+        warp_mma_commit(&sh->dp_full);
+        warp_mma_commit(&sh->kv_empty[t.v.slot]);
+        if (t.n + 1 == t.nb) warp_mma_commit(&sh->do_empty);
         return true;
       };
-      Step t{(long long)blockIdx.x, 0, 0, 0, 0};
+      Step t{(long long)blockIdx.x, 0, 0, 0, {}, {}};
+      t.v.next();
       load_unit(t);
       bool ok = t.nb > 0 && mma_s(t) && mma_dp(t);
-      for (long long i = 0; ok; ++i) {
+      for (int i = 0; ok; ++i) {
         const Step nx = next(t);
         const bool more = nx.nb > 0;
         // phase A has read S
-        if (!mbar_wait(&sh->pa, phase_of(i), A.status)) break;
+        if (!mbar_wait_warp(&sh->pa, phase_of(i), A.status)) break;
         if (more && !mma_s(nx)) break;
-        // phase B has written dS over dP
-        if (!mbar_wait(&sh->pb, phase_of(i), A.status)) break;
-        if (t.n == 0 && t.nu >= 2 && !mbar_wait(&sh->dq_free[t.nu & 1], phase_of(t.nu / 2 - 1), A.status)) break;
+        // phase B has read dP and written dS: dP of the next step first, dQ behind it (dS of step
+        // i + 2 is written only after dP of step i + 2, issued after this product, is there)
+        if (!mbar_wait_warp(&sh->pb, phase_of(i), A.status)) break;
+        if (more && !mma_dp(nx)) break;
+        // (the epilogue of the previous unit has read its dQ: it comes before phase B of this one)
+        if (t.n == 0 && t.nu >= 1 && !mbar_wait_warp(&sh->dq_free, phase_of(t.nu - 1), A.status)) break;
         fence_after_sync();
-        const int slot = (int)(t.nl % kRingQ);
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)  // keys 0-63 in columns 0-31, keys 64-127 in 64-95
-          mma_ts(RQ0 + 128 * (uint32_t)(t.nu & 1), DP + ks * 8 + (ks >= 4 ? 32 : 0),
-                 desc_mnmajor(aR + slot * kTile, 128, ks), id_q, t.n > 0 || ks > 0);
-        mma_commit(&sh->kv_empty[slot]);
-        if (t.n + 1 == t.nb) mma_commit(&sh->dq_full);
-        if (!more || !mma_dp(nx)) break;
+        mma_tn<8, 0>(RQ, DS + 64 * (i & 1), aR + t.k.slot * kTile, t.n > 0);  // dQ += dS K
+        warp_mma_commit(&sh->kv_empty[t.k.slot]);
+        if (t.n + 1 == t.nb) warp_mma_commit(&sh->dq_full);
+        if (!more) break;
         t = nx;
       }
-      mma_commit(&sh->mma_done);
-      mbar_wait(&sh->mma_done, 0, A.status);  // no product may still write tensor memory
+      warp_mma_commit(&sh->mma_done);
+      mbar_wait_warp(&sh->mma_done, 0, A.status);  // no product may still write tensor memory
     }
     __syncwarp();
   } else if (warp == 2) {
     // ---------------------------------------------------------------- TMA stores of dQ
     if (lane == 0) {
-      long long nl = 0, nu = 0;
-      for (long long u = blockIdx.x; u < A.units; u += gridDim.x, ++nu, ++nl) {
+      long long nu = 0;
+      int slot = 0;
+      for (long long u = blockIdx.x; u < A.units; u += gridDim.x, ++nu, slot = (slot + 1) % kRingQ) {
         const DqUnit x = dq_unit<G>(d, u);
-        nl += 2 * x.run.nb;  // the unit's last ring entry
-        const int slot = (int)(nl % kRingQ);
+        slot = (slot + 2 * x.run.nb) % kRingQ;  // the unit's last ring entry
         if (!mbar_wait(&sh->st_full, phase_of(nu), A.status)) break;
         tma_store_rows(&A.dq, aR + slot * kTile, 0, x.g * G, x.t0, x.b);
         tma_store_rows(&A.dq, aR + slot * kTile + kTile / 2, 64, x.g * G, x.t0, x.b);
@@ -706,7 +682,7 @@ __global__ void __launch_bounds__(384, 1) win_dq_kernel(const __grid_constant__ 
     __syncwarp();
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- softmax (thread = row)
-    const int hf = (warp - 4) >> 2;  // keys 64 hf .. 64 hf + 63 of the tile
+    const int part = (warp - 4) >> 2;  // keys 32 part .. 32 part + 31 of the tile
     const int quad = warp & 3;
     const int r = quad * 32 + lane;  // tile row = tensor-memory lane
     const uint32_t lb = static_cast<uint32_t>(quad * 32) << 16;
@@ -719,41 +695,38 @@ __global__ void __launch_bounds__(384, 1) win_dq_kernel(const __grid_constant__ 
       return t < d.S ? __ldg(A.rowm + ((long long)x.b * d.S + t) * d.Hq + x.g * G + r % G)
                      : make_float2(0.f, 0.f);
     };
-    // dQ of unit number `nu` (its ring entry `nl`): tensor memory -> bf16 rows of the swizzled tile
-    auto epilogue = [&](long long nu, long long nl) -> bool {
+    // dQ of unit number `nu` (ring entry `nl`): tensor memory -> bf16 rows of the swizzled tile
+    auto epilogue = [&](int nu, long long nl) -> bool {
       const int slot = (int)(nl % kRingQ);
       if (!mbar_wait_warp(&sh->dq_full, phase_of(nu), A.status) ||
           !mbar_wait_warp(&sh->kv_full[slot], phase_of(nl / kRingQ), A.status))
         return false;
       fence_after_sync();
-      const uint32_t src = RQ0 + 128 * (uint32_t)(nu & 1) + lb + 64 * hf;
-      const uint32_t dst = aR + slot * kTile + hf * (kTile / 2);
-#pragma unroll 1
-      for (int c = 0; c < 2; ++c) {
-        uint32_t v[32];
-        tmem_ld32(src + 32 * c, v);
-        tmem_wait_ld();
+      const uint32_t dst = aR + slot * kTile + (part >> 1) * (kTile / 2);
+      uint32_t v[32];
+      tmem_ld32(RQ + lb + 32 * part, v);
+      tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t w[4];
+      for (int e = 0; e < 4; ++e) {
+        uint32_t w[4];
 #pragma unroll
-          for (int y = 0; y < 4; ++y)
-            w[y] = pack_bf16(__uint_as_float(v[8 * e + 2 * y]), __uint_as_float(v[8 * e + 2 * y + 1]));
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(dst + sw128_chunk(r, 4 * c + e)),
-                       "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                       : "memory");
-        }
+        for (int y = 0; y < 4; ++y)
+          w[y] = pack_bf16(__uint_as_float(v[8 * e + 2 * y]), __uint_as_float(v[8 * e + 2 * y + 1]));
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(dst + sw128_chunk(r, 4 * (part & 1) + e)),
+                     "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                     : "memory");
       }
       fence_before_sync();
       fence_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&sh->dq_free[nu & 1]);
+        mbar_arrive(&sh->dq_free);
         mbar_arrive(&sh->st_full);
       }
       return true;
     };
-    long long i = 0, nu = 0, nl = 0, pending = -1;  // pending: ring entry of the last unit's dQ
+    long long nl = 0, pending = -1;  // pending: ring entry of the last unit's dQ
+    int i = 0, nu = 0;
     float2 m = row_data(blockIdx.x);
     bool ok = true;
     for (long long u = blockIdx.x; u < A.units && ok; u += gridDim.x, ++nu) {
@@ -762,51 +735,51 @@ __global__ void __launch_bounds__(384, 1) win_dq_kernel(const __grid_constant__ 
       const int t = x.t0 + r / G;
       const float2 nl2 = make_float2(-m.x, -m.x), nd2 = make_float2(-m.y * d.scale, -m.y * d.scale);
       for (int n = 0; n < x.run.nb; ++n, ++i) {
-        uint32_t vis[4];
-        visible_cols(d, x.run, n, t, vis);
-        const uint32_t vh[2] = {hf ? vis[2] : vis[0], hf ? vis[3] : vis[1]};
-        const bool full = __all_sync(0xffffffffu, (vh[0] & vh[1]) == 0xffffffffu);
+        const bool full = n >= x.run.f0 && n <= x.run.f1;
+        uint32_t vis = 0xffffffffu;
+        if (!full) {
+          uint32_t vis4[4];
+          visible_cols(d, x.run, n, t, vis4);
+          vis = part == 0 ? vis4[0] : part == 1 ? vis4[1] : part == 2 ? vis4[2] : vis4[3];
+        }
         if (!mbar_wait_warp(&sh->s_full, phase_of(i), A.status)) { ok = false; break; }
         fence_after_sync();
         // ---- phase A
-        float p[64];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        float p[32];
+        {
           uint32_t rs[32];
-          tmem_ld32(SB + lb + 64 * hf + 32 * c, rs);
+          tmem_ld32(SB + lb + 32 * part, rs);
           tmem_wait_ld();
+          fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh->pa);  // S is in registers
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const float2 y = ffma2(make_float2(__uint_as_float(rs[2 * e]), __uint_as_float(rs[2 * e + 1])), sl2x2, nl2);
-            float* pe = p + 32 * c + 2 * e;
-            pe[0] = exp2_ftz(y.x);
-            pe[1] = exp2_ftz(y.y);
+            p[2 * e] = exp2_ftz(y.x);
+            p[2 * e + 1] = exp2_ftz(y.y);
             if (!full) {
-              pe[0] = (vh[c] >> (2 * e)) & 1u ? pe[0] : 0.f;
-              pe[1] = (vh[c] >> (2 * e + 1)) & 1u ? pe[1] : 0.f;
+              p[2 * e] = (vis >> (2 * e)) & 1u ? p[2 * e] : 0.f;
+              p[2 * e + 1] = (vis >> (2 * e + 1)) & 1u ? p[2 * e + 1] : 0.f;
             }
           }
         }
-        fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->pa);
         if (n == 0 && pending >= 0 && !epilogue(nu - 1, pending)) { ok = false; break; }
         // ---- phase B
         if (!mbar_wait_warp(&sh->dp_full, phase_of(i), A.status)) { ok = false; break; }
         fence_after_sync();
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        {
           uint32_t rp[32], dw[16];
-          tmem_ld32(DP + lb + 64 * hf + 32 * c, rp);
+          tmem_ld32(DP + lb + 32 * part, rp);
           tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const float2 y = fmul2(
                 ffma2(make_float2(__uint_as_float(rp[2 * e]), __uint_as_float(rp[2 * e + 1])), sc2, nd2),
-                make_float2(p[32 * c + 2 * e], p[32 * c + 2 * e + 1]));
+                make_float2(p[2 * e], p[2 * e + 1]));
             dw[e] = pack_bf16(y.x, y.y);
           }
-          tmem_st16(DP + lb + 64 * hf + 16 * c, dw);  // over columns of dP this half has read
+          tmem_st16(DS + 64 * (i & 1) + lb + 16 * part, dw);
         }
         tmem_wait_st();
         fence_before_sync();
@@ -850,51 +823,69 @@ WinItems win_items(const WinDims& d) {
   return w;
 }
 
-template <int G>
-static void win_bwd_g(const DkvArgs& a, const DqArgs& b, cudaStream_t st) {
-  const int n = num_sms();
-  const size_t s1 = sizeof(DkvShared) + 1024 + 6 * (size_t)kTile;
-  const size_t s2 = sizeof(DqShared) + 1024 + (2 + kRingQ) * (size_t)kTile;
-  cudaFuncSetAttribute(win_dkv_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s1);
-  cudaFuncSetAttribute(win_dq_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s2);
-  win_dkv_kernel<G><<<a.it.items < n ? a.it.items : n, 384, s1, st>>>(a);
-  win_dq_kernel<G><<<(int)(b.units < n ? b.units : n), 384, s2, st>>>(b);
-  if (a.it.join_blocks)
-    win_join_kernel<G><<<dim3(a.it.join_blocks * a.d.B * a.d.Hkv * 16, 2), 256, 0, st>>>(a.d, a.it, a.part, a.dk, a.dv);
-}
+#define MSA_BY_GROUP(G_, CALL) \
+  switch (G_) {                \
+    case 1: CALL(1); break;    \
+    case 2: CALL(2); break;    \
+    case 4: CALL(4); break;    \
+    case 8: CALL(8); break;    \
+    case 16: CALL(16); break;  \
+    default: return false;     \
+  }
 
-bool launch_win_bwd(const WinDims& d, const void* q, const void* k, const void* v, const void* dout,
-                    const float2* rowm, void* dq, void* dk, void* dv, float* part, unsigned* status,
-                    cudaStream_t st) {
+bool launch_win_dkv(const WinDims& d, const void* q, const void* k, const void* v, const void* dout,
+                    const float2* rowm, void* dk, void* dv, float* part, unsigned* status, cudaStream_t st) {
   DkvArgs a;
-  DqArgs b;
-  const int tt = kBlock / d.G;
+  const int tt = kBlock / d.G, n = num_sms();
   if (!make_tmap_rows(&a.q, q, d.B, d.S, d.Hq, d.G, tt) || !make_tmap_rows(&a.dout, dout, d.B, d.S, d.Hq, d.G, tt) ||
-      !make_tmap_rows(&a.k, k, d.B, d.S, d.Hkv, 1, kBlock) || !make_tmap_rows(&a.v, v, d.B, d.S, d.Hkv, 1, kBlock) ||
-      !make_key_maps(d, k, &b.k) || !make_key_maps(d, v, &b.v) ||
-      !make_tmap_rows(&b.dq, dq, d.B, d.S, d.Hq, d.G, tt))
+      !make_tmap_rows(&a.k, k, d.B, d.S, d.Hkv, 1, kBlock) || !make_tmap_rows(&a.v, v, d.B, d.S, d.Hkv, 1, kBlock))
     return false;
-  a.d = b.d = d;
-  a.rowm = b.rowm = rowm;
-  a.status = b.status = status;
+  a.d = d;
+  a.rowm = rowm;
   a.dk = (bf16*)dk;
   a.dv = (bf16*)dv;
   a.part = part;
+  a.status = status;
   a.sched = reinterpret_cast<int*>(status + kSchedWinDkv);
   a.it = win_items(d);
-  b.q = a.q;
-  b.dout = a.dout;
-  b.nseg = (d.S + tt - 1) / tt;
-  b.units = (long long)b.nseg * d.B * d.Hkv;
-  switch (d.G) {
-    case 1: win_bwd_g<1>(a, b, st); break;
-    case 2: win_bwd_g<2>(a, b, st); break;
-    case 4: win_bwd_g<4>(a, b, st); break;
-    case 8: win_bwd_g<8>(a, b, st); break;
-    case 16: win_bwd_g<16>(a, b, st); break;
-    default: return false;
-  }
+  const size_t smem = sizeof(DkvShared) + 1024 + 6 * (size_t)kTile;
+#define MSA_CALL(G)                                                                                    \
+  cudaFuncSetAttribute(win_dkv_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);      \
+  win_dkv_kernel<G><<<a.it.items < n ? a.it.items : n, kBwdThreads, smem, st>>>(a)
+  MSA_BY_GROUP(d.G, MSA_CALL)
+#undef MSA_CALL
   return true;
 }
+
+bool launch_win_dq(const WinDims& d, const void* q, const void* k, const void* v, const void* dout,
+                   const float2* rowm, void* dq, unsigned* status, cudaStream_t st) {
+  DqArgs a;
+  const int tt = kBlock / d.G, n = num_sms();
+  if (!make_tmap_rows(&a.q, q, d.B, d.S, d.Hq, d.G, tt) || !make_tmap_rows(&a.dout, dout, d.B, d.S, d.Hq, d.G, tt) ||
+      !make_tmap_rows(&a.dq, dq, d.B, d.S, d.Hq, d.G, tt) || !make_key_maps(d, k, &a.k) || !make_key_maps(d, v, &a.v))
+    return false;
+  a.d = d;
+  a.rowm = rowm;
+  a.status = status;
+  a.units = (long long)((d.S + tt - 1) / tt) * d.B * d.Hkv;
+  const size_t smem = sizeof(DqShared) + 1024 + (2 + kRingQ) * (size_t)kTile;
+#define MSA_CALL(G)                                                                                  \
+  cudaFuncSetAttribute(win_dq_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);     \
+  win_dq_kernel<G><<<(int)(a.units < n ? a.units : n), kBwdThreads, smem, st>>>(a)
+  MSA_BY_GROUP(d.G, MSA_CALL)
+#undef MSA_CALL
+  return true;
+}
+
+bool launch_win_join(const WinDims& d, const float* part, void* dk, void* dv, cudaStream_t st) {
+  const WinItems w = win_items(d);
+  if (!w.join_blocks) return true;
+  const dim3 grid(w.join_blocks * d.B * d.Hkv * 16, 2);
+#define MSA_CALL(G) win_join_kernel<G><<<grid, 256, 0, st>>>(d, w, part, (bf16*)dk, (bf16*)dv)
+  MSA_BY_GROUP(d.G, MSA_CALL)
+#undef MSA_CALL
+  return true;
+}
+#undef MSA_BY_GROUP
 
 }  // namespace msa

@@ -20,9 +20,12 @@
 // Q has two buffers, so a unit's loads and first products overlap the previous unit's end; O leaves
 // through the unit's own Q buffer by TMA stores, which also drop the rows past the sequence.
 //
-// Roles (384 threads): warp 0 TMA loads, warp 1 MMA issue, warps 2 / 3 the TMA stores of tile A / B,
-// warps 4-7 / 8-11 softmax and epilogue of tile A / B.  Tensor memory: S_A, S_B, O_A, O_B (512
-// columns).  Units have equal cost but for the sequence's first window: they are dealt in turn,
+// Roles (640 threads): warp 0 TMA loads, warp 1 MMA issue, warps 2 / 3 the TMA stores of tile A / B,
+// warps 4-11 / 12-19 softmax and epilogue of tile A / B: a row belongs to two threads, one per half of
+// the columns, so that a tile's softmax (with one thread a row it took 3,000 cycles, longer than the
+// other tile's products) fits behind the products.  The two share the row maximum: a barrier that ORs
+// "my half exceeds it" across them, and an exchange through shared memory in the rare case it does.
+// Tensor memory: S_A, S_B, O_A, O_B (512 columns).  Units have equal cost but for the sequence's first window: they are dealt in turn,
 // tokens outermost, so that concurrent units share K and V.  Every wait is bounded.
 #include <math.h>
 
@@ -46,7 +49,9 @@ struct FwdArgs {
   int nseg;         // units along a sequence
   long long units;  // nseg B Hkv
 };
+constexpr int kFwdThreads = 640;
 struct FwdShared {
+  float half[2][2][128];  // per tile, half and row: the half's maximum, later its row sum
   uint64_t q_full[2], q_empty[2], kv_full[kRing], kv_empty[kRing], s_full[2], p_full[2], o_full[2],
       o_free[2], st_full[2], mma_done;
   uint32_t tmem;
@@ -75,27 +80,31 @@ __device__ __forceinline__ FwdUnit fwd_unit(const FwdArgs& A, long long u) {
 }  // namespace
 
 template <int G>
-__global__ void __launch_bounds__(384, 1) win_fwd_kernel(const __grid_constant__ FwdArgs A) {
+__global__ void __launch_bounds__(kFwdThreads, 1) win_fwd_kernel(const __grid_constant__ FwdArgs A) {
   using namespace sm100;
   constexpr int TT = 128 / G;
   const WinDims& d = A.d;
-  extern __shared__ uint8_t smem_raw[];
-  FwdShared* sh = reinterpret_cast<FwdShared*>(smem_raw);
-  uint8_t* sQ = align1024(smem_raw + sizeof(FwdShared));  // [2 units][2 tiles][128 rows][128 d]
-  uint8_t* sR = sQ + 4 * kTile;                            // K / V ring
+  extern __shared__ __align__(1024) uint8_t smem_tiles[];
+  uint8_t* sQ = smem_tiles;      // [2 units][2 tiles][128 rows][128 d]
+  uint8_t* sR = sQ + 4 * kTile;  // K / V ring
+  FwdShared* sh = reinterpret_cast<FwdShared*>(sR + kRing * kTile);
   const uint32_t aQ = smem_u32(sQ), aR = smem_u32(sR);
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int tid = threadIdx.x, lane = tid % 32, warp = warp_number();
   const float sl2 = d.scale * kLog2e;
+  if (aQ & 1023u) {  // the swizzled operand layout needs 1024-byte atoms
+    if (tid == 0) atomicOr(A.status, kStatusInternal);
+    return;
+  }
 
   if (tid == 0) {
     for (int x = 0; x < 2; ++x) {
       mbar_init(&sh->q_full[x], 1);
       mbar_init(&sh->q_empty[x], 2);  // the store warps of both tiles
       mbar_init(&sh->s_full[x], 1);
-      mbar_init(&sh->p_full[x], 4);
+      mbar_init(&sh->p_full[x], 8);
       mbar_init(&sh->o_full[x], 1);
-      mbar_init(&sh->o_free[x], 4);
-      mbar_init(&sh->st_full[x], 4);
+      mbar_init(&sh->o_free[x], 8);
+      mbar_init(&sh->st_full[x], 8);
     }
     for (int x = 0; x < kRing; ++x) {
       mbar_init(&sh->kv_full[x], 1);
@@ -120,6 +129,7 @@ __global__ void __launch_bounds__(384, 1) win_fwd_kernel(const __grid_constant__
     if (lane == 0) {
       bool ok = true;
       long long nl = 0, nu = 0;
+      Ring<kRing> kv;
       for (long long u = blockIdx.x; u < A.units && ok; u += gridDim.x, ++nu) {
         const FwdUnit x = fwd_unit<G>(A, u);
         const int qs = (int)(nu & 1);
@@ -131,14 +141,13 @@ __global__ void __launch_bounds__(384, 1) win_fwd_kernel(const __grid_constant__
             tma_load_rows(dq + X * kTile + c * (kTile / 2), &A.q, 64 * c, x.g * G, x.t0 + X * TT, x.b,
                           &sh->q_full[qs]);
         for (int n = 0; n < x.run.nb && ok; ++n)
-          for (int w = 0; w < 2; ++w, ++nl) {  // K_n, then V_n
-            const int slot = (int)(nl % kRing);
-            if (nl >= kRing && !mbar_wait(&sh->kv_empty[slot], phase_of(nl / kRing - 1), A.status)) {
+          for (int w = 0; w < 2; ++w, ++nl, kv.next()) {  // K_n, then V_n
+            if (kv.wrapped && !mbar_wait(&sh->kv_empty[kv.slot], kv.phase ^ 1, A.status)) {
               ok = false;
               break;
             }
-            mbar_expect_tx(&sh->kv_full[slot], kTile);
-            load_key_tile(sR + slot * kTile, w ? A.v : A.k, x.run, n, x.g, x.b, &sh->kv_full[slot]);
+            mbar_expect_tx(&sh->kv_full[kv.slot], kTile);
+            load_key_tile(sR + kv.slot * kTile, w ? A.v : A.k, x.run, n, x.g, x.b, &sh->kv_full[kv.slot]);
           }
       }
       // no copy may still be landing in shared memory when the block exits
@@ -150,62 +159,59 @@ __global__ void __launch_bounds__(384, 1) win_fwd_kernel(const __grid_constant__
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issue
-    if (lane == 0) {
-      constexpr uint32_t id_s = idesc_bf16(128, 128, false, false);  // S = Q K^T
-      constexpr uint32_t id_o = idesc_bf16(128, 128, false, true);   // O += P V
-      long long nl = 0, nu = 0;
-      long long cs[2] = {0, 0};  // S products issued per tile
-      long long cu[2] = {0, 0};  // units begun per tile (o_free phases)
+    {
+      int cs[2] = {0, 0};  // S products issued per tile
+      int cu[2] = {0, 0};  // units begun per tile (o_free phases)
+      Ring<kRing> kv;
+      int v_slot = 0;  // the last V and its phase
+      uint32_t v_phase = 0;
       bool ok = true;
-      // O_X += P_X V for the last S product of tile X; V is load `lv` of the ring
-      auto mma_o = [&](int X, bool first, long long lv, bool last, bool free_v) -> bool {
-        if (!mbar_wait(&sh->p_full[X], phase_of(cs[X] - 1), A.status)) return false;
+      // O_X += P_X V for the last S product of tile X
+      auto mma_o = [&](int X, bool first, bool last, bool free_v) -> bool {
+        if (!mbar_wait_warp(&sh->p_full[X], phase_of(cs[X] - 1), A.status)) return false;
         if (first) {
-          if (cu[X] > 0 && !mbar_wait(&sh->o_free[X], phase_of(cu[X] - 1), A.status)) return false;
+          if (cu[X] > 0 && !mbar_wait_warp(&sh->o_free[X], phase_of(cu[X] - 1), A.status)) return false;
           ++cu[X];
         }
-        const int slot = (int)(lv % kRing);
-        if (!mbar_wait(&sh->kv_full[slot], phase_of(lv / kRing), A.status)) return false;
+        if (!mbar_wait_warp(&sh->kv_full[v_slot], v_phase, A.status)) return false;
         fence_after_sync();
-        const uint32_t aV = aR + slot * kTile;
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          mma_ts(O0 + 128 * X, S0 + 128 * X + ks * 8, desc_mnmajor(aV, 128, ks), id_o, !first || ks > 0);
-        if (last) mma_commit(&sh->o_full[X]);
-        if (free_v) mma_commit(&sh->kv_empty[slot]);
+        mma_tn<4, 64>(O0 + 128 * X, S0 + 128 * X, aR + v_slot * kTile, !first);
+        if (last) warp_mma_commit(&sh->o_full[X]);
+        if (free_v) warp_mma_commit(&sh->kv_empty[v_slot]);
         return true;
       };
       auto mma_s = [&](int X, uint32_t q, int kslot, bool free_k) {
         fence_after_sync();
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          mma_ss(S0 + 128 * X, desc_kmajor(q + X * kTile, 128, ks), desc_kmajor(aR + kslot * kTile, 128, ks),
-                 id_s, ks > 0);
-        mma_commit(&sh->s_full[X]);
-        if (free_k) mma_commit(&sh->kv_empty[kslot]);
+        mma_kk(S0 + 128 * X, q + X * kTile, aR + kslot * kTile, false);  // S = Q K^T
+        warp_mma_commit(&sh->s_full[X]);
+        if (free_k) warp_mma_commit(&sh->kv_empty[kslot]);
         ++cs[X];
       };
+      int nu = 0;
       for (long long u = blockIdx.x; u < A.units && ok; u += gridDim.x, ++nu) {
         const FwdUnit x = fwd_unit<G>(A, u);
-        const int qs = (int)(nu & 1);
+        const int qs = nu & 1;
         const uint32_t q = aQ + qs * 2 * kTile;
-        if (!mbar_wait(&sh->q_full[qs], phase_of(nu >> 1), A.status)) break;
-        for (int n = 0; n < x.run.nb; ++n, nl += 2) {
-          const int kslot = (int)(nl % kRing);
-          if (!mbar_wait(&sh->kv_full[kslot], phase_of(nl / kRing), A.status)) { ok = false; break; }
-          if (n > 0 && !mma_o(0, n == 1, nl - 1, false, !x.two)) { ok = false; break; }
+        if (!mbar_wait_warp(&sh->q_full[qs], phase_of(nu >> 1), A.status)) break;
+        for (int n = 0; n < x.run.nb; ++n) {
+          const int kslot = kv.slot;
+          if (!mbar_wait_warp(&sh->kv_full[kslot], kv.phase, A.status)) { ok = false; break; }
+          if (n > 0 && !mma_o(0, n == 1, false, !x.two)) { ok = false; break; }
           mma_s(0, q, kslot, !x.two);
           if (x.two) {
-            if (n > 0 && !mma_o(1, n == 1, nl - 1, false, true)) { ok = false; break; }
+            if (n > 0 && !mma_o(1, n == 1, false, true)) { ok = false; break; }
             mma_s(1, q, kslot, true);
           }
+          kv.next();
+          v_slot = kv.slot;
+          v_phase = kv.phase;
+          kv.next();
         }
         if (!ok) break;
-        ok = mma_o(0, x.run.nb == 1, nl - 1, true, !x.two) &&
-             (!x.two || mma_o(1, x.run.nb == 1, nl - 1, true, true));
+        ok = mma_o(0, x.run.nb == 1, true, !x.two) && (!x.two || mma_o(1, x.run.nb == 1, true, true));
       }
-      mma_commit(&sh->mma_done);
-      mbar_wait(&sh->mma_done, 0, A.status);  // no product may still write tensor memory
+      warp_mma_commit(&sh->mma_done);
+      mbar_wait_warp(&sh->mma_done, 0, A.status);  // no product may still write tensor memory
     }
     __syncwarp();
   } else if (warp < 4) {
@@ -233,56 +239,70 @@ __global__ void __launch_bounds__(384, 1) win_fwd_kernel(const __grid_constant__
     __syncwarp();
   } else {
     // ---------------------------------------------------------------- softmax + epilogue
-    const int X = (warp - 4) >> 2;  // tile A (warps 4-7) or B (warps 8-11)
-    const int w4 = warp % 4;
-    const int r = w4 * 32 + lane;  // tile row = tensor-memory lane
-    const uint32_t lb = static_cast<uint32_t>(w4 * 32) << 16;
-    const uint32_t Sx = S0 + 128 * X + lb, Ox = O0 + 128 * X + lb;
+    const int X = (warp - 4) >> 3;         // tile A (warps 4-11) or B (warps 12-19)
+    const int hf = ((warp - 4) >> 2) & 1;  // columns 64 hf .. 64 hf + 63
+    const int quad = warp & 3;
+    const int r = quad * 32 + lane;  // tile row = tensor-memory lane
+    const uint32_t lb = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t Sx = S0 + 128 * X + 64 * hf + lb, Ox = O0 + 128 * X + 64 * hf + lb;
     const float2 sl2x2 = make_float2(sl2, sl2);
-    long long cs = 0, nu = 0, nt = 0;  // S products, units, units with this tile
+    const int bar = 1 + X * 4 + quad;  // named barrier of the two warps that share these rows
+    float* mine = &sh->half[X][hf][r];
+    const float* other = &sh->half[X][hf ^ 1][r];
+    int cs = 0, nu = 0, nt = 0;  // S products, units, units with this tile
+    // Both warps of a pair pass the same barriers whatever happens: a wait that gives up only clears
+    // `ok` (warp-uniform), which skips the later waits.
     bool ok = true;
-    for (long long u = blockIdx.x; u < A.units && ok; u += gridDim.x, ++nu) {
+    for (long long u = blockIdx.x; u < A.units; u += gridDim.x, ++nu) {
       const FwdUnit x = fwd_unit<G>(A, u);
       if (X == 1 && !x.two) continue;
       const int t = x.t0 + X * TT + r / G;  // this row's token
       const int h = x.g * G + r % G;         // and query head
       float mr = -INFINITY, l = 0.f;
       for (int n = 0; n < x.run.nb; ++n, ++cs) {
-        uint32_t vis[4];
-        visible_cols(d, x.run, n, t, vis);
-        // tcgen05.ld / st are warp-collective: the masked path is chosen per warp
-        const bool full = __all_sync(0xffffffffu, (vis[0] & vis[1] & vis[2] & vis[3]) == 0xffffffffu);
-        if (!mbar_wait_warp(&sh->s_full[X], phase_of(cs), A.status)) { ok = false; break; }
-        fence_after_sync();
-        float mx = -INFINITY;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t v[32];
-          tmem_ld32(Sx + q * 32, v);
-          tmem_wait_ld();
-          if (full) {
-#pragma unroll
-            for (int c = 0; c < 32; c += 2) mx = fmax3(mx, __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
-          } else {
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-              mx = fmaxf(mx, (vis[q] >> c) & 1u ? __uint_as_float(v[c]) : -INFINITY);
-          }
+        // (the masks cost about as many instructions as the exponentials: only where a tile needs them)
+        const bool full = n >= x.run.f0 && n <= x.run.f1;
+        uint32_t v0 = 0xffffffffu, v1 = v0;
+        if (!full) {
+          uint32_t vis[4];
+          visible_cols(d, x.run, n, t, vis);
+          v0 = hf ? vis[2] : vis[0];
+          v1 = hf ? vis[3] : vis[1];
         }
-        if (n == 0) {
-          mr = mx;
+        if (ok) ok = mbar_wait_warp(&sh->s_full[X], phase_of(cs), A.status);
+        fence_after_sync();
+        uint32_t s0[32], s1[32];
+        tmem_ld32(Sx, s0);
+        tmem_ld32(Sx + 32, s1);
+        tmem_wait_ld();
+        float mx = -INFINITY;
+        if (full) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) mx = fmax3(mx, __uint_as_float(s0[c]), __uint_as_float(s1[c]));
         } else {
-          const bool need = (mx - mr) * sl2 > kSlack;  // (both -inf: NaN, no)
-          if (__any_sync(0xffffffffu, need)) {          // rescale O and l of this warp's rows
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            mx = fmax3(mx, (v0 >> c) & 1u ? __uint_as_float(s0[c]) : -INFINITY,
+                       (v1 >> c) & 1u ? __uint_as_float(s1[c]) : -INFINITY);
+        }
+        if (bar_or(bar, 64, (mx - mr) * sl2 > kSlack || n == 0)) {  // (both -inf: NaN, no)
+          *mine = mx;
+          bar_sync(bar, 64);
+          mx = fmaxf(mx, *other);
+          if (n == 0) {
+            mr = mx;
+          } else if (__any_sync(0xffffffffu, (mx - mr) * sl2 > kSlack)) {
+            // rescale this half of O and l of the rows that need it
+            const bool need = (mx - mr) * sl2 > kSlack;
             const float alpha = need ? exp2_ftz((mr - mx) * sl2) : 1.f;
 #pragma unroll 1
             for (int q = 0; q < 4; ++q) {
-              uint32_t v[32];
-              tmem_ld32(Ox + q * 32, v);
+              uint32_t v[16];
+              tmem_ld16(Ox + q * 16, v);
               tmem_wait_ld();
 #pragma unroll
-              for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * alpha);
-              tmem_st32(Ox + q * 32, v);
+              for (int c = 0; c < 16; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * alpha);
+              tmem_st16(Ox + q * 16, v);
             }
             l *= alpha;
             if (need) mr = mx;
@@ -291,67 +311,64 @@ __global__ void __launch_bounds__(384, 1) win_fwd_kernel(const __grid_constant__
         const float mb = mr == -INFINITY ? 0.f : mr * sl2;
         const float2 nmb = make_float2(-mb, -mb);
         float2 la = make_float2(0.f, 0.f);
-#pragma unroll 1  // (a full unroll makes the compiler spill)
-        for (int q = 0; q < 4; ++q) {
-          uint32_t v[32];
-          tmem_ld32(Sx + q * 32, v);
-          tmem_wait_ld();
+        auto exps = [&](const uint32_t (&s)[32], uint32_t vw, uint32_t at) {
           uint32_t pw[16];
-          const uint32_t vq = q == 0 ? vis[0] : q == 1 ? vis[1] : q == 2 ? vis[2] : vis[3];
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
-            const float2 e = ffma2(make_float2(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1])),
-                                   sl2x2, nmb);
+            const float2 e = ffma2(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), sl2x2, nmb);
             float2 p = make_float2(exp2_ftz(e.x), exp2_ftz(e.y));
             if (!full) {
-              p.x = (vq >> (2 * c)) & 1u ? p.x : 0.f;
-              p.y = (vq >> (2 * c + 1)) & 1u ? p.y : 0.f;
+              p.x = (vw >> (2 * c)) & 1u ? p.x : 0.f;
+              p.y = (vw >> (2 * c + 1)) & 1u ? p.y : 0.f;
             }
             la = fadd2(la, p);
             pw[c] = pack_bf16(p.x, p.y);
           }
-          tmem_st16(Sx + q * 16, pw);
-        }
+          tmem_st16(at, pw);
+        };
+        exps(s0, v0, Sx);
+        // the second 32 columns again: kept in registers all along, they made the compiler spill
+        tmem_ld32(Sx + 32, s1);
+        tmem_wait_ld();
+        exps(s1, v1, Sx + 16);
         l += la.x + la.y;
         tmem_wait_st();
         fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->p_full[X]);
       }
-      if (!ok) break;
       // ---- unit end: O / l into the tile's own Q rows (every S product has read them), as the
       // swizzled tile its TMA store expects; then the LSE
-      if (!mbar_wait_warp(&sh->o_full[X], phase_of(nt), A.status)) break;
+      if (ok) ok = mbar_wait_warp(&sh->o_full[X], phase_of(nt), A.status);
       ++nt;
+      *mine = l;  // (the other warp has read this thread's last maximum: O is there)
+      bar_sync(bar, 64);
+      l += *other;
       fence_after_sync();
       const float sc = __fdividef(1.f, l);
-      const uint32_t dst = aQ + ((int)(nu & 1) * 2 + X) * kTile;
-#pragma unroll 1
-      for (int q = 0; q < 4; ++q) {
-        uint32_t v[32];
-        tmem_ld32(Ox + q * 32, v);
-        tmem_wait_ld();
-        if (q == 3) {  // O_X may now take the next unit's products
-          fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh->o_free[X]);
-        }
+      const uint32_t dst = aQ + ((nu & 1) * 2 + X) * kTile + hf * (kTile / 2);
+      uint32_t v0[32], v1[32];
+      tmem_ld32(Ox, v0);
+      tmem_ld32(Ox + 32, v1);
+      tmem_wait_ld();
+      fence_before_sync();  // O_X may now take the next unit's products
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->o_free[X]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t w[4];
+      for (int c = 0; c < 8; ++c) {
+        const uint32_t(&v)[32] = c < 4 ? v0 : v1;
+        uint32_t w[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            w[e] = pack_bf16(__uint_as_float(v[8 * c + 2 * e]) * sc, __uint_as_float(v[8 * c + 2 * e + 1]) * sc);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(
-                           dst + (q >> 1) * (kTile / 2) + sw128_chunk(r, (q & 1) * 4 + c)),
-                       "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                       : "memory");
-        }
+        for (int e = 0; e < 4; ++e)
+          w[e] = pack_bf16(__uint_as_float(v[8 * (c & 3) + 2 * e]) * sc, __uint_as_float(v[8 * (c & 3) + 2 * e + 1]) * sc);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(dst + sw128_chunk(r, c)), "r"(w[0]),
+                     "r"(w[1]), "r"(w[2]), "r"(w[3])
+                     : "memory");
       }
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->st_full[X]);
-      if (t < d.S) A.lse[((long long)x.b * d.Hq + h) * d.S + t] = (mr * sl2 + __log2f(l)) * kLn2;
+      if (hf == 0 && t < d.S) A.lse[((long long)x.b * d.Hq + h) * d.S + t] = (mr * sl2 + __log2f(l)) * kLn2;
     }
   }
   fence_before_sync();
@@ -370,10 +387,10 @@ bool make_key_maps(const WinDims& d, const void* base, KeyMaps* m) {
 
 template <int G>
 static void win_fwd_g(const FwdArgs& a, cudaStream_t st) {
-  const size_t smem = sizeof(FwdShared) + 1024 + (4 + kRing) * (size_t)kTile;
+  const size_t smem = sizeof(FwdShared) + (4 + kRing) * (size_t)kTile;
   cudaFuncSetAttribute(win_fwd_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   const int n = num_sms();
-  win_fwd_kernel<G><<<(int)(a.units < n ? a.units : n), 384, smem, st>>>(a);
+  win_fwd_kernel<G><<<(int)(a.units < n ? a.units : n), kFwdThreads, smem, st>>>(a);
 }
 
 bool launch_win_fwd(const WinDims& d, const void* q, const void* k, const void* v, void* o,

@@ -21,6 +21,7 @@ struct KeyRun {
   int nsp;  // virtual rows of the sink part (0: the parts meet, the walk starts at key 0)
   int len;  // virtual keys
   int nb;   // 128-key tiles
+  int f0, f1;  // tiles f0 .. f1 (none if f0 > f1) are seen whole by every query of the run
 };
 __device__ __forceinline__ KeyRun key_run(const WinDims& d, int t0, int t1) {
   KeyRun r;
@@ -29,6 +30,10 @@ __device__ __forceinline__ KeyRun key_run(const WinDims& d, int t0, int t1) {
   if (r.ws <= r.nsp) r.ws = r.nsp = 0;
   r.len = r.nsp + t1 + 1 - r.ws;
   r.nb = (r.len + kBlock - 1) / kBlock;
+  const int off = r.nsp - r.ws;  // virtual position of a window key: key + off
+  const int lo = t1 - d.W + 1 + off > r.nsp ? t1 - d.W + 1 + off : r.nsp;  // first key of the last query
+  r.f0 = (lo + kBlock - 1) / kBlock;
+  r.f1 = (t0 + off + 1) / kBlock - 1;
   return r;
 }
 
@@ -97,6 +102,91 @@ __device__ __forceinline__ void load_key_tile(uint8_t* dst, const KeyMaps& m, co
     tma_load_rows(dst + a * 128, &m.rest, 0, head, r.ws, b, mbar);
     tma_load_rows(dst + kPanel + a * 128, &m.rest, 64, head, r.ws, b, mbar);
   }
+}
+
+// One 128 x 128 x 128 product is eight tcgen05.mma of K = 16.  One thread issues every product of a
+// block, so the instructions between two MMAs count: issued by "lane 0" of a divergent branch, with a
+// descriptor built for each, an MMA took 83 cycles alone and about 120 beside the softmax warps,
+// whatever its N up to 128; the tensor core needs 64.  So the whole warp runs the issue code converged
+// and elect.sync inside the instruction sequence picks the thread (the same one every time), which
+// keeps the operands in uniform registers; the descriptors' upper half is one constant and each step
+// adds a constant to the lower half (all tiles are 128 rows: a K-major operand moves 32 bytes a step
+// and to its second panel after four, an MN-major one 16 rows).  64 to 67 cycles an MMA, measured
+// with one block per SM on GB300.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride 1024, version, SW128
+__device__ __forceinline__ uint32_t desc_lo_k(uint32_t tile) { return (tile >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_lo_mn(uint32_t tile) { return (tile >> 4) | ((128u * 128u >> 4) << 16); }
+__device__ __forceinline__ constexpr uint32_t step_k(int ks) { return (ks >> 2) * (128 * 128 >> 4) + (ks & 3) * 2; }
+__device__ __forceinline__ constexpr uint32_t step_mn(int ks) { return ks * (16 * 128 >> 4); }
+__device__ __forceinline__ void warp_mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n.reg .pred p, q;\n.reg .b64 da, db;\n.reg .b32 el;\nsetp.ne.b32 p, %4, 0;\n"
+      "mov.b64 da, {%1, %5};\nmov.b64 db, {%2, %5};\nelect.sync el|q, 0xffffffff;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(acc ? 1u : 0u), "r"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void warp_mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n.reg .pred p, q;\n.reg .b64 db;\n.reg .b32 el;\nsetp.ne.b32 p, %4, 0;\n"
+      "mov.b64 db, {%2, %5};\nelect.sync el|q, 0xffffffff;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(acc ? 1u : 0u), "r"(kDescHi)
+      : "memory");
+}
+// Arrive on an mbarrier once every MMA the warp issued so far has completed.
+__device__ __forceinline__ void warp_mma_commit(uint64_t* mbar) {
+  asm volatile(
+      "{\n.reg .pred q;\n.reg .b32 el;\nelect.sync el|q, 0xffffffff;\n"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(mbar))
+      : "memory");
+}
+// D (+)= A B^T, both K-major tiles in shared memory.
+__device__ __forceinline__ void mma_kk(uint32_t d, uint32_t a_tile, uint32_t b_tile, bool acc) {
+  constexpr uint32_t id = sm100::idesc_bf16(128, 128, false, false);
+  const uint32_t a = desc_lo_k(a_tile), b = desc_lo_k(b_tile);
+  warp_mma_ss(d, a, b, id, acc);
+#pragma unroll
+  for (int ks = 1; ks < 8; ++ks) warp_mma_ss(d, a + step_k(ks), b + step_k(ks), id, true);
+}
+// D (+)= A B, A in tensor memory (16 K values are 8 columns; runs of kRun steps start kPitch columns
+// apart), B an MN-major tile in shared memory.
+template <int kRun, int kPitch>
+__device__ __forceinline__ void mma_tn(uint32_t d, uint32_t a, uint32_t b_tile, bool acc) {
+  constexpr uint32_t id = sm100::idesc_bf16(128, 128, false, true);
+  const uint32_t b = desc_lo_mn(b_tile);
+  warp_mma_ts(d, a, b, id, acc);
+#pragma unroll
+  for (int ks = 1; ks < 8; ++ks)
+    warp_mma_ts(d, a + (ks / kRun) * kPitch + (ks % kRun) * 8, b + step_mn(ks), id, true);
+}
+// This thread's warp number, as a value the compiler knows to be the same in the whole warp.
+__device__ __forceinline__ int warp_number() { return __shfl_sync(0xffffffffu, threadIdx.x / 32, 0); }
+
+// Position in a ring of N slots: the slot and the phase of its barriers' current use.
+template <int N>
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  bool wrapped = false;  // the slot has been used before (its empty barrier has to be waited for)
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      phase ^= 1;
+      wrapped = true;
+    }
+  }
+};
+
+// Named barrier over `n` threads that also ORs a predicate across them.
+__device__ __forceinline__ bool bar_or(int id, int n, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.b32 p, %3, 0;\nbar.red.or.pred q, %1, %2, p;\nselp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(id), "r"(n), "r"((int)p)
+      : "memory");
+  return r != 0;
 }
 
 __device__ __forceinline__ uint32_t phase_of(long long k) { return (uint32_t)(k & 1); }
