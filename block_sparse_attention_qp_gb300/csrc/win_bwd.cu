@@ -14,9 +14,10 @@
 // Both split the softmax of a tile in two phases, so that the tensor core works through each of them:
 //   A  P from S alone, as soon as S is there (kept in fp32 registers for phase B)
 //   B  dS from P and dP.
-// win_dkv: ... dV(i) S(i+1) | dK(i) dP(i+1) ...: the first pair runs behind phase B of tile i, the
-// second behind phase A of tile i+1, and each phase waits for the pair before it only.  P^T and dS^T
-// (bf16) overwrite S^T and dP^T in tensor memory and are the products' A operands from there.
+// win_dkv: ... S(i+1) | dV(i) dK(i) dP(i+1) ...: S(i+1) is issued once S(i) is in registers, the rest
+// after phase B of tile i, running behind phase A of tile i+1.  P^T and dS^T (bf16) take dP^T's columns
+// in tensor memory and are the products' A operands from there; P^T over S^T, with dV(i) before S(i+1),
+// made phase A, dV and S one chain of 2,600 cycles a tile against the products' 2,048.
 // win_dq:  ... S(n+1) | dP(n+1) dQ(n) ...: S(n+1) is issued once S(n) is in registers, the pair after
 // phase B of tile n, which leaves dS in columns of its own (two buffers), so that dP(n+1) need not
 // wait for dQ(n).
@@ -24,8 +25,9 @@
 // into dS, everything else is fp32.  Bound by the tensor core: 32 (dkv) and 24 (dq) instructions of
 // 128 x 128 x 16 a tile pair, about 83 cycles each.
 //
-// Roles of both (640 threads): warp 0 TMA loads, warp 1 MMA issue, warp 2 the tile's row data (dkv)
-// or the TMA stores of dQ (dq), warps 4-19 softmax and epilogue: four per tensor-memory lane quarter,
+// Roles of both (640 threads): warp 0 TMA loads, warp 1 MMA issue (two issuing warps interleaved the
+// products of a chain with the other's and were slower), warp 2 the tile's row data (dkv) or the TMA
+// stores of dQ (dq), warps 4-19 softmax and epilogue: four per tensor-memory lane quarter,
 // one per 32 of the tile's columns (with two, a phase was bound by the latencies of a warp's loads and
 // exponentials: 2,400 cycles a tile of win_dkv against the 2,656 of its products).  Every wait is
 // bounded.
@@ -38,7 +40,7 @@ namespace msa {
 namespace {
 
 constexpr int kTile = 128 * 128 * 2;  // 128 rows x 128 bf16, two SW128 panels
-constexpr int kItemRing = 4, kMetaRing = 4;
+constexpr int kItemRing = 4, kMetaRing = 2, kQRing = 3;
 constexpr int kSoft = 16;        // softmax / epilogue warps
 constexpr int kBwdThreads = 640;  // 4 + kSoft warps
 
@@ -55,8 +57,8 @@ struct DkvArgs {
 struct DkvShared {
   float nlse2[kMetaRing][128], ndrow[kMetaRing][128];  // -(LSE log2 e), -(D scale) per tile row
   int it_ring[kItemRing];
-  uint64_t k_full, v_full, kv_empty, q_full[2], q_empty[2], do_full[2], do_empty[2], m_full[kMetaRing],
-      m_empty[kMetaRing], s_full, dp_full, pa, pb, acc_full, acc_free, it_full[kItemRing],
+  uint64_t k_full, v_full, kv_empty, q_full[kQRing], q_empty[kQRing], do_full[2], do_empty[2], m_full[kMetaRing],
+      m_empty[kMetaRing], s_full, dp_full, sa, pb, acc_full, acc_free, it_full[kItemRing],
       it_empty[kItemRing], mma_done;
   uint32_t tmem;
 };
@@ -107,23 +109,29 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dkv_kernel(const __grid_co
   using namespace sm100;
   constexpr int TT = 128 / G;
   const WinDims& d = A.d;
-  extern __shared__ uint8_t smem_raw[];
-  DkvShared* sh = reinterpret_cast<DkvShared*>(smem_raw);
-  uint8_t* sK = align1024(smem_raw + sizeof(DkvShared));
+  extern __shared__ __align__(1024) uint8_t smem_tiles[];
+  uint8_t* sK = smem_tiles;
   uint8_t* sV = sK + kTile;
-  uint8_t* sQ = sV + kTile;       // [2] query tiles
-  uint8_t* sD = sQ + 2 * kTile;   // [2] dO tiles
+  uint8_t* sQ = sV + kTile;           // [kQRing] query tiles
+  uint8_t* sD = sQ + kQRing * kTile;  // [2] dO tiles
+  DkvShared* sh = reinterpret_cast<DkvShared*>(sD + 2 * kTile);
   const uint32_t aK = smem_u32(sK), aV = smem_u32(sV), aQ = smem_u32(sQ), aD = smem_u32(sD);
   const int tid = threadIdx.x, lane = tid % 32, warp = warp_number();
   const int total = A.it.items;
+  if (aK & 1023u) {  // the swizzled operand layout needs 1024-byte atoms
+    if (tid == 0) atomicOr(A.status, kStatusInternal);
+    return;
+  }
 
   if (tid == 0) {
     mbar_init(&sh->k_full, 1);
     mbar_init(&sh->v_full, 1);
     mbar_init(&sh->kv_empty, 1);
-    for (int x = 0; x < 2; ++x) {
+    for (int x = 0; x < kQRing; ++x) {
       mbar_init(&sh->q_full[x], 1);
       mbar_init(&sh->q_empty[x], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
       mbar_init(&sh->do_full[x], 1);
       mbar_init(&sh->do_empty[x], 1);
     }
@@ -137,7 +145,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dkv_kernel(const __grid_co
     }
     mbar_init(&sh->s_full, 1);
     mbar_init(&sh->dp_full, 1);
-    mbar_init(&sh->pa, kSoft);
+    mbar_init(&sh->sa, kSoft);
     mbar_init(&sh->pb, kSoft);
     mbar_init(&sh->acc_full, 1);
     mbar_init(&sh->acc_free, kSoft);
@@ -167,6 +175,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dkv_kernel(const __grid_co
     // ---------------------------------------------------------------- items + TMA loads
     if (lane == 0) {
       long long nk = 0, i = 0;  // items with tiles, tiles
+      Ring<kQRing> q;
       bool ok = true;
       for (long long k = 0; ok; ++k) {
         const int x = (int)(k % kItemRing);
@@ -185,12 +194,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dkv_kernel(const __grid_co
           tma_load_rows(sK + c * (kTile / 2), &A.k, 64 * c, t.g, t.n * kBlock, t.b, &sh->k_full);
         for (int c = 0; c < 2; ++c)
           tma_load_rows(sV + c * (kTile / 2), &A.v, 64 * c, t.g, t.n * kBlock, t.b, &sh->v_full);
-        for (int tl = t.i0; tl < t.i1; ++tl, ++i) {
+        for (int tl = t.i0; tl < t.i1; ++tl, ++i, q.next()) {
           const int s = (int)(i & 1), tok = t.n * kBlock + tl * TT;
-          if (i >= 2 && !mbar_wait(&sh->q_empty[s], phase_of(i / 2 - 1), A.status)) { ok = false; break; }
-          mbar_expect_tx(&sh->q_full[s], kTile);
+          if (q.wrapped && !mbar_wait(&sh->q_empty[q.slot], q.phase ^ 1, A.status)) { ok = false; break; }
+          mbar_expect_tx(&sh->q_full[q.slot], kTile);
           for (int c = 0; c < 2; ++c)
-            tma_load_rows(sQ + s * kTile + c * (kTile / 2), &A.q, 64 * c, t.g * G, tok, t.b, &sh->q_full[s]);
+            tma_load_rows(sQ + q.slot * kTile + c * (kTile / 2), &A.q, 64 * c, t.g * G, tok, t.b, &sh->q_full[q.slot]);
           if (i >= 2 && !mbar_wait(&sh->do_empty[s], phase_of(i / 2 - 1), A.status)) { ok = false; break; }
           mbar_expect_tx(&sh->do_full[s], kTile);
           for (int c = 0; c < 2; ++c)
@@ -202,68 +211,68 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dkv_kernel(const __grid_co
         mbar_wait(&sh->k_full, phase_of(nk - 1), A.status);
         mbar_wait(&sh->v_full, phase_of(nk - 1), A.status);
       }
-      for (long long x = i >= 2 ? i - 2 : 0; x < i; ++x) {
-        mbar_wait(&sh->q_full[x & 1], phase_of(x >> 1), A.status);
-        mbar_wait(&sh->do_full[x & 1], phase_of(x >> 1), A.status);
-      }
+      for (long long x = i >= kQRing ? i - kQRing : 0; x < i; ++x)
+        mbar_wait(&sh->q_full[x % kQRing], phase_of(x / kQRing), A.status);
+      for (long long x = i >= 2 ? i - 2 : 0; x < i; ++x) mbar_wait(&sh->do_full[x & 1], phase_of(x >> 1), A.status);
     }
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issue
-    {
-      long long nk = 0, i = 0;
-      bool ok = true;
-      auto mma_s = [&](long long j) -> bool {
-        const int s = (int)(j & 1);
-        if (!mbar_wait_warp(&sh->q_full[s], phase_of(j >> 1), A.status)) return false;
-        fence_after_sync();
-        mma_kk(SB, aK, aQ + s * kTile, false);  // S^T = K Q^T
-        warp_mma_commit(&sh->s_full);
-        return true;
-      };
-      auto mma_dp = [&](long long j) -> bool {
-        const int s = (int)(j & 1);
-        if (!mbar_wait_warp(&sh->do_full[s], phase_of(j >> 1), A.status)) return false;
-        fence_after_sync();
-        mma_kk(DB, aV, aD + s * kTile, false);  // dP^T = V dO^T
-        warp_mma_commit(&sh->dp_full);
-        return true;
-      };
-      for (long long k = 0; ok; ++k) {
-        int v;
-        if (!takew(k, v) || v >= total) break;
-        const DkvItem t = dkv_item<G>(d, A.it, v);
-        if (t.i0 >= t.i1) continue;
-        const int n = t.i1 - t.i0;
-        // P^T and dS^T of the previous item's last tile were read by products issued before these
-        ok = mbar_wait_warp(&sh->k_full, phase_of(nk), A.status) && mma_s(i) &&
-             mbar_wait_warp(&sh->v_full, phase_of(nk), A.status) && mma_dp(i);
-        for (int tl = 0; tl < n && ok; ++tl, ++i) {
-          const int s = (int)(i & 1);
-          // phase A has written P^T over S^T
-          if (!mbar_wait_warp(&sh->pa, phase_of(i), A.status)) { ok = false; break; }
-          if (tl == 0 && nk > 0 && !mbar_wait_warp(&sh->acc_free, phase_of(nk - 1), A.status)) { ok = false; break; }
-          fence_after_sync();
-          // dV += P^T dO; P^T of rows 32 p .. 32 p + 31 in columns 32 p .. 32 p + 15
-          mma_tn<2, 32>(RV, SB, aD + s * kTile, tl > 0);
-          warp_mma_commit(&sh->do_empty[s]);
-          if (tl + 1 < n && !mma_s(i + 1)) { ok = false; break; }
-          // phase B has written dS^T over dP^T
-          if (!mbar_wait_warp(&sh->pb, phase_of(i), A.status)) { ok = false; break; }
-          fence_after_sync();
-          mma_tn<2, 32>(RK, DB, aQ + s * kTile, tl > 0);  // dK += dS^T Q
-          warp_mma_commit(&sh->q_empty[s]);
-          if (tl + 1 < n && !mma_dp(i + 1)) { ok = false; break; }
+    int nk = 0, i = 0;
+    Ring<kQRing> q;
+    bool ok = true;
+    auto mma_dp = [&](int j) -> bool {  // dP^T = V dO^T
+      const int s = j & 1;
+      if (!mbar_wait_warp(&sh->do_full[s], phase_of(j >> 1), A.status)) return false;
+      fence_after_sync();
+      mma_kk(DB, aV, aD + s * kTile, false);
+      warp_mma_commit(&sh->dp_full);
+      return true;
+    };
+    auto mma_s = [&](const Ring<kQRing>& x) -> bool {  // S^T = K Q^T
+      if (!mbar_wait_warp(&sh->q_full[x.slot], x.phase, A.status)) return false;
+      fence_after_sync();
+      mma_kk(SB, aK, aQ + x.slot * kTile, false);
+      warp_mma_commit(&sh->s_full);
+      return true;
+    };
+    for (long long k = 0; ok; ++k) {
+      int v;
+      if (!takew(k, v) || v >= total) break;
+      const DkvItem t = dkv_item<G>(d, A.it, v);
+      if (t.i0 >= t.i1) continue;
+      // (the previous item's last S^T, dS^T and P^T were read before its last products were issued, or
+      // by them)
+      if (!mbar_wait_warp(&sh->k_full, phase_of(nk), A.status) || !mma_s(q) ||
+          !mbar_wait_warp(&sh->v_full, phase_of(nk), A.status) || !mma_dp(i))
+        break;
+      for (int tl = t.i0; tl < t.i1; ++tl, ++i) {
+        const bool first = tl == t.i0, more = tl + 1 < t.i1;
+        const int s = i & 1, qs = q.slot;
+        q.next();
+        // S^T is in registers: the next one can be computed behind phase A
+        if (more && (!mbar_wait_warp(&sh->sa, phase_of(i), A.status) || !mma_s(q))) { ok = false; break; }
+        // phase B has written dS^T and P^T over dP^T
+        if ((first && nk > 0 && !mbar_wait_warp(&sh->acc_free, phase_of(nk - 1), A.status)) ||
+            !mbar_wait_warp(&sh->pb, phase_of(i), A.status)) {
+          ok = false;
+          break;
         }
-        if (!ok) break;
-        warp_mma_commit(&sh->acc_full);
-        warp_mma_commit(&sh->kv_empty);
-        ++nk;
+        fence_after_sync();
+        // rows 32 p .. 32 p + 31: dS^T in columns 32 p .. 32 p + 15, P^T in 32 p + 16 .. 32 p + 31
+        mma_tn<2, 32>(RV, DB + 16, aD + s * kTile, !first);  // dV += P^T dO
+        warp_mma_commit(&sh->do_empty[s]);
+        mma_tn<2, 32>(RK, DB, aQ + qs * kTile, !first);  // dK += dS^T Q
+        warp_mma_commit(&sh->q_empty[qs]);
+        if (more && !mma_dp(i + 1)) { ok = false; break; }
       }
-      warp_mma_commit(&sh->mma_done);
-      mbar_wait_warp(&sh->mma_done, 0, A.status);  // no product may still write tensor memory
+      if (!ok) break;
+      warp_mma_commit(&sh->acc_full);
+      warp_mma_commit(&sh->kv_empty);
+      ++nk;
     }
-    __syncwarp();
+    warp_mma_commit(&sh->mma_done);
+    mbar_wait_warp(&sh->mma_done, 0, A.status);  // no product may still write tensor memory
   } else if (warp == 2) {
     // ---------------------------------------------------------------- row data of the tiles
     Ring<kMetaRing> meta;
@@ -328,12 +337,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dkv_kernel(const __grid_co
           break;
         }
         fence_after_sync();
-        // ---- phase A: P^T of this key and 32 rows; kept in fp32 for phase B
+        // ---- phase A: P^T of this key and 32 rows, kept in registers
         float p[32];
         {
-          uint32_t rs[32], pw[16];
+          uint32_t rs[32];
           tmem_ld32(Sx, rs);
           tmem_wait_ld();
+          fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh->sa);
           const float4* l4 = reinterpret_cast<const float4*>(sh->nlse2[s] + 32 * part);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -351,22 +363,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dkv_kernel(const __grid_co
 #pragma unroll
               for (int u = 0; u < 4; ++u) pe[u] = (vis >> (4 * e + u)) & 1u ? pe[u] : 0.f;
             }
-            pw[2 * e] = pack_bf16(pe[0], pe[1]);
-            pw[2 * e + 1] = pack_bf16(pe[2], pe[3]);
           }
-          tmem_st16(Sx, pw);  // over columns of S^T this warp has read
         }
-        tmem_wait_st();
-        fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->pa);
-        // ---- phase B: dS^T = P^T (scale dP^T - scale D)
+        // ---- phase B: dS^T = P^T (scale dP^T - scale D); both to tensor memory as bf16
         if (!mbar_wait_warp(&sh->dp_full, phase_of(i), A.status)) { ok = false; break; }
         fence_after_sync();
         {
-          uint32_t rp[32], dw[16];
+          uint32_t rp[32], dw[16], pw[16];
           tmem_ld32(Dx, rp);
           tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) pw[e] = pack_bf16(p[2 * e], p[2 * e + 1]);
+          tmem_st16(Dx + 16, pw);  // over columns of dP^T this warp has read
           const float4* d4 = reinterpret_cast<const float4*>(sh->ndrow[s] + 32 * part);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -593,70 +601,61 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dq_kernel(const __grid_con
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issue
     {
-      // a step: key tile n of unit nu; its K and V in ring slots k and v
-      struct Step {
-        long long u;
-        int nu, n, nb;
-        Ring<kRingQ> k, v;
-      };
-      auto load_unit = [&](Step& t) { t.nb = t.u < A.units ? dq_unit<G>(d, t.u).run.nb : 0; };
-      auto next = [&](Step t) {
-        t.k = t.v;
-        t.k.next();
-        if (t.n + 1 < t.nb) {
-          ++t.n;
-        } else {
-          t.k.next();  // the tile dQ leaves through
-          t.u += gridDim.x;
-          ++t.nu;
-          t.n = 0;
-          load_unit(t);
-        }
-        t.v = t.k;
-        t.v.next();
-        return t;
-      };
-      auto mma_s = [&](const Step& t) -> bool {
-        if (t.n == 0 && !mbar_wait_warp(&sh->q_full, phase_of(t.nu), A.status)) return false;
-        if (!mbar_wait_warp(&sh->kv_full[t.k.slot], t.k.phase, A.status)) return false;
+      // step i: key tile n of unit nu, whose K is in ring slot k (its V in the one after)
+      Ring<kRingQ> k;
+      auto mma_s = [&](const Ring<kRingQ>& k, bool first, bool last, int nu) -> bool {
+        if (first && !mbar_wait_warp(&sh->q_full, phase_of(nu), A.status)) return false;
+        if (!mbar_wait_warp(&sh->kv_full[k.slot], k.phase, A.status)) return false;
         fence_after_sync();
-        mma_kk(SB, aQ, aR + t.k.slot * kTile, false);  // S = Q K^T
+        mma_kk(SB, aQ, aR + k.slot * kTile, false);  // S = Q K^T
         warp_mma_commit(&sh->s_full);
-        if (t.n + 1 == t.nb) warp_mma_commit(&sh->q_empty);
+        if (last) warp_mma_commit(&sh->q_empty);
         return true;
       };
-      auto mma_dp = [&](const Step& t) -> bool {
-        if (t.n == 0 && !mbar_wait_warp(&sh->do_full, phase_of(t.nu), A.status)) return false;
-        if (!mbar_wait_warp(&sh->kv_full[t.v.slot], t.v.phase, A.status)) return false;
+      // (V's slot is freed by the softmax, which sees dP first: a commit less)
+      auto mma_dp = [&](Ring<kRingQ> k, bool first, bool last, int nu) -> bool {
+        k.next();
+        if (first && !mbar_wait_warp(&sh->do_full, phase_of(nu), A.status)) return false;
+        if (!mbar_wait_warp(&sh->kv_full[k.slot], k.phase, A.status)) return false;
         fence_after_sync();
-        mma_kk(DP, aD, aR + t.v.slot * kTile, false);  // dP = dO V^T
+        mma_kk(DP, aD, aR + k.slot * kTile, false);  // dP = dO V^T
         warp_mma_commit(&sh->dp_full);
-        warp_mma_commit(&sh->kv_empty[t.v.slot]);
-        if (t.n + 1 == t.nb) warp_mma_commit(&sh->do_empty);
+        if (last) warp_mma_commit(&sh->do_empty);
         return true;
       };
-      Step t{(long long)blockIdx.x, 0, 0, 0, {}, {}};
-      t.v.next();
-      load_unit(t);
-      bool ok = t.nb > 0 && mma_s(t) && mma_dp(t);
-      for (int i = 0; ok; ++i) {
-        const Step nx = next(t);
-        const bool more = nx.nb > 0;
-        // phase A has read S
-        if (!mbar_wait_warp(&sh->pa, phase_of(i), A.status)) break;
-        if (more && !mma_s(nx)) break;
-        // phase B has read dP and written dS: dP of the next step first, dQ behind it (dS of step
-        // i + 2 is written only after dP of step i + 2, issued after this product, is there)
-        if (!mbar_wait_warp(&sh->pb, phase_of(i), A.status)) break;
-        if (more && !mma_dp(nx)) break;
-        // (the epilogue of the previous unit has read its dQ: it comes before phase B of this one)
-        if (t.n == 0 && t.nu >= 1 && !mbar_wait_warp(&sh->dq_free, phase_of(t.nu - 1), A.status)) break;
-        fence_after_sync();
-        mma_tn<8, 0>(RQ, DS + 64 * (i & 1), aR + t.k.slot * kTile, t.n > 0);  // dQ += dS K
-        warp_mma_commit(&sh->kv_empty[t.k.slot]);
-        if (t.n + 1 == t.nb) warp_mma_commit(&sh->dq_full);
-        if (!more) break;
-        t = nx;
+      long long u = blockIdx.x;
+      int nb = dq_unit<G>(d, u).run.nb, i = 0;
+      bool ok = mma_s(k, true, nb == 1, 0) && mma_dp(k, true, nb == 1, 0);
+      for (int nu = 0; ok && nb > 0; ++nu) {
+        u += gridDim.x;
+        const int nb2 = u < A.units ? dq_unit<G>(d, u).run.nb : 0;  // of the next unit (0: none)
+        for (int n = 0; n < nb; ++n, ++i) {
+          const bool last = n + 1 == nb;
+          Ring<kRingQ> k2 = k;
+          k2.next();
+          k2.next();
+          if (last) k2.next();  // the tile dQ leaves through
+          const bool more = !last || nb2 > 0, last2 = last ? nb2 == 1 : n + 2 == nb;
+          // phase A has read S
+          if (!mbar_wait_warp(&sh->pa, phase_of(i), A.status) || (more && !mma_s(k2, last, last2, nu + 1))) {
+            ok = false;
+            break;
+          }
+          // phase B has read dP and written dS: dP of the next step first, dQ behind it (dS of step
+          // i + 2 is written only after dP of step i + 2, issued after this product, is there)
+          if (!mbar_wait_warp(&sh->pb, phase_of(i), A.status) || (more && !mma_dp(k2, last, last2, nu + 1)) ||
+              // (the epilogue of the previous unit has read its dQ: it comes before phase B of this one)
+              (n == 0 && nu >= 1 && !mbar_wait_warp(&sh->dq_free, phase_of(nu - 1), A.status))) {
+            ok = false;
+            break;
+          }
+          fence_after_sync();
+          mma_tn<8, 0>(RQ, DS + 64 * (i & 1), aR + k.slot * kTile, n > 0);  // dQ += dS K
+          warp_mma_commit(&sh->kv_empty[k.slot]);
+          if (last) warp_mma_commit(&sh->dq_full);
+          k = k2;
+        }
+        nb = nb2;
       }
       warp_mma_commit(&sh->mma_done);
       mbar_wait_warp(&sh->mma_done, 0, A.status);  // no product may still write tensor memory
@@ -726,7 +725,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dq_kernel(const __grid_con
       return true;
     };
     long long nl = 0, pending = -1;  // pending: ring entry of the last unit's dQ
-    int i = 0, nu = 0;
+    int i = 0, nu = 0, v_slot = 1;
     float2 m = row_data(blockIdx.x);
     bool ok = true;
     for (long long u = blockIdx.x; u < A.units && ok; u += gridDim.x, ++nu) {
@@ -768,6 +767,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dq_kernel(const __grid_con
         // ---- phase B
         if (!mbar_wait_warp(&sh->dp_full, phase_of(i), A.status)) { ok = false; break; }
         fence_after_sync();
+        if (warp == 4 && lane == 0) mbar_arrive(&sh->kv_empty[v_slot]);  // V has been read
+        v_slot += n + 1 < x.run.nb ? 2 : 3;  // (a unit ends with the tile dQ leaves through)
+        v_slot -= v_slot >= kRingQ ? kRingQ : 0;
         {
           uint32_t rp[32], dw[16];
           tmem_ld32(DP + lb + 32 * part, rp);
@@ -801,18 +803,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dq_kernel(const __grid_con
 
 // ========================================================================================== host
 // Key blocks and query tiles are cut so that the key-outer items number about eight per SM, in
-// chunks of at least four tiles; the window blocks are not split where they already have that many.
+// chunks of at least four tiles.  Window blocks stay whole from four per SM on: their partials cost
+// more than the last items' imbalance (2 x 8192 tokens, 8 KV heads, window 1024, 6.7 blocks per SM: 68 us
+// of joining and 30 us of writing partials when split in two).
 WinItems win_items(const WinDims& d) {
   WinItems w;
   const int tt = kBlock / d.G, nblk = (d.S + kBlock - 1) / kBlock, per = d.B * d.Hkv;
   w.sink_blocks = (d.ns + kBlock - 1) / kBlock;
   const long long span = (long long)kBlock + d.W - 1 < d.S ? (long long)kBlock + d.W - 1 : d.S;
   const long long win_tiles = (span + tt - 1) / tt, all_tiles = (d.S + tt - 1) / tt;
-  const long long total = (w.sink_blocks * all_tiles + (nblk - w.sink_blocks) * win_tiles) * per;
+  const long long win_blocks = (long long)(nblk - w.sink_blocks) * per;
+  const long long total = w.sink_blocks * all_tiles * per + win_blocks * win_tiles;
   long long c = (total + 8ll * num_sms() - 1) / (8ll * num_sms());
   if (c < 4) c = 4;
   w.sink_chunk = (int)(c < all_tiles ? c : all_tiles);
-  w.win_chunk = (int)(c < win_tiles ? c : win_tiles);
+  w.win_chunk = (int)(c < win_tiles && win_blocks < 4ll * num_sms() ? c : win_tiles);
   w.win_split = (int)((win_tiles + w.win_chunk - 1) / w.win_chunk);
   const int sink_split = (int)((all_tiles + w.sink_chunk - 1) / w.sink_chunk);
   w.sink_items = w.sink_blocks * sink_split * per;
@@ -848,7 +853,7 @@ bool launch_win_dkv(const WinDims& d, const void* q, const void* k, const void* 
   a.status = status;
   a.sched = reinterpret_cast<int*>(status + kSchedWinDkv);
   a.it = win_items(d);
-  const size_t smem = sizeof(DkvShared) + 1024 + 6 * (size_t)kTile;
+  const size_t smem = sizeof(DkvShared) + 7 * (size_t)kTile;
 #define MSA_CALL(G)                                                                                    \
   cudaFuncSetAttribute(win_dkv_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);      \
   win_dkv_kernel<G><<<a.it.items < n ? a.it.items : n, kBwdThreads, smem, st>>>(a)

@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) win_fwd_kernel(const __grid_co
           if (cu[X] > 0 && !mbar_wait_warp(&sh->o_free[X], phase_of(cu[X] - 1), A.status)) return false;
           ++cu[X];
         }
-        if (!mbar_wait_warp(&sh->kv_full[v_slot], v_phase, A.status)) return false;
+        if (X == 0 && !mbar_wait_warp(&sh->kv_full[v_slot], v_phase, A.status)) return false;
         fence_after_sync();
         mma_tn<4, 64>(O0 + 128 * X, S0 + 128 * X, aR + v_slot * kTile, !first);
         if (last) warp_mma_commit(&sh->o_full[X]);
@@ -195,8 +195,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) win_fwd_kernel(const __grid_co
         if (!mbar_wait_warp(&sh->q_full[qs], phase_of(nu >> 1), A.status)) break;
         for (int n = 0; n < x.run.nb; ++n) {
           const int kslot = kv.slot;
-          if (!mbar_wait_warp(&sh->kv_full[kslot], kv.phase, A.status)) { ok = false; break; }
           if (n > 0 && !mma_o(0, n == 1, false, !x.two)) { ok = false; break; }
+          // (K_n is waited for behind O_A(n-1): its load began when O_B(n-2) freed a slot)
+          if (!mbar_wait_warp(&sh->kv_full[kslot], kv.phase, A.status)) { ok = false; break; }
           mma_s(0, q, kslot, !x.two);
           if (x.two) {
             if (n > 0 && !mma_o(1, n == 1, false, true)) { ok = false; break; }

@@ -149,6 +149,14 @@ __device__ __forceinline__ void mma_kk(uint32_t d, uint32_t a_tile, uint32_t b_t
 #pragma unroll
   for (int ks = 1; ks < 8; ++ks) warp_mma_ss(d, a + step_k(ks), b + step_k(ks), id, true);
 }
+// D (+)= A B, A a K-major, B an MN-major tile in shared memory.
+__device__ __forceinline__ void mma_kn(uint32_t d, uint32_t a_tile, uint32_t b_tile, bool acc) {
+  constexpr uint32_t id = sm100::idesc_bf16(128, 128, false, true);
+  const uint32_t a = desc_lo_k(a_tile), b = desc_lo_mn(b_tile);
+  warp_mma_ss(d, a, b, id, acc);
+#pragma unroll
+  for (int ks = 1; ks < 8; ++ks) warp_mma_ss(d, a + step_k(ks), b + step_mn(ks), id, true);
+}
 // D (+)= A B, A in tensor memory (16 K values are 8 columns; runs of kRun steps start kPitch columns
 // apart), B an MN-major tile in shared memory.
 template <int kRun, int kPitch>
