@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) win_fwd_kernel(const __grid_co
           if (cu[X] > 0 && !mbar_wait_warp(&sh->o_free[X], phase_of(cu[X] - 1), A.status)) return false;
           ++cu[X];
         }
-        if (X == 0 && !mbar_wait_warp(&sh->kv_full[v_slot], v_phase, A.status)) return false;
+        if (!mbar_wait_warp(&sh->kv_full[v_slot], v_phase, A.status)) return false;
         fence_after_sync();
         mma_tn<4, 64>(O0 + 128 * X, S0 + 128 * X, aR + v_slot * kTile, !first);
         if (last) warp_mma_commit(&sh->o_full[X]);
