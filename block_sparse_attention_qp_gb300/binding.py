@@ -21,9 +21,11 @@ What stands around sparse attention in a model:
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
+import struct
 import threading
 
 import torch
@@ -83,6 +85,8 @@ _lock = threading.Lock()
 def load_library(path: str = LIB_PATH):
     """Load libmsa.so (raises MSAError if it is missing: there is no CPU fallback)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -102,7 +106,8 @@ def load_library(path: str = LIB_PATH):
         lib.msa_device_status.argtypes = [P, ctypes.POINTER(ctypes.c_uint), P]
         lib.msa_decode.argtypes = [SP, P, P, P, P, P, P, P, P, P, P, Z, P]
         lib.msa_decode.restype = I
-        WP, RP, RS = (ctypes.POINTER(x) for x in (WindowShape, RopePart, RopeShape))
+        WP, RS = ctypes.POINTER(WindowShape), ctypes.POINTER(RopeShape)
+        RP = P  # an array of RopePart, or its bytes
         lib.msa_window_workspace_size.argtypes = [WP, I]
         lib.msa_window_workspace_size.restype = Z
         lib.msa_window_forward.argtypes = [WP, P, P, P, P, P, P, Z, P]
@@ -471,6 +476,42 @@ def msa_warmup_func(Q_proxy, K_proxy, Q, K, V, top_k: int, scale: float):
 
 
 # ---------------------------------------------------------------- sliding-window attention
+# The entry points below serve single tokens too, where the host's part of a call counts: arguments are
+# looked at once by a fast test, and only a failing one is taken apart for its message.
+_NO_GUARD = contextlib.nullcontext()
+
+
+def _guard(device):
+    """Context with `device` current (entering one costs microseconds: none where it is already)."""
+    return _NO_GUARD if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(device) -> int:
+    if _raw_stream is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _ask(t, name, dtype, shape, device):
+    """t is a contiguous CUDA tensor of this type, shape and device; returns its address."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and t.device == device and t.is_cuda):
+        _req(t, name, dtype, shape)
+        raise MSAError(f"{name} is on {t.device}, the first argument on {device}")
+    return t.data_ptr()
+
+
+def _dims(t, name, n):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dim() != n:
+        raise MSAError(f"{name} has shape {tuple(t.shape)}, expected {n} dimensions")
+    return t.shape
+
+
 def make_window_shape(q, k, window, sinks, scale) -> WindowShape:
     """Shape of a window op: q [B, S, Hq, D] (decode: [B, Hq, D]), k [B, S, Hkv, D]."""
     B, S, Hkv = k.shape[:3]
@@ -486,12 +527,18 @@ def _int32(x, name) -> int:
     return min(x, 2 ** 31 - 1)
 
 
-def msa_window_workspace_size(shape: WindowShape, op: int) -> int:
-    n = load_library().msa_window_workspace_size(ctypes.byref(shape), op)
+@functools.lru_cache(maxsize=4096)
+def _window_bytes(op, *shape):
+    lib = load_library()
+    n = int(lib.msa_window_workspace_size(ctypes.byref(WindowShape(*shape)), op))
     if n == 0:
-        raise MSAError(f"unsupported shape for op {op}: "
-                       f"{load_library().msa_last_error().decode()}")
-    return int(n)
+        raise MSAError(f"unsupported shape for op {op}: {lib.msa_last_error().decode()}")
+    return n
+
+
+def msa_window_workspace_size(shape: WindowShape, op: int) -> int:
+    return _window_bytes(op, shape.B, shape.S, shape.Hq, shape.Hkv, shape.D, shape.window, shape.sinks,
+                         shape.scale)
 
 
 def window_workspace(shape: WindowShape, op: int, device) -> torch.Tensor:
@@ -499,86 +546,77 @@ def window_workspace(shape: WindowShape, op: int, device) -> torch.Tensor:
     return torch.empty(msa_window_workspace_size(shape, op), dtype=torch.uint8, device=device)
 
 
-def _req_ws(ws, device):
-    _req(ws, "ws", torch.uint8)
-    if ws.device != device:
-        raise MSAError(f"ws is on {ws.device}, the inputs on {device}")
+def _ws(ws, need, device):
+    """(address, bytes, tensor) of the caller's workspace, or of a fresh one of need() bytes."""
+    if ws is None:
+        ws = torch.empty(need(), dtype=torch.uint8, device=device)
+    else:
+        _req(ws, "ws", torch.uint8)
+        if ws.device != device:
+            raise MSAError(f"ws is on {ws.device}, the inputs on {device}")
+    return ws.data_ptr(), ws.numel(), ws
 
 
-def _dims(t, name, n):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a tensor")
-    if t.dim() != n:
-        raise MSAError(f"{name} has shape {tuple(t.shape)}, expected {n} dimensions")
+def _window_args(q, k, v, window, sinks, scale, op, ws, dims):
+    """Checks q, k and v; returns (device, addresses, shape, workspace)."""
+    qs = _dims(q, "q", dims)
+    ks = _dims(k, "k" if dims == 4 else "k_cache", 4)
+    dev = q.device
+    n = ("q", "k", "v") if dims == 4 else ("q", "k_cache", "v_cache")
+    want = (ks[0], ks[1], qs[2], qs[3]) if dims == 4 else (ks[0], qs[1], qs[2])
+    kv = (ks[0], ks[1], ks[2], qs[-1])
+    ptrs = (_ask(q, n[0], torch.bfloat16, want, dev), _ask(k, n[1], torch.bfloat16, kv, dev),
+            _ask(v, n[2], torch.bfloat16, kv, dev))
+    shape = make_window_shape(q, k, window, sinks, scale)
+    return dev, ptrs, shape, lambda: msa_window_workspace_size(shape, op)
 
 
-@_on_tensor_device
 def msa_window_forward(q, k, v, window: int, sinks: int, scale: float, ws=None):
     """Causal GQA attention of every query over the last ``window`` tokens (itself included) and the
     first ``sinks`` tokens.  q [B, S, Hq, 128], k, v [B, S, Hkv, 128], any S.  Returns (o, lse)."""
-    _dims(q, "q", 4)
-    _dims(k, "k", 4)
-    B, S, Hq, D = q.shape
-    Hkv = k.shape[2]
-    for t, n, h in ((q, "q", Hq), (k, "k", Hkv), (v, "v", Hkv)):
-        _req(t, n, shape=(B, S, h, D))
-    shape = make_window_shape(q, k, window, sinks, scale)
-    if ws is None:
-        ws = window_workspace(shape, OP_WINDOW_FORWARD, q.device)
-    _req_ws(ws, q.device)
-    o = torch.empty_like(q)
-    lse = torch.empty((B, Hq, S), dtype=torch.float32, device=q.device)
-    _check(load_library().msa_window_forward(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v),
-                                             _ptr(o), _ptr(lse), _ptr(ws), ws.numel(),
-                                             _stream(q.device)), "msa_window_forward")
+    dev, ptrs, shape, need = _window_args(q, k, v, window, sinks, scale, OP_WINDOW_FORWARD, ws, 4)
+    with _guard(dev):
+        wp, wn, ws = _ws(ws, need, dev)
+        o = torch.empty_like(q)
+        lse = torch.empty((shape.B, shape.Hq, shape.S), dtype=torch.float32, device=dev)
+        rc = load_library().msa_window_forward(ctypes.byref(shape), *ptrs, o.data_ptr(), lse.data_ptr(),
+                                               wp, wn, _stream_of(dev))
+    if rc:
+        _check(rc, "msa_window_forward")
     return o, lse
 
 
-@_on_tensor_device
 def msa_window_backward(q, k, v, o, lse, dout, window: int, sinks: int, scale: float, ws=None):
     """Gradients (dq, dk, dv) of sum(o * dout); o, lse from msa_window_forward on the same inputs."""
-    _dims(q, "q", 4)
-    _dims(k, "k", 4)
-    B, S, Hq, D = q.shape
-    Hkv = k.shape[2]
-    for t, n, h in ((q, "q", Hq), (k, "k", Hkv), (v, "v", Hkv), (o, "o", Hq), (dout, "dout", Hq)):
-        _req(t, n, shape=(B, S, h, D))
-    _req(lse, "lse", torch.float32, (B, Hq, S))
-    shape = make_window_shape(q, k, window, sinks, scale)
-    if ws is None:
-        ws = window_workspace(shape, OP_WINDOW_BACKWARD, q.device)
-    _req_ws(ws, q.device)
-    dq, dk, dv = (torch.empty_like(x) for x in (q, k, v))
-    _check(load_library().msa_window_backward(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v),
-                                              _ptr(o), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk),
-                                              _ptr(dv), _ptr(ws), ws.numel(), _stream(q.device)),
-           "msa_window_backward")
+    dev, ptrs, shape, need = _window_args(q, k, v, window, sinks, scale, OP_WINDOW_BACKWARD, ws, 4)
+    op = _ask(o, "o", torch.bfloat16, q.shape, dev)
+    lp = _ask(lse, "lse", torch.float32, (shape.B, shape.Hq, shape.S), dev)
+    dp = _ask(dout, "dout", torch.bfloat16, q.shape, dev)
+    with _guard(dev):
+        wp, wn, ws = _ws(ws, need, dev)
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        rc = load_library().msa_window_backward(ctypes.byref(shape), *ptrs, op, lp, dp, dq.data_ptr(),
+                                                dk.data_ptr(), dv.data_ptr(), wp, wn, _stream_of(dev))
+    if rc:
+        _check(rc, "msa_window_backward")
     return dq, dk, dv
 
 
-@_on_tensor_device
 def msa_window_decode(q, k_cache, v_cache, seq_len, window: int, sinks: int, scale: float, ws=None):
     """Decode step: q [B, Hq, 128] against caches [B, S, Hkv, 128] that already hold the new tokens at
     seq_len - 1 (seq_len [B] int32 on the device).  Returns (o [B, Hq, 128], lse [B, Hq]); the rows of
     a sequence whose length is not in 1 .. S are not written (msa_device_status tells)."""
-    _dims(q, "q", 3)
-    _dims(k_cache, "k_cache", 4)
-    B, Hq, D = q.shape
-    S, Hkv = k_cache.shape[1:3]
-    _req(q, "q")
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _req(t, n, shape=(B, S, Hkv, D))
-    _req(seq_len, "seq_len", torch.int32, (B,))
-    shape = make_window_shape(q, k_cache, window, sinks, scale)
-    if ws is None:
-        ws = window_workspace(shape, OP_WINDOW_DECODE, q.device)
-    _req_ws(ws, q.device)
-    o = torch.empty_like(q)
-    lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
-    _check(load_library().msa_window_decode(ctypes.byref(shape), _ptr(q), _ptr(k_cache),
-                                            _ptr(v_cache), _ptr(seq_len), _ptr(o), _ptr(lse),
-                                            _ptr(ws), ws.numel(), _stream(q.device)),
-           "msa_window_decode")
+    dev, ptrs, shape, need = _window_args(q, k_cache, v_cache, window, sinks, scale, OP_WINDOW_DECODE,
+                                          ws, 3)
+    sp = _ask(seq_len, "seq_len", torch.int32, (shape.B,), dev)
+    with _guard(dev):
+        wp, wn, ws = _ws(ws, need, dev)
+        o = torch.empty_like(q)
+        lse = torch.empty((shape.B, shape.Hq), dtype=torch.float32, device=dev)
+        rc = load_library().msa_window_decode(ctypes.byref(shape), *ptrs, sp, o.data_ptr(),
+                                              lse.data_ptr(), wp, wn, _stream_of(dev))
+    if rc:
+        _check(rc, "msa_window_decode")
     return o, lse
 
 
@@ -607,91 +645,98 @@ def msa_window_func(Q, K, V, window: int, sinks: int, scale: float):
 
 
 # ---------------------------------------------------------------- norm and rotation of the heads
+_PART = struct.Struct("@NqqNqqNqqNNii")  # RopePart
+assert _PART.size == ctypes.sizeof(RopePart)
+
+
 def _rows(t, name, B=None, N=None, H=None, write=False):
     """Checks a part tensor [B, N, H, 128]: rows contiguous, heads 128 apart, batch and token strides
     free.  Returns its (pointer, batch stride, token stride)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
-    if not t.is_cuda:
-        raise MSAError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
-        raise MSAError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 4 or t.shape[3] != 128 or 0 in t.shape:
-        raise MSAError(f"{name} has shape {tuple(t.shape)}, expected [B, N, heads, 128]")
-    want = (B, N, H)
-    if any(w is not None and w != g for w, g in zip(want, t.shape)):
-        raise MSAError(f"{name} has shape {tuple(t.shape)}, expected {want + (128,)}")
+    shape = t.shape
+    if not (t.is_cuda and t.dtype is torch.bfloat16 and len(shape) == 4 and shape[3] == 128):
+        if not t.is_cuda:
+            raise MSAError(f"{name} must be a CUDA tensor")
+        if t.dtype != torch.bfloat16:
+            raise MSAError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+        raise MSAError(f"{name} has shape {tuple(shape)}, expected [B, N, heads, 128]")
+    b, n, h, _ = shape
+    if not (b and n and h) or (B is not None and B != b) or (N is not None and N != n) or (H is not None and H != h):
+        raise MSAError(f"{name} has shape {tuple(shape)}, expected {(B, N, H, 128)}")
     sb, st, sh, sd = t.stride()
-    if sd != 1 or (t.shape[2] > 1 and sh != 128):
+    if sd != 1 or (h > 1 and sh != 128):
         raise MSAError(f"{name}: rows must be contiguous and heads 128 elements apart "
                        f"(strides {t.stride()})")
-    sb, st = sb if t.shape[0] > 1 else 0, st if t.shape[1] > 1 else 0
-    if sb % 8 or st % 8 or t.data_ptr() % 16:
+    if b == 1:
+        sb = 0
+    if n == 1:
+        st = 0
+    ptr = t.data_ptr()
+    if sb % 8 or st % 8 or ptr % 16:
         raise MSAError(f"{name} must be 16-byte aligned, batch and token strides multiples of 8")
     if write:
-        row = t.shape[2] * 128  # a token's rows; no two tokens may share memory
-        need = row
-        for stride, n in sorted(x for x in ((sb, t.shape[0]), (st, t.shape[1])) if x[1] > 1):
-            if stride < need:
-                raise MSAError(f"{name} overlaps itself (strides {t.stride()})")
-            need += stride * (n - 1)
-    return t.data_ptr(), sb, st
+        need = h * 128  # a token's rows; no two tokens may share memory
+        for stride, count in sorted(((sb, b), (st, n))):
+            if count > 1:
+                if stride < need:
+                    raise MSAError(f"{name} overlaps itself (strides {t.stride()})")
+                need += stride * (count - 1)
+    return ptr, sb, st
 
 
-def _rope_parts(xs, weights, rotate, inv_freq, interleaved, eps, positions):
-    """Checks what the norm and rotation entry points share; returns (shape, parts, B, N)."""
-    xs = list(xs)
-    if not 1 <= len(xs) <= ROPE_PARTS:
-        raise MSAError(f"between 1 and {ROPE_PARTS} tensors, got {len(xs)}")
-    weights = [None] * len(xs) if weights is None else list(weights)
-    rotate = [inv_freq is not None] * len(xs) if rotate is None else list(rotate)
-    if len(weights) != len(xs) or len(rotate) != len(xs):
-        raise MSAError(f"{len(xs)} tensors, {len(weights)} weights, {len(rotate)} rotate flags")
-    B, N = (xs[0].shape[0], xs[0].shape[1]) if isinstance(xs[0], torch.Tensor) and xs[0].dim() == 4 else (None, None)
-    parts = (RopePart * len(xs))()
-    for i, (p, x, w, r) in enumerate(zip(parts, xs, weights, rotate)):
-        p.x, p.x_batch, p.x_token = _rows(x, f"xs[{i}]", B, N)
-        if x.device != xs[0].device:
-            raise MSAError(f"xs[{i}] is on {x.device}, xs[0] on {xs[0].device}")
-        if w is not None:
-            _req(w, f"weights[{i}]", torch.float32, (128,))
-            _same(w, f"weights[{i}]", xs[0])
-            p.weight = w.data_ptr()
-        p.heads = x.shape[2]
-        p.flags = ROPE_ROTATE if r else 0
-    rotary = 0
-    if inv_freq is not None:
-        _dims(inv_freq, "inv_freq", 1)
-        _req(inv_freq, "inv_freq", torch.float32)
-        _same(inv_freq, "inv_freq", xs[0])
-        rotary = 2 * inv_freq.numel()
-    elif any(rotate):
-        raise MSAError("inv_freq is needed to rotate")
-    if positions is not None:
-        _req(positions, "positions", torch.int32, (B, N))
-        _same(positions, "positions", xs[0])
-    return RopeShape(B, N, 128, rotary, int(bool(interleaved)), 0, float(eps)), parts, B, N
-
-
-def _same(t, name, x):
-    if t.device != x.device:
-        raise MSAError(f"{name} is on {t.device}, the inputs on {x.device}")
-
-
-def _rope_ws(nparts, op, device, ws):
-    if ws is None:
-        n = int(load_library().msa_norm_rope_workspace_size(nparts, op))
-        return torch.empty(n, dtype=torch.uint8, device=device)
-    _req_ws(ws, device)
-    return ws
-
-
-def _rope_device(xs):
+def _device_of(xs):
     if not xs or not isinstance(xs[0], torch.Tensor):
         raise TypeError("xs must be a sequence of tensors")
     if not xs[0].is_cuda:
         raise MSAError("xs[0] must be a CUDA tensor")
-    return torch.cuda.device(xs[0].device)
+    return xs[0].device
+
+
+def _on(t, name, device):
+    if t.device != device:
+        raise MSAError(f"{name} is on {t.device}, the inputs on {device}")
+
+
+def _rope_args(xs, weights, rotate, inv_freq, interleaved, eps, positions, dev):
+    """Checks what the norm and rotation entry points share; returns (shape, parts, inv_freq's and
+    positions' addresses), a part being (x's pointer and strides, weight's address, heads, flags)."""
+    count = len(xs)
+    if not 1 <= count <= ROPE_PARTS:
+        raise MSAError(f"between 1 and {ROPE_PARTS} tensors, got {count}")
+    weights = [None] * count if weights is None else weights
+    rotate = [inv_freq is not None] * count if rotate is None else rotate
+    if len(weights) != count or len(rotate) != count:
+        raise MSAError(f"{count} tensors, {len(weights)} weights, {len(rotate)} rotate flags")
+    B, N = (xs[0].shape[0], xs[0].shape[1]) if xs[0].dim() == 4 else (None, None)
+    parts = []
+    for i in range(count):
+        x, w = xs[i], weights[i]
+        at = _rows(x, f"xs[{i}]", B, N)
+        if x.device != dev:
+            _on(x, f"xs[{i}]", dev)
+        wp = 0 if w is None else _ask(w, f"weights[{i}]", torch.float32, (128,), dev)
+        parts.append((at, wp, x.shape[2], ROPE_ROTATE if rotate[i] else 0))
+    rotary, fp, pp = 0, None, None
+    if inv_freq is not None:
+        fp = _ask(inv_freq, "inv_freq", torch.float32, tuple(_dims(inv_freq, "inv_freq", 1)), dev)
+        rotary = 2 * inv_freq.shape[0]
+    elif any(rotate):
+        raise MSAError("inv_freq is needed to rotate")
+    if positions is not None:
+        pp = _ask(positions, "positions", torch.int32, (B, N), dev)
+    return RopeShape(B, N, 128, rotary, 1 if interleaved else 0, 0, eps), parts, fp, pp
+
+
+@functools.lru_cache(maxsize=64)
+def _rope_bytes(nparts, op):
+    return int(load_library().msa_norm_rope_workspace_size(nparts, op))
+
+
+def _strides(t):
+    """(pointer, batch stride, token stride) of a contiguous tensor [B, N, heads, 128]."""
+    st = t.shape[2] * 128
+    return t.data_ptr(), st * t.shape[1], st
 
 
 def msa_norm_rope_forward(xs, weights, inv_freq, positions=None, eps: float = 1e-6, rotate=None,
@@ -704,43 +749,48 @@ def msa_norm_rope_forward(xs, weights, inv_freq, positions=None, eps: float = 1e
     ``rotary`` (a multiple of 16) elements of a row turn by position * inv_freq; None: no rotation.
     rotate: one truth value per tensor (default: all).  positions: int32 [B, N], default 0 .. N - 1.
     A tensor without weight and rotation is copied.  Returns contiguous tensors [B, N, heads, 128]."""
-    with _rope_device(xs):
-        shape, parts, B, N = _rope_parts(xs, weights, rotate, inv_freq, interleaved, eps, positions)
-        ys = []
-        for p, x in zip(parts, xs):
-            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-            p.y, p.y_batch, p.y_token = y.data_ptr(), y.stride(0), y.stride(1)
-            ys.append(y)
-        _check(load_library().msa_norm_rope_forward(
-            ctypes.byref(shape), parts, len(ys), _ptr(positions), _ptr(inv_freq),
-            _stream(xs[0].device)), "msa_norm_rope_forward")
-        return tuple(ys)
+    dev = _device_of(xs)
+    shape, parts, fp, pp = _rope_args(xs, weights, rotate, inv_freq, interleaved, eps, positions, dev)
+    with _guard(dev):
+        ys = [torch.empty(x.shape, dtype=torch.bfloat16, device=dev) for x in xs]
+        packed = b"".join([_PART.pack(*at, *_strides(y), 0, 0, 0, w, 0, h, f)
+                           for (at, w, h, f), y in zip(parts, ys)])
+        rc = load_library().msa_norm_rope_forward(ctypes.byref(shape), packed, len(ys), pp, fp,
+                                                  _stream_of(dev))
+    if rc:
+        _check(rc, "msa_norm_rope_forward")
+    return tuple(ys)
 
 
 def msa_norm_rope_backward(xs, weights, dys, inv_freq, positions=None, eps: float = 1e-6,
                            rotate=None, interleaved: bool = False, dxs=None, ws=None):
     """Gradients of msa_norm_rope_forward: (dxs, dweights), dweights fp32 [128] or None per tensor.
-    dxs: where to write them (e.g. the slices of one packed gradient), default new tensors."""
-    with _rope_device(xs):
-        shape, parts, B, N = _rope_parts(xs, weights, rotate, inv_freq, interleaved, eps, positions)
-        if len(dys) != len(xs) or (dxs is not None and len(dxs) != len(xs)):
-            raise MSAError("one dy (and dx, where given) per tensor")
-        dev = xs[0].device
-        dxs = [torch.empty(x.shape, dtype=x.dtype, device=dev) for x in xs] if dxs is None else list(dxs)
-        dws = []
-        for i, (p, x, dy, dx) in enumerate(zip(parts, xs, dys, dxs)):
-            p.y, p.y_batch, p.y_token = _rows(dy, f"dys[{i}]", B, N, x.shape[2])
-            p.dx, p.dx_batch, p.dx_token = _rows(dx, f"dxs[{i}]", B, N, x.shape[2], write=True)
-            _same(dy, f"dys[{i}]", x)
-            _same(dx, f"dxs[{i}]", x)
-            dw = torch.empty(128, dtype=torch.float32, device=dev) if p.weight else None
-            p.dweight = dw.data_ptr() if dw is not None else None
-            dws.append(dw)
-        ws = _rope_ws(len(dxs), OP_NORM_ROPE_BACKWARD, dev, ws)
-        _check(load_library().msa_norm_rope_backward(
-            ctypes.byref(shape), parts, len(dxs), _ptr(positions), _ptr(inv_freq), _ptr(ws),
-            ws.numel(), _stream(dev)), "msa_norm_rope_backward")
-        return tuple(dxs), tuple(dws)
+    dxs: where to write them (e.g. the slices of one packed gradient, or the dys), default new
+    tensors."""
+    dev = _device_of(xs)
+    shape, parts, fp, pp = _rope_args(xs, weights, rotate, inv_freq, interleaved, eps, positions, dev)
+    n = len(xs)
+    if len(dys) != n or (dxs is not None and len(dxs) != n):
+        raise MSAError("one dy (and dx, where given) per tensor")
+    with _guard(dev):
+        # one tensor for the weights' gradients: a row each
+        dws = torch.empty((n, 128), dtype=torch.float32, device=dev)
+        out_w, rows, dw = [], [], dws.data_ptr()
+        out_x = [torch.empty(x.shape, dtype=torch.bfloat16, device=dev) for x in xs] if dxs is None else dxs
+        for i, (at, w, h, f) in enumerate(parts):
+            dy = _rows(dys[i], f"dys[{i}]", shape.B, shape.N, h)
+            dx = _strides(out_x[i]) if dxs is None else _rows(dxs[i], f"dxs[{i}]", shape.B, shape.N, h, write=True)
+            if dys[i].device != dev or out_x[i].device != dev:
+                _on(dys[i], f"dys[{i}]", dev)
+                _on(out_x[i], f"dxs[{i}]", dev)
+            rows.append(_PART.pack(*at, *dy, *dx, w, dw + 512 * i if w else 0, h, f))
+            out_w.append(dws[i] if w else None)
+        wp, wn, ws = _ws(ws, lambda: _rope_bytes(n, OP_NORM_ROPE_BACKWARD), dev)
+        rc = load_library().msa_norm_rope_backward(ctypes.byref(shape), b"".join(rows), n, pp, fp, wp,
+                                                   wn, _stream_of(dev))
+    if rc:
+        _check(rc, "msa_norm_rope_backward")
+    return tuple(out_x), tuple(out_w)
 
 
 def msa_norm_rope_append(xs, weights, inv_freq, seq_len, caches, eps: float = 1e-6, rotate=None,
@@ -754,35 +804,40 @@ def msa_norm_rope_append(xs, weights, inv_freq, seq_len, caches, eps: float = 1e
     caches (None, k_cache, v_cache, None, kp_cache) the arguments of msa_decode and
     msa_window_decode.  Sequences with a length outside N .. S are skipped (msa_device_status of ws
     tells)."""
-    with _rope_device(xs):
-        flat = [isinstance(x, torch.Tensor) and x.dim() == 3 for x in xs]
-        x4 = [x.unsqueeze(1) if f else x for x, f in zip(xs, flat)]
-        shape, parts, B, N = _rope_parts(x4, weights, rotate, inv_freq, interleaved, eps, None)
-        _req(seq_len, "seq_len", torch.int32, (B,))
-        _same(seq_len, "seq_len", x4[0])
-        if len(caches) != len(xs):
-            raise MSAError("one cache (or None) per tensor")
-        caps = {c.shape[1] for c in caches if isinstance(c, torch.Tensor) and c.dim() >= 3}
-        if len(caps) > 1:
-            raise MSAError(f"caches of different capacities: {sorted(caps)}")
-        shape.capacity = caps.pop() if caps else 2 ** 31 - 1
-        outs = []
-        for i, (p, x, c, f) in enumerate(zip(parts, x4, caches, flat)):
+    dev = _device_of(xs)
+    x4 = [x.unsqueeze(1) if isinstance(x, torch.Tensor) and x.dim() == 3 else x for x in xs]
+    shape, parts, fp, _ = _rope_args(x4, weights, rotate, inv_freq, interleaved, eps, None, dev)
+    B = shape.B
+    sp = _ask(seq_len, "seq_len", torch.int32, (B,), dev)
+    if len(caches) != len(x4):
+        raise MSAError("one cache (or None) per tensor")
+    capacity = None
+    with _guard(dev):
+        outs, rows = [], []
+        for i, (at, w, h, f) in enumerate(parts):
+            c = caches[i]
             if c is None:
-                y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-                p.y, p.y_batch, p.y_token = y.data_ptr(), y.stride(0), y.stride(1)
-                outs.append(y.squeeze(1) if f else y)
-                continue
-            c4 = c.unsqueeze(2) if isinstance(c, torch.Tensor) and c.dim() == 3 else c
-            p.y, p.y_batch, p.y_token = _rows(c4, f"caches[{i}]", B, None, x.shape[2], write=True)
-            _same(c4, f"caches[{i}]", x)
-            p.flags |= ROPE_CACHE
-            outs.append(c)
-        ws = _rope_ws(len(outs), OP_NORM_ROPE_APPEND, x4[0].device, ws)
-        _check(load_library().msa_norm_rope_append(
-            ctypes.byref(shape), parts, len(outs), _ptr(seq_len), _ptr(inv_freq), _ptr(ws),
-            ws.numel(), _stream(x4[0].device)), "msa_norm_rope_append")
-        return tuple(outs)
+                y = torch.empty(xs[i].shape, dtype=torch.bfloat16, device=dev)
+                to = (y.data_ptr(), shape.N * h * 128, h * 128)
+                outs.append(y)
+            else:
+                c4 = c.unsqueeze(2) if isinstance(c, torch.Tensor) and c.dim() == 3 else c
+                to = _rows(c4, f"caches[{i}]", B, None, h, write=True)
+                if c4.device != dev:
+                    _on(c4, f"caches[{i}]", dev)
+                if capacity is not None and c4.shape[1] != capacity:
+                    raise MSAError(f"caches of different capacities: {capacity}, {c4.shape[1]}")
+                capacity = c4.shape[1]
+                f |= ROPE_CACHE
+                outs.append(c)
+            rows.append(_PART.pack(*at, *to, 0, 0, 0, w, 0, h, f))
+        shape.capacity = 2 ** 31 - 1 if capacity is None else capacity
+        wp, wn, ws = _ws(ws, lambda: _rope_bytes(len(rows), OP_NORM_ROPE_APPEND), dev)
+        rc = load_library().msa_norm_rope_append(ctypes.byref(shape), b"".join(rows), len(rows), sp, fp,
+                                                 wp, wn, _stream_of(dev))
+    if rc:
+        _check(rc, "msa_norm_rope_append")
+    return tuple(outs)
 
 
 class _NormRopeFunction(torch.autograd.Function):

@@ -855,7 +855,7 @@ bool launch_win_dkv(const WinDims& d, const void* q, const void* k, const void* 
   a.it = win_items(d);
   const size_t smem = sizeof(DkvShared) + 7 * (size_t)kTile;
 #define MSA_CALL(G)                                                                                    \
-  cudaFuncSetAttribute(win_dkv_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);      \
+  allow_smem<win_dkv_kernel<G>>(smem);      \
   win_dkv_kernel<G><<<a.it.items < n ? a.it.items : n, kBwdThreads, smem, st>>>(a)
   MSA_BY_GROUP(d.G, MSA_CALL)
 #undef MSA_CALL
@@ -875,7 +875,7 @@ bool launch_win_dq(const WinDims& d, const void* q, const void* k, const void* v
   a.units = (long long)((d.S + tt - 1) / tt) * d.B * d.Hkv;
   const size_t smem = sizeof(DqShared) + 1024 + (2 + kRingQ) * (size_t)kTile;
 #define MSA_CALL(G)                                                                                  \
-  cudaFuncSetAttribute(win_dq_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);     \
+  allow_smem<win_dq_kernel<G>>(smem);     \
   win_dq_kernel<G><<<(int)(a.units < n ? a.units : n), kBwdThreads, smem, st>>>(a)
   MSA_BY_GROUP(d.G, MSA_CALL)
 #undef MSA_CALL

@@ -305,7 +305,7 @@ WinSplit win_decode_split(const WinDims& d) {
 template <int G>
 static void win_decode_g(const DecArgs& a, cudaStream_t st) {
   const size_t smem = sizeof(DecShared) + 1024 + 2 * (size_t)kTile + 2 * (size_t)kNH * kD * 2;
-  cudaFuncSetAttribute(win_decode_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  allow_smem<win_decode_kernel<G>>(smem);
   win_decode_kernel<G><<<a.d.B * a.d.Hkv * a.nsplit, kDecThreads, smem, st>>>(a);
 }
 

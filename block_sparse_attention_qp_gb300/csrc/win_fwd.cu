@@ -378,18 +378,20 @@ __global__ void __launch_bounds__(kFwdThreads, 1) win_fwd_kernel(const __grid_co
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-// The three maps of K or V.  nsp mod 128 rows of the shared tile are sinks (0: no such tile).
+// The three maps of K or V.  nsp mod 128 rows of the shared tile are sinks (0: there is no such tile,
+// and the two maps are not used).
 bool make_key_maps(const WinDims& d, const void* base, KeyMaps* m) {
   const int a = d.nsp % kBlock;
-  return make_tmap_rows(&m->full, base, d.B, d.S, d.Hkv, 1, kBlock) &&
-         make_tmap_rows(&m->sink, base, d.B, d.S, d.Hkv, 1, a ? a : 8) &&
-         make_tmap_rows(&m->rest, base, d.B, d.S, d.Hkv, 1, a ? kBlock - a : 8);
+  if (!make_tmap_rows(&m->full, base, d.B, d.S, d.Hkv, 1, kBlock)) return false;
+  m->sink = m->rest = m->full;
+  return a == 0 || (make_tmap_rows(&m->sink, base, d.B, d.S, d.Hkv, 1, a) &&
+                    make_tmap_rows(&m->rest, base, d.B, d.S, d.Hkv, 1, kBlock - a));
 }
 
 template <int G>
 static void win_fwd_g(const FwdArgs& a, cudaStream_t st) {
   const size_t smem = sizeof(FwdShared) + (4 + kRing) * (size_t)kTile;
-  cudaFuncSetAttribute(win_fwd_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  allow_smem<win_fwd_kernel<G>>(smem);
   const int n = num_sms();
   win_fwd_kernel<G><<<(int)(a.units < n ? a.units : n), kFwdThreads, smem, st>>>(a);
 }

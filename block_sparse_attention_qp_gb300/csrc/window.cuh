@@ -10,6 +10,8 @@
 #pragma once
 #include <cuda.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "sm100.cuh"
@@ -59,6 +61,19 @@ struct KeyMaps {
   CUtensorMap full, sink, rest;
 };
 bool make_key_maps(const WinDims& d, const void* base, KeyMaps* m);  // win_fwd.cu
+
+// Lets a kernel use `bytes` of dynamic shared memory: once per kernel and device (the attribute
+// belongs to the device's context; a repeated call costs a microsecond of every launch).
+template <auto* Kernel>
+void allow_smem(size_t bytes) {
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return;
+  if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess)
+    done.fetch_or(bit, std::memory_order_relaxed);
+}
 
 __device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* tm, int col, int head,
                                               int row, int b, uint64_t* mbar) {
