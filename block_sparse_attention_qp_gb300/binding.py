@@ -775,7 +775,7 @@ def msa_norm_rope_backward(xs, weights, dys, inv_freq, positions=None, eps: floa
     with _guard(dev):
         # one tensor for the weights' gradients: a row each
         dws = torch.empty((n, 128), dtype=torch.float32, device=dev)
-        out_w, rows, dw = [], [], dws.data_ptr()
+        out_w, rows, dw = list(dws.unbind(0)), [], dws.data_ptr()
         out_x = [torch.empty(x.shape, dtype=torch.bfloat16, device=dev) for x in xs] if dxs is None else dxs
         for i, (at, w, h, f) in enumerate(parts):
             dy = _rows(dys[i], f"dys[{i}]", shape.B, shape.N, h)
@@ -784,7 +784,8 @@ def msa_norm_rope_backward(xs, weights, dys, inv_freq, positions=None, eps: floa
                 _on(dys[i], f"dys[{i}]", dev)
                 _on(out_x[i], f"dxs[{i}]", dev)
             rows.append(_PART.pack(*at, *dy, *dx, w, dw + 512 * i if w else 0, h, f))
-            out_w.append(dws[i] if w else None)
+            if not w:
+                out_w[i] = None
         wp, wn, ws = _ws(ws, lambda: _rope_bytes(n, OP_NORM_ROPE_BACKWARD), dev)
         rc = load_library().msa_norm_rope_backward(ctypes.byref(shape), b"".join(rows), n, pp, fp, wp,
                                                    wn, _stream_of(dev))

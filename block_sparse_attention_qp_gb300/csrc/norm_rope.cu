@@ -20,7 +20,7 @@
 // head.  Bound by memory: forward reads and writes 256 bytes a row, backward reads 512 and writes 256.
 // Few tokens: the heads of a token are split over warps so that a decode step still spreads over SMs.
 // dw: per-warp sums in shared memory, one partial per block, then a second kernel adds the blocks'
-// partials in fp64 in a fixed order: no atomics, the same bits every time.
+// partials in a fixed order: no atomics, the same bits every time.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -214,7 +214,9 @@ __global__ void __launch_bounds__(32 * kRopeWarps) norm_rope_bwd_kernel(RopeArgs
   const int half8 = A.rot / 16;
   const int partner = 8 * l >= A.rot ? l : (l < half8 ? l + half8 : l - half8);
   const long long nwu = ((long long)A.B * A.N + 1) / 2 * A.chunks;
-  constexpr int kR = 2;  // rows in flight: x and dy of each
+  // rows in flight, x and dy of each: 4 read at 5.7 TB/s at 64K tokens x 89 heads (2: 4.8), with two
+  // blocks of 126 registers a thread; three blocks spill
+  constexpr int kR = 4;
   for (long long wu = (long long)blockIdx.x * kRopeWarps + warp; wu < nwu;
        wu += (long long)gridDim.x * kRopeWarps) {
     const Unit u = rope_unit(A, wu, hw);
@@ -291,19 +293,43 @@ __global__ void __launch_bounds__(32 * kRopeWarps) norm_rope_bwd_kernel(RopeArgs
   }
 }
 
-// dw of part blockIdx.x: the blocks' partials added in fp64, eight interleaved runs per element.
+// x += y with the rounding error of the sum kept in c (the error-free transformation of two terms).
+__device__ __forceinline__ void add_exact(float& x, float& c, float y) {
+  const float s = __fadd_rn(x, y), b = __fsub_rn(s, x);
+  c = __fadd_rn(c, __fadd_rn(__fsub_rn(x, __fsub_rn(s, b)), __fsub_rn(y, b)));
+  x = s;
+}
+
+// dw of part blockIdx.x: the blocks' partials, 32 interleaved runs (a warp each, four elements a lane)
+// and then the runs in order.  Compensated fp32 sums: as good as fp64 here, whose few units took 17 us
+// for 188 blocks' partials (this: 4).
 __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(RopeArgs A, int nblocks) {
-  __shared__ double s[8][kD];
-  const int e = threadIdx.x % kD, run = threadIdx.x / kD, p = blockIdx.x;
+  __shared__ float s[32][kD], e[32][kD];
+  const int lane = threadIdx.x % 32, run = threadIdx.x / 32, p = blockIdx.x;
   if (!A.p[p].dw) return;
-  double a = 0.0;
-#pragma unroll 8
-  for (int k = run; k < nblocks; k += 8) a += (double)A.partial[((long long)k * A.nparts + p) * kD + e];
-  s[run][e] = a;
+  float a[4] = {0.f, 0.f, 0.f, 0.f}, c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int k = run; k < nblocks; k += 32) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(A.partial + ((long long)k * A.nparts + p) * kD) + lane);
+    add_exact(a[0], c[0], v.x);
+    add_exact(a[1], c[1], v.y);
+    add_exact(a[2], c[2], v.z);
+    add_exact(a[3], c[3], v.w);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s[run][4 * lane + i] = a[i];
+    e[run][4 * lane + i] = c[i];
+  }
   __syncthreads();
-  if (run == 0) {
-    for (int k = 1; k < 8; ++k) a += s[k][e];
-    A.p[p].dw[e] = (float)a;
+  if (threadIdx.x < kD) {
+    float t = 0.f, u = 0.f;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      add_exact(t, u, s[k][threadIdx.x]);
+      u += e[k][threadIdx.x];
+    }
+    A.p[p].dw[threadIdx.x] = t + u;
   }
 }
 
@@ -329,7 +355,8 @@ constexpr int kRopeFwdBlocks = 3, kRopeBwdBlocks = 2;  // blocks per SM
 int rope_partials() { return num_sms() * kRopeBwdBlocks; }
 
 void launch_norm_rope_fwd(RopeArgs A, cudaStream_t st) {
-  split_rows(A, num_sms() * kRopeWarps);
+  // (two blocks' warps per SM: 3 x 999 tokens x 15 heads in 11.3 us, with one block's 13.7)
+  split_rows(A, num_sms() * 2 * kRopeWarps);
   const int g = rope_grid(A, kRopeFwdBlocks);
   if (A.inter) norm_rope_fwd_kernel<true><<<g, 32 * kRopeWarps, 0, st>>>(A);
   else norm_rope_fwd_kernel<false><<<g, 32 * kRopeWarps, 0, st>>>(A);

@@ -266,26 +266,61 @@ __global__ void __launch_bounds__(kDecThreads, kDecBlocks) win_decode_kernel(con
   if (warp == 0) tmem_dealloc(sh->tmem, 32);
 }
 
-// Merges the splits of every (b, head): one block of 128 threads each, thread = dim.
-__global__ void __launch_bounds__(128) win_decode_join_kernel(int B, int Hq, int S, int nsplit, const int32_t* seq_len,
-                                                              const float* opart, const float* lpart, bf16* o,
-                                                              float* lse) {
+// Merges the splits of every (b, head): one block each.  The splits' weights first, one thread a split;
+// then eight runs of splits at once, 32 threads of four dims each, so that a thread's loads do not wait
+// for one another.
+constexpr int kJoinRuns = 8, kJoinThreads = 32 * kJoinRuns;
+__global__ void __launch_bounds__(kJoinThreads) win_decode_join_kernel(int B, int Hq, int S, int nsplit,
+                                                                       const int32_t* seq_len, const float* opart,
+                                                                       const float* lpart, bf16* o, float* lse) {
+  extern __shared__ float w[];  // [nsplit] weights
+  __shared__ float red[kJoinRuns];
+  __shared__ float4 acc[kJoinRuns][32];
   const long long row = blockIdx.x, rows = (long long)B * Hq;
-  const int len = seq_len[row / Hq];
+  const int len = seq_len[row / Hq], lane = threadIdx.x % 32, run = threadIdx.x / 32;
   if (len < 1 || len > S) return;  // flagged by win_decode_kernel
   float mx = -INFINITY;
-  for (int s = 0; s < nsplit; ++s) mx = fmaxf(mx, __ldg(lpart + s * rows + row));
-  float sum = 0.f, acc = 0.f;
-#pragma unroll 4
-  for (int s = 0; s < nsplit; ++s) {
-    const float ls = __ldg(lpart + s * rows + row);
-    const float w = exp2_ftz(ls - mx);
-    sum += w;
-    // (an empty split wrote no rows)
-    if (ls != -INFINITY) acc = fmaf(w, __ldg(opart + (s * rows + row) * kD + threadIdx.x), acc);
+  for (int s = threadIdx.x; s < nsplit; s += kJoinThreads) {
+    w[s] = __ldg(lpart + s * rows + row);
+    mx = fmaxf(mx, w[s]);
   }
-  o[row * kD + threadIdx.x] = __float2bfloat16_rn(acc / sum);
-  if (threadIdx.x == 0) lse[row] = (mx + log2f(sum)) * kLn2;
+  mx = warp_max(mx);
+  if (lane == 0) red[run] = mx;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kJoinRuns; ++k) mx = fmaxf(mx, red[k]);
+  float sum = 0.f;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = run; s < nsplit; s += kJoinRuns) {
+    const float ls = w[s], p = exp2_ftz(ls - mx);
+    if (ls == -INFINITY) continue;  // an empty split wrote no rows
+    const float4 v = __ldg(reinterpret_cast<const float4*>(opart + (s * rows + row) * kD) + lane);
+    sum += p;
+    a.x = fmaf(p, v.x, a.x);
+    a.y = fmaf(p, v.y, a.y);
+    a.z = fmaf(p, v.z, a.z);
+    a.w = fmaf(p, v.w, a.w);
+  }
+  __syncthreads();  // everyone has read the maxima
+  if (lane == 0) red[run] = sum;
+  acc[run][lane] = a;
+  __syncthreads();
+  if (run > 0) return;
+  sum = red[0];
+#pragma unroll
+  for (int k = 1; k < kJoinRuns; ++k) {
+    const float4 v = acc[k][lane];
+    sum += red[k];
+    a.x += v.x;
+    a.y += v.y;
+    a.z += v.z;
+    a.w += v.w;
+  }
+  const float inv = 1.f / sum;
+  *reinterpret_cast<uint2*>(o + row * kD + 4 * lane) =
+      make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+  if (lane == 0) lse[row] = (mx + log2f(sum)) * kLn2;
 }
 
 // Splits of the key tiles: as many as fill the resident blocks, one where the (b, KV head) pairs do.
@@ -334,7 +369,7 @@ bool launch_win_decode(const WinDims& d, const void* q, const void* k_cache, con
     default: return false;
   }
   if (w.nsplit > 1)
-    win_decode_join_kernel<<<d.B * d.Hq, 128, 0, st>>>(d.B, d.Hq, d.S, w.nsplit, seq_len, opart, lpart, (bf16*)o, lse);
+    win_decode_join_kernel<<<d.B * d.Hq, kJoinThreads, w.nsplit * sizeof(float), st>>>(d.B, d.Hq, d.S, w.nsplit, seq_len, opart, lpart, (bf16*)o, lse);
   return true;
 }
 
