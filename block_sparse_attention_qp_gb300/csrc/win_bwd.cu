@@ -479,7 +479,7 @@ struct DqArgs {
   CUtensorMap q, dout, dq;
   const float2* rowm;
   unsigned* status;
-  long long units;  // one 128-row tile each
+  int units;  // one 128-row tile each
 };
 struct DqShared {
   uint64_t q_full, q_empty, do_full, do_empty, kv_full[kRingQ], kv_empty[kRingQ], s_full, dp_full, pa, pb,
@@ -491,14 +491,14 @@ struct DqUnit {
   KeyRun run;
 };
 template <int G>
-__device__ __forceinline__ DqUnit dq_unit(const WinDims& d, long long u) {
+__device__ __forceinline__ DqUnit dq_unit(const WinDims& d, int u) {
   constexpr int TT = 128 / G;
   const int per = d.B * d.Hkv;
   DqUnit x;
-  const int rem = (int)(u % per);
+  const int rem = u % per;
   x.b = rem / d.Hkv;
   x.g = rem % d.Hkv;
-  x.t0 = (int)(u / per) * TT;
+  x.t0 = u / per * TT;
   x.run = key_run(d, x.t0, x.t0 + TT - 1 < d.S ? x.t0 + TT - 1 : d.S - 1);
   return x;
 }
@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dq_kernel(const __grid_con
         return true;
       };
       bool ok = true;
-      for (long long u = blockIdx.x; u < A.units && ok; u += gridDim.x, ++nu) {
+      for (int u = blockIdx.x; u < A.units && ok; u += gridDim.x, ++nu) {
         const DqUnit x = dq_unit<G>(d, u);
         if (nu > 0 && !mbar_wait(&sh->q_empty, phase_of(nu - 1), A.status)) { ok = false; break; }
         mbar_expect_tx(&sh->q_full, kTile);
@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dq_kernel(const __grid_con
         if (last) warp_mma_commit(&sh->do_empty);
         return true;
       };
-      long long u = blockIdx.x;
+      int u = blockIdx.x;
       int nb = dq_unit<G>(d, u).run.nb, i = 0;
       bool ok = mma_s(k, true, nb == 1, 0) && mma_dp(k, true, nb == 1, 0);
       for (int nu = 0; ok && nb > 0; ++nu) {
@@ -666,7 +666,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dq_kernel(const __grid_con
     if (lane == 0) {
       long long nu = 0;
       int slot = 0;
-      for (long long u = blockIdx.x; u < A.units; u += gridDim.x, ++nu, slot = (slot + 1) % kRingQ) {
+      for (int u = blockIdx.x; u < A.units; u += gridDim.x, ++nu, slot = (slot + 1) % kRingQ) {
         const DqUnit x = dq_unit<G>(d, u);
         slot = (slot + 2 * x.run.nb) % kRingQ;  // the unit's last ring entry
         if (!mbar_wait(&sh->st_full, phase_of(nu), A.status)) break;
@@ -687,7 +687,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dq_kernel(const __grid_con
     const uint32_t lb = static_cast<uint32_t>(quad * 32) << 16;
     const float sl2 = d.scale * kLog2e;
     const float2 sl2x2 = make_float2(sl2, sl2), sc2 = make_float2(d.scale, d.scale);
-    auto row_data = [&](long long u) -> float2 {
+    auto row_data = [&](int u) -> float2 {
       if (u >= A.units) return make_float2(0.f, 0.f);
       const DqUnit x = dq_unit<G>(d, u);
       const int t = x.t0 + r / G;
@@ -728,7 +728,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dq_kernel(const __grid_con
     int i = 0, nu = 0, v_slot = 1;
     float2 m = row_data(blockIdx.x);
     bool ok = true;
-    for (long long u = blockIdx.x; u < A.units && ok; u += gridDim.x, ++nu) {
+    for (int u = blockIdx.x; u < A.units && ok; u += gridDim.x, ++nu) {
       const DqUnit x = dq_unit<G>(d, u);
       const float2 mnext = row_data(u + gridDim.x);
       const int t = x.t0 + r / G;
@@ -872,11 +872,11 @@ bool launch_win_dq(const WinDims& d, const void* q, const void* k, const void* v
   a.d = d;
   a.rowm = rowm;
   a.status = status;
-  a.units = (long long)((d.S + tt - 1) / tt) * d.B * d.Hkv;
+  a.units = (d.S + tt - 1) / tt * d.B * d.Hkv;
   const size_t smem = sizeof(DqShared) + 1024 + (2 + kRingQ) * (size_t)kTile;
 #define MSA_CALL(G)                                                                                  \
   allow_smem<win_dq_kernel<G>>(smem);     \
-  win_dq_kernel<G><<<(int)(a.units < n ? a.units : n), kBwdThreads, smem, st>>>(a)
+  win_dq_kernel<G><<<a.units < n ? a.units : n, kBwdThreads, smem, st>>>(a)
   MSA_BY_GROUP(d.G, MSA_CALL)
 #undef MSA_CALL
   return true;

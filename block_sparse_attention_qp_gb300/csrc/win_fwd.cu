@@ -47,7 +47,7 @@ struct FwdArgs {
   unsigned* status;
   int tiles;        // query tiles per unit, 1 or 2
   int nseg;         // units along a sequence
-  long long units;  // nseg B Hkv
+  int units;  // nseg B Hkv
 };
 constexpr int kFwdThreads = 640;
 struct FwdShared {
@@ -62,12 +62,12 @@ struct FwdUnit {
   KeyRun run;
 };
 template <int G>
-__device__ __forceinline__ FwdUnit fwd_unit(const FwdArgs& A, long long u) {
+__device__ __forceinline__ FwdUnit fwd_unit(const FwdArgs& A, int u) {
   constexpr int TT = 128 / G;
   const WinDims& d = A.d;
   FwdUnit x;
   const int per = d.B * d.Hkv;
-  const int seg = (int)(u / per), rem = (int)(u % per);
+  const int seg = u / per, rem = u % per;
   x.b = rem / d.Hkv;
   x.g = rem % d.Hkv;
   x.t0 = seg * TT * A.tiles;
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) win_fwd_kernel(const __grid_co
       bool ok = true;
       long long nl = 0, nu = 0;
       Ring<kRing> kv;
-      for (long long u = blockIdx.x; u < A.units && ok; u += gridDim.x, ++nu) {
+      for (int u = blockIdx.x; u < A.units && ok; u += gridDim.x, ++nu) {
         const FwdUnit x = fwd_unit<G>(A, u);
         const int qs = (int)(nu & 1);
         if (nu >= 2 && !mbar_wait(&sh->q_empty[qs], phase_of(nu / 2 - 1), A.status)) break;
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) win_fwd_kernel(const __grid_co
         ++cs[X];
       };
       int nu = 0;
-      for (long long u = blockIdx.x; u < A.units && ok; u += gridDim.x, ++nu) {
+      for (int u = blockIdx.x; u < A.units && ok; u += gridDim.x, ++nu) {
         const FwdUnit x = fwd_unit<G>(A, u);
         const int qs = nu & 1;
         const uint32_t q = aQ + qs * 2 * kTile;
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) win_fwd_kernel(const __grid_co
     if (lane == 0) {
       const int X = warp - 2;
       long long nu = 0, ns = 0;
-      for (long long u = blockIdx.x; u < A.units; u += gridDim.x, ++nu) {
+      for (int u = blockIdx.x; u < A.units; u += gridDim.x, ++nu) {
         const FwdUnit x = fwd_unit<G>(A, u);
         const int qs = (int)(nu & 1);
         if (X == 0 || x.two) {
@@ -254,11 +254,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) win_fwd_kernel(const __grid_co
     // Both warps of a pair pass the same barriers whatever happens: a wait that gives up only clears
     // `ok` (warp-uniform), which skips the later waits.
     bool ok = true;
-    for (long long u = blockIdx.x; u < A.units; u += gridDim.x, ++nu) {
+    for (int u = blockIdx.x; u < A.units; u += gridDim.x, ++nu) {
       const FwdUnit x = fwd_unit<G>(A, u);
       if (X == 1 && !x.two) continue;
       const int t = x.t0 + X * TT + r / G;  // this row's token
-      const int h = x.g * G + r % G;         // and query head
       float mr = -INFINITY, l = 0.f;
       for (int n = 0; n < x.run.nb; ++n, ++cs) {
         // (the masks cost about as many instructions as the exponentials: only where a tile needs them)
@@ -369,7 +368,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) win_fwd_kernel(const __grid_co
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->st_full[X]);
-      if (hf == 0 && t < d.S) A.lse[((long long)x.b * d.Hq + h) * d.S + t] = (mr * sl2 + __log2f(l)) * kLn2;
+      if (hf == 0 && t < d.S) A.lse[((long long)x.b * d.Hq + x.g * G + r % G) * d.S + t] = (mr * sl2 + __log2f(l)) * kLn2;
     }
   }
   fence_before_sync();
@@ -393,7 +392,7 @@ static void win_fwd_g(const FwdArgs& a, cudaStream_t st) {
   const size_t smem = sizeof(FwdShared) + (4 + kRing) * (size_t)kTile;
   allow_smem<win_fwd_kernel<G>>(smem);
   const int n = num_sms();
-  win_fwd_kernel<G><<<(int)(a.units < n ? a.units : n), kFwdThreads, smem, st>>>(a);
+  win_fwd_kernel<G><<<a.units < n ? a.units : n, kFwdThreads, smem, st>>>(a);
 }
 
 bool launch_win_fwd(const WinDims& d, const void* q, const void* k, const void* v, void* o,
@@ -410,7 +409,7 @@ bool launch_win_fwd(const WinDims& d, const void* q, const void* k, const void* 
   const long long per = (long long)d.B * d.Hkv;
   a.tiles = (d.S + 2 * tt - 1) / (2 * tt) * per < num_sms() ? 1 : 2;
   a.nseg = (d.S + tt * a.tiles - 1) / (tt * a.tiles);
-  a.units = a.nseg * per;
+  a.units = (int)(a.nseg * per);
   switch (d.G) {
     case 1: win_fwd_g<1>(a, st); break;
     case 2: win_fwd_g<2>(a, st); break;
