@@ -497,11 +497,11 @@ def _stream_of(device) -> int:
 
 def _ask(t, name, dtype, shape, device):
     """t is a contiguous CUDA tensor of this type, shape and device; returns its address."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
-            and t.device == device and t.is_cuda):
-        _req(t, name, dtype, shape)
-        raise MSAError(f"{name} is on {t.device}, the first argument on {device}")
-    return t.data_ptr()
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device \
+            and t.is_contiguous():
+        return t.data_ptr()
+    _req(t, name, dtype, shape)
+    raise MSAError(f"{name} is on {t.device}, the first argument on {device}")
 
 
 def _dims(t, name, n):
@@ -547,9 +547,9 @@ def window_workspace(shape: WindowShape, op: int, device) -> torch.Tensor:
 
 
 def _ws(ws, need, device):
-    """(address, bytes, tensor) of the caller's workspace, or of a fresh one of need() bytes."""
+    """(address, bytes, tensor) of the caller's workspace, or of a fresh one of `need` bytes."""
     if ws is None:
-        ws = torch.empty(need(), dtype=torch.uint8, device=device)
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
     else:
         _req(ws, "ws", torch.uint8)
         if ws.device != device:
@@ -560,15 +560,18 @@ def _ws(ws, need, device):
 def _window_args(q, k, v, window, sinks, scale, op, ws, dims):
     """Checks q, k and v; returns (device, addresses, shape, workspace)."""
     qs = _dims(q, "q", dims)
-    ks = _dims(k, "k" if dims == 4 else "k_cache", 4)
+    nk, nv = ("k", "v") if dims == 4 else ("k_cache", "v_cache")
+    B, S, Hkv, _ = _dims(k, nk, 4)
+    Hq, D = qs[-2:]
     dev = q.device
-    n = ("q", "k", "v") if dims == 4 else ("q", "k_cache", "v_cache")
-    want = (ks[0], ks[1], qs[2], qs[3]) if dims == 4 else (ks[0], qs[1], qs[2])
-    kv = (ks[0], ks[1], ks[2], qs[-1])
-    ptrs = (_ask(q, n[0], torch.bfloat16, want, dev), _ask(k, n[1], torch.bfloat16, kv, dev),
-            _ask(v, n[2], torch.bfloat16, kv, dev))
-    shape = make_window_shape(q, k, window, sinks, scale)
-    return dev, ptrs, shape, lambda: msa_window_workspace_size(shape, op)
+    if not q.is_cuda:
+        raise MSAError("q must be a CUDA tensor")
+    kv = (B, S, Hkv, D)
+    ptrs = (_ask(q, "q", torch.bfloat16, (B, S, Hq, D) if dims == 4 else (B, Hq, D), dev),
+            _ask(k, nk, torch.bfloat16, kv, dev), _ask(v, nv, torch.bfloat16, kv, dev))
+    window, sinks, scale = _int32(window, "window"), _int32(sinks, "sinks"), float(scale)
+    need = _window_bytes(op, B, S, Hq, Hkv, D, window, sinks, scale) if ws is None else 0
+    return dev, ptrs, WindowShape(B, S, Hq, Hkv, D, window, sinks, scale), need
 
 
 def msa_window_forward(q, k, v, window: int, sinks: int, scale: float, ws=None):
@@ -655,7 +658,7 @@ def _rows(t, name, B=None, N=None, H=None, write=False):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     shape = t.shape
-    if not (t.is_cuda and t.dtype is torch.bfloat16 and len(shape) == 4 and shape[3] == 128):
+    if t.dtype is not torch.bfloat16 or len(shape) != 4 or shape[3] != 128 or not t.is_cuda:
         if not t.is_cuda:
             raise MSAError(f"{name} must be a CUDA tensor")
         if t.dtype != torch.bfloat16:
@@ -685,6 +688,10 @@ def _rows(t, name, B=None, N=None, H=None, write=False):
     return ptr, sb, st
 
 
+_X_NAMES = [f"xs[{i}]" for i in range(ROPE_PARTS)]
+_W_NAMES = [f"weights[{i}]" for i in range(ROPE_PARTS)]
+
+
 def _device_of(xs):
     if not xs or not isinstance(xs[0], torch.Tensor):
         raise TypeError("xs must be a sequence of tensors")
@@ -710,13 +717,12 @@ def _rope_args(xs, weights, rotate, inv_freq, interleaved, eps, positions, dev):
         raise MSAError(f"{count} tensors, {len(weights)} weights, {len(rotate)} rotate flags")
     B, N = (xs[0].shape[0], xs[0].shape[1]) if xs[0].dim() == 4 else (None, None)
     parts = []
-    for i in range(count):
-        x, w = xs[i], weights[i]
-        at = _rows(x, f"xs[{i}]", B, N)
+    for x, w, turn, nx, nw in zip(xs, weights, rotate, _X_NAMES, _W_NAMES):
+        at = _rows(x, nx, B, N)
         if x.device != dev:
-            _on(x, f"xs[{i}]", dev)
-        wp = 0 if w is None else _ask(w, f"weights[{i}]", torch.float32, (128,), dev)
-        parts.append((at, wp, x.shape[2], ROPE_ROTATE if rotate[i] else 0))
+            _on(x, nx, dev)
+        parts.append((at, 0 if w is None else _ask(w, nw, torch.float32, (128,), dev), x.shape[2],
+                      ROPE_ROTATE if turn else 0))
     rotary, fp, pp = 0, None, None
     if inv_freq is not None:
         fp = _ask(inv_freq, "inv_freq", torch.float32, tuple(_dims(inv_freq, "inv_freq", 1)), dev)
@@ -786,7 +792,7 @@ def msa_norm_rope_backward(xs, weights, dys, inv_freq, positions=None, eps: floa
             rows.append(_PART.pack(*at, *dy, *dx, w, dw + 512 * i if w else 0, h, f))
             if not w:
                 out_w[i] = None
-        wp, wn, ws = _ws(ws, lambda: _rope_bytes(n, OP_NORM_ROPE_BACKWARD), dev)
+        wp, wn, ws = _ws(ws, _rope_bytes(n, OP_NORM_ROPE_BACKWARD), dev)
         rc = load_library().msa_norm_rope_backward(ctypes.byref(shape), b"".join(rows), n, pp, fp, wp,
                                                    wn, _stream_of(dev))
     if rc:
@@ -806,7 +812,9 @@ def msa_norm_rope_append(xs, weights, inv_freq, seq_len, caches, eps: float = 1e
     msa_window_decode.  Sequences with a length outside N .. S are skipped (msa_device_status of ws
     tells)."""
     dev = _device_of(xs)
-    x4 = [x.unsqueeze(1) if isinstance(x, torch.Tensor) and x.dim() == 3 else x for x in xs]
+    x4 = xs
+    if xs[0].dim() == 3:
+        x4 = [x.unsqueeze(1) if isinstance(x, torch.Tensor) and x.dim() == 3 else x for x in xs]
     shape, parts, fp, _ = _rope_args(x4, weights, rotate, inv_freq, interleaved, eps, None, dev)
     B = shape.B
     sp = _ask(seq_len, "seq_len", torch.int32, (B,), dev)
@@ -833,7 +841,7 @@ def msa_norm_rope_append(xs, weights, inv_freq, seq_len, caches, eps: float = 1e
                 outs.append(c)
             rows.append(_PART.pack(*at, *to, 0, 0, 0, w, 0, h, f))
         shape.capacity = 2 ** 31 - 1 if capacity is None else capacity
-        wp, wn, ws = _ws(ws, lambda: _rope_bytes(len(rows), OP_NORM_ROPE_APPEND), dev)
+        wp, wn, ws = _ws(ws, _rope_bytes(len(rows), OP_NORM_ROPE_APPEND), dev)
         rc = load_library().msa_norm_rope_append(ctypes.byref(shape), b"".join(rows), len(rows), sp, fp,
                                                  wp, wn, _stream_of(dev))
     if rc:

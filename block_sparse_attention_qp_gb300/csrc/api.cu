@@ -1086,8 +1086,7 @@ int msa_window_forward(const msa_window_shape_t* shape, const void* q, const voi
   if ((rc = check_ws_bytes(win_plan(d, MSA_OP_WINDOW_FORWARD).bytes, workspace, workspace_bytes))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaGetLastError();
-  unsigned* status = at<unsigned>(workspace, 0);
-  cudaMemsetAsync(status, 0, 32 * sizeof(unsigned), st);  // status, counters, wait place
+  unsigned* status = at<unsigned>(workspace, 0);  // cleared by the first kernel
   bool ok = true;
   timed("win_fwd", st, [&] { ok = launch_win_fwd(d, q, k, v, o, lse, status, st); });
   if (!ok) {
@@ -1108,8 +1107,7 @@ int msa_window_backward(const msa_window_shape_t* shape, const void* q, const vo
   if ((rc = check_ws_bytes(p.bytes, workspace, workspace_bytes))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaGetLastError();
-  unsigned* status = at<unsigned>(workspace, 0);
-  cudaMemsetAsync(status, 0, 32 * sizeof(unsigned), st);  // status, counters, wait place
+  unsigned* status = at<unsigned>(workspace, 0);  // cleared by the first kernel
   Dims rows{};
   rows.B = d.B;
   rows.S = d.S;
@@ -1118,8 +1116,8 @@ int msa_window_backward(const msa_window_shape_t* shape, const void* q, const vo
   bool ok = true;
   const float2* rowm = at<float2>(workspace, p.rowm);
   float* part = at<float>(workspace, p.part);
-  timed("win_dkv", st, [&] { ok = launch_win_dkv(d, q, k, v, dout, rowm, dk, dv, part, status, st); });
-  if (ok) timed("win_dq", st, [&] { ok = launch_win_dq(d, q, k, v, dout, rowm, dq, status, st); });
+  timed("win_dq", st, [&] { ok = launch_win_dq(d, q, k, v, dout, rowm, dq, status, st); });
+  if (ok) timed("win_dkv", st, [&] { ok = launch_win_dkv(d, q, k, v, dout, rowm, dk, dv, part, status, st); });
   if (ok && win_items(d).join_blocks)
     timed("win_join", st, [&] { ok = launch_win_join(d, part, dk, dv, st); });
   if (!ok) {
@@ -1140,8 +1138,7 @@ int msa_window_decode(const msa_window_shape_t* shape, const void* q, const void
   if ((rc = check_ws_bytes(p.bytes, workspace, workspace_bytes))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaGetLastError();
-  unsigned* status = at<unsigned>(workspace, 0);
-  cudaMemsetAsync(status, 0, 32 * sizeof(unsigned), st);  // status, counters, wait place
+  unsigned* status = at<unsigned>(workspace, 0);  // cleared by the first kernel
   bool ok = true;
   timed("win_decode", st, [&] {
     ok = launch_win_decode(d, q, k_cache, v_cache, seq_len, o, lse, at<float>(workspace, p.opart),

@@ -519,6 +519,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dq_kernel(const __grid_con
   uint8_t* sR = sD + kTile;
   const uint32_t aQ = smem_u32(sQ), aD = smem_u32(sD), aR = smem_u32(sR);
   const int tid = threadIdx.x, lane = tid % 32, warp = warp_number();
+  clear_status(A.status);  // also the item counter of win_dkv_kernel, which runs behind this kernel
 
   if (tid == 0) {
     mbar_init(&sh->q_full, 1);

@@ -70,11 +70,14 @@ __global__ void __launch_bounds__(kDecThreads, kDecBlocks) win_decode_kernel(con
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int split = blockIdx.x % A.nsplit, bg = blockIdx.x / A.nsplit;
   const int b = bg / d.Hkv, g = bg % d.Hkv;
-  const int len = A.seq_len[b];
-  if (len < 1 || len > d.S) {
-    if (tid == 0) atomicOr(A.status, kStatusBadIndex);
-    return;
+  if (blockIdx.x == 0) {  // the status word whole (see clear_status): clear, or a length out of range
+    int bad = 0;
+    for (int x = tid; x < d.B; x += kDecThreads) bad |= A.seq_len[x] < 1 || A.seq_len[x] > d.S;
+    bad = __syncthreads_or(bad);
+    if (tid < 32) A.status[tid] = tid == 0 && bad ? kStatusBadIndex : 0u;
   }
+  const int len = A.seq_len[b];
+  if (len < 1 || len > d.S) return;
   const int t = len - 1;
   const KeyRun run = key_run(d, t, t);
   const int n0 = split * A.tiles, n1 = min(n0 + A.tiles, run.nb), ntile = n1 - n0;

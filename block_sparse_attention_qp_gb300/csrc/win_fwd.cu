@@ -91,6 +91,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) win_fwd_kernel(const __grid_co
   const uint32_t aQ = smem_u32(sQ), aR = smem_u32(sR);
   const int tid = threadIdx.x, lane = tid % 32, warp = warp_number();
   const float sl2 = d.scale * kLog2e;
+  clear_status(A.status);
   if (aQ & 1023u) {  // the swizzled operand layout needs 1024-byte atoms
     if (tid == 0) atomicOr(A.status, kStatusInternal);
     return;

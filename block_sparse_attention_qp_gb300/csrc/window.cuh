@@ -62,6 +62,12 @@ struct KeyMaps {
 };
 bool make_key_maps(const WinDims& d, const void* base, KeyMaps* m);  // win_fwd.cu
 
+// The status area is cleared by the first block of a call's first kernel instead of a memset in front
+// of it: a flag another block sets (a wait that gave up) is set 200 ms later at the earliest.
+__device__ __forceinline__ void clear_status(unsigned* status) {
+  if (blockIdx.x == 0 && threadIdx.x < 32) status[threadIdx.x] = 0u;
+}
+
 // Lets a kernel use `bytes` of dynamic shared memory: once per kernel and device (the attribute
 // belongs to the device's context; a repeated call costs a microsecond of every launch).
 template <auto* Kernel>
