@@ -21,7 +21,6 @@ What stands around sparse attention in a model:
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 import os
@@ -478,12 +477,22 @@ def msa_warmup_func(Q_proxy, K_proxy, Q, K, V, top_k: int, scale: float):
 # ---------------------------------------------------------------- sliding-window attention
 # The entry points below serve single tokens too, where the host's part of a call counts: arguments are
 # looked at once by a fast test, and only a failing one is taken apart for its message.
-_NO_GUARD = contextlib.nullcontext()
+class _Guard:
+    """Makes a device current for a block (torch.cuda.device costs microseconds even where it is)."""
+    __slots__ = ("device", "entered")
 
+    def __init__(self, device):
+        self.device = device
 
-def _guard(device):
-    """Context with `device` current (entering one costs microseconds: none where it is already)."""
-    return _NO_GUARD if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    def __enter__(self):
+        self.entered = None
+        if torch.cuda.current_device() != self.device.index:
+            self.entered = torch.cuda.device(self.device)
+            self.entered.__enter__()
+
+    def __exit__(self, *exc):
+        if self.entered is not None:
+            self.entered.__exit__(*exc)
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -578,7 +587,7 @@ def msa_window_forward(q, k, v, window: int, sinks: int, scale: float, ws=None):
     """Causal GQA attention of every query over the last ``window`` tokens (itself included) and the
     first ``sinks`` tokens.  q [B, S, Hq, 128], k, v [B, S, Hkv, 128], any S.  Returns (o, lse)."""
     dev, ptrs, shape, need = _window_args(q, k, v, window, sinks, scale, OP_WINDOW_FORWARD, ws, 4)
-    with _guard(dev):
+    with _Guard(dev):
         wp, wn, ws = _ws(ws, need, dev)
         o = torch.empty_like(q)
         lse = torch.empty((shape.B, shape.Hq, shape.S), dtype=torch.float32, device=dev)
@@ -595,7 +604,7 @@ def msa_window_backward(q, k, v, o, lse, dout, window: int, sinks: int, scale: f
     op = _ask(o, "o", torch.bfloat16, q.shape, dev)
     lp = _ask(lse, "lse", torch.float32, (shape.B, shape.Hq, shape.S), dev)
     dp = _ask(dout, "dout", torch.bfloat16, q.shape, dev)
-    with _guard(dev):
+    with _Guard(dev):
         wp, wn, ws = _ws(ws, need, dev)
         dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
         rc = load_library().msa_window_backward(ctypes.byref(shape), *ptrs, op, lp, dp, dq.data_ptr(),
@@ -612,7 +621,7 @@ def msa_window_decode(q, k_cache, v_cache, seq_len, window: int, sinks: int, sca
     dev, ptrs, shape, need = _window_args(q, k_cache, v_cache, window, sinks, scale, OP_WINDOW_DECODE,
                                           ws, 3)
     sp = _ask(seq_len, "seq_len", torch.int32, (shape.B,), dev)
-    with _guard(dev):
+    with _Guard(dev):
         wp, wn, ws = _ws(ws, need, dev)
         o = torch.empty_like(q)
         lse = torch.empty((shape.B, shape.Hq), dtype=torch.float32, device=dev)
@@ -678,7 +687,7 @@ def _rows(t, name, B=None, N=None, H=None, write=False):
     ptr = t.data_ptr()
     if sb % 8 or st % 8 or ptr % 16:
         raise MSAError(f"{name} must be 16-byte aligned, batch and token strides multiples of 8")
-    if write:
+    if write and (st != h * 128 or sb != n * st):
         need = h * 128  # a token's rows; no two tokens may share memory
         for stride, count in sorted(((sb, b), (st, n))):
             if count > 1:
@@ -757,7 +766,7 @@ def msa_norm_rope_forward(xs, weights, inv_freq, positions=None, eps: float = 1e
     A tensor without weight and rotation is copied.  Returns contiguous tensors [B, N, heads, 128]."""
     dev = _device_of(xs)
     shape, parts, fp, pp = _rope_args(xs, weights, rotate, inv_freq, interleaved, eps, positions, dev)
-    with _guard(dev):
+    with _Guard(dev):
         ys = [torch.empty(x.shape, dtype=torch.bfloat16, device=dev) for x in xs]
         packed = b"".join([_PART.pack(*at, *_strides(y), 0, 0, 0, w, 0, h, f)
                            for (at, w, h, f), y in zip(parts, ys)])
@@ -778,7 +787,7 @@ def msa_norm_rope_backward(xs, weights, dys, inv_freq, positions=None, eps: floa
     n = len(xs)
     if len(dys) != n or (dxs is not None and len(dxs) != n):
         raise MSAError("one dy (and dx, where given) per tensor")
-    with _guard(dev):
+    with _Guard(dev):
         # one tensor for the weights' gradients: a row each
         dws = torch.empty((n, 128), dtype=torch.float32, device=dev)
         out_w, rows, dw = list(dws.unbind(0)), [], dws.data_ptr()
@@ -821,7 +830,7 @@ def msa_norm_rope_append(xs, weights, inv_freq, seq_len, caches, eps: float = 1e
     if len(caches) != len(x4):
         raise MSAError("one cache (or None) per tensor")
     capacity = None
-    with _guard(dev):
+    with _Guard(dev):
         outs, rows = [], []
         for i, (at, w, h, f) in enumerate(parts):
             c = caches[i]
