@@ -604,32 +604,35 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dq_kernel(const __grid_con
     {
       // step i: key tile n of unit nu, whose K is in ring slot k (its V in the one after)
       Ring<kRingQ> k;
-      auto mma_s = [&](const Ring<kRingQ>& k, bool first, bool last, int nu) -> bool {
+      auto mma_s = [&](const Ring<kRingQ>& k, bool first, bool last, int nu, int keys) -> bool {
         if (first && !mbar_wait_warp(&sh->q_full, phase_of(nu), A.status)) return false;
         if (!mbar_wait_warp(&sh->kv_full[k.slot], k.phase, A.status)) return false;
         fence_after_sync();
-        mma_kk(SB, aQ, aR + k.slot * kTile, false);  // S = Q K^T
+        if (keys >= kBlock) mma_kk(SB, aQ, aR + k.slot * kTile, false);  // S = Q K^T
+        else mma_kk_part(SB, aQ, aR + k.slot * kTile, keys);
         warp_mma_commit(&sh->s_full);
         if (last) warp_mma_commit(&sh->q_empty);
         return true;
       };
       // (V's slot is freed by the softmax, which sees dP first: a commit less)
-      auto mma_dp = [&](Ring<kRingQ> k, bool first, bool last, int nu) -> bool {
+      auto mma_dp = [&](Ring<kRingQ> k, bool first, bool last, int nu, int keys) -> bool {
         k.next();
         if (first && !mbar_wait_warp(&sh->do_full, phase_of(nu), A.status)) return false;
         if (!mbar_wait_warp(&sh->kv_full[k.slot], k.phase, A.status)) return false;
         fence_after_sync();
-        mma_kk(DP, aD, aR + k.slot * kTile, false);  // dP = dO V^T
+        if (keys >= kBlock) mma_kk(DP, aD, aR + k.slot * kTile, false);  // dP = dO V^T
+        else mma_kk_part(DP, aD, aR + k.slot * kTile, keys);
         warp_mma_commit(&sh->dp_full);
         if (last) warp_mma_commit(&sh->do_empty);
         return true;
       };
       int u = blockIdx.x;
-      int nb = dq_unit<G>(d, u).run.nb, i = 0;
-      bool ok = mma_s(k, true, nb == 1, 0) && mma_dp(k, true, nb == 1, 0);
+      int len = dq_unit<G>(d, u).run.len, nb = (len + kBlock - 1) / kBlock, i = 0;
+      bool ok = mma_s(k, true, nb == 1, 0, len) && mma_dp(k, true, nb == 1, 0, len);
       for (int nu = 0; ok && nb > 0; ++nu) {
         u += gridDim.x;
-        const int nb2 = u < A.units ? dq_unit<G>(d, u).run.nb : 0;  // of the next unit (0: none)
+        const int len2 = u < A.units ? dq_unit<G>(d, u).run.len : 0;  // of the next unit (0: none)
+        const int nb2 = (len2 + kBlock - 1) / kBlock;
         for (int n = 0; n < nb; ++n, ++i) {
           const bool last = n + 1 == nb;
           Ring<kRingQ> k2 = k;
@@ -637,26 +640,29 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dq_kernel(const __grid_con
           k2.next();
           if (last) k2.next();  // the tile dQ leaves through
           const bool more = !last || nb2 > 0, last2 = last ? nb2 == 1 : n + 2 == nb;
+          const int keys = len - n * kBlock, keys2 = last ? len2 : keys - kBlock;  // from this tile, the next on
           // phase A has read S
-          if (!mbar_wait_warp(&sh->pa, phase_of(i), A.status) || (more && !mma_s(k2, last, last2, nu + 1))) {
+          if (!mbar_wait_warp(&sh->pa, phase_of(i), A.status) || (more && !mma_s(k2, last, last2, nu + 1, keys2))) {
             ok = false;
             break;
           }
           // phase B has read dP and written dS: dP of the next step first, dQ behind it (dS of step
           // i + 2 is written only after dP of step i + 2, issued after this product, is there)
-          if (!mbar_wait_warp(&sh->pb, phase_of(i), A.status) || (more && !mma_dp(k2, last, last2, nu + 1)) ||
+          if (!mbar_wait_warp(&sh->pb, phase_of(i), A.status) || (more && !mma_dp(k2, last, last2, nu + 1, keys2)) ||
               // (the epilogue of the previous unit has read its dQ: it comes before phase B of this one)
               (n == 0 && nu >= 1 && !mbar_wait_warp(&sh->dq_free, phase_of(nu - 1), A.status))) {
             ok = false;
             break;
           }
           fence_after_sync();
-          mma_tn<8, 0>(RQ, DS + 64 * (i & 1), aR + k.slot * kTile, n > 0);  // dQ += dS K
+          if (keys >= kBlock) mma_tn<8, 0>(RQ, DS + 64 * (i & 1), aR + k.slot * kTile, n > 0);  // dQ += dS K
+          else mma_tn_part<8, 0>(RQ, DS + 64 * (i & 1), aR + k.slot * kTile, n > 0, keys);
           warp_mma_commit(&sh->kv_empty[k.slot]);
           if (last) warp_mma_commit(&sh->dq_full);
           k = k2;
         }
         nb = nb2;
+        len = len2;
       }
       warp_mma_commit(&sh->mma_done);
       mbar_wait_warp(&sh->mma_done, 0, A.status);  // no product may still write tensor memory

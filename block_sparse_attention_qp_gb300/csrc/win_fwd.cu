@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) win_fwd_kernel(const __grid_co
       uint32_t v_phase = 0;
       bool ok = true;
       // O_X += P_X V for the last S product of tile X
-      auto mma_o = [&](int X, bool first, bool last, bool free_v) -> bool {
+      auto mma_o = [&](int X, bool first, bool last, bool free_v, int keys) -> bool {
         if (!mbar_wait_warp(&sh->p_full[X], phase_of(cs[X] - 1), A.status)) return false;
         if (first) {
           if (cu[X] > 0 && !mbar_wait_warp(&sh->o_free[X], phase_of(cu[X] - 1), A.status)) return false;
@@ -176,14 +176,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1) win_fwd_kernel(const __grid_co
         }
         if (!mbar_wait_warp(&sh->kv_full[v_slot], v_phase, A.status)) return false;
         fence_after_sync();
-        mma_tn<4, 64>(O0 + 128 * X, S0 + 128 * X, aR + v_slot * kTile, !first);
+        if (keys >= kBlock) mma_tn<4, 64>(O0 + 128 * X, S0 + 128 * X, aR + v_slot * kTile, !first);
+        else mma_tn_part<4, 64>(O0 + 128 * X, S0 + 128 * X, aR + v_slot * kTile, !first, keys);
         if (last) warp_mma_commit(&sh->o_full[X]);
         if (free_v) warp_mma_commit(&sh->kv_empty[v_slot]);
         return true;
       };
-      auto mma_s = [&](int X, uint32_t q, int kslot, bool free_k) {
+      auto mma_s = [&](int X, uint32_t q, int kslot, bool free_k, int keys) {
         fence_after_sync();
-        mma_kk(S0 + 128 * X, q + X * kTile, aR + kslot * kTile, false);  // S = Q K^T
+        if (keys >= kBlock) mma_kk(S0 + 128 * X, q + X * kTile, aR + kslot * kTile, false);  // S = Q K^T
+        else mma_kk_part(S0 + 128 * X, q + X * kTile, aR + kslot * kTile, keys);
         warp_mma_commit(&sh->s_full[X]);
         if (free_k) warp_mma_commit(&sh->kv_empty[kslot]);
         ++cs[X];
@@ -195,14 +197,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1) win_fwd_kernel(const __grid_co
         const uint32_t q = aQ + qs * 2 * kTile;
         if (!mbar_wait_warp(&sh->q_full[qs], phase_of(nu >> 1), A.status)) break;
         for (int n = 0; n < x.run.nb; ++n) {
-          const int kslot = kv.slot;
-          if (n > 0 && !mma_o(0, n == 1, false, !x.two)) { ok = false; break; }
+          const int kslot = kv.slot, keys = x.run.keys(n);
+          if (n > 0 && !mma_o(0, n == 1, false, !x.two, kBlock)) { ok = false; break; }
           // (K_n is waited for behind O_A(n-1): its load began when O_B(n-2) freed a slot)
           if (!mbar_wait_warp(&sh->kv_full[kslot], kv.phase, A.status)) { ok = false; break; }
-          mma_s(0, q, kslot, !x.two);
+          mma_s(0, q, kslot, !x.two, keys);
           if (x.two) {
-            if (n > 0 && !mma_o(1, n == 1, false, true)) { ok = false; break; }
-            mma_s(1, q, kslot, true);
+            if (n > 0 && !mma_o(1, n == 1, false, true, kBlock)) { ok = false; break; }
+            mma_s(1, q, kslot, true, keys);
           }
           kv.next();
           v_slot = kv.slot;
@@ -210,7 +212,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) win_fwd_kernel(const __grid_co
           kv.next();
         }
         if (!ok) break;
-        ok = mma_o(0, x.run.nb == 1, true, !x.two) && (!x.two || mma_o(1, x.run.nb == 1, true, true));
+        const int rest = x.run.keys(x.run.nb - 1);
+        ok = mma_o(0, x.run.nb == 1, true, !x.two, rest) && (!x.two || mma_o(1, x.run.nb == 1, true, true, rest));
       }
       warp_mma_commit(&sh->mma_done);
       mbar_wait_warp(&sh->mma_done, 0, A.status);  // no product may still write tensor memory

@@ -23,6 +23,7 @@ struct KeyRun {
   int nsp;  // virtual rows of the sink part (0: the parts meet, the walk starts at key 0)
   int len;  // virtual keys
   int nb;   // 128-key tiles
+  __device__ __forceinline__ int keys(int n) const { return len - n * kBlock; }  // of tile n and behind
   int f0, f1;  // tiles f0 .. f1 (none if f0 > f1) are seen whole by every query of the run
 };
 __device__ __forceinline__ KeyRun key_run(const WinDims& d, int t0, int t1) {
@@ -188,6 +189,23 @@ __device__ __forceinline__ void mma_tn(uint32_t d, uint32_t a, uint32_t b_tile, 
 #pragma unroll
   for (int ks = 1; ks < 8; ++ks)
     warp_mma_ts(d, a + (ks / kRun) * kPitch + (ks % kRun) * 8, b + step_mn(ks), id, true);
+}
+// The same for a tile of `keys` < 128: N of the scores and K of the other product rounded up to 16.
+// (A run's keys seldom fill its last tile: at window 512 and 8 heads a group 23 or 39 of 128.)
+__device__ __forceinline__ void mma_kk_part(uint32_t d, uint32_t a_tile, uint32_t b_tile, int keys) {
+  constexpr uint32_t id = sm100::idesc_bf16(128, 0, false, false);
+  const uint32_t a = desc_lo_k(a_tile), b = desc_lo_k(b_tile), idn = id | (uint32_t)((keys + 15) / 16 * 2) << 17;
+#pragma unroll
+  for (int ks = 0; ks < 8; ++ks) warp_mma_ss(d, a + step_k(ks), b + step_k(ks), idn, ks > 0);
+}
+template <int kRun, int kPitch>
+__device__ __forceinline__ void mma_tn_part(uint32_t d, uint32_t a, uint32_t b_tile, bool acc, int keys) {
+  constexpr uint32_t id = sm100::idesc_bf16(128, 128, false, true);
+  const uint32_t b = desc_lo_mn(b_tile);
+  warp_mma_ts(d, a, b, id, acc);
+#pragma unroll
+  for (int ks = 1; ks < 8; ++ks)
+    if (16 * ks < keys) warp_mma_ts(d, a + (ks / kRun) * kPitch + (ks % kRun) * 8, b + step_mn(ks), id, true);
 }
 // This thread's warp number, as a value the compiler knows to be the same in the whole warp.
 __device__ __forceinline__ int warp_number() { return __shfl_sync(0xffffffffu, threadIdx.x / 32, 0); }
