@@ -741,6 +741,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dq_kernel(const __grid_con
       const int t = x.t0 + r / G;
       const float2 nl2 = make_float2(-m.x, -m.x), nd2 = make_float2(-m.y * d.scale, -m.y * d.scale);
       for (int n = 0; n < x.run.nb; ++n, ++i) {
+        if (n > 0 && x.run.keys(n) <= 32 * part) {  // a run's last tile that ends before this part
+          if (!mbar_wait_warp(&sh->s_full, phase_of(i), A.status)) { ok = false; break; }
+          if (lane == 0) mbar_arrive(&sh->pa);
+          if (!mbar_wait_warp(&sh->dp_full, phase_of(i), A.status)) { ok = false; break; }
+          if (lane == 0) mbar_arrive(&sh->pb);
+          continue;
+        }
         const bool full = n >= x.run.f0 && n <= x.run.f1;
         uint32_t vis = 0xffffffffu;
         if (!full) {
