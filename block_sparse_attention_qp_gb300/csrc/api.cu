@@ -1108,13 +1108,18 @@ int msa_window_backward(const msa_window_shape_t* shape, const void* q, const vo
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaGetLastError();
   unsigned* status = at<unsigned>(workspace, 0);  // cleared by the first kernel
-  Dims rows{};
-  rows.B = d.B;
-  rows.S = d.S;
-  rows.Hq = d.Hq;
-  timed("bwd_rowdot", st, [&] { launch_bwd_rowdot(rows, o, dout, lse, at<float2>(workspace, p.rowm), st); });
+  float2* rowdata = at<float2>(workspace, p.rowm);
+  if (d.W + d.ns <= kFewKeys) {
+    timed("win_rowdata", st, [&] { launch_win_rowdata(d, q, k, v, dout, lse, rowdata, st); });
+  } else {
+    Dims rows{};
+    rows.B = d.B;
+    rows.S = d.S;
+    rows.Hq = d.Hq;
+    timed("bwd_rowdot", st, [&] { launch_bwd_rowdot(rows, o, dout, lse, rowdata, st); });
+  }
   bool ok = true;
-  const float2* rowm = at<float2>(workspace, p.rowm);
+  const float2* rowm = rowdata;
   float* part = at<float>(workspace, p.part);
   timed("win_dq", st, [&] { ok = launch_win_dq(d, q, k, v, dout, rowm, dq, status, st); });
   if (ok) timed("win_dkv", st, [&] { ok = launch_win_dkv(d, q, k, v, dout, rowm, dk, dv, part, status, st); });

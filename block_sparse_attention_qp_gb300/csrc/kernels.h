@@ -201,6 +201,10 @@ struct WinItems {
   int items, partials, join_blocks;         // partial slots (2 x 128 x 128 fp32); blocks to join
 };
 WinItems win_items(const WinDims& d);
+// Row data of windows of at most kFewKeys keys and sinks, in place of launch_bwd_rowdot.
+constexpr int kFewKeys = 8;
+void launch_win_rowdata(const WinDims& d, const void* q, const void* k, const void* v, const void* dout,
+                        const float* lse, float2* rowm, cudaStream_t st);
 // dk, dv and dq from rowm (launch_bwd_rowdot); dk, dv of split key blocks go to `part`
 // (win_items(d).partials slots) and are added by the join.
 bool launch_win_dkv(const WinDims& d, const void* q, const void* k, const void* v, const void* dout,

@@ -1,6 +1,6 @@
 // Backward of causal attention over a sliding window and the first tokens (geometry: window.cuh), on
 // the tcgen05 tensor cores.  With P = exp(scale QK^T - LSE) over the visible pairs, dP = dO V^T and
-// D = rowsum(dO O) (rowdot_kernel in bwd.cu):
+// D = rowsum(dO O) (rowdot_kernel in bwd.cu; windows of a few keys: win_rowdata_kernel):
 //   dS = scale P (dP - D),  dV = P^T dO,  dK = dS^T Q,  dQ = dS K.
 //
 // Two kernels, each with its sums in tensor memory and no atomics, so a gradient has the same bits
@@ -440,6 +440,46 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dkv_kernel(const __grid_co
   if (warp == 0) tmem_dealloc(sh->tmem, 512);
 }
 
+// Row data {LSE log2 e, D} of windows of a few keys, D = sum_j P_j dP_j over them: one warp per query
+// row, four dims a lane.  D taken from the stored O (bf16) is off by 2^-9 of |dO| |O| at worst, which the
+// gradients of rows with two or four keys feel as much as their own rounding (relative error of dQ at
+// window 2: 2.7e-3 from O, 2.4e-3 so); with more keys O, and with it the error, shrinks.
+__global__ void win_rowdata_kernel(WinDims d, const bf16* __restrict__ q, const bf16* __restrict__ k,
+                                   const bf16* __restrict__ v, const bf16* __restrict__ dout,
+                                   const float* __restrict__ lse, float2* __restrict__ rowm) {
+  const long long rows = (long long)d.B * d.S * d.Hq, step = (long long)gridDim.x * blockDim.x / 32;
+  const int lane = threadIdx.x % 32;
+  auto load = [&](const bf16* x, long long row, float (&f)[4]) {
+    const uint2 w = *reinterpret_cast<const uint2*>(x + row * kD + 4 * lane);
+    f[0] = __uint_as_float(w.x << 16);
+    f[1] = __uint_as_float(w.x & 0xffff0000u);
+    f[2] = __uint_as_float(w.y << 16);
+    f[3] = __uint_as_float(w.y & 0xffff0000u);
+  };
+  auto dot = [](const float (&a)[4], const float (&b)[4]) {
+    float s = a[0] * b[0] + a[1] * b[1] + (a[2] * b[2] + a[3] * b[3]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    return s;
+  };
+  for (long long r = ((long long)blockIdx.x * blockDim.x + threadIdx.x) / 32; r < rows; r += step) {
+    const int h = (int)(r % d.Hq), t = (int)(r / d.Hq % d.S), b = (int)(r / d.Hq / d.S);
+    const float l2 = lse[((long long)b * d.Hq + h) * d.S + t] * kLog2e;
+    const int w0 = t - d.W + 1 > 0 ? t - d.W + 1 : 0, far = d.ns < w0 ? d.ns : w0;  // sinks before the window
+    float fq[4], fo[4], sum = 0.f;
+    load(q, r, fq);
+    load(dout, r, fo);
+    for (int x = 0; x < far + t - w0 + 1; ++x) {
+      const long long key = ((long long)b * d.S + (x < far ? x : w0 + x - far)) * d.Hkv + h / d.G;
+      float fk[4], fv[4];
+      load(k, key, fk);
+      load(v, key, fv);
+      sum = fmaf(exp2_ftz(dot(fq, fk) * d.scale * kLog2e - l2), dot(fo, fv), sum);
+    }
+    if (lane == 0) rowm[r] = make_float2(l2, sum);
+  }
+}
+
 // dK and dV rows of the key blocks whose query tiles were split: their partials added in order.  One
 // block per 8 rows of (key block, b, g) and tensor; 32 threads a row, four values each.
 template <int G>
@@ -851,6 +891,13 @@ WinItems win_items(const WinDims& d) {
     case 16: CALL(16); break;  \
     default: return false;     \
   }
+
+void launch_win_rowdata(const WinDims& d, const void* q, const void* k, const void* v, const void* dout,
+                        const float* lse, float2* rowm, cudaStream_t st) {
+  const long long blocks = ((long long)d.B * d.S * d.Hq + 7) / 8, most = (long long)num_sms() * 8;
+  win_rowdata_kernel<<<(int)(blocks < most ? blocks : most), 256, 0, st>>>(
+      d, (const bf16*)q, (const bf16*)k, (const bf16*)v, (const bf16*)dout, lse, rowm);
+}
 
 bool launch_win_dkv(const WinDims& d, const void* q, const void* k, const void* v, const void* dout,
                     const float2* rowm, void* dk, void* dv, float* part, unsigned* status, cudaStream_t st) {

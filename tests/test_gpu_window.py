@@ -83,6 +83,18 @@ def test_backward(B, S, Hq, Hkv, W, ns):
         assert rel <= REL_L2 or min(S, W) <= 2, (name, rel)
 
 
+@pytest.mark.parametrize("W,ns,S", [(2, 0, 300), (3, 1, 300), (8, 0, 300), (5, 3, 300), (7, 1, 129), (900, 0, 8)])
+def test_backward_of_a_few_keys(W, ns, S):
+    """Rows of a few keys: D from P and dP instead of the rounded O.  What is left are the roundings of dS and of
+    the result (dV: of P and of the result), each uniform within half a step of 2^-8 at worst and so at most
+    2^-8 / sqrt(3) in the root mean square: 2^-8 sqrt(2 / 3) = 3.2e-3 together (2.4e-3 over all mantissas)."""
+    q, k, v, do = tensors(2, S, 8, 2, seed=40)
+    o, lse = forward(q, k, v, W, ns)
+    want = plain.window(q, k, v, W, ns, SCALE, do)
+    for name, got in zip(("dq", "dk", "dv"), backward(q, k, v, o, lse, do, W, ns)):
+        assert plain.check(name, got, want[name]) <= 2 ** -8 * (2 / 3) ** 0.5
+
+
 @pytest.mark.parametrize("scale,size", [(1.0, 1.0), (0.02, 3.0)])
 def test_sharp_and_flat_softmax(scale, size):
     """Scores up to about +-60 (the running maximum moves, rows are rescaled) and nearly uniform ones."""
