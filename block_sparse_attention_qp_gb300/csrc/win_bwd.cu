@@ -17,20 +17,20 @@
 // win_dkv: ... S(i+1) | dV(i) dK(i) dP(i+1) ...: S(i+1) is issued once S(i) is in registers, the rest
 // after phase B of tile i, running behind phase A of tile i+1.  P^T and dS^T (bf16) take dP^T's columns
 // in tensor memory and are the products' A operands from there; P^T over S^T, with dV(i) before S(i+1),
-// made phase A, dV and S one chain of 2,600 cycles a tile against the products' 2,048.
+// made phase A, dV and S one chain (2.09 ms at 64K tokens, and 1.87 once P^T had moved).
 // win_dq:  ... S(n+1) | dP(n+1) dQ(n) ...: S(n+1) is issued once S(n) is in registers, the pair after
 // phase B of tile n, which leaves dS in columns of its own (two buffers), so that dP(n+1) need not
 // wait for dQ(n).
 // P and dS are rounded to bf16 for their products (2^-9 relative each), the softmax scale is folded
-// into dS, everything else is fp32.  Bound by the tensor core: 32 (dkv) and 24 (dq) instructions of
-// 128 x 128 x 16 a tile pair, about 83 cycles each.
+// into dS, everything else is fp32.  32 (dkv) and 24 (dq) instructions of 128 x 128 x 16 a tile pair, 64
+// to 67 cycles each: at 64K tokens, 64 / 8 heads, window 512 dkv takes 1.90 ms (1,160 TFLOP/s of its four
+// products over visible pairs) and dq 1.59 ms (1,040 of its three).
 //
 // Roles of both (640 threads): warp 0 TMA loads, warp 1 MMA issue (two issuing warps interleaved the
 // products of a chain with the other's and were slower), warp 2 the tile's row data (dkv) or the TMA
 // stores of dQ (dq), warps 4-19 softmax and epilogue: four per tensor-memory lane quarter,
 // one per 32 of the tile's columns (with two, a phase was bound by the latencies of a warp's loads and
-// exponentials: 2,400 cycles a tile of win_dkv against the 2,656 of its products).  Every wait is
-// bounded.
+// exponentials).  Every wait is bounded.
 #include <math.h>
 
 #include "tmap.h"
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dkv_kernel(const __grid_co
   if (warp == 0) {
     // ---------------------------------------------------------------- items + TMA loads
     if (lane == 0) {
-      long long nk = 0, i = 0;  // items with tiles, tiles
+      long long nk = 0, i = 0, nq = 0;  // items with tiles, tiles, query tiles asked for
       Ring<kQRing> q;
       bool ok = true;
       for (long long k = 0; ok; ++k) {
@@ -200,6 +200,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dkv_kernel(const __grid_co
           mbar_expect_tx(&sh->q_full[q.slot], kTile);
           for (int c = 0; c < 2; ++c)
             tma_load_rows(sQ + q.slot * kTile + c * (kTile / 2), &A.q, 64 * c, t.g * G, tok, t.b, &sh->q_full[q.slot]);
+          ++nq;
           if (i >= 2 && !mbar_wait(&sh->do_empty[s], phase_of(i / 2 - 1), A.status)) { ok = false; break; }
           mbar_expect_tx(&sh->do_full[s], kTile);
           for (int c = 0; c < 2; ++c)
@@ -211,7 +212,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dkv_kernel(const __grid_co
         mbar_wait(&sh->k_full, phase_of(nk - 1), A.status);
         mbar_wait(&sh->v_full, phase_of(nk - 1), A.status);
       }
-      for (long long x = i >= kQRing ? i - kQRing : 0; x < i; ++x)
+      for (long long x = nq >= kQRing ? nq - kQRing : 0; x < nq; ++x)
         mbar_wait(&sh->q_full[x % kQRing], phase_of(x / kQRing), A.status);
       for (long long x = i >= 2 ? i - 2 : 0; x < i; ++x) mbar_wait(&sh->do_full[x & 1], phase_of(x >> 1), A.status);
     }
@@ -594,7 +595,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dq_kernel(const __grid_con
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA loads
     if (lane == 0) {
-      long long nl = 0, nu = 0;
+      long long nl = 0, nu = 0, nq = 0, nd = 0;  // ring entries, units, loads of Q and dO
       Ring<kRingQ> ring;
       auto taken = [&]() -> bool {  // the next ring slot is free
         return !ring.wrapped || mbar_wait(&sh->kv_empty[ring.slot], ring.phase ^ 1, A.status);
@@ -614,6 +615,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dq_kernel(const __grid_con
         mbar_expect_tx(&sh->q_full, kTile);
         for (int c = 0; c < 2; ++c)
           tma_load_rows(sQ + c * (kTile / 2), &A.q, 64 * c, x.g * G, x.t0, x.b, &sh->q_full);
+        ++nq;
         for (int n = 0; n < x.run.nb && ok; ++n) {
           if (!(ok = load(A.k, x, n))) break;
           if (n == 0) {
@@ -621,6 +623,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dq_kernel(const __grid_con
             mbar_expect_tx(&sh->do_full, kTile);
             for (int c = 0; c < 2; ++c)
               tma_load_rows(sD + c * (kTile / 2), &A.dout, 64 * c, x.g * G, x.t0, x.b, &sh->do_full);
+            ++nd;
           }
           ok = load(A.v, x, n);
         }
@@ -629,14 +632,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dq_kernel(const __grid_con
         ring.next();
         ++nl;
       }
-      // no copy may still be landing in shared memory when the block exits (after a wait that gave
-      // up, the last loads of Q and dO are waited for by their own phase only as far as issued)
+      // no copy may still be landing in shared memory when the block exits
       for (long long x = nl >= kRingQ ? nl - kRingQ : 0; x < nl; ++x)
         mbar_wait(&sh->kv_full[x % kRingQ], phase_of(x / kRingQ), A.status);
-      if (ok && nu > 0) {
-        mbar_wait(&sh->q_full, phase_of(nu - 1), A.status);
-        mbar_wait(&sh->do_full, phase_of(nu - 1), A.status);
-      }
+      if (nq > 0) mbar_wait(&sh->q_full, phase_of(nq - 1), A.status);
+      if (nd > 0) mbar_wait(&sh->do_full, phase_of(nd - 1), A.status);
     }
     __syncwarp();
   } else if (warp == 1) {

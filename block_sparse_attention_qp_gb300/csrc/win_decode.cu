@@ -7,6 +7,8 @@
 //   thread = key: tile maximum per head (warp reductions, then four values through shared memory),
 //   P = 2^(sl2 S - m) -> bf16, [16 heads][128 keys] in shared memory; row sums per thread
 //   O_n^T = V_n^T P^T    (tensor core, 128 dims x 16), added to the running O (thread = dim)
+// 128 sequences with windows of 1024, 64 / 8 heads: 97 us under ncu, 595 MB read (6.15 TB/s) for the 535
+// that are visible, the rest being the ninth tiles' other keys.
 // 73 KB of shared memory leave three blocks to an SM: the loads of two run behind the chain of the
 // third, and a block's next K tile is loaded as soon as S^T is there, its next V after O_n^T.
 // Keys that no head may see (behind the sequence's end, before the window, between the sinks and the
@@ -326,7 +328,9 @@ __global__ void __launch_bounds__(kJoinThreads) win_decode_join_kernel(int B, in
   if (lane == 0) lse[row] = (mx + log2f(sum)) * kLn2;
 }
 
-// Splits of the key tiles: as many as fill the resident blocks, one where the (b, KV head) pairs do.
+// Splits of the key tiles: as many as fill the resident blocks, one where the (b, KV head) pairs do (1024
+// pairs of nine tiles, 2.25 waves: 100 us whole, 117 in two parts, 119 in three or four; 8 pairs of 257 tiles
+// in 52 parts: 29 us and 8 of joining, while whole they would use 8 SMs).
 WinSplit win_decode_split(const WinDims& d) {
   WinSplit w;
   const long long keys = (long long)d.W + d.nsp < d.S ? (long long)d.W + d.nsp : d.S;

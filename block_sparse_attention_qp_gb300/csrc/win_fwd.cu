@@ -14,16 +14,19 @@
 // rounding of O itself; the row sum l is taken from the fp32 values.  Keys outside a row's window get
 // P = 0 exactly.  A row may see nothing of a tile (its maximum then stays -inf until it does).
 //
-// Bound by the tensor core: 4 x 128 flops a visible pair, and the tiles cost about
-// (W + 256/G + 128) / W of that; K and V come through L2.  The order of products is
+// 4 x 128 flops a visible pair, and the tiles cost about (W + 256/G + 128) / W of that; K and V come
+// through L2.  1,430 TFLOP/s of visible pairs at 32K tokens, 32 / 8 heads, window 2048 (746 us), 990 at 64K
+// tokens, 64 / 8 heads, window 512 (1.11 ms), where the tiles hold 1.2 times the visible pairs.  Bound by
+// the hand-offs of the chain S, softmax, P V of a tile: without exponentials, loads and seven of eight
+// products an earlier form took 690 of its 840 us.  The order of products is
 // O_A(n-1) S_A(n) O_B(n-1) S_B(n), so the softmax of one tile runs behind the products of the other.
 // Q has two buffers, so a unit's loads and first products overlap the previous unit's end; O leaves
 // through the unit's own Q buffer by TMA stores, which also drop the rows past the sequence.
 //
 // Roles (640 threads): warp 0 TMA loads, warp 1 MMA issue, warps 2 / 3 the TMA stores of tile A / B,
 // warps 4-11 / 12-19 softmax and epilogue of tile A / B: a row belongs to two threads, one per half of
-// the columns, so that a tile's softmax (with one thread a row it took 3,000 cycles, longer than the
-// other tile's products) fits behind the products.  The two share the row maximum: a barrier that ORs
+// the columns, so that a tile's softmax fits behind the other tile's products (one thread a row: 1,126 us
+// at 32K tokens, two: 1,012, both before the later steps).  The two share the row maximum: a barrier that ORs
 // "my half exceeds it" across them, and an exchange through shared memory in the rare case it does.
 // Tensor memory: S_A, S_B, O_A, O_B (512 columns).  Units have equal cost but for the sequence's first window: they are dealt in turn,
 // tokens outermost, so that concurrent units share K and V.  Every wait is bounded.
@@ -129,7 +132,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) win_fwd_kernel(const __grid_co
     // ---------------------------------------------------------------- TMA loads
     if (lane == 0) {
       bool ok = true;
-      long long nl = 0, nu = 0;
+      long long nl = 0, nu = 0, nq = 0;  // K / V loads, units, units whose Q was asked for
       Ring<kRing> kv;
       for (int u = blockIdx.x; u < A.units && ok; u += gridDim.x, ++nu) {
         const FwdUnit x = fwd_unit<G>(A, u);
@@ -141,6 +144,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) win_fwd_kernel(const __grid_co
           for (int c = 0; c < 2; ++c)
             tma_load_rows(dq + X * kTile + c * (kTile / 2), &A.q, 64 * c, x.g * G, x.t0 + X * TT, x.b,
                           &sh->q_full[qs]);
+        ++nq;
         for (int n = 0; n < x.run.nb && ok; ++n)
           for (int w = 0; w < 2; ++w, ++nl, kv.next()) {  // K_n, then V_n
             if (kv.wrapped && !mbar_wait(&sh->kv_empty[kv.slot], kv.phase ^ 1, A.status)) {
@@ -154,7 +158,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) win_fwd_kernel(const __grid_co
       // no copy may still be landing in shared memory when the block exits
       for (long long x = nl >= kRing ? nl - kRing : 0; x < nl; ++x)
         mbar_wait(&sh->kv_full[x % kRing], phase_of(x / kRing), A.status);
-      for (long long x = nu >= 2 ? nu - 2 : 0; x < nu; ++x)
+      for (long long x = nq >= 2 ? nq - 2 : 0; x < nq; ++x)
         mbar_wait(&sh->q_full[x & 1], phase_of(x >> 1), A.status);
     }
     __syncwarp();
