@@ -732,6 +732,13 @@ int check_rope(const msa_rope_shape_t* s, const msa_rope_part_t* parts, int npar
       set_err("strides must be multiples of 8 elements");
       return MSA_ERR_INVALID_ARG;
     }
+    for (int j = 0; j < i; ++j) {
+      const msa_rope_part_t& e = parts[j];
+      if (bwd ? p.dx == e.dx || (p.dweight && p.dweight == e.dweight) : p.y == e.y) {
+        set_err("two parts with the same output");
+        return MSA_ERR_INVALID_ARG;
+      }
+    }
     o.x = static_cast<const bf16*>(p.x);
     o.xb = p.x_batch;
     o.xt = p.x_token;
@@ -1194,7 +1201,10 @@ int msa_norm_rope_backward(const msa_rope_shape_t* shape, const msa_rope_part_t*
   cudaGetLastError();
   a.status = at<unsigned>(workspace, 0);
   a.partial = at<float>(workspace, kRopeStatus);
-  timed("norm_rope_bwd", st, [&] { launch_norm_rope_bwd(a, st); }, 2);
+  int launches = 1;  // and one more to join the partials of the weights' gradients, where any is wanted
+  for (int i = 0; i < nparts; ++i)
+    if (a.p[i].dw) launches = 2;
+  timed("norm_rope_bwd", st, [&] { launch_norm_rope_bwd(a, st); }, launches);
   return cuda_fail("msa_norm_rope_backward");
 }
 

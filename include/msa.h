@@ -256,6 +256,7 @@ MSA_API int msa_window_decode(const msa_window_shape_t* shape, const void* q, co
  *         (2 i, 2 i + 1) -- by the angle position * inv_freq[i]   (without MSA_ROPE_ROTATE: y = u)
  * rotary: a multiple of 16, 0 .. 128.  inv_freq: rotary / 2 floats on the device.  positions: int32
  * [B, N] on the device, any value, or NULL for 0 .. N - 1.  Angles are exact to fp32 at every position.
+ * No two parts of a call may have the same output (y; backward: dx, dweight).
  */
 enum msa_rope_flags {
   MSA_ROPE_ROTATE = 1, /* rotate this part */

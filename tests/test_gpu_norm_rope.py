@@ -211,6 +211,123 @@ def test_append_skips_bad_lengths():
     plain.check("q", out[0][1:2], plain.norm_rope(xs[0][1:2], ws[0], pos, f, False, 1e-6)["y"])
 
 
+def test_append_refuses_one_cache_twice():
+    x, xs, _ = make(1, 1, [2, 2], seed=60)
+    kc = rnd(1, 64, 2, 128, seed=61)
+    old = kc.clone()
+    n = torch.ones(1, dtype=torch.int32, device=DEV)
+    with pytest.raises(msa.MSAError, match="same output"):
+        msa.msa_norm_rope_append(xs, None, None, n, [kc, kc])
+    assert torch.equal(kc, old)
+
+
+def test_backward_launches():
+    """The join of the weights' gradients runs only where there is one; without it dx is dy turned back."""
+    x, xs, dys = make(2, 9, [4, 2], seed=62)
+    lib, f = msa.load_library(), freqs(64)
+    count = []
+    for w in ([None, None], [weight(1), None]):
+        before = lib.msa_launch_count()
+        dxs, dws = msa.msa_norm_rope_backward(xs, w, dys, f)
+        count.append(lib.msa_launch_count() - before)
+        assert [g is None for g in dws] == [v is None for v in w]
+    assert count == [1, 2]
+
+
+def test_append_graph_follows_lengths():
+    """One captured append and window step replayed while the sequences grow: each replay writes the
+    lengths' rows and no others, and attends to them."""
+    B, cap, W, ns, scale = 3, 400, 60, 4, 128 ** -0.5
+    f, ws, rotate = freqs(128), layer_params(70), [True, True, False, True, True]
+    kc, vc, pc = caches(B, cap, 2, seed=63)
+    x = rnd(B, sum(HEADS), 128, seed=64)
+    n = torch.tensor([5, 100, 300], dtype=torch.int32, device=DEV)
+
+    def step():
+        q, _, _, _, _ = msa.msa_norm_rope_append(list(x.split(HEADS, 1)), ws, f, n, [None, kc, vc, None, pc], rotate=rotate)
+        return (q,) + msa.msa_window_decode(q, kc, vc, n, W, ns, scale)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q, o, lse = step()
+    for i, lens in enumerate(([6, 101, 301], [7, 102, 302], [400, 1, 399])):
+        x.copy_(rnd(B, sum(HEADS), 128, seed=65 + i))
+        n.copy_(torch.tensor(lens, dtype=torch.int32))
+        before = [t.clone() for t in (kc, vc, pc)]
+        graph.replay()
+        torch.cuda.synchronize()
+        pos = n.long()[:, None] - 1
+        xs = [t.unsqueeze(1) for t in x.split(HEADS, 1)]
+        at = (torch.arange(B, device=DEV), pos[:, 0])
+        for j, row in ((0, q), (1, kc[at]), (2, vc[at]), (4, pc[at].unsqueeze(1))):
+            want = plain.norm_rope(xs[j], ws[j], pos, f if rotate[j] else None, False, 1e-6)["y"]
+            plain.check(f"part {j}", row.unsqueeze(1), want)
+        want = plain.window_decode(q, kc, vc, lens, W, ns, scale)
+        plain.check("o", o, want["o"])
+        plain.check("lse", lse, want["lse"])
+        for c, old in zip((kc, vc, pc), before):
+            now = c.clone()
+            now[at] = old[at]
+            assert torch.equal(now, old)
+
+
+def test_append_and_decode_on_two_streams():
+    """Two requests' steps at once, each with caches of its own: the same bits as one after the other."""
+    B, cap, W, ns, scale = 4, 2000, 700, 4, 128 ** -0.5
+    f, ws, rotate = freqs(128), layer_params(80), [True, True, False, True, True]
+    n = torch.tensor([2000, 900, 1, 1300], dtype=torch.int32, device=DEV)
+    xs = [rnd(B, sum(HEADS), 128, seed=81 + i) for i in range(2)]
+
+    def step(i, kv):
+        q, _, _, _, _ = msa.msa_norm_rope_append(list(xs[i].split(HEADS, 1)), ws, f, n, [None, kv[0], kv[1], None, kv[2]],
+                                                 rotate=rotate)
+        return (q,) + msa.msa_window_decode(q, kv[0], kv[1], n, W, ns, scale)
+
+    want = []
+    for i in range(2):
+        kv = caches(B, cap, 2, seed=90 + 3 * i)
+        want.append(step(i, kv) + tuple(kv))
+    kvs = [caches(B, cap, 2, seed=90 + 3 * i) for i in range(2)]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [None, None]
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i] = step(i, kvs[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(a, b) for a, b in zip(want[i], got[i] + tuple(kvs[i])))
+
+
+def test_long_caches():
+    """Caches of more than 2^31 elements: the last rows of the last sequence are written and read."""
+    B, cap, H, W, ns, scale = 3, 1 << 20, 8, 500, 4, 128 ** -0.5
+    kc, vc = (torch.zeros(B, cap, H, 128, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    assert kc.numel() > 2 ** 31
+    lens = [cap, 7, cap - 1]
+    n = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    for b, m in enumerate(lens):
+        for j, c in enumerate((kc, vc)):
+            c[b, max(0, m - 600):m - 1] = rnd(m - 1 - max(0, m - 600), H, 128, seed=100 + 2 * b + j)
+            c[b, :4] = rnd(4, H, 128, seed=110 + 2 * b + j)
+    x = rnd(B, 3 * H, 128, seed=120)
+    f, ws, rotate = freqs(128), [weight(1), weight(2), None], [True, True, False]
+    q, _, _ = msa.msa_norm_rope_append(list(x.split(H, 1)), ws, f, n, [None, kc, vc], rotate=rotate)
+    pos = n.long()[:, None] - 1
+    at = (torch.arange(B, device=DEV), pos[:, 0])
+    xs = [t.unsqueeze(1) for t in x.split(H, 1)]
+    for j, row in enumerate((q, kc[at], vc[at])):
+        want = plain.norm_rope(xs[j], ws[j], pos, f if rotate[j] else None, False, 1e-6)["y"]
+        plain.check(f"part {j}", row.unsqueeze(1), want)
+    assert not kc[1, 7:].any() and not kc[2, cap - 1].any() and not vc[0, 4:cap - 600].any()
+    o, lse = msa.msa_window_decode(q, kc, vc, n, W, ns, scale)
+    want = plain.window_decode(q, kc, vc, lens, W, ns, scale)
+    plain.check("o", o, want["o"])
+    plain.check("lse", lse, want["lse"])
+
+
 # ------------------------------------------------------------------------------------------ together
 HEADS = [16, 2, 2, 2, 1]  # q, k, v, qp, kp
 

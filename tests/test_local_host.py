@@ -191,3 +191,20 @@ def test_rope_binding_refusals():
         msa.msa_norm_rope_forward([], [], None)
     with pytest.raises(TypeError):
         msa.msa_norm_rope_append([None], [None], None, x, [None])
+
+
+def test_rope_outputs_are_distinct(lib):
+    """One cache (or gradient) given for two parts would be written by both."""
+    s = ctypes.byref(rope_shape())
+    two = lambda **kw: (msa.RopePart * 2)(part(), part(**kw))  # noqa: E731
+    a = part()
+    other = dict(y=a.y + 4096, dx=a.dx + 4096, dweight=a.dweight + 4096)
+    for clash in ("y", "dx", "dweight"):
+        parts = two(**{k: v for k, v in other.items() if k != clash})
+        if clash == "y":  # backward only reads it
+            assert lib.msa_norm_rope_forward(s, parts, 2, A, A, NULL) == 1
+            assert b"same output" in lib.msa_last_error()
+            assert lib.msa_norm_rope_append(s, parts, 2, A, A, A, 1 << 40, NULL) == 1
+        else:
+            assert lib.msa_norm_rope_backward(s, parts, 2, A, A, A, 1 << 40, NULL) == 1
+        assert b"same output" in lib.msa_last_error()
