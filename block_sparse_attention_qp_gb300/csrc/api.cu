@@ -1116,7 +1116,7 @@ int msa_window_backward(const msa_window_shape_t* shape, const void* q, const vo
   cudaGetLastError();
   unsigned* status = at<unsigned>(workspace, 0);  // cleared by the first kernel
   float2* rowdata = at<float2>(workspace, p.rowm);
-  if (d.W + d.ns <= kFewKeys) {
+  if (d.G == 1 && d.W + d.ns <= kFewKeys) {
     timed("win_rowdata", st, [&] { launch_win_rowdata(d, q, k, v, dout, lse, rowdata, st); });
   } else {
     Dims rows{};
@@ -1126,10 +1126,9 @@ int msa_window_backward(const msa_window_shape_t* shape, const void* q, const vo
     timed("bwd_rowdot", st, [&] { launch_bwd_rowdot(rows, o, dout, lse, rowdata, st); });
   }
   bool ok = true;
-  const float2* rowm = rowdata;
   float* part = at<float>(workspace, p.part);
-  timed("win_dq", st, [&] { ok = launch_win_dq(d, q, k, v, dout, rowm, dq, status, st); });
-  if (ok) timed("win_dkv", st, [&] { ok = launch_win_dkv(d, q, k, v, dout, rowm, dk, dv, part, status, st); });
+  timed("win_dq", st, [&] { ok = launch_win_dq(d, q, k, v, dout, rowdata, dq, status, st); });
+  if (ok) timed("win_dkv", st, [&] { ok = launch_win_dkv(d, q, k, v, dout, rowdata, dk, dv, part, status, st); });
   if (ok && win_items(d).join_blocks)
     timed("win_join", st, [&] { ok = launch_win_join(d, part, dk, dv, st); });
   if (!ok) {

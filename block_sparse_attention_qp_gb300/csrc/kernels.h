@@ -201,16 +201,18 @@ struct WinItems {
   int items, partials, join_blocks;         // partial slots (2 x 128 x 128 fp32); blocks to join
 };
 WinItems win_items(const WinDims& d);
-// Row data of windows of at most kFewKeys keys and sinks, in place of launch_bwd_rowdot.
-constexpr int kFewKeys = 8;
+// Row data of one-head groups' windows of at most kFewKeys keys and sinks, in place of
+// launch_bwd_rowdot (larger groups' rows of a few keys lie in one key tile: launch_win_dq).
+constexpr int kFewKeys = 32;
 void launch_win_rowdata(const WinDims& d, const void* q, const void* k, const void* v, const void* dout,
                         const float* lse, float2* rowm, cudaStream_t st);
 // dk, dv and dq from rowm (launch_bwd_rowdot); dk, dv of split key blocks go to `part`
 // (win_items(d).partials slots) and are added by the join.
 bool launch_win_dkv(const WinDims& d, const void* q, const void* k, const void* v, const void* dout,
                     const float2* rowm, void* dk, void* dv, float* part, unsigned* status, cudaStream_t st);
+// (launch_win_dq comes first: where a query tile's keys fit one key tile it replaces D in rowm.)
 bool launch_win_dq(const WinDims& d, const void* q, const void* k, const void* v, const void* dout,
-                   const float2* rowm, void* dq, unsigned* status, cudaStream_t st);
+                   float2* rowm, void* dq, unsigned* status, cudaStream_t st);
 bool launch_win_join(const WinDims& d, const float* part, void* dk, void* dv, cudaStream_t st);
 
 // Decode step over caches of capacity d.S: key tiles per split and splits; opart [nsplit][B][Hq][128],

@@ -1,6 +1,6 @@
 // Backward of causal attention over a sliding window and the first tokens (geometry: window.cuh), on
 // the tcgen05 tensor cores.  With P = exp(scale QK^T - LSE) over the visible pairs, dP = dO V^T and
-// D = rowsum(dO O) (rowdot_kernel in bwd.cu; windows of a few keys: win_rowdata_kernel):
+// D = rowsum(dO O) (rowdot_kernel in bwd.cu), for rows of few keys sum P dP (see win_dq_kernel):
 //   dS = scale P (dP - D),  dV = P^T dO,  dK = dS^T Q,  dQ = dS K.
 //
 // Two kernels, each with its sums in tensor memory and no atomics, so a gradient has the same bits
@@ -441,42 +441,57 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dkv_kernel(const __grid_co
   if (warp == 0) tmem_dealloc(sh->tmem, 512);
 }
 
-// Row data {LSE log2 e, D} of windows of a few keys, D = sum_j P_j dP_j over them: one warp per query
-// row, four dims a lane.  D taken from the stored O (bf16) is off by 2^-9 of |dO| |O| at worst, which the
-// gradients of rows with two or four keys feel as much as their own rounding (relative error of dQ at
-// window 2: 2.7e-3 from O, 2.4e-3 so); with more keys O, and with it the error, shrinks.
+// Row data {LSE log2 e, D} of windows of a few keys where a group is one head (a query tile is then 128
+// tokens and spans two key tiles), D = sum_j P_j dP_j: one warp per query row, four keys at a time, eight
+// lanes a key, 16 dims a lane.
 __global__ void win_rowdata_kernel(WinDims d, const bf16* __restrict__ q, const bf16* __restrict__ k,
                                    const bf16* __restrict__ v, const bf16* __restrict__ dout,
                                    const float* __restrict__ lse, float2* __restrict__ rowm) {
   const long long rows = (long long)d.B * d.S * d.Hq, step = (long long)gridDim.x * blockDim.x / 32;
-  const int lane = threadIdx.x % 32;
-  auto load = [&](const bf16* x, long long row, float (&f)[4]) {
-    const uint2 w = *reinterpret_cast<const uint2*>(x + row * kD + 4 * lane);
-    f[0] = __uint_as_float(w.x << 16);
-    f[1] = __uint_as_float(w.x & 0xffff0000u);
-    f[2] = __uint_as_float(w.y << 16);
-    f[3] = __uint_as_float(w.y & 0xffff0000u);
-  };
-  auto dot = [](const float (&a)[4], const float (&b)[4]) {
-    float s = a[0] * b[0] + a[1] * b[1] + (a[2] * b[2] + a[3] * b[3]);
+  const int lane = threadIdx.x % 32, c = lane % 8, kk = lane / 8;
+  auto load = [&](const bf16* x, long long row, float (&f)[16]) {  // dims 8 c .. and 64 + 8 c ..
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    for (int y = 0; y < 2; ++y) {
+      const uint4 w = *reinterpret_cast<const uint4*>(x + row * kD + 64 * y + 8 * c);
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        f[8 * y + 2 * e] = __uint_as_float(u[e] << 16);
+        f[8 * y + 2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+      }
+    }
+  };
+  auto dot = [](const float (&a)[16], const float (&b)[16]) {
+    float s = 0.f, t = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      s = fmaf(a[e], b[e], s);
+      t = fmaf(a[e + 1], b[e + 1], t);
+    }
+    s += t;
+#pragma unroll
+    for (int off = 4; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
     return s;
   };
   for (long long r = ((long long)blockIdx.x * blockDim.x + threadIdx.x) / 32; r < rows; r += step) {
     const int h = (int)(r % d.Hq), t = (int)(r / d.Hq % d.S), b = (int)(r / d.Hq / d.S);
     const float l2 = lse[((long long)b * d.Hq + h) * d.S + t] * kLog2e;
     const int w0 = t - d.W + 1 > 0 ? t - d.W + 1 : 0, far = d.ns < w0 ? d.ns : w0;  // sinks before the window
-    float fq[4], fo[4], sum = 0.f;
+    const int keys = far + t - w0 + 1;
+    float fq[16], fo[16], sum = 0.f;
     load(q, r, fq);
     load(dout, r, fo);
-    for (int x = 0; x < far + t - w0 + 1; ++x) {
+    for (int x0 = 0; x0 < keys; x0 += 4) {
+      const int x = x0 + kk < keys ? x0 + kk : keys - 1;  // past the end: the last key, not counted
       const long long key = ((long long)b * d.S + (x < far ? x : w0 + x - far)) * d.Hkv + h / d.G;
-      float fk[4], fv[4];
+      float fk[16], fv[16];
       load(k, key, fk);
       load(v, key, fv);
-      sum = fmaf(exp2_ftz(dot(fq, fk) * d.scale * kLog2e - l2), dot(fo, fv), sum);
+      const float p = exp2_ftz(dot(fq, fk) * d.scale * kLog2e - l2), dp = dot(fo, fv);
+      if (x0 + kk < keys) sum = fmaf(p, dp, sum);
     }
+    sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 16);
     if (lane == 0) rowm[r] = make_float2(l2, sum);
   }
 }
@@ -518,13 +533,13 @@ struct DqArgs {
   WinDims d;
   KeyMaps k, v;
   CUtensorMap q, dout, dq;
-  const float2* rowm;
+  float2* rowm;
   unsigned* status;
   int units;  // one 128-row tile each
 };
 struct DqShared {
   uint64_t q_full, q_empty, do_full, do_empty, kv_full[kRingQ], kv_empty[kRingQ], s_full, dp_full, pa, pb,
-      dq_full, dq_free, st_full, mma_done;
+      d_full, dq_full, dq_free, st_full, mma_done;
   uint32_t tmem;
 };
 struct DqUnit {
@@ -545,6 +560,12 @@ __device__ __forceinline__ DqUnit dq_unit(const WinDims& d, int u) {
 }
 }  // namespace
 
+// D of rows of few keys: taken from the stored O it carries the roundings of P and of O, 2^-9 of
+// |dO| |O| each, which raises the relative error of dQ and dK by about sqrt(1 + 2.7 / n) for n keys (1.10
+// at 12, 1.05 at 24) over that of rounding dS and the result.  A unit whose keys fit one tile therefore
+// takes D from P and dP, which it holds anyway, and leaves it for win_dkv_kernel: every row of up to 32
+// keys in groups of two heads and more, and the first 128 / G tokens of every sequence.
+//
 // One unit is one 128-row query tile.  The ring holds, in this order, K_0 V_0 K_1 V_1 .. of a unit and
 // then one tile without a load, through which the unit's dQ leaves.  Q and dO have one buffer each:
 // the next unit's Q is loaded once the last S product has read it, its dO after the last dP product,
@@ -575,6 +596,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dq_kernel(const __grid_con
     mbar_init(&sh->dp_full, 1);
     mbar_init(&sh->pa, kSoft);
     mbar_init(&sh->pb, kSoft);
+    mbar_init(&sh->d_full, kSoft);
     mbar_init(&sh->dq_full, 1);
     mbar_init(&sh->dq_free, kSoft);
     mbar_init(&sh->st_full, kSoft);
@@ -738,8 +760,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dq_kernel(const __grid_con
       if (u >= A.units) return make_float2(0.f, 0.f);
       const DqUnit x = dq_unit<G>(d, u);
       const int t = x.t0 + r / G;
-      return t < d.S ? __ldg(A.rowm + ((long long)x.b * d.S + t) * d.Hq + x.g * G + r % G)
-                     : make_float2(0.f, 0.f);
+      // (a plain load: the kernel itself replaces the D of other rows of it)
+      return t < d.S ? A.rowm[((long long)x.b * d.S + t) * d.Hq + x.g * G + r % G] : make_float2(0.f, 0.f);
     };
     // dQ of unit number `nu` (ring entry `nl`): tensor memory -> bf16 rows of the swizzled tile
     auto epilogue = [&](int nu, long long nl) -> bool {
@@ -772,14 +794,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dq_kernel(const __grid_con
       return true;
     };
     long long nl = 0, pending = -1;  // pending: ring entry of the last unit's dQ
-    int i = 0, nu = 0, v_slot = 1;
+    int i = 0, nu = 0, v_slot = 1, singles = 0;  // singles: units of one key tile
     float2 m = row_data(blockIdx.x);
     bool ok = true;
     for (int u = blockIdx.x; u < A.units && ok; u += gridDim.x, ++nu) {
       const DqUnit x = dq_unit<G>(d, u);
       const float2 mnext = row_data(u + gridDim.x);
       const int t = x.t0 + r / G;
-      const float2 nl2 = make_float2(-m.x, -m.x), nd2 = make_float2(-m.y * d.scale, -m.y * d.scale);
+      const float2 nl2 = make_float2(-m.x, -m.x);
+      float2 nd2 = make_float2(-m.y * d.scale, -m.y * d.scale);
       for (int n = 0; n < x.run.nb; ++n, ++i) {
         if (n > 0 && x.run.keys(n) <= 32 * part) {  // a run's last tile that ends before this part
           if (!mbar_wait_warp(&sh->s_full, phase_of(i), A.status)) { ok = false; break; }
@@ -828,6 +851,33 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dq_kernel(const __grid_con
           uint32_t rp[32], dw[16];
           tmem_ld32(DP + lb + 32 * part, rp);
           tmem_wait_ld();
+          if (x.run.nb == 1) {
+            // D = sum P dP, here and for win_dkv_kernel: the row's four threads meet in columns of dP
+            // that their own warps have read.  Columns behind the run's keys hold anything (the products
+            // leave them out), so the sum picks those with a P; a factor of 0 would not silence a NaN.
+            float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              s0 = fmaf(p[e], p[e] > 0.f ? __uint_as_float(rp[e]) : 0.f, s0);
+              s1 = fmaf(p[e + 1], p[e + 1] > 0.f ? __uint_as_float(rp[e + 1]) : 0.f, s1);
+            }
+            tmem_st1(DP + lb + 32 * part, __float_as_uint(s0 + s1));
+            tmem_wait_st();
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->d_full);
+            if (!mbar_wait_warp(&sh->d_full, phase_of(singles++), A.status)) { ok = false; break; }
+            fence_after_sync();
+            uint32_t c4[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) c4[c] = tmem_ld1(DP + lb + 32 * c);
+            tmem_wait_ld();
+            const float dd = (__uint_as_float(c4[0]) + __uint_as_float(c4[1])) +
+                             (__uint_as_float(c4[2]) + __uint_as_float(c4[3]));
+            if (part == 0 && t < d.S)
+              A.rowm[((long long)x.b * d.S + t) * d.Hq + x.g * G + r % G] = make_float2(m.x, dd);
+            nd2 = make_float2(-dd * d.scale, -dd * d.scale);
+          }
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const float2 y = fmul2(
@@ -924,7 +974,7 @@ bool launch_win_dkv(const WinDims& d, const void* q, const void* k, const void* 
 }
 
 bool launch_win_dq(const WinDims& d, const void* q, const void* k, const void* v, const void* dout,
-                   const float2* rowm, void* dq, unsigned* status, cudaStream_t st) {
+                   float2* rowm, void* dq, unsigned* status, cudaStream_t st) {
   DqArgs a;
   const int tt = kBlock / d.G, n = num_sms();
   if (!make_tmap_rows(&a.q, q, d.B, d.S, d.Hq, d.G, tt) || !make_tmap_rows(&a.dout, dout, d.B, d.S, d.Hq, d.G, tt) ||
