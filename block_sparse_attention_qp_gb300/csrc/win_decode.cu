@@ -5,7 +5,10 @@
 // one (b, KV head) and a run of 128-key tiles of the virtual walk; per tile
 //   S^T = K_n Q^T        (tensor core, 128 keys x 16: the G query heads, the rest zero)
 //   thread = key: tile maximum per head (warp reductions, then four values through shared memory),
-//   P = 2^(sl2 S - m) -> bf16, [16 heads][128 keys] in shared memory; row sums per thread
+//   P = 2^(sl2 S - m) -> bf16, [16 heads][128 keys] in shared memory; row sums per thread.  The rows that
+//   a group of up to eight heads leaves over take P's rounding errors as a second bf16, in the same
+//   product: O then has its own rounding only (relative error 1.7e-3; one bf16 P, as groups of 16 heads
+//   have it, 2.2e-3)
 //   O_n^T = V_n^T P^T    (tensor core, 128 dims x 16), added to the running O (thread = dim)
 // 128 sequences with windows of 1024, 64 / 8 heads: 97 us under ncu, 595 MB read (6.15 TB/s) for the 535
 // that are visible, the rest being the ninth tiles' other keys.
@@ -175,6 +178,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecBlocks) win_decode_kernel(con
     __syncwarp();
   } else {
     // ---------------------------------------------------------------- softmax, accumulation
+    constexpr bool kResidual = 2 * G <= kNH;
     const int kr = tid;  // key row of S^T; head dimension of O^T (tensor-memory lane)
     const uint32_t lrow = static_cast<uint32_t>(warp * 32) << 16;
     const float sl2 = d.scale * kLog2e;
@@ -222,7 +226,10 @@ __global__ void __launch_bounds__(kDecThreads, kDecBlocks) win_decode_kernel(con
         m[h] = mn;
         const float p = exp2_ftz(x[h] - mn);  // masked: 2^-inf = 0
         l[h] = l[h] * alpha[h] + p;
-        *reinterpret_cast<bf16*>(sP + prow + sw128_offset(h, kr & 63)) = __float2bfloat16_rn(p);
+        const bf16 hi = __float2bfloat16_rn(p);
+        *reinterpret_cast<bf16*>(sP + prow + sw128_offset(h, kr & 63)) = hi;
+        if (kResidual)
+          *reinterpret_cast<bf16*>(sP + prow + sw128_offset(G + h, kr & 63)) = __float2bfloat16_rn(p - __bfloat162float(hi));
       }
       if (ok) ok = mbar_wait_warp(&sh->v_full, phase_of(i), A.status);
       if (!vis) {
@@ -241,7 +248,10 @@ __global__ void __launch_bounds__(kDecThreads, kDecBlocks) win_decode_kernel(con
         tmem_wait_ld();
       }
 #pragma unroll
-      for (int h = 0; h < G; ++h) acc[h] = fmaf(acc[h], alpha[h], __uint_as_float(s[h]));
+      for (int h = 0; h < G; ++h) {
+        const float y = __uint_as_float(s[h]);
+        acc[h] = fmaf(acc[h], alpha[h], kResidual ? y + __uint_as_float(s[(G + h) % 16]) : y);
+      }
       fence_before_sync();
     }
 #pragma unroll

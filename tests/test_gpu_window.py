@@ -351,6 +351,19 @@ def test_decode(B, cap, Hq, Hkv, W, ns, lens):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("Hq,Hkv,B,cap", [(8, 8, 40, 500), (16, 8, 40, 500), (64, 8, 20, 700), (16, 2, 2, 20000)])
+def test_decode_rounds_once(Hq, Hkv, B, cap):
+    """Groups of up to eight heads keep P to 2^-17: the error of o is that of rounding the 64-bit result, within 1
+    percent (the second order of 2^-8; fp32 moves few values across a boundary).  P as one bf16 would add 40 percent."""
+    _, k, v, _ = tensors(B, cap, 1, Hkv, seed=44)
+    q = tensors(B, 1, Hq, Hkv, seed=45)[0][:, 0].contiguous()
+    lens = [cap - i for i in range(B)]
+    o, _ = msa.msa_window_decode(q, k, v, torch.tensor(lens, dtype=torch.int32, device=DEV), cap, 0, SCALE)
+    ref = plain.window_decode(q, k, v, lens, cap, 0, SCALE)["o"][0]
+    err, floor = (float((x.double() - ref).norm() / ref.norm()) for x in (o, ref.to(torch.bfloat16)))
+    assert err <= 1.01 * floor, (err, floor)
+
+
 @pytest.mark.parametrize("cap,B", [(400, 3), (9000, 3)])
 def test_decode_skips_bad_lengths(cap, B):
     """Lengths outside 1 .. S: flagged, their rows left as they were, the others right."""
