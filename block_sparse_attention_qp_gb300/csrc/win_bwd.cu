@@ -24,7 +24,7 @@
 // P and dS are rounded to bf16 for their products (2^-9 relative each), the softmax scale is folded
 // into dS, everything else is fp32.  32 (dkv) and 24 (dq) instructions of 128 x 128 x 16 a tile pair, 64
 // to 67 cycles each: at 64K tokens, 64 / 8 heads, window 512 dkv takes 1.90 ms (1,160 TFLOP/s of its four
-// products over visible pairs) and dq 1.59 ms (1,040 of its three).
+// products over visible pairs) and dq 1.62 ms (1,020 of its three).
 //
 // Roles of both (640 threads): warp 0 TMA loads, warp 1 MMA issue (two issuing warps interleaved the
 // products of a chain with the other's and were slower), warp 2 the tile's row data (dkv) or the TMA

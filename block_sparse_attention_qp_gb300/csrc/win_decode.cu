@@ -10,7 +10,7 @@
 //   product: O then has its own rounding only (relative error 1.7e-3; one bf16 P, as groups of 16 heads
 //   have it, 2.2e-3)
 //   O_n^T = V_n^T P^T    (tensor core, 128 dims x 16), added to the running O (thread = dim)
-// 128 sequences with windows of 1024, 64 / 8 heads: 97 us under ncu, 595 MB read (6.15 TB/s) for the 535
+// 128 sequences with windows of 1024, 64 / 8 heads: 100 us, 595 MB read (5.95 TB/s) for the 535
 // that are visible, the rest being the ninth tiles' other keys.
 // 73 KB of shared memory leave three blocks to an SM: the loads of two run behind the chain of the
 // third, and a block's next K tile is loaded as soon as S^T is there, its next V after O_n^T.

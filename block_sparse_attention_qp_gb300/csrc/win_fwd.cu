@@ -15,7 +15,7 @@
 // P = 0 exactly.  A row may see nothing of a tile (its maximum then stays -inf until it does).
 //
 // 4 x 128 flops a visible pair, and the tiles cost about (W + 256/G + 128) / W of that; K and V come
-// through L2.  1,430 TFLOP/s of visible pairs at 32K tokens, 32 / 8 heads, window 2048 (746 us), 990 at 64K
+// through L2.  1,420 TFLOP/s of visible pairs at 32K tokens, 32 / 8 heads, window 2048 (753 us), 990 at 64K
 // tokens, 64 / 8 heads, window 512 (1.11 ms), where the tiles hold 1.2 times the visible pairs.  Bound by
 // the hand-offs of the chain S, softmax, P V of a tile: without exponentials, loads and seven of eight
 // products an earlier form took 690 of its 840 us.  The order of products is
