@@ -781,7 +781,7 @@ def msa_norm_rope_backward(xs, weights, dys, inv_freq, positions=None, eps: floa
                            rotate=None, interleaved: bool = False, dxs=None, ws=None):
     """Gradients of msa_norm_rope_forward: (dxs, dweights), dweights fp32 [128] or None per tensor.
     dxs: where to write them (e.g. the slices of one packed gradient, or the dys), default new
-    tensors."""
+    tensors; each may be its own part's x or dy, but overlap no other tensor of the call."""
     dev = _device_of(xs)
     shape, parts, fp, pp = _rope_args(xs, weights, rotate, inv_freq, interleaved, eps, positions, dev)
     n = len(xs)
@@ -819,7 +819,7 @@ def msa_norm_rope_append(xs, weights, inv_freq, seq_len, caches, eps: float = 1e
     None.  Returns per tensor its cache, or a new tensor of the shape of x: for (q, k, v, qp, kp) with
     caches (None, k_cache, v_cache, None, kp_cache) the arguments of msa_decode and
     msa_window_decode.  Sequences with a length outside N .. S are skipped (msa_device_status of ws
-    tells)."""
+    tells).  Caches may overlap neither each other nor the xs."""
     dev = _device_of(xs)
     x4 = xs
     if xs[0].dim() == 3:

@@ -10,6 +10,7 @@
 #include <memory>
 #include <mutex>
 #include <string>
+#include <utility>
 #include <vector>
 
 #include "../../include/msa.h"
@@ -653,6 +654,119 @@ size_t rope_ws(int nparts, int op) {
   return 0;
 }
 
+// The memory of a part's tensor: n[0] x n[1] runs of `len` bytes, s[0] >= s[1] >= 0 bytes apart.
+struct Runs {
+  long long at, s[2], n[2], len;
+  long long inner() const { return s[1] * (n[1] - 1) + len; }
+  long long end() const { return at + s[0] * (n[0] - 1) + inner(); }
+  bool same(const Runs& o) const {
+    return s[0] == o.s[0] && s[1] == o.s[1] && n[0] == o.n[0] && n[1] == o.n[1];
+  }
+};
+Runs runs(const void* p, int B, long long sb, long long N, long long st, int heads) {
+  Runs r{(long long)reinterpret_cast<uintptr_t>(p), {2 * sb, 2 * st}, {B, N}, 256ll * heads};
+  for (int i = 0; i < 2; ++i) {
+    if (r.n[i] == 1) r.s[i] = 0;
+    if (r.s[i] < 0) {  // the same memory walked upwards
+      r.at += r.s[i] * (r.n[i] - 1);
+      r.s[i] = -r.s[i];
+    }
+  }
+  if (r.s[0] < r.s[1]) {
+    std::swap(r.s[0], r.s[1]);
+    std::swap(r.n[0], r.n[1]);
+  }
+  return r;
+}
+// Indices i in [0, n) with lo < i * s < hi (open): first in *a, one past the last in *z.
+void between(long long lo, long long hi, long long s, long long n, long long* a, long long* z) {
+  if (s == 0) {
+    *a = 0;
+    *z = lo < 0 && 0 < hi ? n : 0;
+    return;
+  }
+  *a = lo < 0 ? 0 : lo / s + 1;
+  *z = hi <= 0 ? 0 : (hi - 1) / s + 1;
+  if (*z > n) *z = n;
+}
+bool hits(const Runs& y, long long lo, long long hi) {  // one of y's runs meets [lo, hi)
+  long long i0, i1, j0, j1;
+  between(lo - y.at - y.inner(), hi - y.at, y.s[0], y.n[0], &i0, &i1);
+  if (i0 < i1 && y.s[0] == 0) i1 = i0 + 1;
+  for (long long i = i0; i < i1; ++i) {
+    const long long at = y.at + i * y.s[0];
+    between(lo - at - y.len, hi - at, y.s[1], y.n[1], &j0, &j1);
+    if (j0 < j1) return true;
+  }
+  return false;
+}
+// Whether two tensors share memory, exactly.  Slices of one tensor have the same strides: then x's first
+// run against y with every difference of indices.  Others are taken apart only where their ranges meet.
+bool overlap(const Runs& x, Runs y) {
+  if (x.at >= y.end() || y.at >= x.end()) return false;
+  if (x.same(y)) {
+    for (int i = 0; i < 2; ++i) {
+      y.at -= y.s[i] * (y.n[i] - 1);
+      y.n[i] = 2 * y.n[i] - 1;
+    }
+    return hits(y, x.at, x.at + x.len);
+  }
+  for (long long i = 0; i < x.n[0]; ++i) {
+    const long long at = x.at + i * x.s[0];
+    if (!hits(y, at, at + x.inner())) continue;
+    for (long long j = 0; j < x.n[1]; ++j)
+      if (hits(y, at + j * x.s[1], at + j * x.s[1] + x.len)) return true;
+  }
+  return false;
+}
+// Rows of a tensor that is written: no two may share memory (counted for strides that nest, as every
+// slice's do).
+bool overlaps_itself(const Runs& r) {
+  return (r.n[1] > 1 && r.s[1] < r.len) || (r.n[0] > 1 && r.s[0] < r.inner());
+}
+
+// Every output of a call apart from every other one and from what other warps still read: an output may
+// only be the same rows as an input of its own part, which a warp has read before it writes them.
+int check_rope_outputs(const msa_rope_shape_t* s, const msa_rope_part_t* parts, int nparts, int op) {
+  const bool bwd = op == MSA_OP_NORM_ROPE_BACKWARD;
+  Runs in[2 * kRopeParts], out[kRopeParts];  // x, and behind them the dy
+  for (int i = 0; i < nparts; ++i) {
+    const msa_rope_part_t& p = parts[i];
+    const bool cache = p.flags & MSA_ROPE_CACHE;
+    in[i] = runs(p.x, s->B, p.x_batch, s->N, p.x_token, p.heads);
+    const Runs y = runs(p.y, s->B, p.y_batch, cache ? s->capacity : s->N, p.y_token, p.heads);
+    out[i] = bwd ? runs(p.dx, s->B, p.dx_batch, s->N, p.dx_token, p.heads) : y;
+    if (bwd) in[nparts + i] = y;
+    if (overlaps_itself(out[i])) {
+      set_err("rows of an output overlap (its strides are too small)");
+      return MSA_ERR_INVALID_ARG;
+    }
+  }
+  for (int i = 0; i < nparts; ++i) {
+    for (int j = 0; j < i; ++j) {
+      const Runs wi = runs(parts[i].dweight, 1, 0, 1, 0, 2), wj = runs(parts[j].dweight, 1, 0, 1, 0, 2);  // 512 bytes
+      if (overlap(out[i], out[j]) || (bwd && parts[i].dweight && parts[j].dweight && overlap(wi, wj))) {
+        set_err("two parts with the same output, or with outputs that overlap");
+        return MSA_ERR_INVALID_ARG;
+      }
+    }
+    const msa_rope_part_t& p = parts[i];
+    const void* to = bwd ? p.dx : p.y;
+    const int64_t tob = bwd ? p.dx_batch : p.y_batch, tot = bwd ? p.dx_token : p.y_token;
+    auto same_rows = [&](const void* from, int64_t sb, int64_t st) {  // row by row, not only as a whole
+      return from == to && (s->B == 1 || sb == tob) && (s->N == 1 || st == tot) && !(p.flags & MSA_ROPE_CACHE);
+    };
+    for (int j = 0; j < (bwd ? 2 : 1) * nparts; ++j) {
+      if (!overlap(out[i], in[j])) continue;
+      if (j == i && same_rows(p.x, p.x_batch, p.x_token)) continue;
+      if (j == nparts + i && same_rows(p.y, p.y_batch, p.y_token)) continue;
+      set_err("an output overlaps an input (it may only be the same rows as an input of its own part)");
+      return MSA_ERR_INVALID_ARG;
+    }
+  }
+  return MSA_OK;
+}
+
 // op: MSA_OP_NORM_ROPE_BACKWARD, MSA_OP_NORM_ROPE_APPEND, or -1 for the forward
 int check_rope(const msa_rope_shape_t* s, const msa_rope_part_t* parts, int nparts, const int32_t* pos,
                const float* inv_freq, int op, RopeArgs* out) {
@@ -732,13 +846,6 @@ int check_rope(const msa_rope_shape_t* s, const msa_rope_part_t* parts, int npar
       set_err("strides must be multiples of 8 elements");
       return MSA_ERR_INVALID_ARG;
     }
-    for (int j = 0; j < i; ++j) {
-      const msa_rope_part_t& e = parts[j];
-      if (bwd ? p.dx == e.dx || (p.dweight && p.dweight == e.dweight) : p.y == e.y) {
-        set_err("two parts with the same output");
-        return MSA_ERR_INVALID_ARG;
-      }
-    }
     o.x = static_cast<const bf16*>(p.x);
     o.xb = p.x_batch;
     o.xt = p.x_token;
@@ -757,6 +864,7 @@ int check_rope(const msa_rope_shape_t* s, const msa_rope_part_t* parts, int npar
               (p.flags & MSA_ROPE_CACHE ? kRopeCache : 0);
     a.rows += p.heads;
   }
+  if ((rc = check_rope_outputs(s, parts, nparts, op))) return rc;
   *out = a;
   return MSA_OK;
 }
