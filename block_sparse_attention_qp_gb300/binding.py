@@ -42,7 +42,7 @@ _SYMBOLS = ("msa_workspace_size", "msa_forward", "msa_backward", "msa_warmup_for
             "msa_warmup_backward", "msa_device_status", "msa_status_string", "msa_last_error",
             "msa_profile_begin", "msa_profile_end", "msa_launch_count", "msa_forward_noalloc",
             "msa_forward_noalloc_status", "msa_selftest_wait_timeout", "msa_decode",
-            "msa_window_workspace_size", "msa_window_forward", "msa_window_backward",
+            "msa_window_workspace_size", "msa_window_wait_limit_ms", "msa_window_forward", "msa_window_backward",
             "msa_window_decode", "msa_norm_rope_forward", "msa_norm_rope_append",
             "msa_norm_rope_backward", "msa_norm_rope_workspace_size")
 
@@ -109,6 +109,8 @@ def load_library(path: str = LIB_PATH):
         RP = P  # an array of RopePart, or its bytes
         lib.msa_window_workspace_size.argtypes = [WP, I]
         lib.msa_window_workspace_size.restype = Z
+        lib.msa_window_wait_limit_ms.argtypes = [WP, I]
+        lib.msa_window_wait_limit_ms.restype = ctypes.c_uint
         lib.msa_window_forward.argtypes = [WP, P, P, P, P, P, P, Z, P]
         lib.msa_window_backward.argtypes = [WP, P, P, P, P, P, P, P, P, P, P, Z, P]
         lib.msa_window_decode.argtypes = [WP, P, P, P, P, P, P, P, Z, P]
@@ -548,6 +550,16 @@ def _window_bytes(op, *shape):
 def msa_window_workspace_size(shape: WindowShape, op: int) -> int:
     return _window_bytes(op, shape.B, shape.S, shape.Hq, shape.Hkv, shape.D, shape.window, shape.sinks,
                          shape.scale)
+
+
+def msa_window_wait_limit_ms(shape: WindowShape, op: int) -> int:
+    """The longest that a wait inside the op's kernels may last before the call ends with the timeout bit in
+    msa_device_status(ws)."""
+    lib = load_library()
+    ms = int(lib.msa_window_wait_limit_ms(ctypes.byref(shape), op))
+    if ms == 0:
+        raise MSAError(f"unsupported shape for op {op}: {lib.msa_last_error().decode()}")
+    return ms
 
 
 def window_workspace(shape: WindowShape, op: int, device) -> torch.Tensor:

@@ -1192,6 +1192,16 @@ size_t msa_window_workspace_size(const msa_window_shape_t* shape, int op) {
   return win_plan(d, op).bytes;
 }
 
+unsigned msa_window_wait_limit_ms(const msa_window_shape_t* shape, int op) {
+  WinDims d;
+  if (op < MSA_OP_WINDOW_FORWARD || op > MSA_OP_WINDOW_DECODE) {
+    set_err("not a window op");
+    return 0;
+  }
+  if (check_window(shape, op, &d) != MSA_OK) return 0;
+  return op == MSA_OP_WINDOW_DECODE ? 200 : (unsigned)((win_unit_wait_ns(d) + 999999) / 1000000);
+}
+
 int msa_window_forward(const msa_window_shape_t* shape, const void* q, const void* k, const void* v,
                        void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
   WinDims d;

@@ -194,6 +194,9 @@ struct WinDims {
 bool launch_win_fwd(const WinDims& d, const void* q, const void* k, const void* v, void* o,
                     float* lse, unsigned* status, cudaStream_t st);
 
+// Limit of the waits that last a whole unit, its rows leaving only at its end (win_fwd.cu).
+unsigned long long win_unit_wait_ns(const WinDims& d);
+
 // Work items of the key-outer backward: first the sink blocks' chunks, then the window blocks'.
 struct WinItems {
   int sink_blocks, sink_chunk, sink_items;  // key blocks that hold sinks; query tiles per item

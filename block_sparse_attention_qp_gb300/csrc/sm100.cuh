@@ -217,7 +217,7 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 }
 // Bounded wait: spins on try_wait (which itself suspends the thread until the phase completes or
 // a short hardware time limit passes) and gives up after `limit_ns` of wall time (legitimate
-// waits here last microseconds), setting the timeout bit (4) of the device status word.
+// waits last microseconds; a caller whose wait may last longer gives its limit), setting the timeout bit (4) of the device status word.
 // Every wait in this library is bounded and callers leave their loops on a timeout, so a logic
 // error can never hang the GPU.
 __device__ __forceinline__ bool mbar_wait(uint64_t* mbar, uint32_t parity, unsigned* err,

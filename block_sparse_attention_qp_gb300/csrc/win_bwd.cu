@@ -535,6 +535,7 @@ struct DqArgs {
   CUtensorMap q, dout, dq;
   float2* rowm;
   unsigned* status;
+  unsigned long long unit_ns;  // win_unit_wait_ns
   int units;  // one 128-row tile each
 };
 struct DqShared {
@@ -738,7 +739,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dq_kernel(const __grid_con
       for (int u = blockIdx.x; u < A.units; u += gridDim.x, ++nu, slot = (slot + 1) % kRingQ) {
         const DqUnit x = dq_unit<G>(d, u);
         slot = (slot + 2 * x.run.nb) % kRingQ;  // the unit's last ring entry
-        if (!mbar_wait(&sh->st_full, phase_of(nu), A.status)) break;
+        if (!mbar_wait(&sh->st_full, phase_of(nu), A.status, A.unit_ns)) break;
         tma_store_rows(&A.dq, aR + slot * kTile, 0, x.g * G, x.t0, x.b);
         tma_store_rows(&A.dq, aR + slot * kTile + kTile / 2, 64, x.g * G, x.t0, x.b);
         bulk_store_commit();
@@ -983,6 +984,7 @@ bool launch_win_dq(const WinDims& d, const void* q, const void* k, const void* v
   a.d = d;
   a.rowm = rowm;
   a.status = status;
+  a.unit_ns = win_unit_wait_ns(d);
   a.units = (d.S + tt - 1) / tt * d.B * d.Hkv;
   const size_t smem = sizeof(DqShared) + 1024 + (2 + kRingQ) * (size_t)kTile;
 #define MSA_CALL(G)                                                                                  \

@@ -29,7 +29,8 @@
 // at 32K tokens, two: 1,012, both before the later steps).  The two share the row maximum: a barrier that ORs
 // "my half exceeds it" across them, and an exchange through shared memory in the rare case it does.
 // Tensor memory: S_A, S_B, O_A, O_B (512 columns).  Units have equal cost but for the sequence's first window: they are dealt in turn,
-// tokens outermost, so that concurrent units share K and V.  Every wait is bounded.
+// tokens outermost, so that concurrent units share K and V.  Every wait is bounded:
+// by 200 ms, and where a warp sits out a whole unit by win_unit_wait_ns.
 #include <math.h>
 
 #include "tmap.h"
@@ -48,6 +49,7 @@ struct FwdArgs {
   CUtensorMap q, o;
   float* lse;
   unsigned* status;
+  unsigned long long unit_ns;  // win_unit_wait_ns
   int tiles;        // query tiles per unit, 1 or 2
   int nseg;         // units along a sequence
   int units;  // nseg B Hkv
@@ -232,13 +234,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1) win_fwd_kernel(const __grid_co
         const FwdUnit x = fwd_unit<G>(A, u);
         const int qs = (int)(nu & 1);
         if (X == 0 || x.two) {
-          if (!mbar_wait(&sh->st_full[X], phase_of(ns++), A.status)) break;
+          if (!mbar_wait(&sh->st_full[X], phase_of(ns++), A.status, A.unit_ns)) break;
           const uint32_t src = aQ + (qs * 2 + X) * kTile;
           tma_store_rows(&A.o, src, 0, x.g * G, x.t0 + X * TT, x.b);
           tma_store_rows(&A.o, src + kTile / 2, 64, x.g * G, x.t0 + X * TT, x.b);
           bulk_store_commit();
           bulk_store_wait_read();
-        } else if (!mbar_wait(&sh->q_full[qs], phase_of(nu >> 1), A.status)) {
+        } else if (!mbar_wait(&sh->q_full[qs], phase_of(nu >> 1), A.status, A.unit_ns)) {
           break;  // (waited for only so that this arrival cannot run ahead into a later phase)
         }
         mbar_arrive(&sh->q_empty[qs]);
@@ -395,6 +397,13 @@ bool make_key_maps(const WinDims& d, const void* base, KeyMaps* m) {
                     make_tmap_rows(&m->rest, base, d.B, d.S, d.Hkv, 1, kBlock - a));
 }
 
+// A unit's walk grows with the window: 65536 tiles at S = 2^23, 1.6 us each at 2,070 MHz and 2.2 at 1,507,
+// so a warp that waits for the end of one gets 25 us a tile beside the 200 ms of every wait.
+unsigned long long win_unit_wait_ns(const WinDims& d) {
+  const long long keys = (long long)d.nsp + d.W + 2 * kBlock < d.S ? (long long)d.nsp + d.W + 2 * kBlock : d.S;
+  return 200000000ull + 25000ull * (unsigned long long)(keys / kBlock + 1);
+}
+
 template <int G>
 static void win_fwd_g(const FwdArgs& a, cudaStream_t st) {
   const size_t smem = sizeof(FwdShared) + (4 + kRing) * (size_t)kTile;
@@ -413,6 +422,7 @@ bool launch_win_fwd(const WinDims& d, const void* q, const void* k, const void* 
   a.d = d;
   a.lse = lse;
   a.status = status;
+  a.unit_ns = win_unit_wait_ns(d);
   const int tt = kBlock / d.G;
   const long long per = (long long)d.B * d.Hkv;
   a.tiles = (d.S + 2 * tt - 1) / (2 * tt) * per < num_sms() ? 1 : 2;

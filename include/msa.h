@@ -223,6 +223,13 @@ typedef struct msa_window_shape {
 /* Bytes of workspace a window op needs (0 if the shape is unsupported). */
 MSA_API size_t msa_window_workspace_size(const msa_window_shape_t* shape, int op);
 
+/*
+ * The longest that a wait inside a window op's kernels may last, in milliseconds (0 if the shape is
+ * unsupported).  A wait that runs out ends its block, sets MSA_DEVICE_TIMEOUT and leaves outputs that
+ * are not valid; the limit grows with the window, whose whole walk the warps that store a row sit out.
+ */
+MSA_API unsigned msa_window_wait_limit_ms(const msa_window_shape_t* shape, int op);
+
 /* Writes o and lse. */
 MSA_API int msa_window_forward(const msa_window_shape_t* shape, const void* q, const void* k,
                        const void* v, void* o, float* lse, void* workspace, size_t workspace_bytes,
