@@ -656,15 +656,14 @@ size_t rope_ws(int nparts, int op) {
 
 // The memory of a part's tensor: n[0] x n[1] runs of `len` bytes, s[0] >= s[1] >= 0 bytes apart.
 struct Runs {
-  long long at, s[2], n[2], len;
+  long long at, s[2], n[2], len, end;
   long long inner() const { return s[1] * (n[1] - 1) + len; }
-  long long end() const { return at + s[0] * (n[0] - 1) + inner(); }
   bool same(const Runs& o) const {
     return s[0] == o.s[0] && s[1] == o.s[1] && n[0] == o.n[0] && n[1] == o.n[1];
   }
 };
 Runs runs(const void* p, int B, long long sb, long long N, long long st, int heads) {
-  Runs r{(long long)reinterpret_cast<uintptr_t>(p), {2 * sb, 2 * st}, {B, N}, 256ll * heads};
+  Runs r{(long long)reinterpret_cast<uintptr_t>(p), {2 * sb, 2 * st}, {B, N}, 256ll * heads, 0};
   for (int i = 0; i < 2; ++i) {
     if (r.n[i] == 1) r.s[i] = 0;
     if (r.s[i] < 0) {  // the same memory walked upwards
@@ -676,6 +675,7 @@ Runs runs(const void* p, int B, long long sb, long long N, long long st, int hea
     std::swap(r.s[0], r.s[1]);
     std::swap(r.n[0], r.n[1]);
   }
+  r.end = r.at + r.s[0] * (r.n[0] - 1) + r.inner();
   return r;
 }
 // Indices i in [0, n) with lo < i * s < hi (open): first in *a, one past the last in *z.
@@ -702,8 +702,7 @@ bool hits(const Runs& y, long long lo, long long hi) {  // one of y's runs meets
 }
 // Whether two tensors share memory, exactly.  Slices of one tensor have the same strides: then x's first
 // run against y with every difference of indices.  Others are taken apart only where their ranges meet.
-bool overlap(const Runs& x, Runs y) {
-  if (x.at >= y.end() || y.at >= x.end()) return false;
+bool shared(const Runs& x, Runs y) {
   if (x.same(y)) {
     for (int i = 0; i < 2; ++i) {
       y.at -= y.s[i] * (y.n[i] - 1);
@@ -718,6 +717,9 @@ bool overlap(const Runs& x, Runs y) {
       if (hits(y, at + j * x.s[1], at + j * x.s[1] + x.len)) return true;
   }
   return false;
+}
+inline bool overlap(const Runs& x, const Runs& y) {  // (most tensors' ranges are apart: a call has up to 84 pairs)
+  return x.at < y.end && y.at < x.end && shared(x, y);
 }
 // Rows of a tensor that is written: no two may share memory (counted for strides that nest, as every
 // slice's do).
@@ -744,8 +746,8 @@ int check_rope_outputs(const msa_rope_shape_t* s, const msa_rope_part_t* parts, 
   }
   for (int i = 0; i < nparts; ++i) {
     for (int j = 0; j < i; ++j) {
-      const Runs wi = runs(parts[i].dweight, 1, 0, 1, 0, 2), wj = runs(parts[j].dweight, 1, 0, 1, 0, 2);  // 512 bytes
-      if (overlap(out[i], out[j]) || (bwd && parts[i].dweight && parts[j].dweight && overlap(wi, wj))) {
+      const float *wi = parts[i].dweight, *wj = parts[j].dweight;
+      if (overlap(out[i], out[j]) || (bwd && wi && wj && wi < wj + kD && wj < wi + kD)) {
         set_err("two parts with the same output, or with outputs that overlap");
         return MSA_ERR_INVALID_ARG;
       }
