@@ -483,6 +483,19 @@ int check_ptrs(std::initializer_list<const void*> ptrs) {
   return MSA_OK;
 }
 
+// Lengths, positions and frequencies: read four bytes at a time, so a slice may start anywhere.
+int check_words(const void* p) {
+  if (!p) {
+    set_err("a required pointer is null");
+    return MSA_ERR_INVALID_ARG;
+  }
+  if (reinterpret_cast<uintptr_t>(p) % 4 != 0) {
+    set_err("seq_len, positions and inv_freq must be 4-byte aligned");
+    return MSA_ERR_INVALID_ARG;
+  }
+  return MSA_OK;
+}
+
 template <typename T>
 T* at(void* ws, size_t off) {
   return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
@@ -810,7 +823,7 @@ int check_rope(const msa_rope_shape_t* s, const msa_rope_part_t* parts, int npar
   a.eps = s->eps;
   int rc;
   if (op == MSA_OP_NORM_ROPE_APPEND) {
-    if ((rc = check_ptrs({pos}))) return rc;
+    if ((rc = check_words(pos))) return rc;
     if (s->capacity < s->N) {
       set_err("capacity must be at least N");
       return MSA_ERR_INVALID_ARG;
@@ -818,10 +831,10 @@ int check_rope(const msa_rope_shape_t* s, const msa_rope_part_t* parts, int npar
     a.cap = s->capacity;
     a.seq_len = pos;
   } else {
-    if (pos && (rc = check_ptrs({pos}))) return rc;
+    if (pos && (rc = check_words(pos))) return rc;
     a.positions = pos;
   }
-  if (a.rot > 0 && (rc = check_ptrs({inv_freq}))) return rc;
+  if (a.rot > 0 && (rc = check_words(inv_freq))) return rc;
   a.inv_freq = inv_freq;
   for (int i = 0; i < nparts; ++i) {
     const msa_rope_part_t& p = parts[i];
@@ -1157,7 +1170,7 @@ int msa_decode(const msa_shape_t* shape, const void* q, const void* qp, const vo
   Dims d;
   int rc = check_shape(shape, MSA_OP_DECODE, &d);
   if (rc) return rc;
-  if ((rc = check_ptrs({q, qp, k_cache, v_cache, kp_cache, seq_len, block_idx, o, lse}))) return rc;
+  if ((rc = check_ptrs({q, qp, k_cache, v_cache, kp_cache, block_idx, o, lse})) || (rc = check_words(seq_len))) return rc;
   const Plan p = make_plan(d, MSA_OP_DECODE);
   if ((rc = check_ws(p, workspace, workspace_bytes))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -1264,7 +1277,7 @@ int msa_window_decode(const msa_window_shape_t* shape, const void* q, const void
   WinDims d;
   int rc = check_window(shape, MSA_OP_WINDOW_DECODE, &d);
   if (rc) return rc;
-  if ((rc = check_ptrs({q, k_cache, v_cache, seq_len, o, lse}))) return rc;
+  if ((rc = check_ptrs({q, k_cache, v_cache, o, lse})) || (rc = check_words(seq_len))) return rc;
   const WinPlan p = win_plan(d, MSA_OP_WINDOW_DECODE);
   if ((rc = check_ws_bytes(p.bytes, workspace, workspace_bytes))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

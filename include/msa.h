@@ -25,7 +25,7 @@
  *   h / (Hq / Hp).  Hq must be a multiple of Hkv and of Hp, and one
  *   of Hp, Hkv a multiple of the other.  The KL teacher of proxy head p is the mean main
  *   softmax of its Hq / Hp query heads.  Key j is visible to token t iff j <= t.
- *   Every pointer must be 16-byte aligned.  Supported: head dim 128, block 128 (blog / package
+ *   Every pointer must be 16-byte aligned (seq_len, positions and inv_freq: 4-byte).  Supported: head dim 128, block 128 (blog / package
  *   caveat 1), S % 128 == 0, 1 <= top_k <= 64, and Hq / max(Hp, Hkv) -- the query heads that
  *   share both one KV head and one selection row -- in {1, 2, 4, 8, 16} for the forward ops and
  *   {4, 8, 16} for the backward ops (the warmup forward, which has no selection: Hq / Hkv).
