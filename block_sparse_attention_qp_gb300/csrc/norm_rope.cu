@@ -12,8 +12,8 @@
 // Angles: pos * inv_freq grows to millions of radians at far positions, where fp32 has lost the
 // angle.  The frequency in turns, inv_freq / 2 pi, is kept as a 64-bit fraction of a turn F; the low
 // 64 bits of pos * F are then the angle's exact fraction of a turn (whole turns wrap away, also for
-// negative positions), whose upper 32 bits go to sincospif.  F is rounded once, from fp64: the angle
-// is off by at most |pos| 2^-54 turns plus fp32 rounding.
+// negative positions), whose upper 32 bits go to sincospif.  F is the nearest 2^-64 turns (from two
+// doubles, for |inv_freq| up to 2^40): the angle is off by at most |pos| 2^-64 turns plus fp32 rounding.
 //
 // Work: 16 lanes hold a row (16 bytes a lane), a warp two tokens at a time, and walks the token's
 // heads with its angles in registers, so they are computed once a token and part list, not once a
@@ -59,9 +59,16 @@ __device__ __forceinline__ void load_w(const float* w, int l, float (&f)[8]) {
 __device__ __forceinline__ void load_freqs(const RopeArgs& A, unsigned long long* sF) {
   const int i = threadIdx.x;
   if (i < A.rot / 2) {
-    double t = (double)A.inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
-    t -= floor(t);
-    sF[i] = (unsigned long long)(t * 18446744073709551616.0);
+    // |f| / 2 pi as a sum of doubles t + lo: the product with the constant's upper half exact (a fused
+    // multiply-add gives its rounding error), its lower half's added.  Whole turns go from t exactly.
+    const double f = (double)A.inv_freq[i], w = fabs(f), up64 = 18446744073709551616.0;
+    const double hi = 0.15915494309189535, t = w * hi;
+    double lo = fma(w, -9.839338337591243e-18, fma(w, hi, -t));
+    lo -= rint(lo);
+    const double a = (t - floor(t)) * up64;
+    const unsigned long long F =
+        (unsigned long long)a + (unsigned long long)__double2ll_rn((a - floor(a)) + lo * up64);
+    sF[i] = f < 0.0 ? 0ull - F : F;
   }
   __syncthreads();
 }

@@ -262,7 +262,8 @@ MSA_API int msa_window_decode(const msa_window_shape_t* shape, const void* q, co
  *     y = u with its first `rotary` elements turned in pairs (i, i + rotary/2) -- interleaved:
  *         (2 i, 2 i + 1) -- by the angle position * inv_freq[i]   (without MSA_ROPE_ROTATE: y = u)
  * rotary: a multiple of 16, 0 .. 128.  inv_freq: rotary / 2 floats on the device.  positions: int32
- * [B, N] on the device, any value, or NULL for 0 .. N - 1.  Angles are exact to fp32 at every position.
+ * [B, N] on the device, any value, or NULL for 0 .. N - 1.  Angles are exact to fp32 at every position
+ * (for inv_freq up to 2^40 either side of zero).
  * The outputs of a call (y; backward: dx, dweight) may overlap neither each other nor an input, only
  * that dx may be the same rows as x or dy of its own part, and y, where it is not a cache, those of x.
  */
