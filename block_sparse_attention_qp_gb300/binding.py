@@ -597,7 +597,8 @@ def _window_args(q, k, v, window, sinks, scale, op, ws, dims):
 
 def msa_window_forward(q, k, v, window: int, sinks: int, scale: float, ws=None):
     """Causal GQA attention of every query over the last ``window`` tokens (itself included) and the
-    first ``sinks`` tokens.  q [B, S, Hq, 128], k, v [B, S, Hkv, 128], any S.  Returns (o, lse)."""
+    first ``sinks`` tokens.  q [B, S, Hq, 128], k, v [B, S, Hkv, 128], any S.  Returns (o, lse).  Rows that a
+    query does not see never reach it, whatever they hold (padding behind a ragged prompt may be uninitialised)."""
     dev, ptrs, shape, need = _window_args(q, k, v, window, sinks, scale, OP_WINDOW_FORWARD, ws, 4)
     with _Guard(dev):
         wp, wn, ws = _ws(ws, need, dev)
@@ -611,7 +612,8 @@ def msa_window_forward(q, k, v, window: int, sinks: int, scale: float, ws=None):
 
 
 def msa_window_backward(q, k, v, o, lse, dout, window: int, sinks: int, scale: float, ws=None):
-    """Gradients (dq, dk, dv) of sum(o * dout); o, lse from msa_window_forward on the same inputs."""
+    """Gradients (dq, dk, dv) of sum(o * dout); o, lse from msa_window_forward on the same inputs, which must all be
+    finite, padding included."""
     dev, ptrs, shape, need = _window_args(q, k, v, window, sinks, scale, OP_WINDOW_BACKWARD, ws, 4)
     op = _ask(o, "o", torch.bfloat16, q.shape, dev)
     lp = _ask(lse, "lse", torch.float32, (shape.B, shape.Hq, shape.S), dev)
@@ -664,7 +666,7 @@ class _WindowFunction(torch.autograd.Function):
 
 def msa_window_func(Q, K, V, window: int, sinks: int, scale: float):
     """Sliding-window attention with autograd (msa_window_forward / msa_window_backward); returns
-    attn_out."""
+    attn_out.  To be trained through, Q, K, V and the gradient have to be finite, padding included."""
     return _WindowFunction.apply(Q, K, V, int(window), int(sinks), float(scale))
 
 

@@ -12,7 +12,8 @@
 //   O_X += P V_n
 // P is rounded to bf16 for its product: relative 2^-9 a key, which averages out to less than the
 // rounding of O itself; the row sum l is taken from the fp32 values.  Keys outside a row's window get
-// P = 0 exactly.  A row may see nothing of a tile (its maximum then stays -inf until it does).
+// P = 0 exactly; a V row that is not finite and that only some of a tile's queries see is taken care of by
+// mend_rows.  A row may see nothing of a tile (its maximum then stays -inf until it does).
 //
 // 4 x 128 flops a visible pair, and the tiles cost about (W + 256/G + 128) / W of that; K and V come
 // through L2.  1,420 TFLOP/s of visible pairs at 32K tokens, 32 / 8 heads, window 2048 (753 us), 990 at 64K
@@ -31,6 +32,7 @@
 // Tensor memory: S_A, S_B, O_A, O_B (512 columns).  Units have equal cost but for the sequence's first window: they are dealt in turn,
 // tokens outermost, so that concurrent units share K and V.  Every wait is bounded:
 // by 200 ms, and where a warp sits out a whole unit by win_unit_wait_ns.
+#include <limits.h>
 #include <math.h>
 
 #include "tmap.h"
@@ -47,6 +49,8 @@ struct FwdArgs {
   WinDims d;
   KeyMaps k, v;
   CUtensorMap q, o;
+  const bf16 *qp, *kp, *vp;  // the same tensors by address (mend_rows)
+  bf16* op;
   float* lse;
   unsigned* status;
   unsigned long long unit_ns;  // win_unit_wait_ns
@@ -60,6 +64,7 @@ struct FwdShared {
   uint64_t q_full[2], q_empty[2], kv_full[kRing], kv_empty[kRing], s_full[2], p_full[2], o_full[2],
       o_free[2], st_full[2], mma_done;
   uint32_t tmem;
+  int bad0, bad1;  // the block's first and last unit with an O that is not finite
 };
 struct FwdUnit {
   int b, g, t0;
@@ -80,6 +85,94 @@ __device__ __forceinline__ FwdUnit fwd_unit(const FwdArgs& A, int u) {
   const int t1 = x.t0 + TT * A.tiles - 1;
   x.run = key_run(d, x.t0, t1 < d.S ? t1 : d.S - 1);
   return x;
+}
+
+__device__ __forceinline__ bool finite4(uint2 w) {  // four bf16
+  auto bad = [](uint32_t x) { return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u; };
+  return !(bad(w.x) || bad(w.y));
+}
+__device__ __forceinline__ float4 widen4(uint2 w) {
+  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                     __uint_as_float(w.y & 0xffff0000u));
+}
+
+// O rows again that an infinity or NaN has reached through a V row which the query does not see: a
+// product of the tensor core takes whole tiles, and P = 0 times NaN is NaN.  A warp takes a token and
+// its group's heads, four dims a lane, and adds up the visible keys alone (the LSE needs nothing: masked
+// scores never enter it).  A query that sees such a V row itself is left as it is.  Runs behind the block's last
+// store and only where an epilogue met a value that is not finite, so that it costs other calls nothing
+// but the look.
+template <int G>
+__device__ __noinline__ void mend_rows(const FwdArgs& A, int u) {
+  constexpr int TT = 128 / G;
+  const WinDims& d = A.d;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, per = d.B * d.Hkv;
+  const int b = u % per / d.Hkv, g = u % per % d.Hkv, t0 = u / per * TT * A.tiles;
+  const float sl2 = d.scale * kLog2e;
+  const long long seq = (long long)b * d.S;
+  auto kv_row = [&](const bf16* x, int key) {
+    return __ldg(reinterpret_cast<const uint2*>(x + ((seq + key) * d.Hkv + g) * kD) + lane);
+  };
+  for (int t = t0 + warp; t < t0 + TT * A.tiles && t < d.S; t += kFwdThreads / 32) {
+    const int w0 = t - d.W + 1 > 0 ? t - d.W + 1 : 0, far = d.ns < w0 ? d.ns : w0;  // sinks before the window
+    const int keys = far + t - w0 + 1;
+    auto key_of = [&](int x) { return x < far ? x : w0 + x - far; };
+    bool look = true;
+    for (int h = g * G; h < g * G + G; ++h) {
+      const long long row = ((seq + t) * d.Hq + h) * kD;
+      if (__all_sync(0xffffffffu, finite4(__ldcg(reinterpret_cast<const uint2*>(A.op + row) + lane)))) continue;
+      for (int x = 0; look && x < keys; x += 4) {
+        bool ok = true;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ok &= finite4(kv_row(A.vp, key_of(x + e < keys ? x + e : keys - 1)));
+        if (!__all_sync(0xffffffffu, ok)) goto next_token;  // seen, for every head of the group
+      }
+      look = false;
+      {
+        const float4 q = widen4(__ldg(reinterpret_cast<const uint2*>(A.qp + row) + lane));
+        float m = -INFINITY, l = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int x = 0; x < keys; x += 4) {
+          float s[4];
+          uint2 v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int key = key_of(x + e < keys ? x + e : keys - 1);
+            const float4 k = widen4(kv_row(A.kp, key));
+            v[e] = kv_row(A.vp, key);
+            s[e] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, q.w * k.w)));
+          }
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[e] += __shfl_xor_sync(0xffffffffu, s[e], off);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[e] = x + e < keys ? s[e] * sl2 : -INFINITY;
+          const float mn = fmaxf(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])), m), alpha = exp2_ftz(m - mn);
+          m = mn;
+          l *= alpha;
+          acc.x *= alpha;
+          acc.y *= alpha;
+          acc.z *= alpha;
+          acc.w *= alpha;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float p = exp2_ftz(s[e] - mn);
+            const float4 f = widen4(v[e]);
+            l += p;
+            acc.x = fmaf(p, f.x, acc.x);
+            acc.y = fmaf(p, f.y, acc.y);
+            acc.z = fmaf(p, f.z, acc.z);
+            acc.w = fmaf(p, f.w, acc.w);
+          }
+        }
+        const float sc = 1.f / l;
+        reinterpret_cast<uint2*>(A.op + row)[lane] =
+            make_uint2(pack_bf16(acc.x * sc, acc.y * sc), pack_bf16(acc.z * sc, acc.w * sc));
+      }
+    }
+  next_token:;
+  }
 }
 
 }  // namespace
@@ -117,6 +210,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) win_fwd_kernel(const __grid_co
       mbar_init(&sh->kv_empty[x], 1);
     }
     mbar_init(&sh->mma_done, 1);
+    sh->bad0 = INT_MAX;
+    sh->bad1 = -1;
     mbar_fence_init();
   }
   if (warp == 0) {
@@ -364,6 +459,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1) win_fwd_kernel(const __grid_co
       fence_before_sync();  // O_X may now take the next unit's products
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->o_free[X]);
+      float nf = 0.f;  // NaN where a value is not finite
+#pragma unroll
+      for (int c = 0; c < 32; ++c) nf = fmaf(__uint_as_float(v0[c]), 0.f, fmaf(__uint_as_float(v1[c]), 0.f, nf));
+      if (nf != 0.f) {
+        atomicMin(&sh->bad0, nu);
+        atomicMax(&sh->bad1, nu);
+      }
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
         const uint32_t(&v)[32] = c < 4 ? v0 : v1;
@@ -385,6 +487,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) win_fwd_kernel(const __grid_co
   __syncthreads();
   fence_after_sync();
   if (warp == 0) tmem_dealloc(tmem, 512);
+  for (int nu = sh->bad0; nu <= sh->bad1; ++nu) mend_rows<G>(A, blockIdx.x + nu * gridDim.x);
 }
 
 // The three maps of K or V.  nsp mod 128 rows of the shared tile are sinks (0: there is no such tile,
@@ -420,6 +523,10 @@ bool launch_win_fwd(const WinDims& d, const void* q, const void* k, const void* 
       !make_tmap_rows(&a.o, o, d.B, d.S, d.Hq, d.G, kBlock / d.G))
     return false;
   a.d = d;
+  a.qp = (const bf16*)q;
+  a.kp = (const bf16*)k;
+  a.vp = (const bf16*)v;
+  a.op = (bf16*)o;
   a.lse = lse;
   a.status = status;
   a.unit_ns = win_unit_wait_ns(d);

@@ -205,9 +205,11 @@ MSA_API int msa_decode(const msa_shape_t* shape, const void* q, const void* qp,
  * stand between sparse ones.  Query t sees key j iff j <= t and (t - j < window or j < sinks); a
  * window of S or more is dense causal attention.  Layouts as above: q, o, dout, dq [B, S, Hq, 128],
  * k, v, dk, dv [B, S, Hkv, 128], lse [B, Hq, S].  Supported: head dim 128, any 1 <= S <= 2^23,
- * Hq / Hkv in {1, 2, 4, 8, 16}, window >= 1, sinks >= 0.  Inputs must be finite: an infinity or NaN
- * in a K or V row reaches the queries whose tiles load it, also those whose window does not hold it
- * (the decode step masks such rows exactly).
+ * Hq / Hkv in {1, 2, 4, 8, 16}, window >= 1, sinks >= 0.  Whatever a K or V row holds, also an
+ * infinity or NaN (the uninitialised padding behind a ragged prompt), the forward and the decode step
+ * keep it from the queries that do not see it; a query that sees one that is not finite has an
+ * undefined row.  The backward's inputs must be finite: every key is seen by a query, its own, whose
+ * gradients would reach all the keys that it sees.
  */
 typedef struct msa_window_shape {
   int32_t B;       /* batch */
