@@ -1247,7 +1247,7 @@ int msa_window_backward(const msa_window_shape_t* shape, const void* q, const vo
   if ((rc = check_ws_bytes(p.bytes, workspace, workspace_bytes))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaGetLastError();
-  unsigned* status = at<unsigned>(workspace, 0);  // cleared by the first kernel
+  unsigned* status = at<unsigned>(workspace, 0);  // cleared by launch_win_dq
   float2* rowdata = at<float2>(workspace, p.rowm);
   if (d.G == 1 && d.W + d.ns <= kFewKeys) {
     timed("win_rowdata", st, [&] { launch_win_rowdata(d, q, k, v, dout, lse, rowdata, st); });

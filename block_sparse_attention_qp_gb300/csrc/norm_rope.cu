@@ -18,7 +18,8 @@
 // Work: 16 lanes hold a row (16 bytes a lane), a warp two tokens at a time, and walks the token's
 // heads with its angles in registers, so they are computed once a token and part list, not once a
 // head.  Bound by memory: forward reads and writes 256 bytes a row (6.0 TB/s at 64K tokens x 89 heads, 494
-// us), backward reads 512 and writes 256 (5.8 TB/s, 768 us with the join of dw); a copy runs at 6.7.
+// us), backward reads 512 (256 where a part has no weight) and writes 256 (5.7 TB/s, 768 us with the join of
+// dw); a copy runs at 6.7.
 // Few tokens: the heads of a token are split over warps so that a decode step still spreads over SMs.
 // dw: per-warp sums in shared memory, one partial per block, then a second kernel adds the blocks'
 // partials in a fixed order: no atomics, the same bits every time.

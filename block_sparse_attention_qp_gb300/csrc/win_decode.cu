@@ -340,7 +340,10 @@ __global__ void __launch_bounds__(kJoinThreads) win_decode_join_kernel(int B, in
 
 // Splits of the key tiles: as many as fill the resident blocks, one where the (b, KV head) pairs do (1024
 // pairs of nine tiles, 2.25 waves: 100 us whole, 117 in two parts, 119 in three or four; 8 pairs of 257 tiles
-// in 52 parts: 29 us and 8 of joining, while whole they would use 8 SMs).
+// in 52 parts: 29 us and 8 of joining, while whole they would use 8 SMs).  Pairs that fill half of the
+// resident blocks already stay whole: fewer blocks an SM have the bandwidth (64 tiles a pair: 224 pairs in two
+// parts 6.2 TB/s, 232 whole 6.6, 456 whole 6.7); just above all of them a second wave costs a fifth (464 pairs:
+// 5.3 TB/s, 608: 6.6).
 WinSplit win_decode_split(const WinDims& d) {
   WinSplit w;
   const long long keys = (long long)d.W + d.nsp < d.S ? (long long)d.W + d.nsp : d.S;

@@ -63,8 +63,8 @@ struct KeyMaps {
 };
 bool make_key_maps(const WinDims& d, const void* base, KeyMaps* m);  // win_fwd.cu
 
-// The status area is cleared by the first block of a call's first kernel instead of a memset in front
-// of it: a flag another block sets (a wait that gave up) is set 200 ms later at the earliest.
+// The status area is cleared by the first block of the call's first kernel that uses it (in the backward
+// win_dq_kernel, behind the row data) instead of a memset in front of it: a flag another block sets (a wait that gave up) is set 200 ms later at the earliest.
 __device__ __forceinline__ void clear_status(unsigned* status) {
   if (blockIdx.x == 0 && threadIdx.x < 32) status[threadIdx.x] = 0u;
 }

@@ -210,6 +210,9 @@ MSA_API int msa_decode(const msa_shape_t* shape, const void* q, const void* qp,
  * keep it from the queries that do not see it; a query that sees one that is not finite has an
  * undefined row.  The backward's inputs must be finite: every key is seen by a query, its own, whose
  * gradients would reach all the keys that it sees.
+ * P and dS enter their products as bf16, as in the sparse ops, everything else is fp32: relative errors
+ * are 2.1e-3 for o and 2.4e-3 for dq and dk, where rounding the exact result to bf16 once gives 1.7e-3.
+ * The decode step of groups of up to eight heads keeps P's rounding errors too (1.7e-3).
  */
 typedef struct msa_window_shape {
   int32_t B;       /* batch */
