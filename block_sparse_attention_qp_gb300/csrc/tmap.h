@@ -37,12 +37,12 @@ inline bool make_tmap_bf16(CUtensorMap* m, const void* base, int rank, const uin
 }
 
 // bf16 rows [B][S][H][128] (contiguous): box of 64 columns x `heads` x `rows` tokens of one sequence,
-// landing as rows * heads rows of 128 bytes, 128-byte swizzled.  Tokens past S read as zero and are
-// not written.
-inline bool make_tmap_rows(CUtensorMap* m, const void* base, int B, int S, int H, int heads, int rows) {
+// landing as rows * heads rows of 128 bytes, 128-byte swizzled.  Tokens past S (or past `last`) read as
+// zero and are not written.
+inline bool make_tmap_rows(CUtensorMap* m, const void* base, int B, int S, int H, int heads, int rows, int last = 0) {
   auto enc = tmap_encoder();
   if (!enc) return false;
-  const cuuint64_t dims[4] = {128, (cuuint64_t)H, (cuuint64_t)S, (cuuint64_t)B};
+  const cuuint64_t dims[4] = {128, (cuuint64_t)H, (cuuint64_t)(last ? last : S), (cuuint64_t)B};
   const cuuint64_t str[3] = {256, (cuuint64_t)H * 256, (cuuint64_t)S * H * 256};
   const cuuint32_t box[4] = {64, (cuuint32_t)heads, (cuuint32_t)rows, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};

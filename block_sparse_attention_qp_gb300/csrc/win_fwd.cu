@@ -101,10 +101,11 @@ __device__ __forceinline__ float4 widen4(uint2 w) {
 
 // O rows again that an infinity or NaN has reached through a V row which the query does not see: a
 // product of the tensor core takes whole tiles, and P = 0 times NaN is NaN.  A warp takes a token and
-// its group's heads, four dims a lane, and adds up the visible keys alone (the LSE needs nothing: masked
-// scores never enter it).  A query that sees such a V row itself is left as it is.  Runs behind the block's last
-// store and only where an epilogue met a value that is not finite, so that it costs other calls nothing
-// but the look.
+// its group's heads, four dims a lane, and adds up the visible keys alone.  Only rows with an LSE (masked
+// scores never enter it: without one the row's own scores are not finite), with such a V row among the few
+// that their tiles hold unseen, and with none that they see are computed again; the others stay as they
+// are, so a run that has diverged costs a look at its rows.  Runs behind the block's last store and only
+// where an epilogue met a value that is not finite.
 template <int G>
 __device__ __noinline__ void mend_rows(const FwdArgs& A, int u) {
   constexpr int TT = 128 / G;
@@ -113,23 +114,35 @@ __device__ __noinline__ void mend_rows(const FwdArgs& A, int u) {
   const int b = u % per / d.Hkv, g = u % per % d.Hkv, t0 = u / per * TT * A.tiles;
   const float sl2 = d.scale * kLog2e;
   const long long seq = (long long)b * d.S;
+  const int t1 = t0 + TT * A.tiles - 1 < d.S ? t0 + TT * A.tiles - 1 : d.S - 1;
+  const KeyRun run = key_run(d, t0, t1);
   auto kv_row = [&](const bf16* x, int key) {
     return __ldg(reinterpret_cast<const uint2*>(x + ((seq + key) * d.Hkv + g) * kD) + lane);
   };
-  for (int t = t0 + warp; t < t0 + TT * A.tiles && t < d.S; t += kFwdThreads / 32) {
+  auto v_finite = [&](auto key_of, int n) {  // V rows key_of(0) .. key_of(n - 1), four at a time
+    for (int x = 0; x < n; x += 4) {
+      bool ok = true;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) ok &= finite4(kv_row(A.vp, key_of(x + e < n ? x + e : n - 1)));
+      if (!__all_sync(0xffffffffu, ok)) return false;
+    }
+    return true;
+  };
+  for (int t = t0 + warp; t <= t1; t += kFwdThreads / 32) {
     const int w0 = t - d.W + 1 > 0 ? t - d.W + 1 : 0, far = d.ns < w0 ? d.ns : w0;  // sinks before the window
     const int keys = far + t - w0 + 1;
     auto key_of = [&](int x) { return x < far ? x : w0 + x - far; };
+    // unseen in the unit's tiles: in front of the window (sinks are zero-filled to eight, see make_key_maps), and
+    // behind the token up to the last tile's end
+    const int c0 = run.ws ? run.ws : d.ns, n0 = w0 - c0, n1 = (t1 + kBlock < d.S ? t1 + kBlock : d.S) - t - 1;
     bool look = true;
     for (int h = g * G; h < g * G + G; ++h) {
       const long long row = ((seq + t) * d.Hq + h) * kD;
       if (__all_sync(0xffffffffu, finite4(__ldcg(reinterpret_cast<const uint2*>(A.op + row) + lane)))) continue;
-      for (int x = 0; look && x < keys; x += 4) {
-        bool ok = true;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) ok &= finite4(kv_row(A.vp, key_of(x + e < keys ? x + e : keys - 1)));
-        if (!__all_sync(0xffffffffu, ok)) goto next_token;  // seen, for every head of the group
-      }
+      if (!isfinite(__ldcg(A.lse + ((long long)b * d.Hq + h) * d.S + t))) continue;
+      if (look && ((v_finite([&](int x) { return c0 + x; }, n0) && v_finite([&](int x) { return t + 1 + x; }, n1)) ||
+                   !v_finite(key_of, keys)))
+        break;  // for every head of the group
       look = false;
       {
         const float4 q = widen4(__ldg(reinterpret_cast<const uint2*>(A.qp + row) + lane));
@@ -174,7 +187,6 @@ __device__ __noinline__ void mend_rows(const FwdArgs& A, int u) {
             make_uint2(pack_bf16(acc.x * sc, acc.y * sc), pack_bf16(acc.z * sc, acc.w * sc));
       }
     }
-  next_token:;
   }
 }
 
@@ -493,14 +505,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1) win_fwd_kernel(const __grid_co
   for (int nu = sh->bad0; nu <= sh->bad1; ++nu) mend_rows<G>(A, blockIdx.x + nu * gridDim.x);
 }
 
-// The three maps of K or V.  nsp mod 128 rows of the shared tile are sinks (0: there is no such tile,
-// and the two maps are not used).
+// The maps of K or V.  Those of sinks end at the last one, so that the rows up to a multiple of eight, which
+// most queries do not see, are zeros.  nsp mod 128 rows of the shared tile are sinks (0: there is no
+// such tile, and its two maps are not used).
 bool make_key_maps(const WinDims& d, const void* base, KeyMaps* m) {
   const int a = d.nsp % kBlock;
   if (!make_tmap_rows(&m->full, base, d.B, d.S, d.Hkv, 1, kBlock)) return false;
-  m->sink = m->rest = m->full;
-  return a == 0 || (make_tmap_rows(&m->sink, base, d.B, d.S, d.Hkv, 1, a) &&
-                    make_tmap_rows(&m->rest, base, d.B, d.S, d.Hkv, 1, kBlock - a));
+  m->head = m->sink = m->rest = m->full;
+  return (d.nsp < kBlock || make_tmap_rows(&m->head, base, d.B, d.S, d.Hkv, 1, kBlock, d.ns)) &&
+         (a == 0 || (make_tmap_rows(&m->sink, base, d.B, d.S, d.Hkv, 1, a, d.ns) &&
+                     make_tmap_rows(&m->rest, base, d.B, d.S, d.Hkv, 1, kBlock - a)));
 }
 
 // A unit's walk grows with the window: 65536 tiles at S = 2^23, 1.6 us each at 2,070 MHz and 2.2 at 1,507,

@@ -56,10 +56,10 @@ __device__ __forceinline__ void visible_cols(const WinDims& d, const KeyRun& r, 
   for (int q = 0; q < 4; ++q) m[q] = bit_range(0, sc - 1, q) | bit_range(lo - v0, hi - v0, q);
 }
 
-// Tensor maps of K or V [B, S, Hkv, 128]: boxes of a whole tile's rows, of the sink rows of a tile
-// shared by both parts, and of that tile's window rows.
+// Tensor maps of K or V [B, S, Hkv, 128]: boxes of a whole tile's rows (head: of sinks only), of the sink
+// rows of a tile shared by both parts, and of that tile's window rows.
 struct KeyMaps {
-  CUtensorMap full, sink, rest;
+  CUtensorMap full, head, sink, rest;
 };
 bool make_key_maps(const WinDims& d, const void* base, KeyMaps* m);  // win_fwd.cu
 
@@ -107,16 +107,18 @@ __device__ __forceinline__ void bulk_store_wait() {
   asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
 }
 
-// Tile n of a key run into dst (two SW128 panels of 128 rows); rows past the sequence are zeros.
+// Tile n of a key run into dst (two SW128 panels of 128 rows); rows past the sequence, and past the
+// sinks in their part, are zeros.
 // The barrier has been told to expect the whole tile.
 __device__ __forceinline__ void load_key_tile(uint8_t* dst, const KeyMaps& m, const KeyRun& r, int n,
                                               int head, int b, uint64_t* mbar) {
   constexpr int kPanel = kBlock * 128;
   const int v0 = n * kBlock;
   if (v0 >= r.nsp || v0 + kBlock <= r.nsp) {
+    const CUtensorMap* tm = v0 >= r.nsp ? &m.full : &m.head;
     const int row = v0 >= r.nsp ? r.ws + v0 - r.nsp : v0;
-    tma_load_rows(dst, &m.full, 0, head, row, b, mbar);
-    tma_load_rows(dst + kPanel, &m.full, 64, head, row, b, mbar);
+    tma_load_rows(dst, tm, 0, head, row, b, mbar);
+    tma_load_rows(dst + kPanel, tm, 64, head, row, b, mbar);
   } else {
     const int a = r.nsp - v0;  // = nsp mod 128, the box height of m.sink; a multiple of eight
     tma_load_rows(dst, &m.sink, 0, head, v0, b, mbar);

@@ -77,6 +77,44 @@ def test_every_row_not_finite():
     assert torch.isnan(o).all()
 
 
+@pytest.mark.parametrize("what", ["q", "k", "huge"])
+def test_diverged_inputs_cost_no_walk(what):
+    """Rows whose own scores are not finite, or that overflow with nothing unseen in their tiles, are not computed again:
+    a long dense call stays within five times a finite one's time (their walks, a warp a row, would take hundreds)."""
+    q, k, v, _ = tensors(1, 32768, 16, 2, seed=75)
+
+    def ms():
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        msa.msa_window_forward(q, k, v, 2 ** 30, 0, SCALE)
+        a.record()
+        for _ in range(3):
+            msa.msa_window_forward(q, k, v, 2 ** 30, 0, SCALE)
+        b.record()
+        b.synchronize()
+        return a.elapsed_time(b)
+
+    clean = ms()
+    if what == "huge":
+        v.fill_(3e38)
+        q.mul_(4)  # row maxima that move: O is held relative to an earlier one
+    else:
+        (q if what == "q" else k).fill_(NAN)
+    assert ms() <= 5 * clean
+
+
+@pytest.mark.parametrize("ns", [1, 125, 131])
+def test_rows_beside_the_sinks(ns):
+    """Sinks are loaded in eights: the rows up to the next multiple reach no later query (125: within a whole tile)."""
+    q, k, v, _ = tensors(1, 3000, 16, 2, seed=76)
+    bad = torch.zeros(1, 3000, dtype=torch.bool, device=DEV)
+    bad[0, ns:ns + 2] = True
+    k[bad], v[bad] = NAN, NAN
+    check_rows(q, k, v, bad, 200, ns)
+    n = torch.tensor([3000], dtype=torch.int32, device=DEV)
+    o, _ = msa.msa_window_decode(q[:, -1].contiguous(), k, v, n, 200, ns, SCALE)
+    assert torch.isfinite(o).all()
+
+
 def test_captured_and_autograd():
     q, k, v, do = tensors(2, 200, 8, 2, seed=74)
     want, _ = forward(q, k, v, 50, 4)
