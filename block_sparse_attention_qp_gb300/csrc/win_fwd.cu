@@ -16,8 +16,8 @@
 // mend_rows.  A row may see nothing of a tile (its maximum then stays -inf until it does).
 //
 // 4 x 128 flops a visible pair, and the tiles cost about (W + 256/G + 128) / W of that; K and V come
-// through L2.  1,420 TFLOP/s of visible pairs at 32K tokens, 32 / 8 heads, window 2048 (753 us), 990 at 64K
-// tokens, 64 / 8 heads, window 512 (1.11 ms), where the tiles hold 1.2 times the visible pairs.  Bound by
+// through L2.  1,420 TFLOP/s of visible pairs at 32K tokens, 32 / 8 heads, window 2048 (754 us), 1,030 at 64K
+// tokens, 64 / 8 heads, window 512 (1.07 ms), where the tiles hold 1.2 times the visible pairs.  Bound by
 // the hand-offs of the chain S, softmax, P V of a tile: without exponentials, loads and seven of eight
 // products an earlier form took 690 of its 840 us.  The order of products is
 // O_A(n-1) S_A(n) O_B(n-1) S_B(n), so the softmax of one tile runs behind the products of the other.
@@ -56,10 +56,10 @@ struct FwdArgs {
   bf16* op;
   float* lse;
   unsigned* status;
-  unsigned long long unit_ns;  // win_unit_wait_ns
   int tiles;        // query tiles per unit, 1 or 2
   int nseg;         // units along a sequence
   int units;  // nseg B Hkv
+  unsigned long long unit_ns;  // win_unit_wait_ns
 };
 constexpr int kFwdThreads = 640;
 struct FwdShared {
@@ -105,9 +105,10 @@ __device__ __forceinline__ float4 widen4(uint2 w) {
 // scores never enter it: without one the row's own scores are not finite), with such a V row among the few
 // that their tiles hold unseen, and with none that they see are computed again; the others stay as they
 // are, so a run that has diverged costs a look at its rows.  Runs behind the block's last store and only
-// where an epilogue met a value that is not finite.
+// where an epilogue met a value that is not finite: 754 us at 32K tokens with it, 748 without, 1,069 and 1,096
+// at 64K, 217 and 219 at 2 x 8192 (inlined; as a function call 760, 1,081 and 221).
 template <int G>
-__device__ __noinline__ void mend_rows(const FwdArgs& A, int u) {
+__device__ __forceinline__ void mend_rows(const FwdArgs& A, int u) {
   constexpr int TT = 128 / G;
   const WinDims& d = A.d;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, per = d.B * d.Hkv;
