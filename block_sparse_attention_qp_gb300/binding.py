@@ -17,7 +17,9 @@ What stands around sparse attention in a model:
   heads, the last one into the decode caches), with the autograd functions msa_norm_rope_func and
   msa_norm_rope_packed_func;
   msa_window_forward, msa_window_backward, msa_window_decode (causal attention over a sliding window
-  and the first tokens), with the autograd function msa_window_func.
+  and the first tokens), with the autograd function msa_window_func;
+  msa_q4_cache, msa_q4_read, msa_window_decode_q4, msa_decode_q4 (K and V caches in 4 bits, which
+  msa_norm_rope_append writes too).
 """
 from __future__ import annotations
 
@@ -35,7 +37,9 @@ LIB_PATH = os.path.join(_HERE, "libmsa.so")
 OP_FORWARD, OP_BACKWARD, OP_WARMUP_FORWARD, OP_WARMUP_BACKWARD, OP_DECODE = 0, 1, 2, 3, 4
 OP_WINDOW_FORWARD, OP_WINDOW_BACKWARD, OP_WINDOW_DECODE = 5, 6, 7
 OP_NORM_ROPE_BACKWARD, OP_NORM_ROPE_APPEND = 8, 9
-ROPE_ROTATE, ROPE_CACHE, ROPE_PARTS = 1, 2, 8
+OP_DECODE_Q4, OP_WINDOW_DECODE_Q4 = 10, 11
+ROPE_ROTATE, ROPE_CACHE, ROPE_CACHE_Q4, ROPE_PARTS, ROPE_AXES = 1, 2, 8, 8, 4
+Q4_BLOCK_BYTES = 128 * 73  # 128 rows of a cache in 4 bits
 STATUS_BITS = {1: "bad block index", 2: "work list overflow", 4: "device wait timeout",
                8: "internal layout check"}
 _SYMBOLS = ("msa_workspace_size", "msa_forward", "msa_backward", "msa_warmup_forward",
@@ -44,7 +48,9 @@ _SYMBOLS = ("msa_workspace_size", "msa_forward", "msa_backward", "msa_warmup_for
             "msa_forward_noalloc_status", "msa_selftest_wait_timeout", "msa_decode",
             "msa_window_workspace_size", "msa_window_wait_limit_ms", "msa_window_forward", "msa_window_backward",
             "msa_window_decode", "msa_norm_rope_forward", "msa_norm_rope_append",
-            "msa_norm_rope_backward", "msa_norm_rope_workspace_size")
+            "msa_norm_rope_backward", "msa_norm_rope_workspace_size", "msa_norm_rope_axes_forward",
+            "msa_norm_rope_axes_append", "msa_norm_rope_axes_backward", "msa_q4_cache_bytes",
+            "msa_q4_read", "msa_window_decode_q4", "msa_decode_q4")
 
 
 class MSAError(RuntimeError):
@@ -75,6 +81,10 @@ class RopeShape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("N", ctypes.c_int32), ("D", ctypes.c_int32),
                 ("rotary", ctypes.c_int32), ("interleaved", ctypes.c_int32),
                 ("capacity", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class RopeAxes(ctypes.Structure):
+    _fields_ = [("count", ctypes.c_int32), ("of_pair", ctypes.c_uint8 * 64)]
 
 
 _lib = None
@@ -121,6 +131,18 @@ def load_library(path: str = LIB_PATH):
         lib.msa_norm_rope_workspace_size.restype = Z
         for name in ("msa_window_forward", "msa_window_backward", "msa_window_decode",
                      "msa_norm_rope_forward", "msa_norm_rope_append", "msa_norm_rope_backward"):
+            getattr(lib, name).restype = I
+        AP = ctypes.POINTER(RopeAxes)
+        lib.msa_norm_rope_axes_forward.argtypes = [RS, RP, I, P, P, AP, P]
+        lib.msa_norm_rope_axes_append.argtypes = [RS, RP, I, P, P, P, AP, P, Z, P]
+        lib.msa_norm_rope_axes_backward.argtypes = [RS, RP, I, P, P, AP, P, Z, P]
+        lib.msa_q4_cache_bytes.argtypes = [I, I, I]
+        lib.msa_q4_cache_bytes.restype = Z
+        lib.msa_q4_read.argtypes = [P, I, I, I, I, I, P, P]
+        lib.msa_window_decode_q4.argtypes = [WP, P, P, P, P, P, P, P, Z, P]
+        lib.msa_decode_q4.argtypes = [SP, P, P, P, P, P, P, P, P, P, P, Z, P]
+        for name in ("msa_norm_rope_axes_forward", "msa_norm_rope_axes_append", "msa_norm_rope_axes_backward",
+                     "msa_q4_read", "msa_window_decode_q4", "msa_decode_q4"):
             getattr(lib, name).restype = I
         lib.msa_status_string.argtypes = [I]
         lib.msa_status_string.restype = ctypes.c_char_p
@@ -728,7 +750,18 @@ def _on(t, name, device):
         raise MSAError(f"{name} is on {t.device}, the inputs on {device}")
 
 
-def _rope_args(xs, weights, rotate, inv_freq, interleaved, eps, positions, dev):
+@functools.lru_cache(maxsize=64)
+def _axes(axes, pairs):
+    """The library's form of the axis of each pair."""
+    if len(axes) != pairs:
+        raise MSAError(f"axes has {len(axes)} entries, one for each of the {pairs} pairs expected")
+    count = max(axes, default=0) + 1
+    if min(axes, default=0) < 0 or count > ROPE_AXES:
+        raise MSAError(f"axes must be 0 .. {ROPE_AXES - 1}, got {min(axes)} .. {count - 1}")
+    return RopeAxes(count, (ctypes.c_uint8 * 64)(*axes))
+
+
+def _rope_args(xs, weights, rotate, inv_freq, interleaved, eps, positions, dev, axes=None):
     """Checks what the norm and rotation entry points share; returns (shape, parts, inv_freq's and
     positions' addresses), a part being (x's pointer and strides, weight's address, heads, flags)."""
     count = len(xs)
@@ -752,7 +785,14 @@ def _rope_args(xs, weights, rotate, inv_freq, interleaved, eps, positions, dev):
         rotary = 2 * inv_freq.shape[0]
     elif any(rotate):
         raise MSAError("inv_freq is needed to rotate")
-    if positions is not None:
+    if axes is not None:
+        axes = _axes(tuple(axes), rotary // 2)
+        if positions is None:
+            raise MSAError("axes need positions")
+        # more axes than the pairs use may be there
+        A = _dims(positions, "positions", 3)[0]
+        pp = _ask(positions, "positions", torch.int32, (max(A, axes.count), B, N), dev)
+    elif positions is not None:
         pp = _ask(positions, "positions", torch.int32, (B, N), dev)
     return RopeShape(B, N, 128, rotary, 1 if interleaved else 0, 0, eps), parts, fp, pp
 
@@ -769,7 +809,7 @@ def _strides(t):
 
 
 def msa_norm_rope_forward(xs, weights, inv_freq, positions=None, eps: float = 1e-6, rotate=None,
-                          interleaved: bool = False):
+                          interleaved: bool = False, axes=None):
     """RMS norm of every head's row and the position rotation, in one pass over several tensors.
 
     xs: up to 8 tensors [B, N, heads, 128] bf16 -- q, k, the proxy heads -- usually the slices of one
@@ -777,27 +817,34 @@ def msa_norm_rope_forward(xs, weights, inv_freq, positions=None, eps: float = 1e
     weights: one fp32 [128] or None (not normed) per tensor.  inv_freq: fp32 [rotary / 2], the first
     ``rotary`` (a multiple of 16) elements of a row turn by position * inv_freq; None: no rotation.
     rotate: one truth value per tensor (default: all).  positions: int32 [B, N], default 0 .. N - 1.
+    axes: the axis (0 .. 3) of each of the rotary / 2 pairs, positions then int32 [axes, B, N] -- time, height
+    and width of images and video: pair i turns by positions[axes[i]] * inv_freq[i].
     A tensor without weight and rotation is copied.  Returns contiguous tensors [B, N, heads, 128]."""
     dev = _device_of(xs)
-    shape, parts, fp, pp = _rope_args(xs, weights, rotate, inv_freq, interleaved, eps, positions, dev)
+    shape, parts, fp, pp = _rope_args(xs, weights, rotate, inv_freq, interleaved, eps, positions, dev, axes)
     with _Guard(dev):
         ys = [torch.empty(x.shape, dtype=torch.bfloat16, device=dev) for x in xs]
         packed = b"".join([_PART.pack(*at, *_strides(y), 0, 0, 0, w, 0, h, f)
                            for (at, w, h, f), y in zip(parts, ys)])
-        rc = load_library().msa_norm_rope_forward(ctypes.byref(shape), packed, len(ys), pp, fp,
-                                                  _stream_of(dev))
+        if axes is None:
+            rc = load_library().msa_norm_rope_forward(ctypes.byref(shape), packed, len(ys), pp, fp,
+                                                      _stream_of(dev))
+        else:
+            rc = load_library().msa_norm_rope_axes_forward(ctypes.byref(shape), packed, len(ys), pp, fp,
+                                                           ctypes.byref(_axes(tuple(axes), shape.rotary // 2)),
+                                                           _stream_of(dev))
     if rc:
         _check(rc, "msa_norm_rope_forward")
     return tuple(ys)
 
 
 def msa_norm_rope_backward(xs, weights, dys, inv_freq, positions=None, eps: float = 1e-6,
-                           rotate=None, interleaved: bool = False, dxs=None, ws=None):
+                           rotate=None, interleaved: bool = False, dxs=None, ws=None, axes=None):
     """Gradients of msa_norm_rope_forward: (dxs, dweights), dweights fp32 [128] or None per tensor.
     dxs: where to write them (e.g. the slices of one packed gradient, or the dys), default new
     tensors; each may be its own part's x or dy, but overlap no other tensor of the call."""
     dev = _device_of(xs)
-    shape, parts, fp, pp = _rope_args(xs, weights, rotate, inv_freq, interleaved, eps, positions, dev)
+    shape, parts, fp, pp = _rope_args(xs, weights, rotate, inv_freq, interleaved, eps, positions, dev, axes)
     n = len(xs)
     if len(dys) != n or (dxs is not None and len(dxs) != n):
         raise MSAError("one dy (and dx, where given) per tensor")
@@ -816,29 +863,36 @@ def msa_norm_rope_backward(xs, weights, dys, inv_freq, positions=None, eps: floa
             if not w:
                 out_w[i] = None
         wp, wn, ws = _ws(ws, _rope_bytes(n, OP_NORM_ROPE_BACKWARD), dev)
-        rc = load_library().msa_norm_rope_backward(ctypes.byref(shape), b"".join(rows), n, pp, fp, wp,
-                                                   wn, _stream_of(dev))
+        if axes is None:
+            rc = load_library().msa_norm_rope_backward(ctypes.byref(shape), b"".join(rows), n, pp, fp, wp,
+                                                       wn, _stream_of(dev))
+        else:
+            rc = load_library().msa_norm_rope_axes_backward(ctypes.byref(shape), b"".join(rows), n, pp, fp,
+                                                            ctypes.byref(_axes(tuple(axes), shape.rotary // 2)),
+                                                            wp, wn, _stream_of(dev))
     if rc:
         _check(rc, "msa_norm_rope_backward")
     return tuple(out_x), tuple(out_w)
 
 
 def msa_norm_rope_append(xs, weights, inv_freq, seq_len, caches, eps: float = 1e-6, rotate=None,
-                         interleaved: bool = False, ws=None):
+                         interleaved: bool = False, ws=None, positions=None, axes=None):
     """Norm and rotation of the newest tokens of sequences of lengths seq_len [B] (int32 on the device),
     those with a cache written to their rows of it.
 
     xs: tensors [B, N, heads, 128] (or [B, heads, 128]: one token), token i at position
     seq_len - N + i.  caches: per tensor a cache [B, S, heads, 128] (one head: also [B, S, 128]) or
-    None.  Returns per tensor its cache, or a new tensor of the shape of x: for (q, k, v, qp, kp) with
+    None; a uint8 cache (msa_q4_cache) takes the rows in 4 bits.  positions, axes: as in
+    msa_norm_rope_forward, where the tokens' positions are not their rows in the caches (int32 [B, N], or
+    [axes, B, N]).  Returns per tensor its cache, or a new tensor of the shape of x: for (q, k, v, qp, kp) with
     caches (None, k_cache, v_cache, None, kp_cache) the arguments of msa_decode and
-    msa_window_decode.  Sequences with a length outside N .. S are skipped (msa_device_status of ws
+    msa_window_decode (msa_decode_q4 and msa_window_decode_q4).  Sequences with a length outside N .. S are skipped (msa_device_status of ws
     tells).  Caches may overlap neither each other nor the xs."""
     dev = _device_of(xs)
     x4 = xs
     if xs[0].dim() == 3:
         x4 = [x.unsqueeze(1) if isinstance(x, torch.Tensor) and x.dim() == 3 else x for x in xs]
-    shape, parts, fp, _ = _rope_args(x4, weights, rotate, inv_freq, interleaved, eps, None, dev)
+    shape, parts, fp, pp = _rope_args(x4, weights, rotate, inv_freq, interleaved, eps, positions, dev, axes)
     B = shape.B
     sp = _ask(seq_len, "seq_len", torch.int32, (B,), dev)
     if len(caches) != len(x4):
@@ -852,6 +906,13 @@ def msa_norm_rope_append(xs, weights, inv_freq, seq_len, caches, eps: float = 1e
                 y = torch.empty(xs[i].shape, dtype=torch.bfloat16, device=dev)
                 to = (y.data_ptr(), shape.N * h * 128, h * 128)
                 outs.append(y)
+            elif isinstance(c, torch.Tensor) and c.dtype is torch.uint8:
+                to = (_q4(c, f"caches[{i}]", (B, h), dev), 0, 0)
+                if capacity is not None and c.shape[2] * 128 != capacity:
+                    raise MSAError(f"caches of different capacities: {capacity}, {c.shape[2] * 128}")
+                capacity = c.shape[2] * 128
+                f |= ROPE_CACHE_Q4
+                outs.append(c)
             else:
                 c4 = c.unsqueeze(2) if isinstance(c, torch.Tensor) and c.dim() == 3 else c
                 to = _rows(c4, f"caches[{i}]", B, None, h, write=True)
@@ -865,8 +926,13 @@ def msa_norm_rope_append(xs, weights, inv_freq, seq_len, caches, eps: float = 1e
             rows.append(_PART.pack(*at, *to, 0, 0, 0, w, 0, h, f))
         shape.capacity = 2 ** 31 - 1 if capacity is None else capacity
         wp, wn, ws = _ws(ws, _rope_bytes(len(rows), OP_NORM_ROPE_APPEND), dev)
-        rc = load_library().msa_norm_rope_append(ctypes.byref(shape), b"".join(rows), len(rows), sp, fp,
-                                                 wp, wn, _stream_of(dev))
+        if pp is None:
+            rc = load_library().msa_norm_rope_append(ctypes.byref(shape), b"".join(rows), len(rows), sp, fp,
+                                                     wp, wn, _stream_of(dev))
+        else:
+            how = None if axes is None else ctypes.byref(_axes(tuple(axes), shape.rotary // 2))
+            rc = load_library().msa_norm_rope_axes_append(ctypes.byref(shape), b"".join(rows), len(rows), sp, pp,
+                                                          fp, how, wp, wn, _stream_of(dev))
     if rc:
         _check(rc, "msa_norm_rope_append")
     return tuple(outs)
@@ -875,20 +941,20 @@ def msa_norm_rope_append(xs, weights, inv_freq, seq_len, caches, eps: float = 1e
 class _NormRopeFunction(torch.autograd.Function):
     """tensors: the weights that are there, then either one packed x (heads given) or the xs."""
     @staticmethod
-    def forward(ctx, heads, has_w, inv_freq, positions, eps, rotate, interleaved, *tensors):
+    def forward(ctx, heads, has_w, inv_freq, positions, eps, rotate, interleaved, axes, *tensors):
         nw = sum(has_w)
         given, xs = list(tensors[:nw]), tensors[nw:]
         weights = [given.pop(0).detach().float().contiguous() if h else None for h in has_w]
         parts = xs[0].split(heads, 2) if heads is not None else xs
-        ys = msa_norm_rope_forward(parts, weights, inv_freq, positions, eps, rotate, interleaved)
+        ys = msa_norm_rope_forward(parts, weights, inv_freq, positions, eps, rotate, interleaved, axes)
         ctx.save_for_backward(inv_freq, positions, *xs, *(w for w in weights if w is not None))
-        ctx.how = (heads, has_w, eps, rotate, interleaved, len(xs), [t.dtype for t in tensors[:nw]])
+        ctx.how = (heads, has_w, eps, rotate, interleaved, axes, len(xs), [t.dtype for t in tensors[:nw]])
         return ys
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, *dys):
-        heads, has_w, eps, rotate, interleaved, nx, dtypes = ctx.how
+        heads, has_w, eps, rotate, interleaved, axes, nx, dtypes = ctx.how
         inv_freq, positions = ctx.saved_tensors[:2]
         xs, saved = ctx.saved_tensors[2:2 + nx], list(ctx.saved_tensors[2 + nx:])
         weights = [saved.pop(0) if h else None for h in has_w]
@@ -898,30 +964,126 @@ class _NormRopeFunction(torch.autograd.Function):
         else:
             parts, out = xs, None
         dxs, dws = msa_norm_rope_backward(parts, weights, [d.contiguous() for d in dys], inv_freq,
-                                          positions, eps, rotate, interleaved, dxs=out)
+                                          positions, eps, rotate, interleaved, dxs=out, axes=axes)
         grads = tuple(w.to(t) for w, t in zip((w for w in dws if w is not None), dtypes))
-        return (None,) * 7 + grads + ((dx,) if heads is not None else dxs)
+        return (None,) * 8 + grads + ((dx,) if heads is not None else dxs)
 
 
-def _norm_rope_apply(heads, xs, weights, inv_freq, positions, eps, rotate, interleaved):
+def _norm_rope_apply(heads, xs, weights, inv_freq, positions, eps, rotate, interleaved, axes):
     n = len(xs) if heads is None else len(heads)
     weights = [None] * n if weights is None else list(weights)
     rotate = None if rotate is None else [bool(r) for r in rotate]
     return _NormRopeFunction.apply(heads, [w is not None for w in weights], inv_freq, positions,
                                    float(eps), rotate, bool(interleaved),
-                                   *(w for w in weights if w is not None), *xs)
+                                   None if axes is None else tuple(axes), *(w for w in weights if w is not None), *xs)
 
 
 def msa_norm_rope_func(xs, weights, inv_freq, positions=None, eps: float = 1e-6, rotate=None,
-                       interleaved: bool = False):
+                       interleaved: bool = False, axes=None):
     """msa_norm_rope_forward with autograd: gradients of the xs and of the weights (any floating dtype;
     used in fp32)."""
-    return _norm_rope_apply(None, tuple(xs), weights, inv_freq, positions, eps, rotate, interleaved)
+    return _norm_rope_apply(None, tuple(xs), weights, inv_freq, positions, eps, rotate, interleaved, axes)
 
 
 def msa_norm_rope_packed_func(x, heads, weights, inv_freq, positions=None, eps: float = 1e-6,
-                              rotate=None, interleaved: bool = False):
+                              rotate=None, interleaved: bool = False, axes=None):
     """The same on one packed projection x [B, N, sum(heads), 128]: returns one contiguous tensor per
     entry of heads; the gradient of x is written packed, without a copy."""
     return _norm_rope_apply([int(h) for h in heads], (x,), weights, inv_freq, positions, eps, rotate,
-                            interleaved)
+                            interleaved, axes)
+
+
+# ---------------------------------------------------------------- caches in 4 bits
+def msa_q4_cache(B: int, heads: int, capacity: int, device) -> torch.Tensor:
+    """An empty cache in 4 bits for B sequences of up to ``capacity`` (a multiple of 128) tokens: uint8
+    [B, heads, capacity / 128, 9344], 73 bytes a row (include/msa.h has the format)."""
+    B, heads, capacity = int(B), int(heads), int(capacity)
+    if not load_library().msa_q4_cache_bytes(B, heads, capacity):
+        raise MSAError(load_library().msa_last_error().decode())
+    return torch.zeros((B, heads, capacity // 128, Q4_BLOCK_BYTES), dtype=torch.uint8, device=device)
+
+
+def _q4(t, name, lead, device):
+    """t is a cache in 4 bits with these first dimensions; returns its address."""
+    if isinstance(t, torch.Tensor) and t.dim() == 4 and t.shape[2] > 0:
+        return _ask(t, name, torch.uint8, (*lead, t.shape[2], Q4_BLOCK_BYTES), device)
+    _dims(t, name, 4)
+    raise MSAError(f"{name} has shape {tuple(t.shape)}, expected a cache of positive capacity")
+
+
+def msa_q4_read(cache, first: int, count: int):
+    """The values that rows first .. first + count - 1 of every sequence stand for: bf16 [B, count, heads, 128]
+    (exact: what the decode steps compute with)."""
+    B, H = _dims(cache, "cache", 4)[:2]
+    dev = cache.device
+    if not cache.is_cuda:
+        raise MSAError("cache must be a CUDA tensor")
+    cp = _q4(cache, "cache", (B, H), dev)
+    first, count = int(first), int(count)
+    if first < 0 or count < 1 or first + count > cache.shape[2] * 128:
+        raise MSAError(f"rows {first} .. {first + count - 1} are not in a cache of {cache.shape[2] * 128}")
+    with _Guard(dev):
+        out = torch.empty((B, count, H, 128), dtype=torch.bfloat16, device=dev)
+        rc = load_library().msa_q4_read(cp, B, H, cache.shape[2] * 128, first, count, out.data_ptr(), _stream_of(dev))
+    if rc:
+        _check(rc, "msa_q4_read")
+    return out
+
+
+def msa_window_decode_q4(q, k_cache, v_cache, seq_len, window: int, sinks: int, scale: float, ws=None):
+    """msa_window_decode over caches in 4 bits (msa_q4_cache, written by msa_norm_rope_append).  Returns
+    (o [B, Hq, 128], lse [B, Hq])."""
+    B, Hq, D = _dims(q, "q", 3)
+    dev = q.device
+    if not q.is_cuda:
+        raise MSAError("q must be a CUDA tensor")
+    _, Hkv, blocks, _ = _dims(k_cache, "k_cache", 4)
+    ptrs = (_ask(q, "q", torch.bfloat16, (B, Hq, D), dev), _q4(k_cache, "k_cache", (B, Hkv), dev),
+            _ask(v_cache, "v_cache", torch.uint8, k_cache.shape, dev),
+            _ask(seq_len, "seq_len", torch.int32, (B,), dev))
+    window, sinks, scale = _int32(window, "window"), _int32(sinks, "sinks"), float(scale)
+    shape = (B, blocks * 128, Hq, Hkv, D, window, sinks, scale)
+    with _Guard(dev):
+        wp, wn, ws = _ws(ws, _window_bytes(OP_WINDOW_DECODE_Q4, *shape) if ws is None else 0, dev)
+        o = torch.empty_like(q)
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+        rc = load_library().msa_window_decode_q4(ctypes.byref(WindowShape(*shape)), *ptrs, o.data_ptr(),
+                                                 lse.data_ptr(), wp, wn, _stream_of(dev))
+    if rc:
+        _check(rc, "msa_window_decode_q4")
+    return o, lse
+
+
+@functools.lru_cache(maxsize=1024)
+def _decode_q4_bytes(*shape):
+    return msa_workspace_size(Shape(*shape), OP_DECODE_Q4)
+
+
+def msa_decode_q4(q, qp, k_cache, v_cache, kp_cache, seq_len, top_k: int, scale: float, ws=None):
+    """msa_decode with K and V caches in 4 bits (kp_cache [B, S, 1, 128] or [B, S, 128] stays bf16, so the
+    selection is the same).  Returns (o [B, Hq, 128], lse [B, Hq], block_idx [B, Hp, top_k])."""
+    B, Hq, D = _dims(q, "q", 3)
+    Hp = _dims(qp, "qp", 3)[1]
+    dev = q.device
+    if not q.is_cuda:
+        raise MSAError("q must be a CUDA tensor")
+    _, Hkv, blocks, _ = _dims(k_cache, "k_cache", 4)
+    S = blocks * 128
+    if not isinstance(kp_cache, torch.Tensor):
+        raise TypeError("kp_cache must be a tensor")
+    ptrs = (_ask(q, "q", torch.bfloat16, (B, Hq, D), dev), _ask(qp, "qp", torch.bfloat16, (B, Hp, D), dev),
+            _q4(k_cache, "k_cache", (B, Hkv), dev), _ask(v_cache, "v_cache", torch.uint8, k_cache.shape, dev),
+            _ask(kp_cache, "kp_cache", torch.bfloat16, (B, S, D) if kp_cache.dim() == 3 else (B, S, 1, D), dev),
+            _ask(seq_len, "seq_len", torch.int32, (B,), dev))
+    shape = (B, S, Hq, Hkv, Hp, D, _int32(top_k, "top_k"), float(scale))
+    with _Guard(dev):
+        need = _decode_q4_bytes(*shape)
+        wp, wn, ws = _ws(ws, need, dev)
+        o = torch.empty_like(q)
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+        idx = torch.empty((B, Hp, shape[6]), dtype=torch.int32, device=dev)
+        rc = load_library().msa_decode_q4(ctypes.byref(Shape(*shape)), *ptrs, idx.data_ptr(), o.data_ptr(),
+                                          lse.data_ptr(), wp, wn, _stream_of(dev))
+    if rc:
+        _check(rc, "msa_decode_q4")
+    return o, lse, idx

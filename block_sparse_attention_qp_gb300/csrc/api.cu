@@ -16,6 +16,7 @@
 #include "../../include/msa.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "q4.cuh"
 
 namespace msa {
 namespace {
@@ -667,6 +668,9 @@ size_t rope_ws(int nparts, int op) {
   return 0;
 }
 
+// Bytes of a cache in 4 bits (q4.cuh).
+size_t q4_bytes(long long B, long long heads, long long capacity) { return (size_t)B * heads * (capacity / kBlock) * kQ4Block; }
+
 // The memory of a part's tensor: n[0] x n[1] runs of `len` bytes, s[0] >= s[1] >= 0 bytes apart.
 struct Runs {
   long long at, s[2], n[2], len, end;
@@ -747,9 +751,14 @@ int check_rope_outputs(const msa_rope_shape_t* s, const msa_rope_part_t* parts, 
   Runs in[2 * kRopeParts], out[kRopeParts];  // x, and behind them the dy
   for (int i = 0; i < nparts; ++i) {
     const msa_rope_part_t& p = parts[i];
-    const bool cache = p.flags & MSA_ROPE_CACHE;
+    const bool cache = p.flags & MSA_ROPE_CACHE, q4 = p.flags & MSA_ROPE_CACHE_Q4;
     in[i] = runs(p.x, s->B, p.x_batch, s->N, p.x_token, p.heads);
     const Runs y = runs(p.y, s->B, p.y_batch, cache ? s->capacity : s->N, p.y_token, p.heads);
+    if (q4) {  // one run
+      const long long at = (long long)reinterpret_cast<uintptr_t>(p.y), n = (long long)q4_bytes(s->B, p.heads, s->capacity);
+      out[i] = Runs{at, {0, 0}, {1, 1}, n, at + n};
+      continue;
+    }
     out[i] = bwd ? runs(p.dx, s->B, p.dx_batch, s->N, p.dx_token, p.heads) : y;
     if (bwd) in[nparts + i] = y;
     if (overlaps_itself(out[i])) {
@@ -769,7 +778,8 @@ int check_rope_outputs(const msa_rope_shape_t* s, const msa_rope_part_t* parts, 
     const void* to = bwd ? p.dx : p.y;
     const int64_t tob = bwd ? p.dx_batch : p.y_batch, tot = bwd ? p.dx_token : p.y_token;
     auto same_rows = [&](const void* from, int64_t sb, int64_t st) {  // row by row, not only as a whole
-      return from == to && (s->B == 1 || sb == tob) && (s->N == 1 || st == tot) && !(p.flags & MSA_ROPE_CACHE);
+      return from == to && (s->B == 1 || sb == tob) && (s->N == 1 || st == tot) &&
+             !(p.flags & (MSA_ROPE_CACHE | MSA_ROPE_CACHE_Q4));
     };
     for (int j = 0; j < (bwd ? 2 : 1) * nparts; ++j) {
       if (!overlap(out[i], in[j])) continue;
@@ -847,10 +857,15 @@ int check_rope(const msa_rope_shape_t* s, const msa_rope_part_t* parts, int npar
       set_err("a part has 1 .. 1024 heads");
       return MSA_ERR_UNSUPPORTED;
     }
-    if ((p.flags & ~(MSA_ROPE_ROTATE | MSA_ROPE_CACHE)) ||
-        ((p.flags & MSA_ROPE_CACHE) && op != MSA_OP_NORM_ROPE_APPEND)) {
+    const int caches = p.flags & (MSA_ROPE_CACHE | MSA_ROPE_CACHE_Q4);
+    if ((p.flags & ~(MSA_ROPE_ROTATE | MSA_ROPE_CACHE | MSA_ROPE_CACHE_Q4)) || (caches & (caches - 1)) ||
+        (caches && op != MSA_OP_NORM_ROPE_APPEND)) {
       set_err("unknown part flag, or MSA_ROPE_CACHE outside msa_norm_rope_append");
       return MSA_ERR_INVALID_ARG;
+    }
+    if ((p.flags & MSA_ROPE_CACHE_Q4) && s->capacity % kBlock) {
+      set_err("the capacity of a cache in 4 bits must be a multiple of 128");
+      return MSA_ERR_UNSUPPORTED;
     }
     if (bwd && p.dweight && !p.weight) {
       set_err("dweight of a part without a weight");
@@ -876,11 +891,60 @@ int check_rope(const msa_rope_shape_t* s, const msa_rope_part_t* parts, int npar
     o.w = p.weight;
     o.H = p.heads;
     o.flags = ((p.flags & MSA_ROPE_ROTATE) && a.rot > 0 ? kRopeRotate : 0) |
-              (p.flags & MSA_ROPE_CACHE ? kRopeCache : 0);
+              (p.flags & MSA_ROPE_CACHE ? kRopeCache : 0) | (p.flags & MSA_ROPE_CACHE_Q4 ? kRopeQ4 : 0);
     a.rows += p.heads;
   }
   if ((rc = check_rope_outputs(s, parts, nparts, op))) return rc;
   *out = a;
+  return MSA_OK;
+}
+
+// The axes of a rotation; positions [count][B][N] (checked as words by the caller).
+int check_axes(const msa_rope_axes_t* axes, const int32_t* positions, RopeArgs* a) {
+  if (!positions) {
+    set_err("positions is null");
+    return MSA_ERR_INVALID_ARG;
+  }
+  a->naxes = axes ? axes->count : 1;
+  if (a->naxes < 1 || a->naxes > kRopeAxes) {
+    set_err("positions have 1 .. 4 axes");
+    return MSA_ERR_UNSUPPORTED;
+  }
+  for (int i = 0; axes && i < a->rot / 2; ++i) {
+    if (axes->of_pair[i] >= a->naxes) {
+      set_err("a pair's axis is out of range");
+      return MSA_ERR_INVALID_ARG;
+    }
+    a->axis[i] = axes->of_pair[i];
+  }
+  a->positions = positions;
+  return MSA_OK;
+}
+
+// ---- caches in 4 bits
+struct Q4Plan {
+  size_t opart = 0, lpart = 0, bytes = 0;
+};
+Q4Plan q4_plan(size_t before, const WinSplit& w, long long rows) {  // behind `before` bytes of the call's own
+  Q4Plan p;
+  Carver c;
+  c.take(before);
+  const size_t n = w.nsplit > 1 ? (size_t)w.nsplit * rows : 0;
+  p.opart = c.take(n * kD * sizeof(float));
+  p.lpart = c.take(n * sizeof(float));
+  p.bytes = c.off;
+  return p;
+}
+Q4Plan q4_window_plan(const WinDims& d) { return q4_plan(256, q4_window_split(d), (long long)d.B * d.Hq); }
+Q4Plan q4_sparse_plan(const Dims& d, const Plan& p) { return q4_plan(p.bytes, q4_sparse_split(d), (long long)d.B * d.Hq); }
+
+int check_q4_window(const msa_window_shape_t* s, WinDims* d) {
+  const int rc = check_window(s, MSA_OP_WINDOW_DECODE, d);
+  if (rc) return rc;
+  if (s->S % kBlock) {
+    set_err("the capacity of a cache in 4 bits must be a multiple of 128");
+    return MSA_ERR_UNSUPPORTED;
+  }
   return MSA_OK;
 }
 
@@ -891,12 +955,66 @@ void set_api_error(const char* what) { set_err(what); }
 
 }  // namespace msa
 
+// The norm and rotation entry points, with and without axes (more: positions are theirs).
+namespace msa {
+namespace {
+
+int rope_forward(const msa_rope_shape_t* shape, const msa_rope_part_t* parts, int nparts, const int32_t* positions,
+                 const float* inv_freq, bool more, const msa_rope_axes_t* axes, void* stream, const char* name) {
+  RopeArgs a;
+  int rc = check_rope(shape, parts, nparts, positions, inv_freq, -1, &a);
+  if (rc || (more && (rc = check_axes(axes, positions, &a)))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaGetLastError();
+  timed("norm_rope_fwd", st, [&] { launch_norm_rope_fwd(a, st); });
+  return cuda_fail(name);
+}
+
+int rope_append(const msa_rope_shape_t* shape, const msa_rope_part_t* parts, int nparts, const int32_t* seq_len,
+                const int32_t* positions, const float* inv_freq, bool more, const msa_rope_axes_t* axes, void* workspace,
+                size_t workspace_bytes, void* stream, const char* name) {
+  RopeArgs a;
+  int rc = check_rope(shape, parts, nparts, seq_len, inv_freq, MSA_OP_NORM_ROPE_APPEND, &a);
+  if (rc || (more && ((rc = check_axes(axes, positions, &a)) || (rc = check_words(positions))))) return rc;
+  if ((rc = check_ws_bytes(kRopeStatus, workspace, workspace_bytes))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaGetLastError();
+  a.status = at<unsigned>(workspace, 0);  // written whole by the kernel
+  timed("norm_rope_append", st, [&] { launch_norm_rope_fwd(a, st); });
+  return cuda_fail(name);
+}
+
+int rope_backward(const msa_rope_shape_t* shape, const msa_rope_part_t* parts, int nparts, const int32_t* positions,
+                  const float* inv_freq, bool more, const msa_rope_axes_t* axes, void* workspace, size_t workspace_bytes,
+                  void* stream, const char* name) {
+  RopeArgs a;
+  int rc = check_rope(shape, parts, nparts, positions, inv_freq, MSA_OP_NORM_ROPE_BACKWARD, &a);
+  if (rc || (more && (rc = check_axes(axes, positions, &a)))) return rc;
+  if ((rc = check_ws_bytes(rope_ws(nparts, MSA_OP_NORM_ROPE_BACKWARD), workspace, workspace_bytes))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaGetLastError();
+  a.status = at<unsigned>(workspace, 0);
+  a.partial = at<float>(workspace, kRopeStatus);
+  int launches = 1;  // and one more to join the partials of the weights' gradients, where any is wanted
+  for (int i = 0; i < nparts; ++i)
+    if (a.p[i].dw) launches = 2;
+  timed("norm_rope_bwd", st, [&] { launch_norm_rope_bwd(a, st); }, launches);
+  return cuda_fail(name);
+}
+
+}  // namespace
+}  // namespace msa
+
 using namespace msa;
 
 extern "C" {
 
 size_t msa_workspace_size(const msa_shape_t* shape, int op) {
   Dims d;
+  if (op == MSA_OP_DECODE_Q4) {
+    if (check_shape(shape, MSA_OP_DECODE, &d) != MSA_OK) return 0;
+    return q4_sparse_plan(d, make_plan(d, MSA_OP_DECODE)).bytes;
+  }
   if (op < MSA_OP_FORWARD || op > MSA_OP_DECODE) return 0;
   if (check_shape(shape, op, &d) != MSA_OK) return 0;
   return make_plan(d, op).bytes;
@@ -1199,6 +1317,7 @@ int msa_decode(const msa_shape_t* shape, const void* q, const void* qp, const vo
 
 size_t msa_window_workspace_size(const msa_window_shape_t* shape, int op) {
   WinDims d;
+  if (op == MSA_OP_WINDOW_DECODE_Q4) return check_q4_window(shape, &d) == MSA_OK ? q4_window_plan(d).bytes : 0;
   if (op < MSA_OP_WINDOW_FORWARD || op > MSA_OP_WINDOW_DECODE) {
     set_err("not a window op");
     return 0;
@@ -1295,49 +1414,117 @@ int msa_window_decode(const msa_window_shape_t* shape, const void* q, const void
   return cuda_fail("msa_window_decode");
 }
 
+int msa_window_decode_q4(const msa_window_shape_t* shape, const void* q, const void* k_cache,
+                         const void* v_cache, const int32_t* seq_len, void* o, float* lse,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+  WinDims d;
+  int rc = check_q4_window(shape, &d);
+  if (rc) return rc;
+  if ((rc = check_ptrs({q, k_cache, v_cache, o, lse})) || (rc = check_words(seq_len))) return rc;
+  const Q4Plan p = q4_window_plan(d);
+  if ((rc = check_ws_bytes(p.bytes, workspace, workspace_bytes))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaGetLastError();
+  timed("q4_decode", st, [&] {
+    launch_q4_window(d, q, k_cache, v_cache, seq_len, o, lse, at<float>(workspace, p.opart), at<float>(workspace, p.lpart),
+                     at<unsigned>(workspace, 0), st);
+  }, q4_window_split(d).nsplit > 1 ? 2 : 1);
+  return cuda_fail("msa_window_decode_q4");
+}
+
+int msa_decode_q4(const msa_shape_t* shape, const void* q, const void* qp, const void* k_cache,
+                  const void* v_cache, const void* kp_cache, const int32_t* seq_len,
+                  int32_t* block_idx, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                  void* stream) {
+  Dims d;
+  int rc = check_shape(shape, MSA_OP_DECODE, &d);
+  if (rc) return rc;
+  if ((rc = check_ptrs({q, qp, k_cache, v_cache, kp_cache, block_idx, o, lse})) || (rc = check_words(seq_len))) return rc;
+  const Plan p = make_plan(d, MSA_OP_DECODE);
+  const Q4Plan p4 = q4_sparse_plan(d, p);
+  if ((rc = check_ws_bytes(p4.bytes, workspace, workspace_bytes))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaGetLastError();
+  unsigned* status = at<unsigned>(workspace, p.status);
+  cudaMemsetAsync(status, 0, 32 * sizeof(unsigned), st);  // status, counters, wait place
+  float* scores = at<float>(workspace, p.scores);
+  bool ok = true;
+  timed("decode_scores", st, [&] {
+    ok = launch_decode_scores(d, qp, kp_cache, seq_len, scores, status, st);
+  });
+  if (!ok) {
+    set_err("msa_decode_q4: could not create TMA tensor maps (cuTensorMapEncodeTiled)");
+    return MSA_ERR_CUDA;
+  }
+  timed("decode_select", st, [&] { launch_decode_select(d, scores, seq_len, block_idx, st); });
+  timed("q4_decode", st, [&] {
+    launch_q4_sparse(d, q, k_cache, v_cache, seq_len, block_idx, o, lse, at<float>(workspace, p4.opart),
+                     at<float>(workspace, p4.lpart), status, st);
+  }, q4_sparse_split(d).nsplit > 1 ? 2 : 1);
+  return cuda_fail("msa_decode_q4");
+}
+
+size_t msa_q4_cache_bytes(int32_t B, int32_t heads, int32_t capacity) {
+  if (B < 1 || heads < 1 || capacity < 1 || capacity % kBlock) {
+    set_err("a cache in 4 bits needs positive sizes and a capacity that is a multiple of 128");
+    return 0;
+  }
+  return q4_bytes(B, heads, capacity);
+}
+
+int msa_q4_read(const void* cache, int32_t B, int32_t heads, int32_t capacity, int32_t first, int32_t count, void* out,
+                void* stream) {
+  if (!msa_q4_cache_bytes(B, heads, capacity)) return MSA_ERR_INVALID_ARG;
+  if (first < 0 || count < 1 || count > capacity - first) {
+    set_err("the rows to read must lie in the cache");
+    return MSA_ERR_INVALID_ARG;
+  }
+  const int rc = check_ptrs({cache, out});
+  if (rc) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaGetLastError();
+  timed("q4_read", st, [&] { launch_q4_read(cache, B, heads, capacity, first, count, out, st); });
+  return cuda_fail("msa_q4_read");
+}
+
 size_t msa_norm_rope_workspace_size(int nparts, int op) { return rope_ws(nparts, op); }
 
 int msa_norm_rope_forward(const msa_rope_shape_t* shape, const msa_rope_part_t* parts, int nparts,
                           const int32_t* positions, const float* inv_freq, void* stream) {
-  RopeArgs a;
-  const int rc = check_rope(shape, parts, nparts, positions, inv_freq, -1, &a);
-  if (rc) return rc;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaGetLastError();
-  timed("norm_rope_fwd", st, [&] { launch_norm_rope_fwd(a, st); });
-  return cuda_fail("msa_norm_rope_forward");
+  return rope_forward(shape, parts, nparts, positions, inv_freq, false, nullptr, stream, "msa_norm_rope_forward");
 }
 
 int msa_norm_rope_append(const msa_rope_shape_t* shape, const msa_rope_part_t* parts, int nparts,
                          const int32_t* seq_len, const float* inv_freq, void* workspace,
                          size_t workspace_bytes, void* stream) {
-  RopeArgs a;
-  int rc = check_rope(shape, parts, nparts, seq_len, inv_freq, MSA_OP_NORM_ROPE_APPEND, &a);
-  if (rc) return rc;
-  if ((rc = check_ws_bytes(kRopeStatus, workspace, workspace_bytes))) return rc;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaGetLastError();
-  a.status = at<unsigned>(workspace, 0);  // written whole by the kernel
-  timed("norm_rope_append", st, [&] { launch_norm_rope_fwd(a, st); });
-  return cuda_fail("msa_norm_rope_append");
+  return rope_append(shape, parts, nparts, seq_len, nullptr, inv_freq, false, nullptr, workspace, workspace_bytes, stream,
+                     "msa_norm_rope_append");
 }
 
 int msa_norm_rope_backward(const msa_rope_shape_t* shape, const msa_rope_part_t* parts, int nparts,
                            const int32_t* positions, const float* inv_freq, void* workspace,
                            size_t workspace_bytes, void* stream) {
-  RopeArgs a;
-  int rc = check_rope(shape, parts, nparts, positions, inv_freq, MSA_OP_NORM_ROPE_BACKWARD, &a);
-  if (rc) return rc;
-  if ((rc = check_ws_bytes(rope_ws(nparts, MSA_OP_NORM_ROPE_BACKWARD), workspace, workspace_bytes))) return rc;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaGetLastError();
-  a.status = at<unsigned>(workspace, 0);
-  a.partial = at<float>(workspace, kRopeStatus);
-  int launches = 1;  // and one more to join the partials of the weights' gradients, where any is wanted
-  for (int i = 0; i < nparts; ++i)
-    if (a.p[i].dw) launches = 2;
-  timed("norm_rope_bwd", st, [&] { launch_norm_rope_bwd(a, st); }, launches);
-  return cuda_fail("msa_norm_rope_backward");
+  return rope_backward(shape, parts, nparts, positions, inv_freq, false, nullptr, workspace, workspace_bytes, stream,
+                       "msa_norm_rope_backward");
+}
+
+int msa_norm_rope_axes_forward(const msa_rope_shape_t* shape, const msa_rope_part_t* parts, int nparts,
+                               const int32_t* positions, const float* inv_freq, const msa_rope_axes_t* axes, void* stream) {
+  return rope_forward(shape, parts, nparts, positions, inv_freq, true, axes, stream, "msa_norm_rope_axes_forward");
+}
+
+int msa_norm_rope_axes_append(const msa_rope_shape_t* shape, const msa_rope_part_t* parts, int nparts,
+                              const int32_t* seq_len, const int32_t* positions, const float* inv_freq,
+                              const msa_rope_axes_t* axes, void* workspace, size_t workspace_bytes, void* stream) {
+  return rope_append(shape, parts, nparts, seq_len, positions, inv_freq, true, axes, workspace, workspace_bytes, stream,
+                     "msa_norm_rope_axes_append");
+}
+
+int msa_norm_rope_axes_backward(const msa_rope_shape_t* shape, const msa_rope_part_t* parts, int nparts,
+                                const int32_t* positions, const float* inv_freq, const msa_rope_axes_t* axes,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  return rope_backward(shape, parts, nparts, positions, inv_freq, true, axes, workspace, workspace_bytes, stream,
+                       "msa_norm_rope_axes_backward");
 }
 
 int msa_device_status(void* workspace, unsigned* flags, void* stream) {

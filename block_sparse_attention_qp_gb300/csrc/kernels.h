@@ -153,13 +153,15 @@ bool launch_decode_attn(const Dims& d, const void* q, const void* k_cache, const
                         unsigned* status, cudaStream_t st);  // false: no tensor map
 
 // ------------------------------------------- norm and rotation of the heads (norm_rope.cu)
-constexpr int kRopeRotate = 1, kRopeCache = 2;  // RopePart::flags
+constexpr int kRopeRotate = 1, kRopeCache = 2, kRopeQ4 = 8;  // RopePart::flags
+constexpr int kRopeAxes = 4;                    // axes of positions at most
 constexpr int kRopeParts = 8;                   // parts of one call at most
 // One part: H consecutive heads (128 elements apart) of every token, with its own norm weight.
 struct RopePart {
   const __nv_bfloat16* x;  // [B][N][H][128], batch and token strides in elements
   long long xb, xt;
-  __nv_bfloat16* y;  // forward: the output (kRopeCache: its rows by position); backward: dy (read)
+  __nv_bfloat16* y;  // forward: the output (kRopeCache: its rows by position; kRopeQ4: a cache in 4 bits,
+                     // without strides); backward: dy (read)
   long long yb, yt;
   __nv_bfloat16* dx;
   long long dxb, dxt;
@@ -171,12 +173,14 @@ struct RopeArgs {
   int B, N, rot, inter, nparts, rows;  // rows: heads of all parts
   int cap;                             // append: rows of a cache
   float eps;
-  const int32_t* positions;  // [B][N] or NULL: 0 .. N - 1
+  const int32_t* positions;  // [B][N] or NULL: 0 .. N - 1; with axes [naxes][B][N]
   const int32_t* seq_len;    // append: [B], the new tokens are the last N of it
   const float* inv_freq;     // [rot / 2]
   unsigned* status;          // append, backward: written whole by the call
   float* partial;            // backward: [rope_partials()][nparts][128]
   int rows_chunk, chunks;    // set by the launch
+  int naxes;                 // 0: positions as above, in an append those of the cache rows
+  uint8_t axis[64];          // of each of the rot / 2 pairs
   RopePart p[kRopeParts];
 };
 int rope_partials();
@@ -227,6 +231,24 @@ WinSplit win_decode_split(const WinDims& d);
 bool launch_win_decode(const WinDims& d, const void* q, const void* k_cache, const void* v_cache,
                        const int32_t* seq_len, void* o, float* lse, float* opart, float* lpart,
                        unsigned* status, cudaStream_t st);
+
+// Joins the splits of a decode step (win_decode.cu): opart [nsplit][B][Hq][128] normalised, lpart
+// [nsplit][B][Hq] in log2 units, -inf for an empty split; sequences whose length is not in 1 .. cap are skipped.
+void launch_decode_join(int B, int Hq, int cap, int nsplit, const int32_t* seq_len, const float* opart,
+                        const float* lpart, void* o, float* lse, cudaStream_t st);
+
+// ------------------------------------------- caches in 4 bits (q4.cuh, q4.cu)
+// Decode steps over K and V caches [B][Hkv][capacity / 128][9344 bytes]; d.S is the capacity.
+WinSplit q4_window_split(const WinDims& d);
+WinSplit q4_sparse_split(const Dims& d);
+void launch_q4_window(const WinDims& d, const void* q, const void* k, const void* v, const int32_t* seq_len, void* o,
+                      float* lse, float* opart, float* lpart, unsigned* status, cudaStream_t st);
+// Over the key blocks block_idx [B, Hp, top_k] of launch_decode_select.
+void launch_q4_sparse(const Dims& d, const void* q, const void* k, const void* v, const int32_t* seq_len,
+                      const int32_t* block_idx, void* o, float* lse, float* opart, float* lpart, unsigned* status,
+                      cudaStream_t st);
+// Rows first .. first + count - 1 of every sequence and head: out [B, count, H, 128] bf16.
+void launch_q4_read(const void* cache, int B, int H, int cap, int first, int count, void* out, cudaStream_t st);
 
 int num_sms();
 void set_api_error(const char* what);

@@ -25,6 +25,7 @@
 // partials in a fixed order: no atomics, the same bits every time.
 #include "common.cuh"
 #include "kernels.h"
+#include "q4.cuh"
 
 namespace msa {
 namespace {
@@ -56,9 +57,11 @@ __device__ __forceinline__ void load_w(const float* w, int l, float (&f)[8]) {
   f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
 }
 
-// The block's frequencies as 64-bit fractions of a turn.
-__device__ __forceinline__ void load_freqs(const RopeArgs& A, unsigned long long* sF) {
+// The block's frequencies as 64-bit fractions of a turn (and the pairs' axes).
+template <bool kMore>
+__device__ __forceinline__ void load_freqs(const RopeArgs& A, unsigned long long* sF, uint8_t* sA) {
   const int i = threadIdx.x;
+  if (kMore && i < 64) sA[i] = A.axis[i];
   if (i < A.rot / 2) {
     // |f| / 2 pi as a sum of doubles t + lo: the product with the constant's upper half exact (a fused
     // multiply-add gives its rounding error), its lower half's added.  Whole turns go from t exactly.
@@ -79,9 +82,9 @@ __device__ __forceinline__ void load_freqs(const RopeArgs& A, unsigned long long
 struct Turn {
   float c[8], s[8];
 };
-template <bool kInter>
-__device__ __forceinline__ void make_turn(const RopeArgs& A, const unsigned long long* sF, int l,
-                                          int pos, float dir, Turn& t) {
+template <bool kInter, bool kMore>
+__device__ __forceinline__ void make_turn(const RopeArgs& A, const unsigned long long* sF, const uint8_t* sA, int l,
+                                          int pos, long long tok, float dir, Turn& t) {
   const int half = A.rot / 2;
   const bool in = 8 * l < A.rot;
 #pragma unroll
@@ -90,9 +93,18 @@ __device__ __forceinline__ void make_turn(const RopeArgs& A, const unsigned long
     t.s[i] = 0.f;
   }
   if (!in) return;
+  int at[kRopeAxes];
+  if (kMore && A.naxes) {
+#pragma unroll
+    for (int x = 0; x < kRopeAxes; ++x) at[x] = __ldg(A.positions + (x < A.naxes ? x : 0) * ((long long)A.B * A.N) + tok);
+  }
 #pragma unroll
   for (int i = 0; i < (kInter ? 4 : 8); ++i) {
     const int e = kInter ? 4 * l + i : (8 * l < half ? 8 * l + i : 8 * l + i - half);
+    if (kMore && A.naxes) {
+      const int x = sA[e];
+      pos = x == 0 ? at[0] : x == 1 ? at[1] : x == 2 ? at[2] : at[3];
+    }
     const unsigned long long a = (unsigned long long)(long long)pos * sF[e];
     const int turn = (int)(a >> 32);  // in 2^-32 turns, -1/2 .. 1/2
     float sn, cs;
@@ -121,7 +133,8 @@ __device__ __forceinline__ void turn_row(const Turn& t, int partner, float (&u)[
 // the token's heads.  Warp-uniform but for the token; a half-warp past the last token repeats it
 // (its loads are valid) and stores nothing.
 struct Unit {
-  int b, i, pos, r0, r1;
+  long long tok;
+  int b, i, pos, r0, r1;  // pos: with axes a cache's row only
   bool live;
 };
 __device__ __forceinline__ Unit rope_unit(const RopeArgs& A, long long wu, int hw) {
@@ -131,6 +144,7 @@ __device__ __forceinline__ Unit rope_unit(const RopeArgs& A, long long wu, int h
   long long tok = (wu % pairs) * 2 + hw;
   u.live = tok < T;
   if (!u.live) tok = T - 1;
+  u.tok = tok;
   u.b = (int)(tok / A.N);
   u.i = (int)(tok % A.N);
   u.r0 = chunk * A.rows_chunk;
@@ -143,17 +157,20 @@ __device__ __forceinline__ Unit rope_unit(const RopeArgs& A, long long wu, int h
       u.pos = 0;
     }
   } else {
-    u.pos = A.positions ? A.positions[tok] : u.i;
+    u.pos = A.positions && !A.naxes ? A.positions[tok] : u.i;
   }
   return u;
 }
 
 }  // namespace
 
-template <bool kInter>
+// kMore: positions of several axes (or an append's own), parts that go to caches in 4 bits.  Calls without
+// either keep a kernel without their registers.
+template <bool kInter, bool kMore>
 __global__ void __launch_bounds__(32 * kRopeWarps) norm_rope_fwd_kernel(RopeArgs A) {
   __shared__ unsigned long long sF[64];
-  load_freqs(A, sF);
+  __shared__ uint8_t sA[64];
+  load_freqs<kMore>(A, sF, sA);
   const int lane = threadIdx.x % 32, l = lane % 16, hw = lane / 16;
   const int half8 = A.rot / 16;  // lanes per half of the rotated elements
   const int partner = 8 * l >= A.rot ? l : (l < half8 ? l + half8 : l - half8);
@@ -169,7 +186,7 @@ __global__ void __launch_bounds__(32 * kRopeWarps) norm_rope_fwd_kernel(RopeArgs
        wu += (long long)gridDim.x * kRopeWarps) {
     const Unit u = rope_unit(A, wu, hw);
     Turn t;
-    make_turn<kInter>(A, sF, l, u.pos, 1.f, t);
+    make_turn<kInter, kMore>(A, sF, sA, l, u.pos, u.tok, 1.f, t);
     int base = 0;
     for (int p = 0; p < A.nparts; ++p) {
       const RopePart& P = A.p[p];
@@ -204,7 +221,12 @@ __global__ void __launch_bounds__(32 * kRopeWarps) norm_rope_fwd_kernel(RopeArgs
               if (turn) turn_row<kInter>(t, partner, f);
               v[k] = pack8(f);
             }
-            if (u.live) *reinterpret_cast<uint4*>(y + (long long)(h + k) * kD) = v[k];
+            if (kMore && (P.flags & kRopeQ4)) {
+              const long long block = ((long long)u.b * P.H + h + k) * (A.cap / kBlock) + u.pos / kBlock;
+              q4_store_row(v[k], reinterpret_cast<uint8_t*>(P.y) + block * kQ4Block, u.pos % kBlock, l, u.live);
+            } else if (u.live) {
+              *reinterpret_cast<uint4*>(y + (long long)(h + k) * kD) = v[k];
+            }
           }
         }
       }
@@ -212,12 +234,13 @@ __global__ void __launch_bounds__(32 * kRopeWarps) norm_rope_fwd_kernel(RopeArgs
   }
 }
 
-template <bool kInter>
+template <bool kInter, bool kMore>
 __global__ void __launch_bounds__(32 * kRopeWarps) norm_rope_bwd_kernel(RopeArgs A) {
   __shared__ unsigned long long sF[64];
+  __shared__ uint8_t sA[64];
   extern __shared__ float sw[];  // [warps][parts][128]: the warps' shares of dw
   for (int i = threadIdx.x; i < kRopeWarps * A.nparts * kD; i += blockDim.x) sw[i] = 0.f;
-  load_freqs(A, sF);  // also the barrier behind the zeroes
+  load_freqs<kMore>(A, sF, sA);  // also the barrier behind the zeroes
   if (blockIdx.x == 0 && threadIdx.x == 0) *A.status = 0u;
   const int lane = threadIdx.x % 32, l = lane % 16, hw = lane / 16, warp = threadIdx.x / 32;
   const int half8 = A.rot / 16;
@@ -230,7 +253,7 @@ __global__ void __launch_bounds__(32 * kRopeWarps) norm_rope_bwd_kernel(RopeArgs
        wu += (long long)gridDim.x * kRopeWarps) {
     const Unit u = rope_unit(A, wu, hw);
     Turn t;
-    make_turn<kInter>(A, sF, l, u.pos, -1.f, t);
+    make_turn<kInter, kMore>(A, sF, sA, l, u.pos, u.tok, -1.f, t);
     int base = 0;
     for (int p = 0; p < A.nparts; ++p) {
       const RopePart& P = A.p[p];
@@ -367,16 +390,28 @@ void launch_norm_rope_fwd(RopeArgs A, cudaStream_t st) {
   // (two blocks' warps per SM: 3 x 999 tokens x 15 heads in 11.3 us, with one block's 13.7)
   split_rows(A, num_sms() * 2 * kRopeWarps);
   const int g = rope_grid(A, kRopeFwdBlocks);
-  if (A.inter) norm_rope_fwd_kernel<true><<<g, 32 * kRopeWarps, 0, st>>>(A);
-  else norm_rope_fwd_kernel<false><<<g, 32 * kRopeWarps, 0, st>>>(A);
+  bool more = A.naxes > 0;
+  for (int p = 0; p < A.nparts; ++p) more |= (A.p[p].flags & kRopeQ4) != 0;
+  if (more) {
+    if (A.inter) norm_rope_fwd_kernel<true, true><<<g, 32 * kRopeWarps, 0, st>>>(A);
+    else norm_rope_fwd_kernel<false, true><<<g, 32 * kRopeWarps, 0, st>>>(A);
+  } else {
+    if (A.inter) norm_rope_fwd_kernel<true, false><<<g, 32 * kRopeWarps, 0, st>>>(A);
+    else norm_rope_fwd_kernel<false, false><<<g, 32 * kRopeWarps, 0, st>>>(A);
+  }
 }
 
 void launch_norm_rope_bwd(RopeArgs A, cudaStream_t st) {
   split_rows(A, num_sms() * kRopeWarps);
   const int g = rope_grid(A, kRopeBwdBlocks);
   const size_t smem = (size_t)kRopeWarps * A.nparts * kD * sizeof(float);  // at most 32 KB
-  if (A.inter) norm_rope_bwd_kernel<true><<<g, 32 * kRopeWarps, smem, st>>>(A);
-  else norm_rope_bwd_kernel<false><<<g, 32 * kRopeWarps, smem, st>>>(A);
+  if (A.naxes) {
+    if (A.inter) norm_rope_bwd_kernel<true, true><<<g, 32 * kRopeWarps, smem, st>>>(A);
+    else norm_rope_bwd_kernel<false, true><<<g, 32 * kRopeWarps, smem, st>>>(A);
+  } else {
+    if (A.inter) norm_rope_bwd_kernel<true, false><<<g, 32 * kRopeWarps, smem, st>>>(A);
+    else norm_rope_bwd_kernel<false, false><<<g, 32 * kRopeWarps, smem, st>>>(A);
+  }
   bool any = false;
   for (int p = 0; p < A.nparts; ++p) any |= A.p[p].dw != nullptr;
   if (any) norm_rope_dw_kernel<<<A.nparts, 1024, 0, st>>>(A, g);

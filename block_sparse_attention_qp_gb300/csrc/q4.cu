@@ -1,0 +1,551 @@
+// Attention of single new tokens over caches in 4 bits (format: q4.cuh), and the rows of such a cache as bf16.
+//
+// A block takes one sequence and attention group (the up to 16 query heads that share a KV head and see the same keys) and
+// a run of the group's 128-key tiles: those of a window and the first tokens, or the key blocks that the
+// proxy selected.  With codes c, scales s and the rows' exponents e (K) and f (V):
+//   S[j, h] = 2^e_j sum_d (s c)[j, d] q[h, d]          x = scale log2(e) S,  masked keys -inf
+//   m_h >= max_j (x + f) - 8,  l_h = sum_j 2^(x - m),  O[h, :] = sum_j 2^(x + f - m) (s c)[j, :] / l_h
+// The exponents of V are folded into the weights, so every weight that enters a product is at most 2^8 and
+// the products' V operand s c is exact in fp16, as K's is; q is exact there after a power of two per head.  The only
+// roundings are those of the weights to fp16 (2^-11 relative) and of O.
+//
+// Bound by memory, 73 bytes a key, head and tensor (bf16: 256), as long as the codes become operands with few
+// instructions: 47 values a cycle and SM at 7 TB/s.  So no operand passes through shared memory as 16-bit values:
+// the raw blocks arrive there by bulk copies, and each thread turns what it needs into fragments of warp-level
+// products (m16n8k16, fp16, fp32 sums) in registers, K^T and V^T as the 16-row operands, the heads as the 8 columns.
+// (As tiles for tcgen05 they would be written to and read from shared memory at 512 bytes a key, four times
+// what its bandwidth allows at this rate; the tensor work itself is small, 2 x 8 products for 16 keys.)
+// Which dims and keys a fragment's places stand for is free as long as both operands agree, so that
+//   K: a thread's 32 values of a row are 32 consecutive dims, one 16-byte load and two scales;
+//   V: a thread's 16 values of a row are one scale's dims, one 8-byte load; keys are dealt such that 32 lanes
+//      read consecutive bytes, and the score rows are dealt alike.
+// A tile's four warps take 32 keys each with sums of their own, joined at the end; a fifth keeps a ring of tiles
+// loading.  Few (sequence, group) pairs: their tiles are split over blocks and joined by a second kernel.
+#include <math.h>
+
+#include <type_traits>
+
+#include "q4.cuh"
+#include "window.cuh"
+
+namespace msa {
+namespace {
+
+constexpr int kStages = 4;
+constexpr int kStageBytes = 2 * kQ4Block;  // K, V
+constexpr int kQ4Threads = 160;            // warps 0-3 products, 4 loads
+constexpr float kSlack = 8.f;              // log2 of the largest weight kept without moving the maximum
+
+struct Q4Args {
+  const uint8_t *k, *v;
+  const bf16* q;
+  const int32_t* seq_len;
+  const int32_t* list;  // [B][Hp][top_k] key blocks; NULL: window and sinks
+  bf16* o;
+  float* lse;
+  float *opart, *lpart;  // [split][B][Hq][128], [split][B][Hq] (log2 units)
+  unsigned* status;
+  int B, cap, blocks, Hq, Hkv, Hp, groups, G;
+  int W, ns, top_k;
+  float scale;
+  int nsplit, tiles;
+  bool own_status;  // this kernel writes the status word
+};
+struct Q4Tile {
+  int block, r0, r1;  // rows r0 .. r1 - 1 of the block hold every visible key
+  int full;           // and all 128 are
+};
+struct Q4Shared {
+  uint64_t full[kStages], empty[kStages];
+  Q4Tile tile[kStages];
+  float m[4][16], l[4][16];
+};
+// The tiles of a sequence of n keys.
+struct Q4Walk {
+  int t, ws, ns, sink_tiles, first, count;
+};
+__device__ __forceinline__ Q4Walk q4_walk(const Q4Args& A, int n) {
+  Q4Walk w;
+  w.t = n - 1;
+  const int last = w.t / kBlock;
+  if (A.list) {
+    w.ws = w.ns = w.sink_tiles = w.first = 0;
+    w.count = min(A.top_k, last + 1);
+    return w;
+  }
+  w.ws = max(0, n - A.W);
+  w.ns = min(A.ns, w.ws);
+  w.first = w.ws / kBlock;
+  w.sink_tiles = min((w.ns + kBlock - 1) / kBlock, w.first);
+  w.count = w.sink_tiles + last - w.first + 1;
+  return w;
+}
+__device__ __forceinline__ Q4Tile q4_tile(const Q4Args& A, const Q4Walk& w, const int32_t* list, int i) {
+  Q4Tile x;
+  if (A.list) {
+    x.block = __ldg(list + i);
+    x.r0 = 0;
+    if (x.block < 0 || x.block > w.t / kBlock) x.block = -1;  // (msa_decode's selection has none)
+  } else {
+    x.block = i < w.sink_tiles ? i : w.first + i - w.sink_tiles;
+    x.r0 = x.block * kBlock < w.ns ? 0 : max(0, w.ws - x.block * kBlock);
+  }
+  x.r1 = i < w.sink_tiles ? w.ns - x.block * kBlock : w.t + 1 - x.block * kBlock;
+  x.r1 = x.block < 0 ? 0 : min(kBlock, x.r1);
+  x.full = x.r0 == 0 && x.r1 == kBlock && x.block * kBlock >= w.ws;
+  return x;
+}
+__device__ __forceinline__ bool q4_visible(const Q4Walk& w, int j) { return j <= w.t && (j >= w.ws || j < w.ns); }
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                               uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {  // of an 8 x 8 matrix of 16-bit values
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// Half kHalf of x times s (s, 0) plus that of y times t (0, t): no rounding.
+template <int kHalf>
+__device__ __forceinline__ uint32_t pair_of(uint32_t x, uint32_t s, uint32_t y, uint32_t t) {
+  const __half2 hx = *reinterpret_cast<const __half2*>(&x), hy = *reinterpret_cast<const __half2*>(&y);
+  const __half2 r = __hfma2(kHalf ? __high2half2(hy) : __low2half2(hy), *reinterpret_cast<const __half2*>(&t),
+                            __hmul2(kHalf ? __high2half2(hx) : __low2half2(hx), *reinterpret_cast<const __half2*>(&s)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  const __half2 r = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+}  // namespace
+
+// NT: runs of eight heads.
+template <int NT>
+__global__ void __launch_bounds__(kQ4Threads, NT == 1 ? 3 : 2) q4_decode_kernel(const __grid_constant__ Q4Args A) {
+  using namespace sm100;
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ Q4Shared sh;
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int split = blockIdx.x % A.nsplit, bg = blockIdx.x / A.nsplit;
+  const int b = bg / A.groups, grp = bg % A.groups;
+  if (A.own_status && blockIdx.x == 0) {  // the status word whole: clear, or a length out of range
+    int bad = 0;
+    for (int x = tid; x < A.B; x += kQ4Threads) bad |= A.seq_len[x] < 1 || A.seq_len[x] > A.cap;
+    bad = __syncthreads_or(bad);
+    if (tid < 32) A.status[tid] = tid == 0 && bad ? kStatusBadIndex : 0u;
+  }
+  const int len = A.seq_len[b];
+  if (len < 1 || len > A.cap) return;
+  const Q4Walk w = q4_walk(A, len);
+  const int n0 = split * A.tiles, ntile = min(A.tiles, w.count - n0);
+  const long long row0 = (long long)b * A.Hq + (long long)grp * A.G;  // first query head of the group
+  const long long part0 = (long long)split * A.B * A.Hq + row0;
+  if (ntile <= 0) {  // a sequence with fewer tiles than the longest possible
+    if (tid < A.G) A.lpart[part0 + tid] = -INFINITY;
+    return;
+  }
+  const int32_t* list = A.list ? A.list + ((long long)b * A.Hp + (long long)grp * A.Hp / A.groups) * A.top_k : nullptr;
+  if (tid == 0) {
+    for (int x = 0; x < kStages; ++x) {
+      mbar_init(&sh.full[x], 1);
+      mbar_init(&sh.empty[x], 4);
+    }
+    mbar_fence_init();
+  }
+  __syncthreads();
+
+  if (warp == 4) {
+    // ---------------------------------------------------------------- loads
+    if (lane == 0) {
+      const long long head = ((long long)b * A.Hkv + (long long)grp * A.Hkv / A.groups) * A.blocks;
+      int i = 0;
+      for (; i < ntile; ++i) {
+        const int s = i % kStages;
+        if (i >= kStages && !mbar_wait(&sh.empty[s], phase_of(i / kStages - 1), A.status)) break;
+        const Q4Tile x = q4_tile(A, w, list, n0 + i);
+        // rows in units of 16: every piece then starts and ends on 16 bytes
+        const int r0 = x.r0 & ~15, rows = (x.r1 + 15 & ~15) - r0;
+        const long long at = (head + max(x.block, 0)) * (long long)kQ4Block;
+        uint8_t* dst = ring + s * kStageBytes;
+        sh.tile[s] = x;
+        mbar_expect_tx(&sh.full[s], 2 * rows * (kQ4Codes + kQ4Scales + 1));
+        if (rows == kBlock) {
+          bulk_load(dst, A.k + at, kQ4Block, &sh.full[s]);
+          bulk_load(dst + kQ4Block, A.v + at, kQ4Block, &sh.full[s]);
+        } else if (rows > 0) {
+          for (int y = 0; y < 2; ++y) {
+            const uint8_t* src = (y ? A.v : A.k) + at;
+            uint8_t* to = dst + y * kQ4Block;
+            bulk_load(to + r0 * kQ4Codes, src + r0 * kQ4Codes, rows * kQ4Codes, &sh.full[s]);
+            bulk_load(to + kQ4ScaleAt + r0 * kQ4Scales, src + kQ4ScaleAt + r0 * kQ4Scales, rows * kQ4Scales, &sh.full[s]);
+            bulk_load(to + kQ4ExpAt + r0, src + kQ4ExpAt + r0, rows, &sh.full[s]);
+          }
+        }
+      }
+      // no copy may still be landing when the block exits
+      for (int x = i > kStages ? i - kStages : 0; x < i; ++x) mbar_wait(&sh.full[x % kStages], phase_of(x / kStages), A.status);
+    }
+    __syncwarp();
+  }
+  const int g = lane >> 2, q4 = lane & 3;
+  float m[NT][2], top[NT][2], l[NT][2], acc[NT][8][4];  // top: m + kSlack
+  if (warp < 4) {
+    // ---------------------------------------------------------------- queries: column g of run y, dims 32 q4 ..
+    uint32_t qf[NT][8][2];
+    float qs[NT][2];  // scale log2(e) 2^f of heads 2 q4, 2 q4 + 1
+#pragma unroll
+    for (int y = 0; y < NT; ++y) {
+      const int h = 8 * y + g;
+      uint4 v[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        v[c] = h < A.G ? __ldg(reinterpret_cast<const uint4*>(A.q + (row0 + h) * kD + 32 * q4) + c) : make_uint4(0u, 0u, 0u, 0u);
+      uint32_t big = 0;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        big = __vmaxu2(big, __vmaxu2(__vmaxu2(v[c].x & 0x7fff7fffu, v[c].y & 0x7fff7fffu), __vmaxu2(v[c].z & 0x7fff7fffu, v[c].w & 0x7fff7fffu)));
+      big = max(big & 0xffffu, big >> 16);
+      big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+      big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      const int f = min(max((int)(big >> 7) - 127, -120), 120);
+      const float down = pow2f(-f), up = A.scale * kLog2e * pow2f(f);
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) {
+        const uint32_t wd[4] = {v[ks >> 1].x, v[ks >> 1].y, v[ks >> 1].z, v[ks >> 1].w};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t u = wd[2 * (ks & 1) + e];
+          qf[y][ks][e] = pack_half(__uint_as_float(u << 16) * down, __uint_as_float(u & 0xffff0000u) * down);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        qs[y][e] = __shfl_sync(0xffffffffu, up, 4 * (2 * q4 + e));
+        m[y][e] = top[y][e] = -INFINITY;
+        l[y][e] = 0.f;
+      }
+#pragma unroll
+      for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[y][mt][e] = 0.f;
+    }
+    const int krow = 4 * (g & 1) + (g >> 1);  // key of score row g of a run of 16; row g + 8: 8 more
+    // Two runs of 16 keys, rows r0 .. r0 + 31 of a tile; kFull: every key of the tile is visible.
+    auto keys32 = [&](auto full, const uint8_t* sk, int r0, int block) {
+      constexpr bool kFull = decltype(full)::value;
+      const uint8_t* sv = sk + kQ4Block;
+      float x2[2][NT][4], xv[2][NT][4];  // scores of two runs of 16 keys, with and without V's exponent
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int ra = r0 + 16 * c + krow, rb = ra + 8;
+        const uint4 ka = *reinterpret_cast<const uint4*>(sk + ra * kQ4Codes + 16 * q4);
+        const uint4 kb = *reinterpret_cast<const uint4*>(sk + rb * kQ4Codes + 16 * q4);
+        const uint32_t fa = q4_scales(*reinterpret_cast<const uint16_t*>(sk + kQ4ScaleAt + ra * kQ4Scales + 2 * q4));
+        const uint32_t fb = q4_scales(*reinterpret_cast<const uint16_t*>(sk + kQ4ScaleAt + rb * kQ4Scales + 2 * q4));
+        const uint32_t fa0 = __byte_perm(fa, 0, 0x1010), fa1 = __byte_perm(fa, 0, 0x3232);
+        const uint32_t fb0 = __byte_perm(fb, 0, 0x1010), fb1 = __byte_perm(fb, 0, 0x3232);
+        float sc[NT][4];
+        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+        for (int k2 = 0; k2 < 4; ++k2) {  // two steps of 16 dims
+          uint32_t ca[4], cb[4];
+          q4_codes(wa[k2], ca);
+          q4_codes(wb[k2], cb);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            ca[e] = hmul2(ca[e], k2 < 2 ? fa0 : fa1);
+            cb[e] = hmul2(cb[e], k2 < 2 ? fb0 : fb1);
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int y = 0; y < NT; ++y) {
+              const uint32_t b0 = qf[y][2 * k2 + e][0], b1 = qf[y][2 * k2 + e][1];
+              if (k2 + e == 0) mma16816_first(sc[y], ca[0], cb[0], ca[1], cb[1], b0, b1);
+              else mma16816(sc[y], ca[2 * e], cb[2 * e], ca[2 * e + 1], cb[2 * e + 1], b0, b1);
+            }
+        }
+        const float ea = __uint_as_float((uint32_t)sk[kQ4ExpAt + ra] << 23), eb = __uint_as_float((uint32_t)sk[kQ4ExpAt + rb] << 23);
+        const float va = (float)((int)sv[kQ4ExpAt + ra] - 127), vb = (float)((int)sv[kQ4ExpAt + rb] - 127);
+        const bool vis_a = kFull || q4_visible(w, block * kBlock + ra), vis_b = kFull || q4_visible(w, block * kBlock + rb);
+#pragma unroll
+        for (int y = 0; y < NT; ++y)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const bool vis = e < 2 ? vis_a : vis_b;
+            const float z = sc[y][e] * ((e < 2 ? ea : eb) * qs[y][e & 1]);
+            x2[c][y][e] = vis ? z : -INFINITY;
+            xv[c][y][e] = vis ? z + (e < 2 ? va : vb) : -INFINITY;
+          }
+      }
+      // ---- the running maxima, moved only where a weight would pass 2^8
+      bool up = false;
+#pragma unroll
+      for (int y = 0; y < NT; ++y)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          up |= fmax3(xv[0][y][e], xv[0][y][e + 2], fmaxf(xv[1][y][e], xv[1][y][e + 2])) > top[y][e];
+      if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+        for (int y = 0; y < NT; ++y)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mx = fmax3(xv[0][y][e], xv[0][y][e + 2], fmaxf(xv[1][y][e], xv[1][y][e + 2]));
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            mx = fmaxf(mx, m[y][e]);
+            const float alpha = mx == m[y][e] ? 1.f : exp2_ftz(m[y][e] - mx);  // 0 at the first keys
+            m[y][e] = mx;
+            top[y][e] = mx + kSlack;
+            l[y][e] *= alpha;
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt) {
+              acc[y][mt][e] *= alpha;
+              acc[y][mt][e + 2] *= alpha;
+            }
+          }
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t pb[NT][2];
+#pragma unroll
+        for (int y = 0; y < NT; ++y) {
+          float p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float mb = !kFull && m[y][e & 1] == -INFINITY ? 0.f : m[y][e & 1];
+            l[y][e & 1] += exp2_ftz(x2[c][y][e] - mb);
+            p[e] = exp2_ftz(xv[c][y][e] - mb);
+          }
+          pb[y][0] = transpose8(pack_half(p[0], p[1]));
+          pb[y][1] = transpose8(pack_half(p[2], p[3]));
+        }
+        // ---- V: keys 4 i + q4 of the run, dims 16 g .. 16 g + 15
+        uint2 v[4];
+        uint32_t fs[4];  // of even keys (s, 0), of odd ones (0, s)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = r0 + 16 * c + 4 * e + q4;
+          v[e] = *reinterpret_cast<const uint2*>(sv + r * kQ4Codes + 8 * g);
+          uint32_t sb = sv[kQ4ScaleAt + r * kQ4Scales + g];
+          if (!kFull && !q4_visible(w, block * kBlock + r)) sb = 0;  // whatever an unseen row holds
+          fs[e] = q4_scales(e & 1 ? sb << 8 : sb);
+        }
+        // Pairs of keys from pairs of dims: the transposition is in the scales' products (a pair of keys is
+        // (s, 0) d + (0, s') d'), on the pipe that has room.  (With byte permutations the conversions' pipe had 79 %
+        // of its slots taken at a third of the bandwidth.)
+#pragma unroll
+        for (int m4 = 0; m4 < 2; ++m4) {
+          uint32_t c4[4][4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) q4_codes(m4 ? v[e].y : v[e].x, c4[e]);
+#pragma unroll
+          for (int mm = 0; mm < 4; ++mm) {
+            const uint32_t a0 = pair_of<0>(c4[0][mm], fs[0], c4[1][mm], fs[1]), a1 = pair_of<1>(c4[0][mm], fs[0], c4[1][mm], fs[1]);
+            const uint32_t a2 = pair_of<0>(c4[2][mm], fs[2], c4[3][mm], fs[3]), a3 = pair_of<1>(c4[2][mm], fs[2], c4[3][mm], fs[3]);
+#pragma unroll
+            for (int y = 0; y < NT; ++y) mma16816(acc[y][4 * m4 + mm], a0, a1, a2, a3, pb[y][0], pb[y][1]);
+          }
+        }
+      }
+    };
+    int s = 0;
+    uint32_t phase = 0;
+    const int r0 = 32 * warp;
+    for (int i = 0; i < ntile; ++i) {
+      if (!mbar_wait_warp(&sh.full[s], phase, A.status)) break;
+      const Q4Tile x = sh.tile[s];
+      const uint8_t* sk = ring + s * kStageBytes;
+      if (x.full) keys32(std::true_type{}, sk, r0, x.block);
+      else if (r0 < x.r1 && r0 + 32 > x.r0) keys32(std::false_type{}, sk, r0, x.block);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.empty[s]);
+      if (++s == kStages) {
+        s = 0;
+        phase ^= 1;
+      }
+    }
+#pragma unroll
+    for (int y = 0; y < NT; ++y)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) l[y][e] += __shfl_xor_sync(0xffffffffu, l[y][e], off);
+        if (g == 0) {
+          sh.m[warp][8 * y + 2 * q4 + e] = m[y][e];
+          sh.l[warp][8 * y + 2 * q4 + e] = l[y][e];
+        }
+      }
+  }
+  // ---- the warps' sums: [warp][head][128 dims] over the ring, which every copy has reached and every warp has read
+  __syncthreads();
+  float* sums = reinterpret_cast<float*>(ring);
+  if (warp < 4) {
+#pragma unroll
+    for (int y = 0; y < NT; ++y)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float* to = sums + ((warp * NT * 8) + 8 * y + 2 * q4 + e) * kD + 16 * g;
+#pragma unroll
+        for (int mt = 0; mt < 8; mt += 2)
+          *reinterpret_cast<float4*>(to + 2 * mt) = make_float4(acc[y][mt][e], acc[y][mt][e + 2], acc[y][mt + 1][e], acc[y][mt + 1][e + 2]);
+      }
+  }
+  __syncthreads();
+  if (tid < kD) {
+    for (int h = 0; h < A.G; ++h) {
+      const float mx = fmaxf(fmaxf(sh.m[0][h], sh.m[1][h]), fmaxf(sh.m[2][h], sh.m[3][h]));
+      float sum = 0.f, y = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float a = sh.m[k][h] == -INFINITY ? 0.f : exp2_ftz(sh.m[k][h] - mx);
+        sum = fmaf(a, sh.l[k][h], sum);
+        y = fmaf(a, sums[(k * NT * 8 + h) * kD + tid], y);
+      }
+      y /= sum;
+      const float ls = mx + log2f(sum);
+      if (A.nsplit == 1) {
+        A.o[(row0 + h) * kD + tid] = __float2bfloat16_rn(y);
+        if (tid == 0) A.lse[row0 + h] = ls * kLn2;
+      } else {
+        A.opart[(part0 + h) * kD + tid] = y;
+        if (tid == 0) A.lpart[part0 + h] = ls;
+      }
+    }
+  }
+}
+
+// Rows first .. first + count - 1 of every sequence and head as the bf16 values they stand for: 16 lanes a row.
+__global__ void __launch_bounds__(256) q4_read_kernel(const uint8_t* cache, int H, int blocks, int first, int count, long long rows, bf16* out) {
+  const int l = threadIdx.x % 16;
+  for (long long r = ((long long)blockIdx.x * blockDim.x + threadIdx.x) / 16; r < rows; r += (long long)gridDim.x * blockDim.x / 16) {
+    const int h = (int)(r % H), n = first + (int)(r / H % count);
+    const long long b = r / H / count;
+    const uint8_t* block = cache + ((b * H + h) * blocks + n / kBlock) * (long long)kQ4Block;
+    const int row = n % kBlock;
+    const uint32_t code = *reinterpret_cast<const uint32_t*>(block + row * kQ4Codes + 4 * l);
+    const uint32_t s2 = q4_scales(block[kQ4ScaleAt + row * kQ4Scales + (l >> 1)]);
+    const float s = __half2float(*reinterpret_cast<const __half*>(&s2)) * __uint_as_float((uint32_t)block[kQ4ExpAt + row] << 23);
+    uint32_t w[4], c[4];
+    q4_codes(code, c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&c[i]));
+      w[i] = pack_bf16(f.x * s, f.y * s);  // exact
+    }
+    reinterpret_cast<uint4*>(out + r * kD)[l] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+void launch_q4_read(const void* cache, int B, int H, int cap, int first, int count, void* out, cudaStream_t st) {
+  const long long rows = (long long)B * count * H, g = (rows + 15) / 16, most = (long long)num_sms() * 32;
+  q4_read_kernel<<<(int)(g < most ? g : most), 256, 0, st>>>((const uint8_t*)cache, H, cap / kBlock, first, count, rows, (bf16*)out);
+}
+
+// Splits of a pair's tiles: as many as fill the resident blocks, of at least four tiles.
+WinSplit q4_split(long long pairs, int tiles, int G) {
+  WinSplit w;
+  const long long room = (long long)num_sms() * (G > 8 ? 2 : 3);
+  long long n = room / pairs;
+  if (n > (tiles + 3) / 4) n = (tiles + 3) / 4;
+  if (n < 1) n = 1;
+  w.tiles = (int)((tiles + n - 1) / n);
+  w.nsplit = (tiles + w.tiles - 1) / w.tiles;
+  return w;
+}
+WinSplit q4_window_split(const WinDims& d) {
+  // sinks, and a window that may begin inside a block
+  const long long keys = (long long)(d.ns + kBlock - 1) / kBlock * kBlock + d.W + kBlock - 1;
+  const long long most = (d.S + kBlock - 1) / kBlock, n = (keys + kBlock - 1) / kBlock;
+  return q4_split((long long)d.B * d.Hkv, (int)(n < most ? n : most), d.G);
+}
+WinSplit q4_sparse_split(const Dims& d) {
+  const int blocks = d.S / kBlock;
+  return q4_split((long long)d.B * d.Hp * d.R, d.top_k < blocks ? d.top_k : blocks, d.G);
+}
+
+static void launch_q4(Q4Args& a, const WinSplit& w, cudaStream_t st) {
+  a.nsplit = w.nsplit;
+  a.tiles = w.tiles;
+  const int grid = a.B * a.groups * w.nsplit;
+  constexpr size_t smem = (size_t)kStages * kStageBytes;
+  if (a.G > 8) {
+    allow_smem<q4_decode_kernel<2>>(smem);
+    q4_decode_kernel<2><<<grid, kQ4Threads, smem, st>>>(a);
+  } else {
+    allow_smem<q4_decode_kernel<1>>(smem);
+    q4_decode_kernel<1><<<grid, kQ4Threads, smem, st>>>(a);
+  }
+  if (w.nsplit > 1) launch_decode_join(a.B, a.Hq, a.cap, w.nsplit, a.seq_len, a.opart, a.lpart, a.o, a.lse, st);
+}
+
+void launch_q4_window(const WinDims& d, const void* q, const void* k, const void* v, const int32_t* seq_len, void* o,
+                      float* lse, float* opart, float* lpart, unsigned* status, cudaStream_t st) {
+  Q4Args a{};
+  a.k = (const uint8_t*)k;
+  a.v = (const uint8_t*)v;
+  a.q = (const bf16*)q;
+  a.seq_len = seq_len;
+  a.o = (bf16*)o;
+  a.lse = lse;
+  a.opart = opart;
+  a.lpart = lpart;
+  a.status = status;
+  a.B = d.B;
+  a.cap = d.S;
+  a.blocks = d.S / kBlock;
+  a.Hq = d.Hq;
+  a.Hkv = a.groups = d.Hkv;
+  a.Hp = 1;
+  a.G = d.G;
+  a.W = d.W;
+  a.ns = d.ns;
+  a.scale = d.scale;
+  a.own_status = true;
+  launch_q4(a, q4_window_split(d), st);
+}
+
+void launch_q4_sparse(const Dims& d, const void* q, const void* k, const void* v, const int32_t* seq_len,
+                      const int32_t* block_idx, void* o, float* lse, float* opart, float* lpart, unsigned* status,
+                      cudaStream_t st) {
+  Q4Args a{};
+  a.k = (const uint8_t*)k;
+  a.v = (const uint8_t*)v;
+  a.q = (const bf16*)q;
+  a.seq_len = seq_len;
+  a.list = block_idx;
+  a.o = (bf16*)o;
+  a.lse = lse;
+  a.opart = opart;
+  a.lpart = lpart;
+  a.status = status;
+  a.B = d.B;
+  a.cap = d.S;
+  a.blocks = d.S / kBlock;
+  a.Hq = d.Hq;
+  a.Hkv = d.Hkv;
+  a.Hp = d.Hp;
+  a.groups = d.Hp * d.R;
+  a.G = d.G;
+  a.top_k = d.top_k;
+  a.scale = d.scale;
+  launch_q4(a, q4_sparse_split(d), st);
+}
+
+}  // namespace msa

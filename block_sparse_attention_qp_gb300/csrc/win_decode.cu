@@ -388,9 +388,13 @@ bool launch_win_decode(const WinDims& d, const void* q, const void* k_cache, con
     case 16: win_decode_g<16>(a, st); break;
     default: return false;
   }
-  if (w.nsplit > 1)
-    win_decode_join_kernel<<<d.B * d.Hq, kJoinThreads, w.nsplit * sizeof(float), st>>>(d.B, d.Hq, d.S, w.nsplit, seq_len, opart, lpart, (bf16*)o, lse);
+  if (w.nsplit > 1) launch_decode_join(d.B, d.Hq, d.S, w.nsplit, seq_len, opart, lpart, o, lse, st);
   return true;
+}
+
+void launch_decode_join(int B, int Hq, int cap, int nsplit, const int32_t* seq_len, const float* opart,
+                        const float* lpart, void* o, float* lse, cudaStream_t st) {
+  win_decode_join_kernel<<<B * Hq, kJoinThreads, nsplit * sizeof(float), st>>>(B, Hq, cap, nsplit, seq_len, opart, lpart, (bf16*)o, lse);
 }
 
 }  // namespace msa

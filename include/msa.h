@@ -89,7 +89,9 @@ enum msa_op {
   MSA_OP_WINDOW_BACKWARD = 6,
   MSA_OP_WINDOW_DECODE = 7,
   MSA_OP_NORM_ROPE_BACKWARD = 8, /* msa_norm_rope_workspace_size */
-  MSA_OP_NORM_ROPE_APPEND = 9
+  MSA_OP_NORM_ROPE_APPEND = 9,
+  MSA_OP_DECODE_Q4 = 10,       /* msa_workspace_size */
+  MSA_OP_WINDOW_DECODE_Q4 = 11 /* msa_window_workspace_size */
 };
 
 /* Bits of the device status word. */
@@ -274,7 +276,8 @@ MSA_API int msa_window_decode(const msa_window_shape_t* shape, const void* q, co
  */
 enum msa_rope_flags {
   MSA_ROPE_ROTATE = 1, /* rotate this part */
-  MSA_ROPE_CACHE = 2   /* append only: y is a cache, its token index the token's position */
+  MSA_ROPE_CACHE = 2,  /* append only: y is a cache, its token index the token's position */
+  MSA_ROPE_CACHE_Q4 = 8 /* append only: y is a cache in 4 bits (below; its strides are not used) */
 };
 typedef struct msa_rope_part {
   const void* x;
@@ -319,6 +322,64 @@ MSA_API int msa_norm_rope_append(const msa_rope_shape_t* shape, const msa_rope_p
 MSA_API int msa_norm_rope_backward(const msa_rope_shape_t* shape, const msa_rope_part_t* parts,
                            int nparts, const int32_t* positions, const float* inv_freq,
                            void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The same three with positions of several axes -- time, height and width of images and video:
+ * positions: int32 [axes->count][B][N] on the device, pair i turns by positions[axes->of_pair[i]] *
+ * inv_freq[i].  axes NULL: one axis.  In the append they stand beside seq_len, which then says only which row
+ * of a cache a token goes to (a text token's position behind an image is not its cache row).
+ */
+typedef struct msa_rope_axes {
+  int32_t count;       /* 1 .. 4 */
+  uint8_t of_pair[64]; /* axis of each of the rotary / 2 pairs */
+} msa_rope_axes_t;
+MSA_API int msa_norm_rope_axes_forward(const msa_rope_shape_t* shape, const msa_rope_part_t* parts,
+                          int nparts, const int32_t* positions, const float* inv_freq,
+                          const msa_rope_axes_t* axes, void* stream);
+MSA_API int msa_norm_rope_axes_append(const msa_rope_shape_t* shape, const msa_rope_part_t* parts,
+                          int nparts, const int32_t* seq_len, const int32_t* positions,
+                          const float* inv_freq, const msa_rope_axes_t* axes, void* workspace,
+                          size_t workspace_bytes, void* stream);
+MSA_API int msa_norm_rope_axes_backward(const msa_rope_shape_t* shape, const msa_rope_part_t* parts,
+                          int nparts, const int32_t* positions, const float* inv_freq,
+                          const msa_rope_axes_t* axes, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/*
+ * Caches in 4 bits.  A row x of 128 values (a key, after norm and rotation, or a value) is kept as
+ *     x[i] ~ 2^e s[i / 16] c[i],
+ * c four bits (sign, two exponent bits, one of mantissa: 0, 1/2, 1, 3/2, 2, 3, 4, 6 and their negatives), s eight
+ * (sign, four exponent bits, three of mantissa), e one byte:
+ *     a = max |x| / 6,  e = floor(log2 a) - 7, at least -100 and at most 90
+ *     s[g] = 2^-e max |x[16 g .. 16 g + 15]| / 6,  c[i] = 2^-e x[i] / s[i / 16],
+ * each rounded to nearest, ties to even (c: at most 6; s = 0: c = 0).  x is first rounded to bf16.  Every kept
+ * value is exact in bf16.  A row with an infinity or NaN is NaN throughout.
+ * A cache is [B][heads][capacity / 128] blocks of 9344 bytes, 16-byte aligned, capacity a multiple of 128.  A block
+ * is 128 rows of one head: [128][64] bytes of codes (low nibble first), [128][8] of scales, [128] of e + 127: 73
+ * bytes a row, where bf16 takes 256.
+ * msa_norm_rope_append writes them (parts with MSA_ROPE_CACHE_Q4), new tokens as well as whole prompts.
+ */
+/* Bytes of such a cache (0: a size that is not positive, or a capacity that is no multiple of 128). */
+MSA_API size_t msa_q4_cache_bytes(int32_t B, int32_t heads, int32_t capacity);
+
+/* The values that rows first .. first + count - 1 of every sequence and head stand for: out [B, count, heads, 128]
+ * bf16.  The rows have to lie in the cache. */
+MSA_API int msa_q4_read(const void* cache, int32_t B, int32_t heads, int32_t capacity, int32_t first,
+                        int32_t count, void* out, void* stream);
+
+/*
+ * msa_window_decode and msa_decode over K and V caches in 4 bits (kp_cache stays bf16, so the selection is that
+ * of msa_decode).  Arguments, limits, status bits and the rows that are left as they were are those of the two;
+ * S is the capacity.  The caches' values are used as they are kept; the softmax weights are rounded to 11 bits for
+ * their product, everything else is fp32.  Workspace: MSA_OP_WINDOW_DECODE_Q4, MSA_OP_DECODE_Q4.
+ */
+MSA_API int msa_window_decode_q4(const msa_window_shape_t* shape, const void* q, const void* k_cache,
+                      const void* v_cache, const int32_t* seq_len, void* o, float* lse,
+                      void* workspace, size_t workspace_bytes, void* stream);
+MSA_API int msa_decode_q4(const msa_shape_t* shape, const void* q, const void* qp,
+                       const void* k_cache, const void* v_cache, const void* kp_cache,
+                       const int32_t* seq_len, int32_t* block_idx, void* o, float* lse,
+                       void* workspace, size_t workspace_bytes, void* stream);
 
 /* Bytes of workspace MSA_OP_NORM_ROPE_BACKWARD or MSA_OP_NORM_ROPE_APPEND needs for nparts parts (0:
  * another op, or nparts out of range). */
