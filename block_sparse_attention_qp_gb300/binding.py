@@ -18,6 +18,8 @@ What stands around sparse attention in a model:
   msa_norm_rope_packed_func;
   msa_window_forward, msa_window_backward, msa_window_decode (causal attention over a sliding window
   and the first tokens), with the autograd function msa_window_func;
+  msa_packed_plan, msa_packed_forward, msa_packed_backward (causal attention over packed sequences of
+  different lengths), with the autograd function msa_packed_func;
   msa_q4_cache, msa_q4_read, msa_window_decode_q4, msa_decode_q4 (K and V caches in 4 bits, which
   msa_norm_rope_append writes too).
 """
@@ -38,6 +40,7 @@ OP_FORWARD, OP_BACKWARD, OP_WARMUP_FORWARD, OP_WARMUP_BACKWARD, OP_DECODE = 0, 1
 OP_WINDOW_FORWARD, OP_WINDOW_BACKWARD, OP_WINDOW_DECODE = 5, 6, 7
 OP_NORM_ROPE_BACKWARD, OP_NORM_ROPE_APPEND = 8, 9
 OP_DECODE_Q4, OP_WINDOW_DECODE_Q4 = 10, 11
+OP_PACKED_FORWARD, OP_PACKED_BACKWARD = 12, 13
 ROPE_ROTATE, ROPE_CACHE, ROPE_CACHE_Q4, ROPE_PARTS, ROPE_AXES = 1, 2, 8, 8, 4
 Q4_BLOCK_BYTES = 128 * 73  # 128 rows of a cache in 4 bits
 STATUS_BITS = {1: "bad block index", 2: "work list overflow", 4: "device wait timeout",
@@ -50,7 +53,8 @@ _SYMBOLS = ("msa_workspace_size", "msa_forward", "msa_backward", "msa_warmup_for
             "msa_window_decode", "msa_norm_rope_forward", "msa_norm_rope_append",
             "msa_norm_rope_backward", "msa_norm_rope_workspace_size", "msa_norm_rope_axes_forward",
             "msa_norm_rope_axes_append", "msa_norm_rope_axes_backward", "msa_q4_cache_bytes",
-            "msa_q4_read", "msa_window_decode_q4", "msa_decode_q4")
+            "msa_q4_read", "msa_window_decode_q4", "msa_decode_q4", "msa_packed_table_bytes",
+            "msa_packed_plan", "msa_packed_workspace_size", "msa_packed_forward", "msa_packed_backward")
 
 
 class MSAError(RuntimeError):
@@ -81,6 +85,15 @@ class RopeShape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("N", ctypes.c_int32), ("D", ctypes.c_int32),
                 ("rotary", ctypes.c_int32), ("interleaved", ctypes.c_int32),
                 ("capacity", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class PackedShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "Hq", "Hkv", "D", "window")]
+
+
+class PackedCounts(ctypes.Structure):  # msa_packed_plan_t
+    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "tokens", "Hq", "Hkv", "window", "fwd_tiles", "fwd_units",
+                                              "dq_units", "chunk", "items", "slots", "joins")]
 
 
 class RopeAxes(ctypes.Structure):
@@ -141,6 +154,16 @@ def load_library(path: str = LIB_PATH):
         lib.msa_q4_read.argtypes = [P, I, I, I, I, I, P, P]
         lib.msa_window_decode_q4.argtypes = [WP, P, P, P, P, P, P, P, Z, P]
         lib.msa_decode_q4.argtypes = [SP, P, P, P, P, P, P, P, P, P, P, Z, P]
+        KP, LP, CP = ctypes.POINTER(PackedShape), ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(PackedCounts)
+        lib.msa_packed_table_bytes.argtypes = [KP, LP, I]
+        lib.msa_packed_table_bytes.restype = Z
+        lib.msa_packed_plan.argtypes = [KP, LP, I, CP, P, Z, P]
+        lib.msa_packed_workspace_size.argtypes = [CP, I]
+        lib.msa_packed_workspace_size.restype = Z
+        lib.msa_packed_forward.argtypes = [CP, P, Z, P, P, P, F, P, P, P, Z, P]
+        lib.msa_packed_backward.argtypes = [CP, P, Z, P, P, P, P, P, P, F, P, P, P, P, Z, P]
+        for name in ("msa_packed_plan", "msa_packed_forward", "msa_packed_backward"):
+            getattr(lib, name).restype = I
         for name in ("msa_norm_rope_axes_forward", "msa_norm_rope_axes_append", "msa_norm_rope_axes_backward",
                      "msa_q4_read", "msa_window_decode_q4", "msa_decode_q4"):
             getattr(lib, name).restype = I
@@ -690,6 +713,136 @@ def msa_window_func(Q, K, V, window: int, sinks: int, scale: float):
     """Sliding-window attention with autograd (msa_window_forward / msa_window_backward); returns
     attn_out.  To be trained through, Q, K, V and the gradient have to be finite, padding included."""
     return _WindowFunction.apply(Q, K, V, int(window), int(sinks), float(scale))
+
+
+# ---------------------------------------------------------------- attention over packed sequences
+class PackedPlan:
+    """What msa_packed_plan returns: the lengths' tables on the device, for the calls of one step (any number of
+    layers) over tensors of ``rows`` rows.  Made in the order of the stream that was current."""
+    __slots__ = ("counts", "table", "rows", "tokens", "Hq", "Hkv", "device", "_bytes")
+
+    def __init__(self, counts, table):
+        self.counts, self.table, self.device = counts, table, table.device
+        self.rows, self.tokens, self.Hq, self.Hkv = counts.rows, counts.tokens, counts.Hq, counts.Hkv
+        self._bytes = {}
+
+    def workspace_size(self, op: int) -> int:
+        n = self._bytes.get(op)
+        if n is None:
+            lib = load_library()
+            n = self._bytes[op] = int(lib.msa_packed_workspace_size(ctypes.byref(self.counts), op))
+            if n == 0:
+                raise MSAError(f"op {op}: {lib.msa_last_error().decode()}")
+        return n
+
+
+def msa_packed_plan(lengths, heads: int, kv_heads: int, rows: int | None = None, window: int | None = None,
+                    device=None) -> PackedPlan:
+    """Plan of sequences of these lengths (numbers on the host, zeros among them) that lie one behind the other in
+    tensors of ``rows`` rows (default: their sum), each token seeing the tokens before it of its own sequence and,
+    with a window, the last ``window`` of them.  Neither copies from the host nor waits."""
+    if isinstance(lengths, torch.Tensor):
+        if lengths.is_cuda:
+            raise MSAError("lengths must be on the host (a plan does not wait for the device)")
+        lengths = lengths.tolist()
+    lengths = [int(n) for n in lengths]
+    if lengths and not 0 <= min(lengths) <= max(lengths) < 2 ** 31:
+        raise MSAError("lengths must be in 0 .. 2^31 - 1")
+    total = sum(lengths)
+    rows = total if rows is None else int(rows)
+    if not total <= rows < 2 ** 31:
+        raise MSAError(f"{total} tokens in {rows} rows")
+    n = len(lengths)
+    arr = (ctypes.c_int32 * max(n, 1))(*lengths)
+    shape = PackedShape(rows, int(heads), int(kv_heads), 128, rows if window is None else _int32(window, "window"))
+    dev = torch.device("cuda" if device is None else device)
+    if dev.type != "cuda":
+        raise MSAError(f"device must be a CUDA device, got {dev}")
+    if dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
+    lib = load_library()
+    with _Guard(dev):
+        need = int(lib.msa_packed_table_bytes(ctypes.byref(shape), arr, n))
+        if need == 0:
+            raise MSAError(f"msa_packed_plan: {lib.msa_last_error().decode()}")
+        table, counts = torch.empty(need, dtype=torch.uint8, device=dev), PackedCounts()
+        rc = lib.msa_packed_plan(ctypes.byref(shape), arr, n, ctypes.byref(counts), table.data_ptr(), need,
+                                 _stream_of(dev))
+    if rc:
+        _check(rc, "msa_packed_plan")
+    return PackedPlan(counts, table)
+
+
+def _packed_args(q, k, v, plan):
+    """Checks q, k and v against the plan; returns their addresses."""
+    if not isinstance(plan, PackedPlan):
+        raise TypeError("plan must be a PackedPlan (msa_packed_plan)")
+    _dims(q, "q", 3)
+    if not q.is_cuda:
+        raise MSAError("q must be a CUDA tensor")
+    dev = plan.device
+    if q.device != dev:
+        raise MSAError(f"q is on {q.device}, the plan on {dev}")
+    kv = (plan.rows, plan.Hkv, 128)
+    return (_ask(q, "q", torch.bfloat16, (plan.rows, plan.Hq, 128), dev), _ask(k, "k", torch.bfloat16, kv, dev),
+            _ask(v, "v", torch.bfloat16, kv, dev))
+
+
+def msa_packed_forward(q, k, v, plan: PackedPlan, scale: float, ws=None):
+    """Causal GQA attention over packed sequences: q [rows, Hq, 128], k, v [rows, Hkv, 128].  Returns (o, lse
+    [Hq, rows]); rows behind the last sequence are 0 and -inf whatever the inputs hold there."""
+    ptrs = _packed_args(q, k, v, plan)
+    dev = plan.device
+    with _Guard(dev):
+        wp, wn, ws = _ws(ws, plan.workspace_size(OP_PACKED_FORWARD) if ws is None else 0, dev)
+        o = torch.empty_like(q)
+        lse = torch.empty((plan.Hq, plan.rows), dtype=torch.float32, device=dev)
+        rc = load_library().msa_packed_forward(ctypes.byref(plan.counts), plan.table.data_ptr(), plan.table.numel(), *ptrs,
+                                               float(scale), o.data_ptr(), lse.data_ptr(), wp, wn, _stream_of(dev))
+    if rc:
+        _check(rc, "msa_packed_forward")
+    return o, lse
+
+
+def msa_packed_backward(q, k, v, o, lse, dout, plan: PackedPlan, scale: float, ws=None):
+    """Gradients (dq, dk, dv) of sum(o * dout); o, lse from msa_packed_forward on the same inputs, whose rows of the
+    sequences must be finite.  Rows behind the last sequence are 0 whatever the inputs hold there."""
+    ptrs = _packed_args(q, k, v, plan)
+    dev = plan.device
+    op = _ask(o, "o", torch.bfloat16, q.shape, dev)
+    lp = _ask(lse, "lse", torch.float32, (plan.Hq, plan.rows), dev)
+    dp = _ask(dout, "dout", torch.bfloat16, q.shape, dev)
+    with _Guard(dev):
+        wp, wn, ws = _ws(ws, plan.workspace_size(OP_PACKED_BACKWARD) if ws is None else 0, dev)
+        grads = dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        rc = load_library().msa_packed_backward(ctypes.byref(plan.counts), plan.table.data_ptr(), plan.table.numel(), *ptrs, op,
+                                                lp, dp, float(scale), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), wp, wn,
+                                                _stream_of(dev))
+    if rc:
+        _check(rc, "msa_packed_backward")
+    return grads
+
+
+class _PackedFunction(torch.autograd.Function):
+    # (workspaces per call, as in _WindowFunction)
+    @staticmethod
+    def forward(ctx, q, k, v, plan, scale):
+        q, k, v = (x.contiguous() for x in (q, k, v))
+        o, lse = msa_packed_forward(q, k, v, plan, scale)
+        ctx.save_for_backward(q, k, v, o, lse)
+        ctx.how = (plan, scale)
+        return o
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, do):
+        q, k, v, o, lse = ctx.saved_tensors
+        return msa_packed_backward(q, k, v, o, lse, do.contiguous(), *ctx.how) + (None,) * 2
+
+
+def msa_packed_func(Q, K, V, plan: PackedPlan, scale: float):
+    """Attention over packed sequences with autograd; returns attn_out."""
+    return _PackedFunction.apply(Q, K, V, plan, float(scale))
 
 
 # ---------------------------------------------------------------- norm and rotation of the heads

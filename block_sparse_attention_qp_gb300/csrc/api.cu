@@ -17,6 +17,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "q4.cuh"
+#include "window.cuh"
 
 namespace msa {
 namespace {
@@ -921,6 +922,125 @@ int check_axes(const msa_rope_axes_t* axes, const int32_t* positions, RopeArgs* 
   return MSA_OK;
 }
 
+// ---- packed sequences
+int check_group(int Hq, int Hkv, int* G) {
+  *G = Hq % Hkv == 0 ? Hq / Hkv : 0;
+  if (*G == 1 || *G == 2 || *G == 4 || *G == 8 || *G == 16) return MSA_OK;
+  set_err("Hq / Hkv must be 1, 2, 4, 8 or 16");
+  return MSA_ERR_UNSUPPORTED;
+}
+int check_packed_shape(const msa_packed_shape_t* s, const int32_t* lengths, int n, PackedDims* out) {
+  if (!s || (n > 0 && !lengths)) {
+    set_err("shape or lengths is null");
+    return MSA_ERR_INVALID_ARG;
+  }
+  if (s->rows < 1 || s->Hq < 1 || s->Hkv < 1 || n < 0) {
+    set_err("rows, Hq and Hkv must be positive, the number of sequences not negative");
+    return MSA_ERR_INVALID_ARG;
+  }
+  if (s->window < 1) {
+    set_err("window must be at least 1");
+    return MSA_ERR_INVALID_ARG;
+  }
+  if (s->D != kD) {
+    set_err("only head dim 128 is supported");
+    return MSA_ERR_UNSUPPORTED;
+  }
+  int G;
+  const int rc = check_group(s->Hq, s->Hkv, &G);
+  if (rc) return rc;
+  if (s->rows > (1 << 23) || (long long)s->rows * s->Hq >= (1ll << 31)) {
+    set_err("rows must be at most 2^23 and rows*Hq below 2^31");
+    return MSA_ERR_UNSUPPORTED;
+  }
+  long long tokens = 0;
+  for (int i = 0; i < n; ++i) {
+    if (lengths[i] < 0) {
+      set_err("a sequence's length is negative");
+      return MSA_ERR_INVALID_ARG;
+    }
+    tokens += lengths[i];
+  }
+  if (tokens > s->rows) {
+    set_err("the sequences have more tokens than there are rows");
+    return MSA_ERR_INVALID_ARG;
+  }
+  PackedDims x{};
+  x.d.B = 1;
+  x.d.S = (int)tokens;
+  x.d.Hq = s->Hq;
+  x.d.Hkv = s->Hkv;
+  x.d.G = G;
+  x.d.W = s->window < s->rows ? s->window : s->rows;
+  x.rows = s->rows;
+  if (tokens) packed_count(lengths, n, &x);
+  *out = x;
+  return MSA_OK;
+}
+// The plan that a caller hands back, with the sizes of the table that it stands for.
+int check_plan(const msa_packed_plan_t* p, const void* table, size_t table_bytes, float scale, PackedDims* out) {
+  if (!p) {
+    set_err("plan is null");
+    return MSA_ERR_INVALID_ARG;
+  }
+  PackedDims x{};
+  x.d.B = 1;
+  x.d.S = p->tokens;
+  x.d.Hq = p->Hq;
+  x.d.Hkv = p->Hkv;
+  x.d.W = p->window;
+  x.d.scale = scale;
+  x.rows = p->rows;
+  x.fwd_tiles = p->fwd_tiles;
+  x.fwd_units = p->fwd_units;
+  x.dq_units = p->dq_units;
+  x.chunk = p->chunk;
+  x.items = p->items;
+  x.slots = p->slots;
+  x.joins = p->joins;
+  const int32_t least = p->tokens > 0;
+  if (p->rows < 1 || p->rows > (1 << 23) || p->tokens < 0 || p->tokens > p->rows || p->Hq < 1 || p->Hkv < 1 || p->window < 1 ||
+      p->fwd_units < least || p->dq_units < least || p->items < least || p->slots < 0 || p->joins < 0 || p->joins > p->slots || (long long)p->rows * p->Hq >= (1ll << 31)) {
+    set_err("not a plan of msa_packed_plan");
+    return MSA_ERR_INVALID_ARG;
+  }
+  int rc = check_group(p->Hq, p->Hkv, &x.d.G);
+  if (rc) return rc;
+  const int tt = kBlock / x.d.G;
+  if (p->tokens && ((p->fwd_tiles != 1 && p->fwd_tiles != 2) || p->fwd_units != (p->tokens + tt * p->fwd_tiles - 1) / (tt * p->fwd_tiles) ||
+                    p->dq_units != (p->tokens + tt - 1) / tt)) {
+    set_err("not a plan of msa_packed_plan");
+    return MSA_ERR_INVALID_ARG;
+  }
+  if (!(scale > 0.f) || scale > 3e38f) {
+    set_err("scale must be positive and finite");
+    return MSA_ERR_INVALID_ARG;
+  }
+  if (p->tokens) {
+    if ((rc = check_ptrs({table}))) return rc;
+    if (table_bytes < packed_table_bytes(x)) {
+      set_err("the plan's table is too small");
+      return MSA_ERR_INVALID_ARG;
+    }
+  }
+  *out = x;
+  return MSA_OK;
+}
+struct PackedWs {
+  size_t rowm = 0, part = 0, bytes = 0;
+};
+PackedWs packed_ws(const PackedDims& x, int op) {
+  PackedWs p;
+  Carver c;
+  c.take(256);  // status word and work counters
+  if (op == MSA_OP_PACKED_BACKWARD) {
+    p.rowm = c.take((size_t)x.rows * x.d.Hq * sizeof(float2));
+    p.part = c.take((size_t)x.slots * x.d.Hkv * 2 * kBlock * kD * sizeof(float));
+  }
+  p.bytes = c.off;
+  return p;
+}
+
 // ---- caches in 4 bits
 struct Q4Plan {
   size_t opart = 0, lpart = 0, bytes = 0;
@@ -1412,6 +1532,106 @@ int msa_window_decode(const msa_window_shape_t* shape, const void* q, const void
     return MSA_ERR_CUDA;
   }
   return cuda_fail("msa_window_decode");
+}
+
+size_t msa_packed_table_bytes(const msa_packed_shape_t* shape, const int32_t* lengths, int32_t nseq) {
+  PackedDims x;
+  if (check_packed_shape(shape, lengths, nseq, &x) != MSA_OK) return 0;
+  return x.d.S ? packed_table_bytes(x) : 256;
+}
+
+int msa_packed_plan(const msa_packed_shape_t* shape, const int32_t* lengths, int32_t nseq, msa_packed_plan_t* plan,
+                    void* table, size_t table_bytes, void* stream) {
+  PackedDims x;
+  int rc = check_packed_shape(shape, lengths, nseq, &x);
+  if (rc) return rc;
+  if (!plan) {
+    set_err("plan is null");
+    return MSA_ERR_INVALID_ARG;
+  }
+  if ((rc = check_ptrs({table}))) return rc;
+  if (x.d.S && table_bytes < packed_table_bytes(x)) {
+    set_err("the plan's table is too small");
+    return MSA_ERR_WORKSPACE;
+  }
+  *plan = msa_packed_plan_t{(int32_t)x.rows, x.d.S, x.d.Hq, x.d.Hkv, x.d.W, x.fwd_tiles, x.fwd_units, x.dq_units, x.chunk, x.items, x.slots, x.joins};
+  if (!x.d.S) return MSA_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaGetLastError();
+  timed("packed_plan", st, [&] { launch_packed_plan(x, lengths, nseq, table, st); }, packed_launches(nseq));
+  return cuda_fail("msa_packed_plan");
+}
+
+size_t msa_packed_workspace_size(const msa_packed_plan_t* plan, int op) {
+  PackedDims x;
+  if (op != MSA_OP_PACKED_FORWARD && op != MSA_OP_PACKED_BACKWARD) {
+    set_err("not a packed op");
+    return 0;
+  }
+  static const char none = 0;  // (the table is not looked at)
+  if (check_plan(plan, &none - (reinterpret_cast<uintptr_t>(&none) & 15), ~(size_t)0, 1.f, &x) != MSA_OK) return 0;
+  return packed_ws(x, op).bytes;
+}
+
+int msa_packed_forward(const msa_packed_plan_t* plan, const void* table, size_t table_bytes, const void* q, const void* k,
+                       const void* v, float scale, void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  PackedDims x;
+  int rc = check_plan(plan, table, table_bytes, scale, &x);
+  if (rc) return rc;
+  if ((rc = check_ptrs({q, k, v, o, lse}))) return rc;
+  if ((rc = check_ws_bytes(packed_ws(x, MSA_OP_PACKED_FORWARD).bytes, workspace, workspace_bytes))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaGetLastError();
+  unsigned* status = at<unsigned>(workspace, 0);  // cleared by the first kernel
+  bool ok = true;
+  if (x.d.S)
+    timed("packed_fwd", st, [&] { ok = launch_packed_fwd(x, packed_tables(x, table), q, k, v, o, lse, status, st); });
+  else
+    cudaMemsetAsync(status, 0, 32 * sizeof(unsigned), st);
+  if (ok && x.d.S < x.rows)
+    timed("packed_pad", st, [&] { launch_packed_pad(x, o, x.d.Hq, nullptr, 0, nullptr, 0, lse, st); });
+  if (!ok) {
+    set_err("msa_packed_forward: could not create TMA tensor maps (cuTensorMapEncodeTiled)");
+    return MSA_ERR_CUDA;
+  }
+  return cuda_fail("msa_packed_forward");
+}
+
+int msa_packed_backward(const msa_packed_plan_t* plan, const void* table, size_t table_bytes, const void* q, const void* k,
+                        const void* v, const void* o, const float* lse, const void* dout, float scale, void* dq, void* dk,
+                        void* dv, void* workspace, size_t workspace_bytes, void* stream) {
+  PackedDims x;
+  int rc = check_plan(plan, table, table_bytes, scale, &x);
+  if (rc) return rc;
+  if ((rc = check_ptrs({q, k, v, o, lse, dout, dq, dk, dv}))) return rc;
+  const PackedWs w = packed_ws(x, MSA_OP_PACKED_BACKWARD);
+  if ((rc = check_ws_bytes(w.bytes, workspace, workspace_bytes))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaGetLastError();
+  unsigned* status = at<unsigned>(workspace, 0);  // cleared by launch_packed_dq
+  if (x.d.S < x.rows)
+    timed("packed_pad", st, [&] { launch_packed_pad(x, dq, x.d.Hq, dk, x.d.Hkv, dv, x.d.Hkv, nullptr, st); });
+  if (!x.d.S) {
+    cudaMemsetAsync(status, 0, 32 * sizeof(unsigned), st);
+    return cuda_fail("msa_packed_backward");
+  }
+  const PackedTables t = packed_tables(x, table);
+  float2* rowdata = at<float2>(workspace, w.rowm);
+  float* part = at<float>(workspace, w.part);
+  Dims rows{};
+  rows.B = 1;
+  rows.S = (int)x.rows;
+  rows.Hq = x.d.Hq;
+  timed("bwd_rowdot", st, [&] { launch_bwd_rowdot(rows, o, dout, lse, rowdata, st); });
+  bool ok = true;
+  timed("packed_dq", st, [&] { ok = launch_packed_dq(x, t, q, k, v, dout, rowdata, dq, status, st); });
+  if (ok) timed("packed_dkv", st, [&] { ok = launch_packed_dkv(x, t, q, k, v, dout, rowdata, dk, dv, part, status, st); });
+  if (ok && x.slots) timed("packed_join", st, [&] { ok = launch_packed_join(x, t, part, dk, dv, st); });
+  if (!ok) {
+    set_err("msa_packed_backward: could not create TMA tensor maps (cuTensorMapEncodeTiled)");
+    return MSA_ERR_CUDA;
+  }
+  return cuda_fail("msa_packed_backward");
 }
 
 int msa_window_decode_q4(const msa_window_shape_t* shape, const void* q, const void* k_cache,

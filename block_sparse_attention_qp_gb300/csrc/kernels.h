@@ -198,6 +198,31 @@ struct WinDims {
 bool launch_win_fwd(const WinDims& d, const void* q, const void* k, const void* v, void* o,
                     float* lse, unsigned* status, cudaStream_t st);
 
+// Packed sequences (packed.cu, window.cuh): tokens of sequences of different lengths one behind the other.
+struct PackedDims {
+  WinDims d;                 // B 1, S the tokens of all sequences, W the window; no sinks
+  int fwd_tiles, fwd_units;  // query tiles per unit of the forward, units along the tokens
+  int dq_units;              // query tiles
+  int chunk;                 // query tiles of an item of the key-outer backward at most
+  int items, slots, joins;   // its items along the tokens, those that leave partials, the blocks these belong to
+  long long rows;            // of the tensors, at least S
+};
+struct PackedTables;
+// Counts the work of sequences of these lengths (host); d, rows filled.
+void packed_count(const int32_t* lengths, int n, PackedDims* x);
+size_t packed_table_bytes(const PackedDims& x);
+PackedTables packed_tables(const PackedDims& x, const void* table);
+int packed_launches(int n);
+void launch_packed_plan(const PackedDims& x, const int32_t* lengths, int n, void* table, cudaStream_t st);
+bool launch_packed_fwd(const PackedDims& x, const PackedTables& p, const void* q, const void* k, const void* v, void* o,
+                       float* lse, unsigned* status, cudaStream_t st);
+bool launch_packed_dq(const PackedDims& x, const PackedTables& p, const void* q, const void* k, const void* v,
+                      const void* dout, float2* rowm, void* dq, unsigned* status, cudaStream_t st);
+bool launch_packed_dkv(const PackedDims& x, const PackedTables& p, const void* q, const void* k, const void* v,
+                       const void* dout, const float2* rowm, void* dk, void* dv, float* part, unsigned* status, cudaStream_t st);
+void launch_packed_pad(const PackedDims& x, void* a, int ha, void* b, int hb, void* c, int hc, float* lse, cudaStream_t st);
+bool launch_packed_join(const PackedDims& x, const PackedTables& p, const float* part, void* dk, void* dv, cudaStream_t st);
+
 // Limit of the waits that last a whole unit, its rows leaving only at its end (win_fwd.cu).
 unsigned long long win_unit_wait_ns(const WinDims& d);
 

@@ -53,6 +53,7 @@ struct DkvArgs {
   unsigned* status;
   int* sched;
   WinItems it;
+  PackedTables p;  // packed form only; d.S is then the number of tokens
 };
 struct DkvShared {
   float nlse2[kMetaRing][128], ndrow[kMetaRing][128];  // -(LSE log2 e), -(D scale) per tile row
@@ -67,6 +68,7 @@ struct DkvShared {
 // partial goes, -1 when the block has no other item.
 struct DkvItem {
   int b, g, n, i0, i1, slot;
+  int tfull;  // queries below it see the block's first key
 };
 template <int G>
 __device__ __forceinline__ int block_tiles(const WinDims& d, int n) {  // query tiles that see block n
@@ -75,9 +77,22 @@ __device__ __forceinline__ int block_tiles(const WinDims& d, int n) {  // query 
   if (k0 < d.ns || last >= d.S) last = d.S - 1;
   return (int)((last - k0) / (128 / G)) + 1;
 }
-template <int G>
-__device__ __forceinline__ DkvItem dkv_item(const WinDims& d, const WinItems& w, int it) {
+template <int G, bool kPacked>
+__device__ __forceinline__ DkvItem dkv_item(const DkvArgs& A, int it) {
+  const WinDims& d = A.d;
+  const WinItems& w = A.it;
   DkvItem x;
+  if (kPacked) {
+    const int4 e = __ldg(A.p.items + 2 * (it / d.Hkv)), f = __ldg(A.p.items + 2 * (it / d.Hkv) + 1);
+    x.b = 0;
+    x.g = it % d.Hkv;
+    x.n = e.x;
+    x.i0 = e.y;
+    x.i1 = e.z;
+    x.slot = e.w < 0 ? -1 : e.w * d.Hkv + x.g;
+    x.tfull = f.x + 1;
+    return x;
+  }
   const int per = d.B * d.Hkv;
   int c, chunk, bh;
   if (it < w.sink_items) {  // chunk-major: concurrent items share query tiles
@@ -99,12 +114,14 @@ __device__ __forceinline__ DkvItem dkv_item(const WinDims& d, const WinItems& w,
   x.i0 = c * chunk;
   x.i1 = x.i0 + chunk < nt ? x.i0 + chunk : nt;
   x.slot = nt > chunk ? it : -1;
+  const int k0 = x.n * kBlock;
+  x.tfull = k0 + kBlock <= d.ns || k0 + d.W >= d.S ? d.S : k0 + d.W;
   return x;
 }
 
 }  // namespace
 
-template <int G>
+template <int G, bool kPacked>
 __global__ void __launch_bounds__(kBwdThreads, 1) win_dkv_kernel(const __grid_constant__ DkvArgs A) {
   using namespace sm100;
   constexpr int TT = 128 / G;
@@ -184,7 +201,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dkv_kernel(const __grid_co
         sh->it_ring[x] = v;
         mbar_arrive(&sh->it_full[x]);
         if (v >= total) break;
-        const DkvItem t = dkv_item<G>(d, A.it, v);
+        const DkvItem t = dkv_item<G, kPacked>(A, v);
         if (t.i0 >= t.i1) continue;
         if (nk > 0 && !mbar_wait(&sh->kv_empty, phase_of(nk - 1), A.status)) break;
         ++nk;
@@ -240,7 +257,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dkv_kernel(const __grid_co
     for (long long k = 0; ok; ++k) {
       int v;
       if (!takew(k, v) || v >= total) break;
-      const DkvItem t = dkv_item<G>(d, A.it, v);
+      const DkvItem t = dkv_item<G, kPacked>(A, v);
       if (t.i0 >= t.i1) continue;
       // (the previous item's last S^T, dS^T and P^T were read before its last products were issued, or
       // by them)
@@ -281,7 +298,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dkv_kernel(const __grid_co
     for (long long k = 0; ok; ++k) {
       int v;
       if (!takew(k, v) || v >= total) break;
-      const DkvItem t = dkv_item<G>(d, A.it, v);
+      const DkvItem t = dkv_item<G, kPacked>(A, v);
       for (int tl = t.i0; tl < t.i1; ++tl, meta.next()) {
         const int s = meta.slot, tok = t.n * kBlock + tl * TT;
         float2 m[4];
@@ -319,17 +336,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dkv_kernel(const __grid_co
     for (long long k = 0; ok; ++k) {
       int v;
       if (!takew(k, v) || v >= total) break;
-      const DkvItem t = dkv_item<G>(d, A.it, v);
+      const DkvItem t = dkv_item<G, kPacked>(A, v);
       if (t.i0 >= t.i1) continue;
       const int j = t.n * kBlock + kr;  // this thread's key
       // queries that see it: j .. tmax
-      const int tmax = j >= d.S ? -1 : j < d.ns || j + d.W - 1 >= d.S ? d.S - 1 : j + d.W - 1;
+      const int tmax = j >= d.S ? -1 : kPacked ? __ldg(A.p.hi + j) : j < d.ns || j + d.W - 1 >= d.S ? d.S - 1 : j + d.W - 1;
       const int k0 = t.n * kBlock;
-      const int tfull = k0 + kBlock <= d.ns || k0 + d.W >= d.S ? d.S : k0 + d.W;  // queries below it see key k0
       for (int tl = t.i0; tl < t.i1; ++tl, ++i, meta.next()) {
         const int s = meta.slot, tok = t.n * kBlock + tl * TT;
         // the whole block behind every query of the tile, and inside its window?
-        const bool full = tok >= k0 + kBlock - 1 && tok + TT <= tfull;
+        const bool full = tok >= k0 + kBlock - 1 && tok + TT <= t.tfull;
         uint32_t vis = 0xffffffffu;  // else the visible rows of this part, as a mask
         if (!full) vis = bit_range((j - tok) * G - 32 * part, (tmax - tok + 1) * G - 1 - 32 * part, 0);
         if (!mbar_wait_warp(&sh->m_full[s], meta.phase, A.status) ||
@@ -498,19 +514,20 @@ __global__ void win_rowdata_kernel(WinDims d, const bf16* __restrict__ q, const 
 
 // dK and dV rows of the key blocks whose query tiles were split: their partials added in order.  One
 // block per 8 rows of (key block, b, g) and tensor; 32 threads a row, four values each.
-template <int G>
-__global__ void __launch_bounds__(256) win_join_kernel(WinDims d, WinItems w, const float* part, bf16* dk, bf16* dv) {
+template <int G, bool kPacked>
+__global__ void __launch_bounds__(256) win_join_kernel(WinDims d, WinItems w, PackedTables p, const float* part, bf16* dk, bf16* dv) {
   const int per = d.B * d.Hkv;
   const int unit = blockIdx.x / 16, row = (blockIdx.x % 16) * 8 + threadIdx.x / 32, c = threadIdx.x % 32;
-  const int n = unit / per, bh = unit % per, b = bh / d.Hkv, g = bh % d.Hkv;
+  const int4 e = kPacked ? __ldg(p.joins + unit / per) : make_int4(0, 0, 0, 0);
+  const int n = kPacked ? e.x : unit / per, bh = unit % per, b = bh / d.Hkv, g = bh % d.Hkv;
   const int hf = blockIdx.y;  // 0: dV, 1: dK
   const bool sink = n < w.sink_blocks;
   const int chunk = sink ? w.sink_chunk : w.win_chunk;
-  const int nt = block_tiles<G>(d, n), nc = (nt + chunk - 1) / chunk, j = n * kBlock + row;
+  const int nt = kPacked ? 0 : block_tiles<G>(d, n), nc = kPacked ? e.z : (nt + chunk - 1) / chunk, j = n * kBlock + row;
   if (nc == 1 || j >= d.S) return;
-  const long long first = sink ? (long long)n * per + bh
+  const long long first = kPacked ? (long long)e.y * per + bh : sink ? (long long)n * per + bh
                                : w.sink_items + ((long long)(n - w.sink_blocks) * w.win_split) * per + bh;
-  const long long step = sink ? (long long)w.sink_blocks * per : per;
+  const long long step = !kPacked && sink ? (long long)w.sink_blocks * per : per;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int x = 0; x < nc; ++x) {
@@ -537,6 +554,7 @@ struct DqArgs {
   unsigned* status;
   unsigned long long unit_ns;  // win_unit_wait_ns
   int units;  // one 128-row tile each
+  PackedTables p;  // packed form only; d.S is then the number of tokens
 };
 struct DqShared {
   uint64_t q_full, q_empty, do_full, do_empty, kv_full[kRingQ], kv_empty[kRingQ], s_full, dp_full, pa, pb,
@@ -547,9 +565,15 @@ struct DqUnit {
   int b, g, t0;
   KeyRun run;
 };
-template <int G>
-__device__ __forceinline__ DqUnit dq_unit(const WinDims& d, int u) {
+template <int G, bool kPacked>
+__device__ __forceinline__ DqUnit dq_unit(const DqArgs& A, int u) {
+  const WinDims& d = A.d;
   constexpr int TT = 128 / G;
+  if (kPacked) {
+    const int4 e = __ldg(A.p.dq + u / d.Hkv);
+    const int t1 = e.x + TT - 1;
+    return DqUnit{0, u % d.Hkv, e.x, packed_run(e.x, t1 < d.S ? t1 : d.S - 1, e.y, e.z)};
+  }
   const int per = d.B * d.Hkv;
   DqUnit x;
   const int rem = u % per;
@@ -571,7 +595,7 @@ __device__ __forceinline__ DqUnit dq_unit(const WinDims& d, int u) {
 // then one tile without a load, through which the unit's dQ leaves.  Q and dO have one buffer each:
 // the next unit's Q is loaded once the last S product has read it, its dO after the last dP product,
 // both a step before the unit ends.
-template <int G>
+template <int G, bool kPacked>
 __global__ void __launch_bounds__(kBwdThreads, 1) win_dq_kernel(const __grid_constant__ DqArgs A) {
   using namespace sm100;
   const WinDims& d = A.d;
@@ -632,8 +656,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dq_kernel(const __grid_con
         return true;
       };
       bool ok = true;
-      for (int u = blockIdx.x; u < A.units && ok; u += gridDim.x, ++nu) {
-        const DqUnit x = dq_unit<G>(d, u);
+      for (int u = blockIdx.x; u < A.units && ok; u = unit_at<kPacked>((int)++nu)) {
+        const DqUnit x = dq_unit<G, kPacked>(A, u);
         if (nu > 0 && !mbar_wait(&sh->q_empty, phase_of(nu - 1), A.status)) { ok = false; break; }
         mbar_expect_tx(&sh->q_full, kTile);
         for (int c = 0; c < 2; ++c)
@@ -690,11 +714,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dq_kernel(const __grid_con
         return true;
       };
       int u = blockIdx.x;
-      int len = dq_unit<G>(d, u).run.len, nb = (len + kBlock - 1) / kBlock, i = 0;
+      int len = dq_unit<G, kPacked>(A, u).run.len, nb = (len + kBlock - 1) / kBlock, i = 0;
       bool ok = mma_s(k, true, nb == 1, 0, len) && mma_dp(k, true, nb == 1, 0, len);
       for (int nu = 0; ok && nb > 0; ++nu) {
-        u += gridDim.x;
-        const int len2 = u < A.units ? dq_unit<G>(d, u).run.len : 0;  // of the next unit (0: none)
+        u = unit_at<kPacked>(nu + 1);
+        const int len2 = u < A.units ? dq_unit<G, kPacked>(A, u).run.len : 0;  // of the next unit (0: none)
         const int nb2 = (len2 + kBlock - 1) / kBlock;
         for (int n = 0; n < nb; ++n, ++i) {
           const bool last = n + 1 == nb;
@@ -736,8 +760,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dq_kernel(const __grid_con
     if (lane == 0) {
       long long nu = 0;
       int slot = 0;
-      for (int u = blockIdx.x; u < A.units; u += gridDim.x, ++nu, slot = (slot + 1) % kRingQ) {
-        const DqUnit x = dq_unit<G>(d, u);
+      for (int u = blockIdx.x; u < A.units; u = unit_at<kPacked>((int)++nu), slot = (slot + 1) % kRingQ) {
+        const DqUnit x = dq_unit<G, kPacked>(A, u);
         slot = (slot + 2 * x.run.nb) % kRingQ;  // the unit's last ring entry
         if (!mbar_wait(&sh->st_full, phase_of(nu), A.status, A.unit_ns)) break;
         tma_store_rows(&A.dq, aR + slot * kTile, 0, x.g * G, x.t0, x.b);
@@ -759,7 +783,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dq_kernel(const __grid_con
     const float2 sl2x2 = make_float2(sl2, sl2), sc2 = make_float2(d.scale, d.scale);
     auto row_data = [&](int u) -> float2 {
       if (u >= A.units) return make_float2(0.f, 0.f);
-      const DqUnit x = dq_unit<G>(d, u);
+      const DqUnit x = dq_unit<G, kPacked>(A, u);
       const int t = x.t0 + r / G;
       // (a plain load: the kernel itself replaces the D of other rows of it)
       return t < d.S ? A.rowm[((long long)x.b * d.S + t) * d.Hq + x.g * G + r % G] : make_float2(0.f, 0.f);
@@ -798,10 +822,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dq_kernel(const __grid_con
     int i = 0, nu = 0, v_slot = 1, singles = 0;  // singles: units of one key tile
     float2 m = row_data(blockIdx.x);
     bool ok = true;
-    for (int u = blockIdx.x; u < A.units && ok; u += gridDim.x, ++nu) {
-      const DqUnit x = dq_unit<G>(d, u);
-      const float2 mnext = row_data(u + gridDim.x);
+    for (int u = blockIdx.x; u < A.units && ok; u = unit_at<kPacked>(++nu)) {
+      const DqUnit x = dq_unit<G, kPacked>(A, u);
+      const float2 mnext = row_data(unit_at<kPacked>(nu + 1));
       const int t = x.t0 + r / G;
+      const int t_lo = kPacked ? __ldg(A.p.lo + (t < d.S ? t : d.S - 1)) : 0;
       const float2 nl2 = make_float2(-m.x, -m.x);
       float2 nd2 = make_float2(-m.y * d.scale, -m.y * d.scale);
       for (int n = 0; n < x.run.nb; ++n, ++i) {
@@ -816,7 +841,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dq_kernel(const __grid_con
         uint32_t vis = 0xffffffffu;
         if (!full) {
           uint32_t vis4[4];
-          visible_cols(d, x.run, n, t, vis4);
+          if (kPacked) visible_cols_packed(x.run, n, t, t_lo, vis4);
+          else visible_cols(d, x.run, n, t, vis4);
           vis = part == 0 ? vis4[0] : part == 1 ? vis4[1] : part == 2 ? vis4[2] : vis4[3];
         }
         if (!mbar_wait_warp(&sh->s_full, phase_of(i), A.status)) { ok = false; break; }
@@ -950,13 +976,7 @@ void launch_win_rowdata(const WinDims& d, const void* q, const void* k, const vo
       d, (const bf16*)q, (const bf16*)k, (const bf16*)v, (const bf16*)dout, lse, rowm);
 }
 
-bool launch_win_dkv(const WinDims& d, const void* q, const void* k, const void* v, const void* dout,
-                    const float2* rowm, void* dk, void* dv, float* part, unsigned* status, cudaStream_t st) {
-  DkvArgs a;
-  const int tt = kBlock / d.G, n = num_sms();
-  if (!make_tmap_rows(&a.q, q, d.B, d.S, d.Hq, d.G, tt) || !make_tmap_rows(&a.dout, dout, d.B, d.S, d.Hq, d.G, tt) ||
-      !make_tmap_rows(&a.k, k, d.B, d.S, d.Hkv, 1, kBlock) || !make_tmap_rows(&a.v, v, d.B, d.S, d.Hkv, 1, kBlock))
-    return false;
+static void dkv_args(DkvArgs& a, const WinDims& d, const float2* rowm, void* dk, void* dv, float* part, unsigned* status) {
   a.d = d;
   a.rowm = rowm;
   a.dk = (bf16*)dk;
@@ -964,45 +984,91 @@ bool launch_win_dkv(const WinDims& d, const void* q, const void* k, const void* 
   a.part = part;
   a.status = status;
   a.sched = reinterpret_cast<int*>(status + kSchedWinDkv);
-  a.it = win_items(d);
+}
+template <bool kPacked>
+static bool dkv_any(DkvArgs& a, const void* q, const void* k, const void* v, const void* dout, cudaStream_t st) {
+  const WinDims& d = a.d;
+  const int tt = kBlock / d.G, n = num_sms();
+  if (!make_tmap_rows(&a.q, q, d.B, d.S, d.Hq, d.G, tt) || !make_tmap_rows(&a.dout, dout, d.B, d.S, d.Hq, d.G, tt) ||
+      !make_tmap_rows(&a.k, k, d.B, d.S, d.Hkv, 1, kBlock) || !make_tmap_rows(&a.v, v, d.B, d.S, d.Hkv, 1, kBlock))
+    return false;
   const size_t smem = sizeof(DkvShared) + 7 * (size_t)kTile;
-#define MSA_CALL(G)                                                                                    \
-  allow_smem<win_dkv_kernel<G>>(smem);      \
-  win_dkv_kernel<G><<<a.it.items < n ? a.it.items : n, kBwdThreads, smem, st>>>(a)
+#define MSA_CALL(G)                             \
+  allow_smem<win_dkv_kernel<G, kPacked>>(smem); \
+  win_dkv_kernel<G, kPacked><<<a.it.items < n ? a.it.items : n, kBwdThreads, smem, st>>>(a)
   MSA_BY_GROUP(d.G, MSA_CALL)
 #undef MSA_CALL
   return true;
 }
+bool launch_win_dkv(const WinDims& d, const void* q, const void* k, const void* v, const void* dout,
+                    const float2* rowm, void* dk, void* dv, float* part, unsigned* status, cudaStream_t st) {
+  DkvArgs a{};
+  dkv_args(a, d, rowm, dk, dv, part, status);
+  a.it = win_items(d);
+  return dkv_any<false>(a, q, k, v, dout, st);
+}
+bool launch_packed_dkv(const PackedDims& x, const PackedTables& p, const void* q, const void* k, const void* v, const void* dout,
+                       const float2* rowm, void* dk, void* dv, float* part, unsigned* status, cudaStream_t st) {
+  DkvArgs a{};
+  dkv_args(a, x.d, rowm, dk, dv, part, status);
+  a.p = p;
+  a.it.items = x.items * x.d.Hkv;
+  return dkv_any<true>(a, q, k, v, dout, st);
+}
 
-bool launch_win_dq(const WinDims& d, const void* q, const void* k, const void* v, const void* dout,
-                   float2* rowm, void* dq, unsigned* status, cudaStream_t st) {
-  DqArgs a;
+template <bool kPacked>
+static bool dq_any(DqArgs& a, const void* q, const void* k, const void* v, const void* dout, void* dq, cudaStream_t st) {
+  const WinDims& d = a.d;
   const int tt = kBlock / d.G, n = num_sms();
   if (!make_tmap_rows(&a.q, q, d.B, d.S, d.Hq, d.G, tt) || !make_tmap_rows(&a.dout, dout, d.B, d.S, d.Hq, d.G, tt) ||
       !make_tmap_rows(&a.dq, dq, d.B, d.S, d.Hq, d.G, tt) || !make_key_maps(d, k, &a.k) || !make_key_maps(d, v, &a.v))
     return false;
-  a.d = d;
-  a.rowm = rowm;
-  a.status = status;
   a.unit_ns = win_unit_wait_ns(d);
-  a.units = (d.S + tt - 1) / tt * d.B * d.Hkv;
   const size_t smem = sizeof(DqShared) + 1024 + (2 + kRingQ) * (size_t)kTile;
-#define MSA_CALL(G)                                                                                  \
-  allow_smem<win_dq_kernel<G>>(smem);     \
-  win_dq_kernel<G><<<a.units < n ? a.units : n, kBwdThreads, smem, st>>>(a)
+#define MSA_CALL(G)                            \
+  allow_smem<win_dq_kernel<G, kPacked>>(smem); \
+  win_dq_kernel<G, kPacked><<<a.units < n ? a.units : n, kBwdThreads, smem, st>>>(a)
   MSA_BY_GROUP(d.G, MSA_CALL)
 #undef MSA_CALL
   return true;
 }
+bool launch_win_dq(const WinDims& d, const void* q, const void* k, const void* v, const void* dout,
+                   float2* rowm, void* dq, unsigned* status, cudaStream_t st) {
+  DqArgs a{};
+  a.d = d;
+  a.rowm = rowm;
+  a.status = status;
+  const int tt = kBlock / d.G;
+  a.units = (d.S + tt - 1) / tt * d.B * d.Hkv;
+  return dq_any<false>(a, q, k, v, dout, dq, st);
+}
+bool launch_packed_dq(const PackedDims& x, const PackedTables& p, const void* q, const void* k, const void* v, const void* dout,
+                      float2* rowm, void* dq, unsigned* status, cudaStream_t st) {
+  DqArgs a{};
+  a.d = x.d;
+  a.p = p;
+  a.rowm = rowm;
+  a.status = status;
+  a.units = x.dq_units * x.d.Hkv;
+  return dq_any<true>(a, q, k, v, dout, dq, st);
+}
 
-bool launch_win_join(const WinDims& d, const float* part, void* dk, void* dv, cudaStream_t st) {
-  const WinItems w = win_items(d);
-  if (!w.join_blocks) return true;
+template <bool kPacked>
+static bool join_any(const WinDims& d, const WinItems& w, const PackedTables& p, const float* part, void* dk, void* dv, cudaStream_t st) {
   const dim3 grid(w.join_blocks * d.B * d.Hkv * 16, 2);
-#define MSA_CALL(G) win_join_kernel<G><<<grid, 256, 0, st>>>(d, w, part, (bf16*)dk, (bf16*)dv)
+#define MSA_CALL(G) win_join_kernel<G, kPacked><<<grid, 256, 0, st>>>(d, w, p, part, (bf16*)dk, (bf16*)dv)
   MSA_BY_GROUP(d.G, MSA_CALL)
 #undef MSA_CALL
   return true;
+}
+bool launch_win_join(const WinDims& d, const float* part, void* dk, void* dv, cudaStream_t st) {
+  const WinItems w = win_items(d);
+  return !w.join_blocks || join_any<false>(d, w, PackedTables{}, part, dk, dv, st);
+}
+bool launch_packed_join(const PackedDims& x, const PackedTables& p, const float* part, void* dk, void* dv, cudaStream_t st) {
+  WinItems w{};
+  w.join_blocks = x.joins;
+  return !w.join_blocks || join_any<true>(x.d, w, p, part, dk, dv, st);
 }
 #undef MSA_BY_GROUP
 

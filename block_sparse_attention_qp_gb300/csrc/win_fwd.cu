@@ -60,6 +60,7 @@ struct FwdArgs {
   int nseg;         // units along a sequence
   int units;  // nseg B Hkv
   unsigned long long unit_ns;  // win_unit_wait_ns
+  PackedTables p;              // packed form only; d.S is then the number of tokens
 };
 constexpr int kFwdThreads = 640;
 struct FwdShared {
@@ -74,11 +75,21 @@ struct FwdUnit {
   bool two;  // the second tile has a token
   KeyRun run;
 };
-template <int G>
+template <int G, bool kPacked>
 __device__ __forceinline__ FwdUnit fwd_unit(const FwdArgs& A, int u) {
   constexpr int TT = 128 / G;
   const WinDims& d = A.d;
   FwdUnit x;
+  if (kPacked) {
+    const int4 e = __ldg(A.p.fwd + u / d.Hkv);
+    x.b = 0;
+    x.g = u % d.Hkv;
+    x.t0 = e.x;
+    x.two = A.tiles == 2 && x.t0 + TT < d.S;
+    const int t1 = x.t0 + TT * A.tiles - 1;
+    x.run = packed_run(x.t0, t1 < d.S ? t1 : d.S - 1, e.y, e.z);
+    return x;
+  }
   const int per = d.B * d.Hkv;
   const int seg = u / per, rem = u % per;
   x.b = rem / d.Hkv;
@@ -107,16 +118,17 @@ __device__ __forceinline__ float4 widen4(uint2 w) {
 // are, so a run that has diverged costs a look at its rows.  Runs behind the block's last store and only
 // where an epilogue met a value that is not finite: 754 us at 32K tokens with it, 748 without, 1,069 and 1,096
 // at 64K, 217 and 219 at 2 x 8192 (inlined; as a function call 760, 1,081 and 221).
-template <int G>
+template <int G, bool kPacked>
 __device__ __forceinline__ void mend_rows(const FwdArgs& A, int u) {
   constexpr int TT = 128 / G;
   const WinDims& d = A.d;
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, per = d.B * d.Hkv;
-  const int b = u % per / d.Hkv, g = u % per % d.Hkv, t0 = u / per * TT * A.tiles;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const FwdUnit unit = fwd_unit<G, kPacked>(A, u);
+  const int b = unit.b, g = unit.g, t0 = unit.t0;
   const float sl2 = d.scale * kLog2e;
-  const long long seq = (long long)b * d.S;
+  const long long seq = (long long)b * d.S, lse_rows = kPacked ? A.p.rows : d.S;
   const int t1 = t0 + TT * A.tiles - 1 < d.S ? t0 + TT * A.tiles - 1 : d.S - 1;
-  const KeyRun run = key_run(d, t0, t1);
+  const KeyRun run = unit.run;
   auto kv_row = [&](const bf16* x, int key) {
     return __ldg(reinterpret_cast<const uint2*>(x + ((seq + key) * d.Hkv + g) * kD) + lane);
   };
@@ -130,17 +142,18 @@ __device__ __forceinline__ void mend_rows(const FwdArgs& A, int u) {
     return true;
   };
   for (int t = t0 + warp; t <= t1; t += kFwdThreads / 32) {
-    const int w0 = t - d.W + 1 > 0 ? t - d.W + 1 : 0, far = d.ns < w0 ? d.ns : w0;  // sinks before the window
+    const int w0 = kPacked ? A.p.lo[t] : t - d.W + 1 > 0 ? t - d.W + 1 : 0;
+    const int far = kPacked ? 0 : d.ns < w0 ? d.ns : w0;  // sinks before the window
     const int keys = far + t - w0 + 1;
     auto key_of = [&](int x) { return x < far ? x : w0 + x - far; };
     // unseen in the unit's tiles: in front of the window (sinks are zero-filled to eight, see make_key_maps), and
     // behind the token up to the last tile's end
-    const int c0 = run.ws ? run.ws : d.ns, n0 = w0 - c0, n1 = (t1 + kBlock < d.S ? t1 + kBlock : d.S) - t - 1;
+    const int c0 = kPacked || run.ws ? run.ws : d.ns, n0 = w0 - c0, n1 = (t1 + kBlock < d.S ? t1 + kBlock : d.S) - t - 1;
     bool look = true;
     for (int h = g * G; h < g * G + G; ++h) {
       const long long row = ((seq + t) * d.Hq + h) * kD;
       if (__all_sync(0xffffffffu, finite4(__ldcg(reinterpret_cast<const uint2*>(A.op + row) + lane)))) continue;
-      if (!isfinite(__ldcg(A.lse + ((long long)b * d.Hq + h) * d.S + t))) continue;
+      if (!isfinite(__ldcg(A.lse + ((long long)b * d.Hq + h) * lse_rows + t))) continue;
       if (look && ((v_finite([&](int x) { return c0 + x; }, n0) && v_finite([&](int x) { return t + 1 + x; }, n1)) ||
                    !v_finite(key_of, keys)))
         break;  // for every head of the group
@@ -193,7 +206,7 @@ __device__ __forceinline__ void mend_rows(const FwdArgs& A, int u) {
 
 }  // namespace
 
-template <int G>
+template <int G, bool kPacked>
 __global__ void __launch_bounds__(kFwdThreads, 1) win_fwd_kernel(const __grid_constant__ FwdArgs A) {
   using namespace sm100;
   constexpr int TT = 128 / G;
@@ -247,8 +260,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) win_fwd_kernel(const __grid_co
       bool ok = true;
       long long nl = 0, nu = 0, nq = 0;  // K / V loads, units, units whose Q was asked for
       Ring<kRing> kv;
-      for (int u = blockIdx.x; u < A.units && ok; u += gridDim.x, ++nu) {
-        const FwdUnit x = fwd_unit<G>(A, u);
+      for (int u = blockIdx.x; u < A.units && ok; u = unit_at<kPacked>((int)++nu)) {
+        const FwdUnit x = fwd_unit<G, kPacked>(A, u);
         const int qs = (int)(nu & 1);
         if (nu >= 2 && !mbar_wait(&sh->q_empty[qs], phase_of(nu / 2 - 1), A.status)) break;
         uint8_t* dq = sQ + qs * 2 * kTile;
@@ -308,8 +321,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) win_fwd_kernel(const __grid_co
         ++cs[X];
       };
       int nu = 0;
-      for (int u = blockIdx.x; u < A.units && ok; u += gridDim.x, ++nu) {
-        const FwdUnit x = fwd_unit<G>(A, u);
+      for (int u = blockIdx.x; u < A.units && ok; u = unit_at<kPacked>(++nu)) {
+        const FwdUnit x = fwd_unit<G, kPacked>(A, u);
         const int qs = nu & 1;
         const uint32_t q = aQ + qs * 2 * kTile;
         if (!mbar_wait_warp(&sh->q_full[qs], phase_of(nu >> 1), A.status)) break;
@@ -341,8 +354,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) win_fwd_kernel(const __grid_co
     if (lane == 0) {
       const int X = warp - 2;
       long long nu = 0, ns = 0;
-      for (int u = blockIdx.x; u < A.units; u += gridDim.x, ++nu) {
-        const FwdUnit x = fwd_unit<G>(A, u);
+      for (int u = blockIdx.x; u < A.units; u = unit_at<kPacked>((int)++nu)) {
+        const FwdUnit x = fwd_unit<G, kPacked>(A, u);
         const int qs = (int)(nu & 1);
         if (X == 0 || x.two) {
           if (!mbar_wait(&sh->st_full[X], phase_of(ns++), A.status, A.unit_ns)) break;
@@ -375,10 +388,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) win_fwd_kernel(const __grid_co
     // Both warps of a pair pass the same barriers whatever happens: a wait that gives up only clears
     // `ok` (warp-uniform), which skips the later waits.
     bool ok = true;
-    for (int u = blockIdx.x; u < A.units; u += gridDim.x, ++nu) {
-      const FwdUnit x = fwd_unit<G>(A, u);
+    for (int u = blockIdx.x; u < A.units; u = unit_at<kPacked>(++nu)) {
+      const FwdUnit x = fwd_unit<G, kPacked>(A, u);
       if (X == 1 && !x.two) continue;
       const int t = x.t0 + X * TT + r / G;  // this row's token
+      const int t_lo = kPacked ? __ldg(A.p.lo + (t < d.S ? t : d.S - 1)) : 0;
       float mr = -INFINITY, l = 0.f;
       for (int n = 0; n < x.run.nb; ++n, ++cs) {
         // (the masks cost about as many instructions as the exponentials: only where a tile needs them)
@@ -386,7 +400,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) win_fwd_kernel(const __grid_co
         uint32_t v0 = 0xffffffffu, v1 = v0;
         if (!full) {
           uint32_t vis[4];
-          visible_cols(d, x.run, n, t, vis);
+          if (kPacked) visible_cols_packed(x.run, n, t, t_lo, vis);
+          else visible_cols(d, x.run, n, t, vis);
           v0 = hf ? vis[2] : vis[0];
           v1 = hf ? vis[3] : vis[1];
         }
@@ -496,14 +511,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1) win_fwd_kernel(const __grid_co
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->st_full[X]);
-      if (hf == 0 && t < d.S) A.lse[((long long)x.b * d.Hq + x.g * G + r % G) * d.S + t] = (mr * sl2 + __log2f(l)) * kLn2;
+      if (hf == 0 && t < d.S)
+        A.lse[((long long)x.b * d.Hq + x.g * G + r % G) * (kPacked ? A.p.rows : d.S) + t] = (mr * sl2 + __log2f(l)) * kLn2;
     }
   }
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
   if (warp == 0) tmem_dealloc(tmem, 512);
-  for (int nu = sh->bad0; nu <= sh->bad1; ++nu) mend_rows<G>(A, blockIdx.x + nu * gridDim.x);
+  for (int nu = sh->bad0; nu <= sh->bad1; ++nu) mend_rows<G, kPacked>(A, unit_at<kPacked>(nu));
 }
 
 // The maps of K or V.  Those of sinks end at the last one, so that the rows up to a multiple of eight, which
@@ -525,12 +541,25 @@ unsigned long long win_unit_wait_ns(const WinDims& d) {
   return 200000000ull + 25000ull * (unsigned long long)(keys / kBlock + 1);
 }
 
-template <int G>
+template <int G, bool kPacked>
 static void win_fwd_g(const FwdArgs& a, cudaStream_t st) {
   const size_t smem = sizeof(FwdShared) + (4 + kRing) * (size_t)kTile;
-  allow_smem<win_fwd_kernel<G>>(smem);
+  allow_smem<win_fwd_kernel<G, kPacked>>(smem);
   const int n = num_sms();
-  win_fwd_kernel<G><<<a.units < n ? a.units : n, kFwdThreads, smem, st>>>(a);
+  win_fwd_kernel<G, kPacked><<<a.units < n ? a.units : n, kFwdThreads, smem, st>>>(a);
+}
+
+template <bool kPacked>
+static bool win_fwd_any(const FwdArgs& a, cudaStream_t st) {
+  switch (a.d.G) {
+    case 1: win_fwd_g<1, kPacked>(a, st); break;
+    case 2: win_fwd_g<2, kPacked>(a, st); break;
+    case 4: win_fwd_g<4, kPacked>(a, st); break;
+    case 8: win_fwd_g<8, kPacked>(a, st); break;
+    case 16: win_fwd_g<16, kPacked>(a, st); break;
+    default: return false;
+  }
+  return true;
 }
 
 bool launch_win_fwd(const WinDims& d, const void* q, const void* k, const void* v, void* o,
@@ -553,15 +582,29 @@ bool launch_win_fwd(const WinDims& d, const void* q, const void* k, const void* 
   a.tiles = (d.S + 2 * tt - 1) / (2 * tt) * per < num_sms() ? 1 : 2;
   a.nseg = (d.S + tt * a.tiles - 1) / (tt * a.tiles);
   a.units = (int)(a.nseg * per);
-  switch (d.G) {
-    case 1: win_fwd_g<1>(a, st); break;
-    case 2: win_fwd_g<2>(a, st); break;
-    case 4: win_fwd_g<4>(a, st); break;
-    case 8: win_fwd_g<8>(a, st); break;
-    case 16: win_fwd_g<16>(a, st); break;
-    default: return false;
-  }
-  return true;
+  return win_fwd_any<false>(a, st);
+}
+
+bool launch_packed_fwd(const PackedDims& x, const PackedTables& p, const void* q, const void* k, const void* v, void* o,
+                       float* lse, unsigned* status, cudaStream_t st) {
+  const WinDims& d = x.d;
+  FwdArgs a{};
+  // (maps that end with the last sequence: rows behind it read as zeros and are not written)
+  if (!make_key_maps(d, k, &a.k) || !make_key_maps(d, v, &a.v) ||
+      !make_tmap_rows(&a.q, q, 1, d.S, d.Hq, d.G, kBlock / d.G) || !make_tmap_rows(&a.o, o, 1, d.S, d.Hq, d.G, kBlock / d.G))
+    return false;
+  a.d = d;
+  a.p = p;
+  a.qp = (const bf16*)q;
+  a.kp = (const bf16*)k;
+  a.vp = (const bf16*)v;
+  a.op = (bf16*)o;
+  a.lse = lse;
+  a.status = status;
+  a.unit_ns = win_unit_wait_ns(d);
+  a.tiles = x.fwd_tiles;
+  a.units = x.fwd_units * d.Hkv;
+  return win_fwd_any<true>(a, st);
 }
 
 }  // namespace msa

@@ -7,6 +7,11 @@
 // from wherever they start.  So the sinks share a tile with the first window keys instead of taking
 // 128-key blocks of their own, and the window starts at the tile row where it has to.  Where the
 // two ranges meet, the walk is simply 0 .. t1.
+//
+// Packed sequences (packed.cu): the forward and backward kernels' second form.  Tokens of sequences of different
+// lengths lie one behind the other, and query t sees the keys lo(t) .. t, lo(t) the later of its sequence's start
+// and its window's; key j is seen by the queries j .. hi(j).  Both grow with their argument, so a run of queries
+// t0 .. t1, of however many sequences, needs the keys lo(t0) .. t1 and tiles stay whole across borders.
 #pragma once
 #include <cuda.h>
 
@@ -40,6 +45,31 @@ __device__ __forceinline__ KeyRun key_run(const WinDims& d, int t0, int t1) {
   return r;
 }
 
+// Tables of packed sequences, made by launch_packed_plan.
+struct PackedTables {
+  const int32_t *lo, *hi;  // [tokens]
+  const int4 *fwd, *dq;    // runs of queries: {t0, lo(t0), lo(t1), 0}, the longest walks first
+  const int4* items;       // two a run of query tiles of one key block: {block, first tile, last tile + 1, slot}, {hi of its first key, ..}
+  const int4* joins;       // {block, first slot, items, 0} of the key blocks in several items
+  long long rows;          // rows of the tensors: the stride of lse
+};
+__device__ __forceinline__ KeyRun packed_run(int t0, int t1, int lo0, int lo1) {
+  KeyRun r;
+  r.ws = lo0;
+  r.nsp = 0;
+  r.len = t1 + 1 - lo0;
+  r.nb = (r.len + kBlock - 1) / kBlock;
+  r.f0 = (lo1 - lo0 + kBlock - 1) / kBlock;
+  r.f1 = (t0 - lo0 + 1) / kBlock - 1;
+  return r;
+}
+// Number of this block's k-th unit.  Packed units come in descending cost: every second round is dealt backwards,
+// so that the blocks' sums differ by less than one round's spread.
+template <bool kPacked>
+__device__ __forceinline__ int unit_at(int k) {
+  return kPacked && (k & 1) ? (k + 1) * (int)gridDim.x - 1 - (int)blockIdx.x : k * (int)gridDim.x + (int)blockIdx.x;
+}
+
 // Visible columns of tile n for query t: bit c of word c / 32 of `m`.
 __device__ __forceinline__ uint32_t bit_range(int lo, int hi, int q) {  // columns lo .. hi of word q
   const int a = lo - 32 * q > 0 ? lo - 32 * q : 0, z = hi - 32 * q < 31 ? hi - 32 * q : 31;
@@ -54,6 +84,12 @@ __device__ __forceinline__ void visible_cols(const WinDims& d, const KeyRun& r, 
   const int hi = t - r.ws + r.nsp;
 #pragma unroll
   for (int q = 0; q < 4; ++q) m[q] = bit_range(0, sc - 1, q) | bit_range(lo - v0, hi - v0, q);
+}
+
+__device__ __forceinline__ void visible_cols_packed(const KeyRun& r, int n, int t, int lo, uint32_t (&m)[4]) {
+  const int v0 = r.ws + n * kBlock;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) m[q] = bit_range(lo - v0, t - v0, q);
 }
 
 // Tensor maps of K or V [B, S, Hkv, 128]: boxes of a whole tile's rows (head: of sinks only), of the sink

@@ -91,7 +91,9 @@ enum msa_op {
   MSA_OP_NORM_ROPE_BACKWARD = 8, /* msa_norm_rope_workspace_size */
   MSA_OP_NORM_ROPE_APPEND = 9,
   MSA_OP_DECODE_Q4 = 10,       /* msa_workspace_size */
-  MSA_OP_WINDOW_DECODE_Q4 = 11 /* msa_window_workspace_size */
+  MSA_OP_WINDOW_DECODE_Q4 = 11, /* msa_window_workspace_size */
+  MSA_OP_PACKED_FORWARD = 12,   /* msa_packed_workspace_size */
+  MSA_OP_PACKED_BACKWARD = 13
 };
 
 /* Bits of the device status word. */
@@ -258,6 +260,48 @@ MSA_API int msa_window_backward(const msa_window_shape_t* shape, const void* q, 
 MSA_API int msa_window_decode(const msa_window_shape_t* shape, const void* q, const void* k_cache,
                       const void* v_cache, const int32_t* seq_len, void* o, float* lse,
                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Causal GQA attention over packed sequences: the tokens of sequences of different lengths -- prompts of one
+ * batch, documents of one training step -- lie one behind the other in q, o, dout, dq [rows, Hq, 128] and k, v, dk, dv
+ * [rows, Hkv, 128], lse [Hq, rows].  Token t of a sequence sees its tokens j <= t with t - j < window (a window of
+ * rows or more: all of them).  Rows behind the last sequence reach no other row; they are 0 in o and
+ * the gradients and -inf in lse.
+ * Hq / Hkv in {1, 2, 4, 8, 16}, rows <= 2^23, rows Hq < 2^31, sequences of length 0 among the others.
+ *
+ * msa_packed_plan makes the tables that a forward and a backward (of any number of layers) work by, on `stream`, from
+ * lengths on the host, which are not read after the call and travel as kernel arguments: no copy, no wait, and a
+ * captured plan keeps its lengths.  `plan` gets the host's part, `table` (device, msa_packed_table_bytes) the other; both
+ * belong to the device and lengths that they were made for.  The plan is ready in the order of its stream.
+ * NaN or infinities in one sequence's V reach no other sequence's o; the backward's inputs must be finite.
+ * Precision as in the window ops; a gradient has the same bits every time.
+ */
+typedef struct msa_packed_shape {
+  int32_t rows;   /* of the tensors, at least the sum of the lengths */
+  int32_t Hq;     /* query heads */
+  int32_t Hkv;    /* key/value heads */
+  int32_t D;      /* head dim, must be 128 */
+  int32_t window; /* keys a query sees, itself included */
+} msa_packed_shape_t;
+typedef struct msa_packed_plan {
+  int32_t rows, tokens, Hq, Hkv, window; /* tokens: of all sequences */
+  int32_t fwd_tiles, fwd_units, dq_units, chunk, items, slots, joins; /* how the work is cut */
+} msa_packed_plan_t;
+
+/* Bytes of a plan's table (0 if the shape or a length is not supported). */
+MSA_API size_t msa_packed_table_bytes(const msa_packed_shape_t* shape, const int32_t* lengths, int32_t nseq);
+MSA_API int msa_packed_plan(const msa_packed_shape_t* shape, const int32_t* lengths, int32_t nseq,
+                    msa_packed_plan_t* plan, void* table, size_t table_bytes, void* stream);
+/* Bytes of workspace of MSA_OP_PACKED_FORWARD or MSA_OP_PACKED_BACKWARD (0: another op, or not a plan). */
+MSA_API size_t msa_packed_workspace_size(const msa_packed_plan_t* plan, int op);
+/* Writes o and lse. */
+MSA_API int msa_packed_forward(const msa_packed_plan_t* plan, const void* table, size_t table_bytes, const void* q,
+                       const void* k, const void* v, float scale, void* o, float* lse, void* workspace,
+                       size_t workspace_bytes, void* stream);
+/* Gradients of sum(o * dout); o and lse are the outputs of msa_packed_forward for the same inputs. */
+MSA_API int msa_packed_backward(const msa_packed_plan_t* plan, const void* table, size_t table_bytes, const void* q,
+                        const void* k, const void* v, const void* o, const float* lse, const void* dout, float scale,
+                        void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * RMS norm of every head's row and the position rotation in one pass, for the inputs of the
