@@ -58,10 +58,10 @@ __device__ __forceinline__ void load_w(const float* w, int l, float (&f)[8]) {
 }
 
 // The block's frequencies as 64-bit fractions of a turn (and the pairs' axes).
-template <bool kMore>
+template <bool kAxes>
 __device__ __forceinline__ void load_freqs(const RopeArgs& A, unsigned long long* sF, uint8_t* sA) {
   const int i = threadIdx.x;
-  if (kMore && i < 64) sA[i] = A.axis[i];
+  if (kAxes && i < 64) sA[i] = A.axis[i];
   if (i < A.rot / 2) {
     // |f| / 2 pi as a sum of doubles t + lo: the product with the constant's upper half exact (a fused
     // multiply-add gives its rounding error), its lower half's added.  Whole turns go from t exactly.
@@ -82,7 +82,7 @@ __device__ __forceinline__ void load_freqs(const RopeArgs& A, unsigned long long
 struct Turn {
   float c[8], s[8];
 };
-template <bool kInter, bool kMore>
+template <bool kInter, bool kAxes>
 __device__ __forceinline__ void make_turn(const RopeArgs& A, const unsigned long long* sF, const uint8_t* sA, int l,
                                           int pos, long long tok, float dir, Turn& t) {
   const int half = A.rot / 2;
@@ -94,14 +94,14 @@ __device__ __forceinline__ void make_turn(const RopeArgs& A, const unsigned long
   }
   if (!in) return;
   int at[kRopeAxes];
-  if (kMore && A.naxes) {
+  if (kAxes && A.naxes) {
 #pragma unroll
     for (int x = 0; x < kRopeAxes; ++x) at[x] = __ldg(A.positions + (x < A.naxes ? x : 0) * ((long long)A.B * A.N) + tok);
   }
 #pragma unroll
   for (int i = 0; i < (kInter ? 4 : 8); ++i) {
     const int e = kInter ? 4 * l + i : (8 * l < half ? 8 * l + i : 8 * l + i - half);
-    if (kMore && A.naxes) {
+    if (kAxes && A.naxes) {
       const int x = sA[e];
       pos = x == 0 ? at[0] : x == 1 ? at[1] : x == 2 ? at[2] : at[3];
     }
@@ -164,13 +164,15 @@ __device__ __forceinline__ Unit rope_unit(const RopeArgs& A, long long wu, int h
 
 }  // namespace
 
-// kMore: positions of several axes (or an append's own), parts that go to caches in 4 bits.  Calls without
-// either keep a kernel without their registers.
-template <bool kInter, bool kMore>
-__global__ void __launch_bounds__(32 * kRopeWarps) norm_rope_fwd_kernel(RopeArgs A) {
+// kAxes: positions of several axes, or an append's own; kQ4: parts that go to caches in 4 bits (with kAxes).  Each has
+// instances of its own: with the code of the caches in one the forward over three axes ran two blocks an SM of the
+// three that it is launched with (271 us for 956 MB at 32768 tokens x 57 heads; 178 without).
+template <bool kInter, bool kAxes, bool kQ4>
+__global__ void __launch_bounds__(32 * kRopeWarps, kAxes ? 3 : 0) norm_rope_fwd_kernel(RopeArgs A) {
+  constexpr int kR = kQ4 ? 2 : kRows;
   __shared__ unsigned long long sF[64];
   __shared__ uint8_t sA[64];
-  load_freqs<kMore>(A, sF, sA);
+  load_freqs<kAxes>(A, sF, sA);
   const int lane = threadIdx.x % 32, l = lane % 16, hw = lane / 16;
   const int half8 = A.rot / 16;  // lanes per half of the rotated elements
   const int partner = 8 * l >= A.rot ? l : (l < half8 ? l + half8 : l - half8);
@@ -186,7 +188,7 @@ __global__ void __launch_bounds__(32 * kRopeWarps) norm_rope_fwd_kernel(RopeArgs
        wu += (long long)gridDim.x * kRopeWarps) {
     const Unit u = rope_unit(A, wu, hw);
     Turn t;
-    make_turn<kInter, kMore>(A, sF, sA, l, u.pos, u.tok, 1.f, t);
+    make_turn<kInter, kAxes>(A, sF, sA, l, u.pos, u.tok, 1.f, t);
     int base = 0;
     for (int p = 0; p < A.nparts; ++p) {
       const RopePart& P = A.p[p];
@@ -198,14 +200,39 @@ __global__ void __launch_bounds__(32 * kRopeWarps) norm_rope_fwd_kernel(RopeArgs
       bf16* y = P.y + (long long)u.b * P.yb + (long long)(P.flags & kRopeCache ? u.pos : u.i) * P.yt + 8 * l;
       float w[8];
       const bool norm = P.w != nullptr, turn = (P.flags & kRopeRotate) != 0;
-      if (norm) load_w(P.w, l, w);
-      for (int h = h0; h < h1; h += kRows) {
-        uint4 v[kRows];
+      uint8_t* cache = nullptr;  // in 4 bits: the block of the token's row of head h is head_blocks * h behind it
+      long long head_blocks = 0;
+      if (kQ4 && (P.flags & kRopeQ4)) {
+        head_blocks = (long long)(A.cap / kBlock) * kQ4Block;
+        cache = reinterpret_cast<uint8_t*>(P.y) + (long long)u.b * P.H * head_blocks + (long long)(u.pos / kBlock) * kQ4Block;
+        if (!norm && !turn) {
+          // rows as they are: eight lanes a row, two heads of the half-warp's token at a time, two of them in flight
+          const int l8 = lane & 7, second = lane >> 3 & 1;
+          for (int h = h0; h < h1; h += 4) {
+            uint4 a[2], b[2];
 #pragma unroll
-        for (int k = 0; k < kRows; ++k)
+            for (int k = 0; k < 2; ++k) {
+              const uint4* from = reinterpret_cast<const uint4*>(x - 8 * l + (long long)min(h + 2 * k + second, h1 - 1) * kD + 16 * l8);
+              a[k] = from[0];
+              b[k] = from[1];
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int hh = h + 2 * k + second;
+              q4_store_row8(a[k], b[k], cache + hh * head_blocks, u.pos % kBlock, l8, u.live && hh < h1);
+            }
+          }
+          continue;
+        }
+      }
+      if (norm) load_w(P.w, l, w);
+      for (int h = h0; h < h1; h += kR) {
+        uint4 v[kR];
+#pragma unroll
+        for (int k = 0; k < kR; ++k)
           if (h + k < h1) v[k] = *reinterpret_cast<const uint4*>(x + (long long)(h + k) * kD);
 #pragma unroll
-        for (int k = 0; k < kRows; ++k) {
+        for (int k = 0; k < kR; ++k) {
           if (h + k < h1) {
             if (norm || turn) {
               float f[8];
@@ -221,9 +248,8 @@ __global__ void __launch_bounds__(32 * kRopeWarps) norm_rope_fwd_kernel(RopeArgs
               if (turn) turn_row<kInter>(t, partner, f);
               v[k] = pack8(f);
             }
-            if (kMore && (P.flags & kRopeQ4)) {
-              const long long block = ((long long)u.b * P.H + h + k) * (A.cap / kBlock) + u.pos / kBlock;
-              q4_store_row(v[k], reinterpret_cast<uint8_t*>(P.y) + block * kQ4Block, u.pos % kBlock, l, u.live);
+            if (kQ4 && cache) {
+              q4_store_row(v[k], cache + (h + k) * head_blocks, u.pos % kBlock, l, u.live);
             } else if (u.live) {
               *reinterpret_cast<uint4*>(y + (long long)(h + k) * kD) = v[k];
             }
@@ -234,13 +260,13 @@ __global__ void __launch_bounds__(32 * kRopeWarps) norm_rope_fwd_kernel(RopeArgs
   }
 }
 
-template <bool kInter, bool kMore>
+template <bool kInter, bool kAxes>
 __global__ void __launch_bounds__(32 * kRopeWarps) norm_rope_bwd_kernel(RopeArgs A) {
   __shared__ unsigned long long sF[64];
   __shared__ uint8_t sA[64];
   extern __shared__ float sw[];  // [warps][parts][128]: the warps' shares of dw
   for (int i = threadIdx.x; i < kRopeWarps * A.nparts * kD; i += blockDim.x) sw[i] = 0.f;
-  load_freqs<kMore>(A, sF, sA);  // also the barrier behind the zeroes
+  load_freqs<kAxes>(A, sF, sA);  // also the barrier behind the zeroes
   if (blockIdx.x == 0 && threadIdx.x == 0) *A.status = 0u;
   const int lane = threadIdx.x % 32, l = lane % 16, hw = lane / 16, warp = threadIdx.x / 32;
   const int half8 = A.rot / 16;
@@ -253,7 +279,7 @@ __global__ void __launch_bounds__(32 * kRopeWarps) norm_rope_bwd_kernel(RopeArgs
        wu += (long long)gridDim.x * kRopeWarps) {
     const Unit u = rope_unit(A, wu, hw);
     Turn t;
-    make_turn<kInter, kMore>(A, sF, sA, l, u.pos, u.tok, -1.f, t);
+    make_turn<kInter, kAxes>(A, sF, sA, l, u.pos, u.tok, -1.f, t);
     int base = 0;
     for (int p = 0; p < A.nparts; ++p) {
       const RopePart& P = A.p[p];
@@ -390,15 +416,12 @@ void launch_norm_rope_fwd(RopeArgs A, cudaStream_t st) {
   // (two blocks' warps per SM: 3 x 999 tokens x 15 heads in 11.3 us, with one block's 13.7)
   split_rows(A, num_sms() * 2 * kRopeWarps);
   const int g = rope_grid(A, kRopeFwdBlocks);
-  bool more = A.naxes > 0;
-  for (int p = 0; p < A.nparts; ++p) more |= (A.p[p].flags & kRopeQ4) != 0;
-  if (more) {
-    if (A.inter) norm_rope_fwd_kernel<true, true><<<g, 32 * kRopeWarps, 0, st>>>(A);
-    else norm_rope_fwd_kernel<false, true><<<g, 32 * kRopeWarps, 0, st>>>(A);
-  } else {
-    if (A.inter) norm_rope_fwd_kernel<true, false><<<g, 32 * kRopeWarps, 0, st>>>(A);
-    else norm_rope_fwd_kernel<false, false><<<g, 32 * kRopeWarps, 0, st>>>(A);
-  }
+  bool q4 = false;
+  for (int p = 0; p < A.nparts; ++p) q4 |= (A.p[p].flags & kRopeQ4) != 0;
+  auto launch = [&](auto kernel) { kernel<<<g, 32 * kRopeWarps, 0, st>>>(A); };
+  if (q4) launch(A.inter ? norm_rope_fwd_kernel<true, true, true> : norm_rope_fwd_kernel<false, true, true>);
+  else if (A.naxes) launch(A.inter ? norm_rope_fwd_kernel<true, true, false> : norm_rope_fwd_kernel<false, true, false>);
+  else launch(A.inter ? norm_rope_fwd_kernel<true, false, false> : norm_rope_fwd_kernel<false, false, false>);
 }
 
 void launch_norm_rope_bwd(RopeArgs A, cudaStream_t st) {

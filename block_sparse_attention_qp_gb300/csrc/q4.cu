@@ -80,10 +80,10 @@ __device__ __forceinline__ Q4Walk q4_walk(const Q4Args& A, int n) {
   w.count = w.sink_tiles + last - w.first + 1;
   return w;
 }
-__device__ __forceinline__ Q4Tile q4_tile(const Q4Args& A, const Q4Walk& w, const int32_t* list, int i) {
+__device__ __forceinline__ Q4Tile q4_tile(const Q4Args& A, const Q4Walk& w, int listed, int i) {
   Q4Tile x;
   if (A.list) {
-    x.block = __ldg(list + i);
+    x.block = listed;
     x.r0 = 0;
     if (x.block < 0 || x.block > w.t / kBlock) x.block = -1;  // (msa_decode's selection has none)
   } else {
@@ -172,17 +172,20 @@ __global__ void __launch_bounds__(kQ4Threads, NT == 1 ? 3 : 2) q4_decode_kernel(
 
   if (warp == 4) {
     // ---------------------------------------------------------------- loads
-    if (lane == 0) {
-      const long long head = ((long long)b * A.Hkv + (long long)grp * A.Hkv / A.groups) * A.blocks;
-      int i = 0;
-      for (; i < ntile; ++i) {
-        const int s = i % kStages;
-        if (i >= kStages && !mbar_wait(&sh.empty[s], phase_of(i / kStages - 1), A.status)) break;
-        const Q4Tile x = q4_tile(A, w, list, n0 + i);
-        // rows in units of 16: every piece then starts and ends on 16 bytes
-        const int r0 = x.r0 & ~15, rows = (x.r1 + 15 & ~15) - r0;
-        const long long at = (head + max(x.block, 0)) * (long long)kQ4Block;
-        uint8_t* dst = ring + s * kStageBytes;
+    // (the selected blocks first, two a lane: read one by one they cost their latency at every tile)
+    const int at0 = n0 + lane, at1 = at0 + 32;
+    const int e0 = list && at0 < w.count ? __ldg(list + at0) : -1, e1 = list && at1 < w.count ? __ldg(list + at1) : -1;
+    const long long head = ((long long)b * A.Hkv + (long long)grp * A.Hkv / A.groups) * A.blocks;
+    int i = 0;
+    for (; i < ntile; ++i) {
+      const int s = i % kStages;
+      if (i >= kStages && !mbar_wait_warp(&sh.empty[s], phase_of(i / kStages - 1), A.status)) break;
+      const Q4Tile x = q4_tile(A, w, __shfl_sync(0xffffffffu, i < 32 ? e0 : e1, i & 31), n0 + i);
+      // rows in units of 16: every piece then starts and ends on 16 bytes
+      const int r0 = x.r0 & ~15, rows = (x.r1 + 15 & ~15) - r0;
+      const long long at = (head + max(x.block, 0)) * (long long)kQ4Block;
+      uint8_t* dst = ring + s * kStageBytes;
+      if (lane == 0) {
         sh.tile[s] = x;
         mbar_expect_tx(&sh.full[s], 2 * rows * (kQ4Codes + kQ4Scales + 1));
         if (rows == kBlock) {
@@ -198,10 +201,10 @@ __global__ void __launch_bounds__(kQ4Threads, NT == 1 ? 3 : 2) q4_decode_kernel(
           }
         }
       }
-      // no copy may still be landing when the block exits
-      for (int x = i > kStages ? i - kStages : 0; x < i; ++x) mbar_wait(&sh.full[x % kStages], phase_of(x / kStages), A.status);
+      __syncwarp();
     }
-    __syncwarp();
+    // no copy may still be landing when the block exits
+    for (int x = i > kStages ? i - kStages : 0; x < i; ++x) mbar_wait_warp(&sh.full[x % kStages], phase_of(x / kStages), A.status);
   }
   const int g = lane >> 2, q4 = lane & 3;
   float m[NT][2], top[NT][2], l[NT][2], acc[NT][8][4];  // top: m + kSlack
@@ -219,7 +222,7 @@ __global__ void __launch_bounds__(kQ4Threads, NT == 1 ? 3 : 2) q4_decode_kernel(
       uint32_t big = 0;
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        big = __vmaxu2(big, __vmaxu2(__vmaxu2(v[c].x & 0x7fff7fffu, v[c].y & 0x7fff7fffu), __vmaxu2(v[c].z & 0x7fff7fffu, v[c].w & 0x7fff7fffu)));
+        big = __vmaxu2(big, q4_top(v[c]));
       big = max(big & 0xffffu, big >> 16);
       big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
       big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
@@ -431,31 +434,49 @@ __global__ void __launch_bounds__(kQ4Threads, NT == 1 ? 3 : 2) q4_decode_kernel(
   }
 }
 
-// Rows first .. first + count - 1 of every sequence and head as the bf16 values they stand for: 16 lanes a row.
-__global__ void __launch_bounds__(256) q4_read_kernel(const uint8_t* cache, int H, int blocks, int first, int count, long long rows, bf16* out) {
-  const int l = threadIdx.x % 16;
-  for (long long r = ((long long)blockIdx.x * blockDim.x + threadIdx.x) / 16; r < rows; r += (long long)gridDim.x * blockDim.x / 16) {
-    const int h = (int)(r % H), n = first + (int)(r / H % count);
-    const long long b = r / H / count;
-    const uint8_t* block = cache + ((b * H + h) * blocks + n / kBlock) * (long long)kQ4Block;
-    const int row = n % kBlock;
-    const uint32_t code = *reinterpret_cast<const uint32_t*>(block + row * kQ4Codes + 4 * l);
-    const uint32_t s2 = q4_scales(block[kQ4ScaleAt + row * kQ4Scales + (l >> 1)]);
-    const float s = __half2float(*reinterpret_cast<const __half*>(&s2)) * __uint_as_float((uint32_t)block[kQ4ExpAt + row] << 23);
-    uint32_t w[4], c[4];
-    q4_codes(code, c);
+// Rows first .. first + count - 1 of every sequence and head as the bf16 values they stand for.  A warp takes 16 tokens of
+// a head, which lie together in the cache: four at a time, 8 lanes a row, all loads before the first store.
+__global__ void __launch_bounds__(256) q4_read_kernel(const uint8_t* cache, int H, int blocks, int first, int count, long long units, bf16* out) {
+  const int lane = threadIdx.x % 32, l8 = lane & 7, runs = (count + 15) / 16;
+  for (long long u = ((long long)blockIdx.x * blockDim.x + threadIdx.x) / 32; u < units; u += (long long)gridDim.x * blockDim.x / 32) {
+    const int h = (int)(u % H), n0 = (int)(u / H % runs) * 16 + (lane >> 3);
+    const long long b = u / H / runs;
+    uint2 code[4];
+    uint32_t sb[4], eb[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&c[i]));
-      w[i] = pack_bf16(f.x * s, f.y * s);  // exact
+    for (int k = 0; k < 4; ++k) {
+      const int n = first + min(n0 + 4 * k, count - 1), row = n % kBlock;
+      const uint8_t* block = cache + ((b * H + h) * blocks + n / kBlock) * (long long)kQ4Block;
+      code[k] = __ldg(reinterpret_cast<const uint2*>(block + row * kQ4Codes + 8 * l8));
+      sb[k] = __ldg(block + kQ4ScaleAt + row * kQ4Scales + l8);
+      eb[k] = __ldg(block + kQ4ExpAt + row);
     }
-    reinterpret_cast<uint4*>(out + r * kD)[l] = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t s2 = q4_scales(sb[k]);
+      const float s = __half2float(*reinterpret_cast<const __half*>(&s2)) * __uint_as_float(eb[k] << 23);
+      uint32_t w[2][4];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        uint32_t c[4];
+        q4_codes(x ? code[k].y : code[k].x, c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&c[i]));
+          w[x][i] = pack_bf16(f.x * s, f.y * s);  // exact
+        }
+      }
+      if (n0 + 4 * k >= count) continue;
+      uint4* to = reinterpret_cast<uint4*>(out + ((b * count + n0 + 4 * k) * H + h) * kD) + 2 * l8;
+      to[0] = make_uint4(w[0][0], w[0][1], w[0][2], w[0][3]);
+      to[1] = make_uint4(w[1][0], w[1][1], w[1][2], w[1][3]);
+    }
   }
 }
 
 void launch_q4_read(const void* cache, int B, int H, int cap, int first, int count, void* out, cudaStream_t st) {
-  const long long rows = (long long)B * count * H, g = (rows + 15) / 16, most = (long long)num_sms() * 32;
-  q4_read_kernel<<<(int)(g < most ? g : most), 256, 0, st>>>((const uint8_t*)cache, H, cap / kBlock, first, count, rows, (bf16*)out);
+  const long long units = (long long)B * ((count + 15) / 16) * H, g = (units + 7) / 8, most = (long long)num_sms() * 16;
+  q4_read_kernel<<<(int)(g < most ? g : most), 256, 0, st>>>((const uint8_t*)cache, H, cap / kBlock, first, count, units, (bf16*)out);
 }
 
 // Splits of a pair's tiles: as many as fill the resident blocks, of at least four tiles.

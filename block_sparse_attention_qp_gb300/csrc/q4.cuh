@@ -41,47 +41,84 @@ __device__ __forceinline__ uint32_t q4_scales(uint32_t two) {
   return (uint32_t)h.x | (uint32_t)h.y << 16;
 }
 
-// One row held by 16 lanes, eight bf16 each (v), to `row` of a block.  All lanes of the warp take part;
-// those whose row is not wanted pass store = false.
+// What a row's largest magnitude (bf16 bits; they compare as integers, infinities and NaN above the rest) makes of it:
+// the exponent, and with a run's largest magnitude the scale's byte and its reciprocal (0 for a scale of 0).
+struct Q4Row {
+  int e;
+  float down;  // 2^-e
+  bool finite;
+};
+__device__ __forceinline__ Q4Row q4_row(uint32_t top) {
+  Q4Row r;
+  r.finite = top < 0x7f80u;
+  const int p = (int)(__float_as_uint(__fdiv_rn(__uint_as_float(top << 16), 6.f)) >> 23) - 127;  // floor of log2
+  r.e = r.finite ? min(max(p - 7, kQ4MinExp), kQ4MaxExp) : 0;
+  r.down = pow2f(-r.e);
+  return r;
+}
+__device__ __forceinline__ uint32_t q4_scale(const Q4Row& r, uint32_t top16, float& s, float& inv) {
+  const float want = __fdiv_rn(__uint_as_float(top16 << 16) * r.down, 6.f);
+  const uint32_t sb = r.finite ? __nv_cvt_float_to_fp8(want, __NV_SATFINITE, __NV_E4M3) : kQ4NaN;
+  s = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)sb, __NV_E4M3)));
+  inv = s > 0.f ? __frcp_rn(s) : 0.f;
+  return sb;
+}
+// Codes of eight bf16.  x / s is the product with the rounded reciprocal corrected by its remainder: exact wherever
+// the quotient lies on a border between two codes (x has 8 bits, a border times s at most 7); elsewhere it is 2^-12 away
+// from one.
+__device__ __forceinline__ uint32_t q4_encode(const Q4Row& r, uint4 v, float s, float inv) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t code = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float2 x = make_float2(__uint_as_float(w[i] << 16) * r.down, __uint_as_float(w[i] & 0xffff0000u) * r.down);
+    const float a = x.x * inv, b = x.y * inv;
+    x.x = fmaf(fmaf(-a, s, x.x), inv, a);
+    x.y = fmaf(fmaf(-b, s, x.y), inv, b);
+    code |= (uint32_t)__nv_cvt_float2_to_fp4x2(x, __NV_E2M1, cudaRoundNearest) << (8 * i);
+  }
+  return r.finite ? code : 0u;
+}
+__device__ __forceinline__ uint32_t q4_top(uint4 v) {  // two bf16 magnitudes whose larger is the largest of the eight
+  return __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+}
+
+// One row held by 16 lanes, eight bf16 each, to `row` of a block.  All lanes of the warp take part; those whose row is
+// not wanted pass store = false.
 __device__ __forceinline__ void q4_store_row(uint4 v, uint8_t* block, int row, int l, bool store) {
   constexpr uint32_t kFull = 0xffffffffu;
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  // magnitudes of bf16 compare as integers, infinities and NaN above the rest
-  uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+  uint32_t m = q4_top(v);
   m = max(m & 0xffffu, m >> 16);
   const uint32_t top16 = max(m, __shfl_xor_sync(kFull, m, 1));
   uint32_t top = max(top16, __shfl_xor_sync(kFull, top16, 2));
   top = max(top, __shfl_xor_sync(kFull, top, 4));
   top = max(top, __shfl_xor_sync(kFull, top, 8));
-  const bool finite = top < 0x7f80u;
-  const int p = (int)(__float_as_uint(__fdiv_rn(__uint_as_float(top << 16), 6.f)) >> 23) - 127;  // floor of log2
-  const int e = finite ? min(max(p - 7, kQ4MinExp), kQ4MaxExp) : 0;
-  const float down = pow2f(-e);
-  const float want = __fdiv_rn(__uint_as_float(top16 << 16) * down, 6.f);
-  uint32_t sb = __nv_cvt_float_to_fp8(want, __NV_SATFINITE, __NV_E4M3);
-  if (!finite) sb = kQ4NaN;
-  const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)sb, __NV_E4M3)));
-  const float r = s > 0.f ? __frcp_rn(s) : 0.f;
-  uint32_t code = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float2 x = make_float2(__uint_as_float(w[i] << 16) * down, __uint_as_float(w[i] & 0xffff0000u) * down);
-    // x / s: the product with the rounded reciprocal corrected by its remainder.  Exact wherever the quotient
-    // lies on a border between two codes (x has 8 bits, a border times s at most 7); elsewhere it is 2^-12 away
-    // from one.
-    const float a = x.x * r, b = x.y * r;
-    x.x = fmaf(fmaf(-a, s, x.x), r, a);
-    x.y = fmaf(fmaf(-b, s, x.y), r, b);
-    code |= (uint32_t)__nv_cvt_float2_to_fp4x2(x, __NV_E2M1, cudaRoundNearest) << (8 * i);
-  }
-  if (!finite) code = 0;
-  sb <<= 8 * ((l >> 1) & 3);
-  sb |= __shfl_xor_sync(kFull, sb, 2);
-  sb |= __shfl_xor_sync(kFull, sb, 4);
+  const Q4Row r = q4_row(top);
+  float s, inv;
+  const uint32_t sb = q4_scale(r, top16, s, inv);
+  const uint32_t code = q4_encode(r, v, s, inv);
   if (!store) return;
   *reinterpret_cast<uint32_t*>(block + row * kQ4Codes + 4 * l) = code;
-  if ((l & 7) == 0) *reinterpret_cast<uint32_t*>(block + kQ4ScaleAt + row * kQ4Scales + (l >> 1)) = sb;
-  if (l == 0) block[kQ4ExpAt + row] = (uint8_t)(e + 127);
+  if (!(l & 1)) block[kQ4ScaleAt + row * kQ4Scales + (l >> 1)] = (uint8_t)sb;
+  if (l == 0) block[kQ4ExpAt + row] = (uint8_t)(r.e + 127);
+}
+
+// The same for a row held by 8 lanes, the 16 bf16 of one scale each: rows that are stored as they are.
+__device__ __forceinline__ void q4_store_row8(uint4 a, uint4 b, uint8_t* block, int row, int l8, bool store) {
+  constexpr uint32_t kFull = 0xffffffffu;
+  uint32_t m = __vmaxu2(q4_top(a), q4_top(b));
+  const uint32_t top16 = max(m & 0xffffu, m >> 16);
+  uint32_t top = max(top16, __shfl_xor_sync(kFull, top16, 1));
+  top = max(top, __shfl_xor_sync(kFull, top, 2));
+  top = max(top, __shfl_xor_sync(kFull, top, 4));
+  const Q4Row r = q4_row(top);
+  float s, inv;
+  const uint32_t sb = q4_scale(r, top16, s, inv);
+  const uint2 code = make_uint2(q4_encode(r, a, s, inv), q4_encode(r, b, s, inv));
+  if (!store) return;
+  *reinterpret_cast<uint2*>(block + row * kQ4Codes + 8 * l8) = code;
+  block[kQ4ScaleAt + row * kQ4Scales + l8] = (uint8_t)sb;
+  if (l8 == 0) block[kQ4ExpAt + row] = (uint8_t)(r.e + 127);
 }
 
 }  // namespace msa
