@@ -5,6 +5,7 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <algorithm>
 #include <atomic>
 #include <map>
 #include <memory>
@@ -1558,7 +1559,7 @@ int msa_packed_plan(const msa_packed_shape_t* shape, const int32_t* lengths, int
   if (!x.d.S) return MSA_OK;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaGetLastError();
-  timed("packed_plan", st, [&] { launch_packed_plan(x, lengths, nseq, table, st); }, packed_launches(nseq));
+  timed("packed_plan", st, [&] { launch_packed_plan(x, lengths, nseq, table, st); }, packed_launches((int)std::count_if(lengths, lengths + nseq, [](int32_t n) { return n > 0; })));
   return cuda_fail("msa_packed_plan");
 }
 

@@ -2,10 +2,11 @@
 // (window.cuh) in the order that they are dealt in.
 //
 // The lengths are known on the host and travel to the device as kernel arguments, so a plan needs no copy from
-// host memory and no wait, and a captured graph holds the lengths it was captured with.  packed_token_kernel (one
-// launch for up to kSeqs sequences) writes lo(t) and hi(t); packed_unit_kernel, one block, cuts the units and sorts them by
-// the length of their walks (a counting sort in shared memory): costs differ from unit to unit by the sequences' lengths,
-// and the longest must not come last.  Both are bound by latency: 9 us for 16384 tokens of 33 sequences.
+// host memory and no wait, and a captured graph holds the lengths it was captured with.  packed_plan_kernel, one launch
+// for up to kSeqs sequences, writes lo(t) and hi(t); three blocks of the last launch cut the units and sort them by the
+// length of their walks (a counting sort in shared memory): costs differ from unit to unit by the sequences' lengths, and
+// the longest must not come last.  They find lo and hi of the tokens that they look at for themselves where all sequences
+// are in their launch, and else in the tables of the launches before.  Bound by latency.
 #include "window.cuh"
 
 namespace msa {
@@ -13,7 +14,7 @@ namespace {
 
 constexpr int kSeqs = 960;  // sequences of one launch: 3.8 KB of arguments
 struct Starts {
-  int at[kSeqs + 1];
+  int n, at[kSeqs + 1];
 };
 constexpr int kBins = 1024;
 
@@ -25,19 +26,16 @@ struct UnitArgs {
   int shift, shift2;  // of the costs of units (key tiles) and items (query tiles), to fit the bins
 };
 
-__global__ void __launch_bounds__(256) packed_token_kernel(const __grid_constant__ Starts s, int n, int W, int32_t* lo, int32_t* hi) {
-  const int first = s.at[0], end = s.at[n];
-  for (int t = first + blockIdx.x * 256 + threadIdx.x; t < end; t += gridDim.x * 256) {
-    int a = 0, z = n;  // s.at[a] <= t < s.at[z]
-    while (z - a > 1) {
-      const int m = (a + z) / 2;
-      if (s.at[m] <= t) a = m;
-      else z = m;
-    }
-    const int t0 = s.at[a], t1 = s.at[a + 1];
-    lo[t] = t - t0 >= W ? t - W + 1 : t0;
-    hi[t] = t1 - t > W ? t + W - 1 : t1 - 1;
+// {lo, hi} of token t, one of the n sequences that begin at at[0] .. at[n - 1].
+__device__ __forceinline__ int2 seen(const int* at, int n, int W, int t) {
+  int a = 0, z = n;  // at[a] <= t < at[z]
+  while (z - a > 1) {
+    const int m = (a + z) / 2;
+    if (at[m] <= t) a = m;
+    else z = m;
   }
+  const int t0 = at[a], t1 = at[a + 1];
+  return make_int2(t - t0 >= W ? t - W + 1 : t0, t1 - t > W ? t + W - 1 : t1 - 1);
 }
 
 // Items of a key block that nt query tiles see, of equal length; one up to a quarter above the aim.
@@ -85,18 +83,34 @@ __device__ __forceinline__ void deal(int n, int shift, int* bins, F&& f) {
   __syncthreads();
 }
 
-// Block 0: the forward's units, 1: dQ's, 2: the key-outer items.
-__global__ void __launch_bounds__(kBins) packed_unit_kernel(const __grid_constant__ UnitArgs A) {
-  __shared__ int bins[kBins], slots, joins;
+// units: with block 0 for the forward's, 1 for dQ's, 2 for the key-outer items (one: the launch has all sequences, s.n of
+// them); the other blocks write the tokens' tables.
+__global__ void __launch_bounds__(kBins) packed_plan_kernel(const __grid_constant__ UnitArgs A, const __grid_constant__ Starts s,
+                                                            bool units, bool one, int32_t* to_lo, int32_t* to_hi) {
+  __shared__ int bins[kBins], slots, joins, at[kSeqs + 1];
   const WinDims& d = A.x.d;
   const int tt = kBlock / d.G;
+  if (one || !units)
+    for (int i = threadIdx.x; i <= s.n; i += kBins) at[i] = s.at[i];
+  __syncthreads();
+  if (!units || blockIdx.x >= 3) {
+    const int first = units ? 3 : 0, step = ((int)gridDim.x - first) * kBins;
+    for (int t = at[0] + ((int)blockIdx.x - first) * kBins + (int)threadIdx.x; t < at[s.n]; t += step) {
+      const int2 e = seen(at, s.n, d.W, t);
+      to_lo[t] = e.x;
+      to_hi[t] = e.y;
+    }
+    return;
+  }
+  auto lo_of = [&](int t) { return one ? seen(at, s.n, d.W, t).x : A.lo[t]; };
+  auto hi_of = [&](int t) { return one ? seen(at, s.n, d.W, t).y : A.hi[t]; };
   if (threadIdx.x == 0) slots = joins = 0;
   if (blockIdx.x < 2) {
     const int per = blockIdx.x == 0 ? tt * A.x.fwd_tiles : tt;
     int4* out = blockIdx.x == 0 ? A.fwd : A.dq;
     deal((d.S + per - 1) / per, A.shift, bins, [&](int i, auto&& emit) {
-      const int t0 = i * per, t1 = min(t0 + per, d.S) - 1, lo = A.lo[t0];
-      emit((t1 - lo) / kBlock, [&](int at) { out[at] = make_int4(t0, lo, A.lo[t1], 0); });
+      const int t0 = i * per, t1 = min(t0 + per, d.S) - 1, lo = lo_of(t0);
+      emit((t1 - lo) / kBlock, [&](int at) { out[at] = make_int4(t0, lo, lo_of(t1), 0); });
     });
     return;
   }
@@ -104,14 +118,14 @@ __global__ void __launch_bounds__(kBins) packed_unit_kernel(const __grid_constan
   int* first = A.first;  // slot of a split block's first item
   __syncthreads();
   for (int n = threadIdx.x; n < nblk; n += blockDim.x) {
-    const int k0 = n * kBlock, nt = (A.hi[min(k0 + kBlock, d.S) - 1] - k0) / tt + 1, nc = packed_pieces(nt, A.x.chunk);
+    const int k0 = n * kBlock, nt = (hi_of(min(k0 + kBlock, d.S) - 1) - k0) / tt + 1, nc = packed_pieces(nt, A.x.chunk);
     if (nc == 1) continue;
     first[n] = atomicAdd(&slots, nc);
     A.joins[atomicAdd(&joins, 1)] = make_int4(n, first[n], nc, 0);
   }
   __syncthreads();
   deal(nblk, A.shift2, bins, [&](int n, auto&& emit) {
-    const int k0 = n * kBlock, hi0 = A.hi[k0], nt = (A.hi[min(k0 + kBlock, d.S) - 1] - k0) / tt + 1;
+    const int k0 = n * kBlock, hi0 = hi_of(k0), nt = (hi_of(min(k0 + kBlock, d.S) - 1) - k0) / tt + 1;
     const int nc = packed_pieces(nt, A.x.chunk), step = (nt + nc - 1) / nc, s0 = nc > 1 ? first[n] : -1;
     for (int c = 0; c < nc; ++c) {
       const int i0 = min(c * step, nt), i1 = min(i0 + step, nt);
@@ -233,23 +247,11 @@ PackedTables packed_tables(const PackedDims& x, const void* table) {
   return t;
 }
 
-int packed_launches(int n) { return (n + kSeqs - 1) / kSeqs + 1; }
+// (of n sequences, empty ones not counted)
+int packed_launches(int n) { return n <= kSeqs ? 1 : (n + kSeqs - 1) / kSeqs + 1; }
 
 void launch_packed_plan(const PackedDims& x, const int32_t* lengths, int n, void* table, cudaStream_t st) {
   const PackedTables p = packed_tables(x, table);
-  Starts s;
-  int at = 0;
-  for (int i = 0; i < n;) {
-    int m = 0;
-    s.at[0] = at;
-    for (; m < kSeqs && i < n; ++i) {
-      if (lengths[i] == 0) continue;
-      at += lengths[i];
-      s.at[++m] = at;
-    }
-    const int tokens = at - s.at[0], g = (tokens + 255) / 256, most = num_sms() * 8;
-    if (m) packed_token_kernel<<<g < most ? g : most, 256, 0, st>>>(s, m, x.d.W, const_cast<int32_t*>(p.lo), const_cast<int32_t*>(p.hi));
-  }
   UnitArgs a;
   a.x = x;
   a.lo = p.lo;
@@ -262,7 +264,24 @@ void launch_packed_plan(const PackedDims& x, const int32_t* lengths, int n, void
   a.shift = a.shift2 = 0;
   while ((x.d.S / kBlock + 1) >> a.shift >= kBins) ++a.shift;
   while (x.dq_units >> a.shift2 >= kBins) ++a.shift2;
-  packed_unit_kernel<<<3, kBins, 0, st>>>(a);
+  int32_t *lo = const_cast<int32_t*>(p.lo), *hi = const_cast<int32_t*>(p.hi);
+  Starts s;
+  int at = 0, filled = 0;
+  for (int i = 0; i < n; ++i) filled += lengths[i] > 0;
+  const bool one = filled <= kSeqs;
+  for (int i = 0; i < n && at < x.d.S;) {
+    s.n = 0;
+    s.at[0] = at;
+    for (; s.n < kSeqs && i < n; ++i) {
+      if (lengths[i] == 0) continue;
+      at += lengths[i];
+      s.at[++s.n] = at;
+    }
+    const int tokens = at - s.at[0], g = (tokens + kBins - 1) / kBins, most = num_sms() * 2;
+    packed_plan_kernel<<<(g < most ? g : most) + (one ? 3 : 0), kBins, 0, st>>>(a, s, one, one, lo, hi);
+  }
+  s.n = 0;
+  if (!one) packed_plan_kernel<<<3, kBins, 0, st>>>(a, s, true, false, lo, hi);
 }
 
 }  // namespace msa
