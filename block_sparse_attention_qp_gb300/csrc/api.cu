@@ -1619,11 +1619,7 @@ int msa_packed_backward(const msa_packed_plan_t* plan, const void* table, size_t
   const PackedTables t = packed_tables(x, table);
   float2* rowdata = at<float2>(workspace, w.rowm);
   float* part = at<float>(workspace, w.part);
-  Dims rows{};
-  rows.B = 1;
-  rows.S = (int)x.rows;
-  rows.Hq = x.d.Hq;
-  timed("bwd_rowdot", st, [&] { launch_bwd_rowdot(rows, o, dout, lse, rowdata, st); });
+  timed("packed_rowdata", st, [&] { launch_packed_rowdata(x, t, q, k, v, o, dout, lse, rowdata, st); });
   bool ok = true;
   timed("packed_dq", st, [&] { ok = launch_packed_dq(x, t, q, k, v, dout, rowdata, dq, status, st); });
   if (ok) timed("packed_dkv", st, [&] { ok = launch_packed_dkv(x, t, q, k, v, dout, rowdata, dk, dv, part, status, st); });

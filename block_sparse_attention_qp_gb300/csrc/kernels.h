@@ -216,6 +216,8 @@ int packed_launches(int n);
 void launch_packed_plan(const PackedDims& x, const int32_t* lengths, int n, void* table, cudaStream_t st);
 bool launch_packed_fwd(const PackedDims& x, const PackedTables& p, const void* q, const void* k, const void* v, void* o,
                        float* lse, unsigned* status, cudaStream_t st);
+void launch_packed_rowdata(const PackedDims& x, const PackedTables& p, const void* q, const void* k, const void* v,
+                           const void* o, const void* dout, const float* lse, float2* rowm, cudaStream_t st);
 bool launch_packed_dq(const PackedDims& x, const PackedTables& p, const void* q, const void* k, const void* v,
                       const void* dout, float2* rowm, void* dq, unsigned* status, cudaStream_t st);
 bool launch_packed_dkv(const PackedDims& x, const PackedTables& p, const void* q, const void* k, const void* v,

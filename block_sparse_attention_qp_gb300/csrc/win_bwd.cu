@@ -457,58 +457,103 @@ __global__ void __launch_bounds__(kBwdThreads, 1) win_dkv_kernel(const __grid_co
   if (warp == 0) tmem_dealloc(sh->tmem, 512);
 }
 
+// Helpers of the row data kernels below: 16 dims a lane, eight lanes a row.
+struct Dims16 {
+  float f[16];
+};
+__device__ __forceinline__ Dims16 load16(const bf16* x, long long row, int c) {  // dims 8 c .. and 64 + 8 c ..
+  Dims16 r;
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    const uint4 w = *reinterpret_cast<const uint4*>(x + row * kD + 64 * y + 8 * c);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      r.f[8 * y + 2 * e] = __uint_as_float(u[e] << 16);
+      r.f[8 * y + 2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+    }
+  }
+  return r;
+}
+__device__ __forceinline__ float dot16(const Dims16& a, const Dims16& b) {  // over the row's eight lanes
+  float s = 0.f, t = 0.f;
+#pragma unroll
+  for (int e = 0; e < 16; e += 2) {
+    s = fmaf(a.f[e], b.f[e], s);
+    t = fmaf(a.f[e + 1], b.f[e + 1], t);
+  }
+  s += t;
+#pragma unroll
+  for (int off = 4; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+  return s;
+}
+// D = sum_j P_j dP_j of one query row over a few keys (key_of(0) .. key_of(keys - 1): their rows of k and v), by a whole
+// warp: four keys at a time, eight lanes a key.
+template <typename F>
+__device__ __forceinline__ float row_sum(const WinDims& d, const bf16* q, const bf16* k, const bf16* v, const bf16* dout, long long r,
+                                         float l2, int keys, F&& key_of) {
+  const int lane = threadIdx.x % 32, c = lane % 8, kk = lane / 8;
+  const Dims16 fq = load16(q, r, c), fo = load16(dout, r, c);
+  float sum = 0.f;
+  for (int x0 = 0; x0 < keys; x0 += 4) {
+    const long long key = key_of(x0 + kk < keys ? x0 + kk : keys - 1);  // past the end: the last key, not counted
+    const Dims16 fk = load16(k, key, c), fv = load16(v, key, c);
+    const float p = exp2_ftz(dot16(fq, fk) * d.scale * kLog2e - l2), dp = dot16(fo, fv);
+    if (x0 + kk < keys) sum = fmaf(p, dp, sum);
+  }
+  sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+  return sum + __shfl_xor_sync(0xffffffffu, sum, 16);
+}
+
 // Row data {LSE log2 e, D} of windows of a few keys where a group is one head (a query tile is then 128
-// tokens and spans two key tiles), D = sum_j P_j dP_j: one warp per query row, four keys at a time, eight
-// lanes a key, 16 dims a lane.
+// tokens and spans two key tiles): one warp per query row.
 __global__ void win_rowdata_kernel(WinDims d, const bf16* __restrict__ q, const bf16* __restrict__ k,
                                    const bf16* __restrict__ v, const bf16* __restrict__ dout,
                                    const float* __restrict__ lse, float2* __restrict__ rowm) {
   const long long rows = (long long)d.B * d.S * d.Hq, step = (long long)gridDim.x * blockDim.x / 32;
-  const int lane = threadIdx.x % 32, c = lane % 8, kk = lane / 8;
-  auto load = [&](const bf16* x, long long row, float (&f)[16]) {  // dims 8 c .. and 64 + 8 c ..
-#pragma unroll
-    for (int y = 0; y < 2; ++y) {
-      const uint4 w = *reinterpret_cast<const uint4*>(x + row * kD + 64 * y + 8 * c);
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        f[8 * y + 2 * e] = __uint_as_float(u[e] << 16);
-        f[8 * y + 2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
-      }
-    }
-  };
-  auto dot = [](const float (&a)[16], const float (&b)[16]) {
-    float s = 0.f, t = 0.f;
-#pragma unroll
-    for (int e = 0; e < 16; e += 2) {
-      s = fmaf(a[e], b[e], s);
-      t = fmaf(a[e + 1], b[e + 1], t);
-    }
-    s += t;
-#pragma unroll
-    for (int off = 4; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    return s;
-  };
   for (long long r = ((long long)blockIdx.x * blockDim.x + threadIdx.x) / 32; r < rows; r += step) {
     const int h = (int)(r % d.Hq), t = (int)(r / d.Hq % d.S), b = (int)(r / d.Hq / d.S);
     const float l2 = lse[((long long)b * d.Hq + h) * d.S + t] * kLog2e;
     const int w0 = t - d.W + 1 > 0 ? t - d.W + 1 : 0, far = d.ns < w0 ? d.ns : w0;  // sinks before the window
-    const int keys = far + t - w0 + 1;
-    float fq[16], fo[16], sum = 0.f;
-    load(q, r, fq);
-    load(dout, r, fo);
-    for (int x0 = 0; x0 < keys; x0 += 4) {
-      const int x = x0 + kk < keys ? x0 + kk : keys - 1;  // past the end: the last key, not counted
-      const long long key = ((long long)b * d.S + (x < far ? x : w0 + x - far)) * d.Hkv + h / d.G;
-      float fk[16], fv[16];
-      load(k, key, fk);
-      load(v, key, fv);
-      const float p = exp2_ftz(dot(fq, fk) * d.scale * kLog2e - l2), dp = dot(fo, fv);
-      if (x0 + kk < keys) sum = fmaf(p, dp, sum);
+    const float sum = row_sum(d, q, k, v, dout, r, l2, far + t - w0 + 1, [&](int x) {
+      return ((long long)b * d.S + (x < far ? x : w0 + x - far)) * d.Hkv + h / d.G;
+    });
+    if (threadIdx.x % 32 == 0) rowm[r] = make_float2(l2, sum);
+  }
+}
+
+// Row data of packed sequences: D = rowsum(dO O), four rows a warp; but rows of a few keys -- the first ones of every
+// sequence -- whose query tile spans several key tiles (win_dq_kernel leaves D of the others) have it from P and dP.
+__global__ void __launch_bounds__(256, 4) packed_rowdata_kernel(WinDims d, PackedTables p, const bf16* __restrict__ q, const bf16* __restrict__ k,
+                                                             const bf16* __restrict__ v, const bf16* __restrict__ o,
+                                                             const bf16* __restrict__ dout, const float* __restrict__ lse,
+                                                             float2* __restrict__ rowm) {
+  const unsigned rows = (unsigned)d.S * d.Hq, step = gridDim.x * blockDim.x / 32;  // (below 2^31)
+  const int lane = threadIdx.x % 32, c = lane % 8, part = lane / 8, tt = kBlock / d.G;
+  // (a warp's rows a quarter of the tensor apart: the rows of a few keys lie together, and four of them in turn by one
+  // warp were a tail of 35 us)
+  const unsigned quarter = (rows + 3) / 4;
+  for (unsigned w = (blockIdx.x * blockDim.x + threadIdx.x) / 32; w < quarter; w += step) {
+    const unsigned r = w + part * quarter < rows ? w + part * quarter : rows - 1;
+    const int t = (int)(r / (unsigned)d.Hq), h = (int)(r % (unsigned)d.Hq), lo = __ldg(p.lo + t);
+    float sum = dot16(load16(o, r, c), load16(dout, r, c));
+    const float l2 = __ldg(lse + h * p.rows + t) * kLog2e;
+    bool few = t - lo < kFewKeys;
+    if (few) {
+      const int t0 = t / tt * tt, t1 = t0 + tt - 1 < d.S ? t0 + tt - 1 : d.S - 1;
+      few = t1 - __ldg(p.lo + t0) >= kBlock;
     }
-    sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-    sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-    if (lane == 0) rowm[r] = make_float2(l2, sum);
+    const unsigned which = __ballot_sync(0xffffffffu, few);
+    for (int x = 0; x < 4; ++x) {
+      if (!(which >> (8 * x) & 1u)) continue;
+      const unsigned rx = __shfl_sync(0xffffffffu, r, 8 * x);
+      const int first = __shfl_sync(0xffffffffu, lo, 8 * x), keys = __shfl_sync(0xffffffffu, t, 8 * x) - first + 1;
+      const int g = __shfl_sync(0xffffffffu, h, 8 * x) / d.G;
+      const float s = row_sum(d, q, k, v, dout, rx, __shfl_sync(0xffffffffu, l2, 8 * x), keys,
+                              [&](int y) { return (long long)(first + y) * d.Hkv + g; });
+      if (part == x) sum = s;
+    }
+    if (c == 0) rowm[r] = make_float2(l2, sum);
   }
 }
 
@@ -1006,6 +1051,12 @@ bool launch_win_dkv(const WinDims& d, const void* q, const void* k, const void* 
   dkv_args(a, d, rowm, dk, dv, part, status);
   a.it = win_items(d);
   return dkv_any<false>(a, q, k, v, dout, st);
+}
+void launch_packed_rowdata(const PackedDims& x, const PackedTables& p, const void* q, const void* k, const void* v, const void* o,
+                           const void* dout, const float* lse, float2* rowm, cudaStream_t st) {
+  const long long blocks = ((long long)x.d.S * x.d.Hq + 31) / 32, most = (long long)num_sms() * 16;
+  packed_rowdata_kernel<<<(int)(blocks < most ? blocks : most), 256, 0, st>>>(
+      x.d, p, (const bf16*)q, (const bf16*)k, (const bf16*)v, (const bf16*)o, (const bf16*)dout, lse, rowm);
 }
 bool launch_packed_dkv(const PackedDims& x, const PackedTables& p, const void* q, const void* k, const void* v, const void* dout,
                        const float2* rowm, void* dk, void* dv, float* part, unsigned* status, cudaStream_t st) {
