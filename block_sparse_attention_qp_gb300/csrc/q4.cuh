@@ -13,7 +13,6 @@
 // 128 x 64 bytes of codes, 128 x 8 scales, 128 bytes e + 127.
 #pragma once
 #include <cuda_fp16.h>
-#include <cuda_fp4.h>
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -41,42 +40,57 @@ __device__ __forceinline__ uint32_t q4_scales(uint32_t two) {
   return (uint32_t)h.x | (uint32_t)h.y << 16;
 }
 
+// a / b in a few instructions, with c within 2^-22 of 1 / b: the product corrected by its remainder (exact in a fused
+// multiply-add).  Wherever the quotient is a number of few bits, as the borders between two members of the grids below are, it
+// is found exactly; the quotients here (a of 8 bits, b of 4 or 6) are 2^-12 away from any border that they do not lie on.
+__device__ __forceinline__ float quotient(float a, float b, float c) {
+  const float q = a * c;
+  return fmaf(fmaf(-q, b, a), c, q);
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // What a row's largest magnitude (bf16 bits; they compare as integers, infinities and NaN above the rest) makes of it:
-// the exponent, and with a run's largest magnitude the scale's byte and its reciprocal (0 for a scale of 0).
+// the exponent, and with a run's largest magnitude the scale's byte, the scale times 2^e and its reciprocal (0 for a
+// scale of 0).
 struct Q4Row {
   int e;
-  float down;  // 2^-e
   bool finite;
 };
 __device__ __forceinline__ Q4Row q4_row(uint32_t top) {
   Q4Row r;
   r.finite = top < 0x7f80u;
-  const int p = (int)(__float_as_uint(__fdiv_rn(__uint_as_float(top << 16), 6.f)) >> 23) - 127;  // floor of log2
+  // floor(log2(top / 6)): 6 is 3/2 4, so a mantissa from 3/2 on loses two, a smaller one three (subnormal ones are far
+  // below the least exponent)
+  const int p = (int)(top >> 7) - 127 - ((top & 0x7f) >= 64 ? 2 : 3);
   r.e = r.finite ? min(max(p - 7, kQ4MinExp), kQ4MaxExp) : 0;
-  r.down = pow2f(-r.e);
   return r;
 }
 __device__ __forceinline__ uint32_t q4_scale(const Q4Row& r, uint32_t top16, float& s, float& inv) {
-  const float want = __fdiv_rn(__uint_as_float(top16 << 16) * r.down, 6.f);
+  const float want = quotient(__uint_as_float(top16 << 16) * pow2f(-r.e), 6.f, 1.f / 6.f);
   const uint32_t sb = r.finite ? __nv_cvt_float_to_fp8(want, __NV_SATFINITE, __NV_E4M3) : kQ4NaN;
-  s = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)sb, __NV_E4M3)));
-  inv = s > 0.f ? __frcp_rn(s) : 0.f;
+  const uint32_t h = q4_scales(sb);
+  s = __half2float(*reinterpret_cast<const __half*>(&h)) * pow2f(r.e);
+  inv = sb != 0 ? rcp_approx(s) : 0.f;
   return sb;
 }
-// Codes of eight bf16.  x / s is the product with the rounded reciprocal corrected by its remainder: exact wherever
-// the quotient lies on a border between two codes (x has 8 bits, a border times s at most 7); elsewhere it is 2^-12 away
-// from one.
+// Codes of eight bf16.
 __device__ __forceinline__ uint32_t q4_encode(const Q4Row& r, uint4 v, float s, float inv) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t code = 0;
+  float x[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float2 x = make_float2(__uint_as_float(w[i] << 16) * r.down, __uint_as_float(w[i] & 0xffff0000u) * r.down);
-    const float a = x.x * inv, b = x.y * inv;
-    x.x = fmaf(fmaf(-a, s, x.x), inv, a);
-    x.y = fmaf(fmaf(-b, s, x.y), inv, b);
-    code |= (uint32_t)__nv_cvt_float2_to_fp4x2(x, __NV_E2M1, cudaRoundNearest) << (8 * i);
+    x[2 * i] = quotient(__uint_as_float(w[i] << 16), s, inv);
+    x[2 * i + 1] = quotient(__uint_as_float(w[i] & 0xffff0000u), s, inv);
   }
+  uint32_t code;
+  asm("{\n.reg .b8 a, b, c, d;\ncvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\ncvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\ncvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\nmov.b32 %0, {a, b, c, d};\n}\n"
+      : "=r"(code)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
   return r.finite ? code : 0u;
 }
 __device__ __forceinline__ uint32_t q4_top(uint4 v) {  // two bf16 magnitudes whose larger is the largest of the eight
