@@ -1,6 +1,7 @@
 // Shared device helpers for the MSA kernels (sm_103a): constants of the method, the device status
 // word, asynchronous copies with L2 cache hints, and bf16 packing.  Every contraction of the
-// library runs on the tcgen05 tensor cores (sm100.cuh); nothing here issues warp-level MMAs.
+// library runs on the tcgen05 tensor cores (sm100.cuh), but for decode over caches in 4 bits (q4.cu), whose operands
+// are made in registers and go into warp-level products.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -21,6 +21,16 @@
 //      read consecutive bytes, and the score rows are dealt alike.
 // A tile's four warps take 32 keys each with sums of their own, joined at the end; a fifth keeps a ring of tiles
 // loading.  Few (sequence, group) pairs: their tiles are split over blocks and joined by a second kernel.
+//
+// One wave of resident blocks over 16384 keys each (456 pairs): 5.7 TB/s, 0.84 of a copy; 128 sequences of 4096 keys, 8 KV heads
+// (2.25 waves): 121 us, 5.1 TB/s; the same with lengths from 1 to 4096: 105 us, 4.5 TB/s; one sequence of 65536 keys: 23 us
+// and 8 of joining; 32 sequences with 16 of 64 blocks selected, 256 pairs on 152 SMs: 25 us, 2.8 TB/s.  16 heads a group
+// (twice the products and weights): 104 us for 64 sequences of 4096 keys.  340 instructions a run of 16 keys are issued in
+// 66 % of the cycles; the pipes are busy at half that or less.  Measured on the way (first line's 128 sequences): codes by
+// shifts and masks and keys paired by byte permutations 260 us (660 instructions); both as below 149; tile data by the
+// loading warp, full tiles without masks 123.  Tried and not kept: four blocks an SM with three stages (123) or with more
+// (156, spills); the P of even and odd dims as two halves of the 16 rows, half of the multiplications and 24 instead of 16
+// products (130); two chains of K products (121); the tiles of all pairs dealt out evenly (134 and 16 of joining).
 #include <math.h>
 
 #include <type_traits>
@@ -479,7 +489,8 @@ void launch_q4_read(const void* cache, int B, int H, int cap, int first, int cou
   q4_read_kernel<<<(int)(g < most ? g : most), 256, 0, st>>>((const uint8_t*)cache, H, cap / kBlock, first, count, units, (bf16*)out);
 }
 
-// Splits of a pair's tiles: as many as fill the resident blocks, of at least four tiles.
+// Splits of a pair's tiles: as many as fill the resident blocks, of at least four tiles (a part's start, end and share of
+// the join cost about as much as three).
 WinSplit q4_split(long long pairs, int tiles, int G) {
   WinSplit w;
   const long long room = (long long)num_sms() * (G > 8 ? 2 : 3);
