@@ -1587,10 +1587,10 @@ int msa_packed_forward(const msa_packed_plan_t* plan, const void* table, size_t 
   bool ok = true;
   if (x.d.S)
     timed("packed_fwd", st, [&] { ok = launch_packed_fwd(x, packed_tables(x, table), q, k, v, o, lse, status, st); });
-  else
+  else {
     cudaMemsetAsync(status, 0, 32 * sizeof(unsigned), st);
-  if (ok && x.d.S < x.rows)
     timed("packed_pad", st, [&] { launch_packed_pad(x, o, x.d.Hq, nullptr, 0, nullptr, 0, lse, st); });
+  }
   if (!ok) {
     set_err("msa_packed_forward: could not create TMA tensor maps (cuTensorMapEncodeTiled)");
     return MSA_ERR_CUDA;
@@ -1610,16 +1610,15 @@ int msa_packed_backward(const msa_packed_plan_t* plan, const void* table, size_t
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaGetLastError();
   unsigned* status = at<unsigned>(workspace, 0);  // cleared by launch_packed_dq
-  if (x.d.S < x.rows)
-    timed("packed_pad", st, [&] { launch_packed_pad(x, dq, x.d.Hq, dk, x.d.Hkv, dv, x.d.Hkv, nullptr, st); });
   if (!x.d.S) {
+    timed("packed_pad", st, [&] { launch_packed_pad(x, dq, x.d.Hq, dk, x.d.Hkv, dv, x.d.Hkv, nullptr, st); });
     cudaMemsetAsync(status, 0, 32 * sizeof(unsigned), st);
     return cuda_fail("msa_packed_backward");
   }
   const PackedTables t = packed_tables(x, table);
   float2* rowdata = at<float2>(workspace, w.rowm);
   float* part = at<float>(workspace, w.part);
-  timed("packed_rowdata", st, [&] { launch_packed_rowdata(x, t, q, k, v, o, dout, lse, rowdata, st); });
+  timed("packed_rowdata", st, [&] { launch_packed_rowdata(x, t, q, k, v, o, dout, lse, rowdata, dq, dk, dv, st); });
   bool ok = true;
   timed("packed_dq", st, [&] { ok = launch_packed_dq(x, t, q, k, v, dout, rowdata, dq, status, st); });
   if (ok) timed("packed_dkv", st, [&] { ok = launch_packed_dkv(x, t, q, k, v, dout, rowdata, dk, dv, part, status, st); });

@@ -217,11 +217,13 @@ void launch_packed_plan(const PackedDims& x, const int32_t* lengths, int n, void
 bool launch_packed_fwd(const PackedDims& x, const PackedTables& p, const void* q, const void* k, const void* v, void* o,
                        float* lse, unsigned* status, cudaStream_t st);
 void launch_packed_rowdata(const PackedDims& x, const PackedTables& p, const void* q, const void* k, const void* v,
-                           const void* o, const void* dout, const float* lse, float2* rowm, cudaStream_t st);
+                           const void* o, const void* dout, const float* lse, float2* rowm, void* dq, void* dk, void* dv,
+                           cudaStream_t st);
 bool launch_packed_dq(const PackedDims& x, const PackedTables& p, const void* q, const void* k, const void* v,
                       const void* dout, float2* rowm, void* dq, unsigned* status, cudaStream_t st);
 bool launch_packed_dkv(const PackedDims& x, const PackedTables& p, const void* q, const void* k, const void* v,
                        const void* dout, const float2* rowm, void* dk, void* dv, float* part, unsigned* status, cudaStream_t st);
+// Zeros (and -inf) where there is no sequence at all; else the forward and the row data write the rows behind the last one.
 void launch_packed_pad(const PackedDims& x, void* a, int ha, void* b, int hb, void* c, int hc, float* lse, cudaStream_t st);
 bool launch_packed_join(const PackedDims& x, const PackedTables& p, const float* part, void* dk, void* dv, cudaStream_t st);
 

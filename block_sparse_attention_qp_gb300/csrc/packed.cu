@@ -168,7 +168,7 @@ Layout layout(const PackedDims& x) {
   return l;
 }
 
-// The rows behind the last sequence: zeros, and -inf in lse.
+// The rows behind the last sequence: zeros, and -inf in lse (launched where there is no sequence at all).
 struct PadArgs {
   uint4* rows[3];    // from the first such row on
   long long n[3];    // 16-byte pieces

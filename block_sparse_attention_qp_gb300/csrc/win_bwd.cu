@@ -522,12 +522,18 @@ __global__ void win_rowdata_kernel(WinDims d, const bf16* __restrict__ q, const 
   }
 }
 
-// Row data of packed sequences: D = rowsum(dO O), four rows a warp; but rows of a few keys -- the first ones of every
+// Row data of packed sequences (and zeros for the gradients' rows behind the last one): D = rowsum(dO O), four rows a warp; but rows of a few keys -- the first ones of every
 // sequence -- whose query tile spans several key tiles (win_dq_kernel leaves D of the others) have it from P and dP.
 __global__ void __launch_bounds__(256, 4) packed_rowdata_kernel(WinDims d, PackedTables p, const bf16* __restrict__ q, const bf16* __restrict__ k,
                                                              const bf16* __restrict__ v, const bf16* __restrict__ o,
                                                              const bf16* __restrict__ dout, const float* __restrict__ lse,
-                                                             float2* __restrict__ rowm) {
+                                                             float2* __restrict__ rowm, bf16* dq, bf16* dk, bf16* dv) {
+  for (int x = 0; x < 3; ++x) {
+    const int heads = x ? d.Hkv : d.Hq;
+    uint4* to = reinterpret_cast<uint4*>((x == 0 ? dq : x == 1 ? dk : dv) + (long long)d.S * heads * kD);
+    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < (p.rows - d.S) * heads * (kD / 8); i += (long long)gridDim.x * blockDim.x)
+      to[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
   const unsigned rows = (unsigned)d.S * d.Hq, step = gridDim.x * blockDim.x / 32;  // (below 2^31)
   const int lane = threadIdx.x % 32, c = lane % 8, part = lane / 8, tt = kBlock / d.G;
   // (a warp's rows a quarter of the tensor apart: the rows of a few keys lie together, and four of them in turn by one
@@ -1053,10 +1059,10 @@ bool launch_win_dkv(const WinDims& d, const void* q, const void* k, const void* 
   return dkv_any<false>(a, q, k, v, dout, st);
 }
 void launch_packed_rowdata(const PackedDims& x, const PackedTables& p, const void* q, const void* k, const void* v, const void* o,
-                           const void* dout, const float* lse, float2* rowm, cudaStream_t st) {
+                           const void* dout, const float* lse, float2* rowm, void* dq, void* dk, void* dv, cudaStream_t st) {
   const long long blocks = ((long long)x.d.S * x.d.Hq + 31) / 32, most = (long long)num_sms() * 16;
   packed_rowdata_kernel<<<(int)(blocks < most ? blocks : most), 256, 0, st>>>(
-      x.d, p, (const bf16*)q, (const bf16*)k, (const bf16*)v, (const bf16*)o, (const bf16*)dout, lse, rowm);
+      x.d, p, (const bf16*)q, (const bf16*)k, (const bf16*)v, (const bf16*)o, (const bf16*)dout, lse, rowm, (bf16*)dq, (bf16*)dk, (bf16*)dv);
 }
 bool launch_packed_dkv(const PackedDims& x, const PackedTables& p, const void* q, const void* k, const void* v, const void* dout,
                        const float2* rowm, void* dk, void* dv, float* part, unsigned* status, cudaStream_t st) {

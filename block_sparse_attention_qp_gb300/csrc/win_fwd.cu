@@ -519,6 +519,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1) win_fwd_kernel(const __grid_co
   __syncthreads();
   fence_after_sync();
   if (warp == 0) tmem_dealloc(tmem, 512);
+  if (kPacked && A.p.rows > d.S) {  // the rows behind the last sequence
+    const long long pad = A.p.rows - d.S, at = (long long)blockIdx.x * kFwdThreads + tid, step = (long long)gridDim.x * kFwdThreads;
+    uint4* o = reinterpret_cast<uint4*>(A.op + (long long)d.S * d.Hq * kD);
+    for (long long i = at; i < pad * d.Hq * (kD / 8); i += step) o[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (long long i = at; i < pad * d.Hq; i += step) A.lse[i / pad * A.p.rows + d.S + i % pad] = -INFINITY;
+  }
   for (int nu = sh->bad0; nu <= sh->bad1; ++nu) mend_rows<G, kPacked>(A, unit_at<kPacked>(nu));
 }
 
