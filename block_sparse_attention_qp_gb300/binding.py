@@ -524,8 +524,12 @@ def msa_warmup_func(Q_proxy, K_proxy, Q, K, V, top_k: int, scale: float):
 # ---------------------------------------------------------------- sliding-window attention
 # The entry points below serve single tokens too, where the host's part of a call counts: arguments are
 # looked at once by a fast test, and only a failing one is taken apart for its message.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 class _Guard:
-    """Makes a device current for a block (torch.cuda.device costs microseconds even where it is)."""
+    """Makes a device current for a block (torch.cuda.device costs microseconds even where it is).  Entered with a CUDA
+    tensor at hand, so CUDA is up."""
     __slots__ = ("device", "entered")
 
     def __init__(self, device):
@@ -533,7 +537,7 @@ class _Guard:
 
     def __enter__(self):
         self.entered = None
-        if torch.cuda.current_device() != self.device.index:
+        if _current_device() != self.device.index:
             self.entered = torch.cuda.device(self.device)
             self.entered.__enter__()
 
@@ -590,6 +594,12 @@ def _window_bytes(op, *shape):
     if n == 0:
         raise MSAError(f"unsupported shape for op {op}: {lib.msa_last_error().decode()}")
     return n
+
+
+@functools.lru_cache(maxsize=4096)
+def _window_call(op, *shape):
+    """(the shape as an argument of the library, bytes of workspace); nothing writes to the shape."""
+    return ctypes.byref(WindowShape(*shape)), _window_bytes(op, *shape)
 
 
 def msa_window_workspace_size(shape: WindowShape, op: int) -> int:
@@ -888,6 +898,9 @@ def _rows(t, name, B=None, N=None, H=None, write=False):
 
 _X_NAMES = [f"xs[{i}]" for i in range(ROPE_PARTS)]
 _W_NAMES = [f"weights[{i}]" for i in range(ROPE_PARTS)]
+_DY_NAMES = [f"dys[{i}]" for i in range(ROPE_PARTS)]
+_DX_NAMES = [f"dxs[{i}]" for i in range(ROPE_PARTS)]
+_C_NAMES = [f"caches[{i}]" for i in range(ROPE_PARTS)]
 
 
 def _device_of(xs):
@@ -916,7 +929,7 @@ def _axes(axes, pairs):
 
 def _rope_args(xs, weights, rotate, inv_freq, interleaved, eps, positions, dev, axes=None):
     """Checks what the norm and rotation entry points share; returns (shape, parts, inv_freq's and
-    positions' addresses), a part being (x's pointer and strides, weight's address, heads, flags)."""
+    positions' addresses, the axes), a part being (x's pointer and strides, weight's address, heads, flags)."""
     count = len(xs)
     if not 1 <= count <= ROPE_PARTS:
         raise MSAError(f"between 1 and {ROPE_PARTS} tensors, got {count}")
@@ -947,18 +960,12 @@ def _rope_args(xs, weights, rotate, inv_freq, interleaved, eps, positions, dev, 
         pp = _ask(positions, "positions", torch.int32, (max(A, axes.count), B, N), dev)
     elif positions is not None:
         pp = _ask(positions, "positions", torch.int32, (B, N), dev)
-    return RopeShape(B, N, 128, rotary, 1 if interleaved else 0, 0, eps), parts, fp, pp
+    return RopeShape(B, N, 128, rotary, 1 if interleaved else 0, 0, eps), parts, fp, pp, axes
 
 
 @functools.lru_cache(maxsize=64)
 def _rope_bytes(nparts, op):
     return int(load_library().msa_norm_rope_workspace_size(nparts, op))
-
-
-def _strides(t):
-    """(pointer, batch stride, token stride) of a contiguous tensor [B, N, heads, 128]."""
-    st = t.shape[2] * 128
-    return t.data_ptr(), st * t.shape[1], st
 
 
 def msa_norm_rope_forward(xs, weights, inv_freq, positions=None, eps: float = 1e-6, rotate=None,
@@ -974,18 +981,21 @@ def msa_norm_rope_forward(xs, weights, inv_freq, positions=None, eps: float = 1e
     and width of images and video: pair i turns by positions[axes[i]] * inv_freq[i].
     A tensor without weight and rotation is copied.  Returns contiguous tensors [B, N, heads, 128]."""
     dev = _device_of(xs)
-    shape, parts, fp, pp = _rope_args(xs, weights, rotate, inv_freq, interleaved, eps, positions, dev, axes)
+    shape, parts, fp, pp, axes = _rope_args(xs, weights, rotate, inv_freq, interleaved, eps, positions, dev, axes)
+    B, N, pack = shape.B, shape.N, _PART.pack
     with _Guard(dev):
-        ys = [torch.empty(x.shape, dtype=torch.bfloat16, device=dev) for x in xs]
-        packed = b"".join([_PART.pack(*at, *_strides(y), 0, 0, 0, w, 0, h, f)
-                           for (at, w, h, f), y in zip(parts, ys)])
+        ys, rows = [], []
+        for (px, sb, st), w, h, f in parts:
+            y = torch.empty((B, N, h, 128), dtype=torch.bfloat16, device=dev)
+            ys.append(y)
+            rows.append(pack(px, sb, st, y.data_ptr(), N * h * 128, h * 128, 0, 0, 0, w, 0, h, f))
+        packed = b"".join(rows)
         if axes is None:
             rc = load_library().msa_norm_rope_forward(ctypes.byref(shape), packed, len(ys), pp, fp,
                                                       _stream_of(dev))
         else:
             rc = load_library().msa_norm_rope_axes_forward(ctypes.byref(shape), packed, len(ys), pp, fp,
-                                                           ctypes.byref(_axes(tuple(axes), shape.rotary // 2)),
-                                                           _stream_of(dev))
+                                                           ctypes.byref(axes), _stream_of(dev))
     if rc:
         _check(rc, "msa_norm_rope_forward")
     return tuple(ys)
@@ -997,7 +1007,7 @@ def msa_norm_rope_backward(xs, weights, dys, inv_freq, positions=None, eps: floa
     dxs: where to write them (e.g. the slices of one packed gradient, or the dys), default new
     tensors; each may be its own part's x or dy, but overlap no other tensor of the call."""
     dev = _device_of(xs)
-    shape, parts, fp, pp = _rope_args(xs, weights, rotate, inv_freq, interleaved, eps, positions, dev, axes)
+    shape, parts, fp, pp, axes = _rope_args(xs, weights, rotate, inv_freq, interleaved, eps, positions, dev, axes)
     n = len(xs)
     if len(dys) != n or (dxs is not None and len(dxs) != n):
         raise MSAError("one dy (and dx, where given) per tensor")
@@ -1005,14 +1015,21 @@ def msa_norm_rope_backward(xs, weights, dys, inv_freq, positions=None, eps: floa
         # one tensor for the weights' gradients: a row each
         dws = torch.empty((n, 128), dtype=torch.float32, device=dev)
         out_w, rows, dw = list(dws.unbind(0)), [], dws.data_ptr()
-        out_x = [torch.empty(x.shape, dtype=torch.bfloat16, device=dev) for x in xs] if dxs is None else dxs
+        B, N, pack, out_x = shape.B, shape.N, _PART.pack, [] if dxs is None else dxs
         for i, (at, w, h, f) in enumerate(parts):
-            dy = _rows(dys[i], f"dys[{i}]", shape.B, shape.N, h)
-            dx = _strides(out_x[i]) if dxs is None else _rows(dxs[i], f"dxs[{i}]", shape.B, shape.N, h, write=True)
-            if dys[i].device != dev or out_x[i].device != dev:
-                _on(dys[i], f"dys[{i}]", dev)
-                _on(out_x[i], f"dxs[{i}]", dev)
-            rows.append(_PART.pack(*at, *dy, *dx, w, dw + 512 * i if w else 0, h, f))
+            dy = dys[i]
+            pdy = _rows(dy, _DY_NAMES[i], B, N, h)
+            if dxs is None:
+                dx = torch.empty((B, N, h, 128), dtype=torch.bfloat16, device=dev)
+                out_x.append(dx)
+                pdx = (dx.data_ptr(), N * h * 128, h * 128)
+            else:
+                dx = dxs[i]
+                pdx = _rows(dx, _DX_NAMES[i], B, N, h, True)
+            if dy.device != dev or dx.device != dev:
+                _on(dy, _DY_NAMES[i], dev)
+                _on(dx, _DX_NAMES[i], dev)
+            rows.append(pack(*at, *pdy, *pdx, w, dw + 512 * i if w else 0, h, f))
             if not w:
                 out_w[i] = None
         wp, wn, ws = _ws(ws, _rope_bytes(n, OP_NORM_ROPE_BACKWARD), dev)
@@ -1021,8 +1038,7 @@ def msa_norm_rope_backward(xs, weights, dys, inv_freq, positions=None, eps: floa
                                                        wn, _stream_of(dev))
         else:
             rc = load_library().msa_norm_rope_axes_backward(ctypes.byref(shape), b"".join(rows), n, pp, fp,
-                                                            ctypes.byref(_axes(tuple(axes), shape.rotary // 2)),
-                                                            wp, wn, _stream_of(dev))
+                                                            ctypes.byref(axes), wp, wn, _stream_of(dev))
     if rc:
         _check(rc, "msa_norm_rope_backward")
     return tuple(out_x), tuple(out_w)
@@ -1045,7 +1061,7 @@ def msa_norm_rope_append(xs, weights, inv_freq, seq_len, caches, eps: float = 1e
     x4 = xs
     if xs[0].dim() == 3:
         x4 = [x.unsqueeze(1) if isinstance(x, torch.Tensor) and x.dim() == 3 else x for x in xs]
-    shape, parts, fp, pp = _rope_args(x4, weights, rotate, inv_freq, interleaved, eps, positions, dev, axes)
+    shape, parts, fp, pp, axes = _rope_args(x4, weights, rotate, inv_freq, interleaved, eps, positions, dev, axes)
     B = shape.B
     sp = _ask(seq_len, "seq_len", torch.int32, (B,), dev)
     if len(caches) != len(x4):
@@ -1060,7 +1076,7 @@ def msa_norm_rope_append(xs, weights, inv_freq, seq_len, caches, eps: float = 1e
                 to = (y.data_ptr(), shape.N * h * 128, h * 128)
                 outs.append(y)
             elif isinstance(c, torch.Tensor) and c.dtype is torch.uint8:
-                to = (_q4(c, f"caches[{i}]", (B, h), dev), 0, 0)
+                to = (_q4(c, _C_NAMES[i], (B, h), dev), 0, 0)
                 if capacity is not None and c.shape[2] * 128 != capacity:
                     raise MSAError(f"caches of different capacities: {capacity}, {c.shape[2] * 128}")
                 capacity = c.shape[2] * 128
@@ -1068,9 +1084,9 @@ def msa_norm_rope_append(xs, weights, inv_freq, seq_len, caches, eps: float = 1e
                 outs.append(c)
             else:
                 c4 = c.unsqueeze(2) if isinstance(c, torch.Tensor) and c.dim() == 3 else c
-                to = _rows(c4, f"caches[{i}]", B, None, h, write=True)
+                to = _rows(c4, _C_NAMES[i], B, None, h, write=True)
                 if c4.device != dev:
-                    _on(c4, f"caches[{i}]", dev)
+                    _on(c4, _C_NAMES[i], dev)
                 if capacity is not None and c4.shape[1] != capacity:
                     raise MSAError(f"caches of different capacities: {capacity}, {c4.shape[1]}")
                 capacity = c4.shape[1]
@@ -1083,7 +1099,7 @@ def msa_norm_rope_append(xs, weights, inv_freq, seq_len, caches, eps: float = 1e
             rc = load_library().msa_norm_rope_append(ctypes.byref(shape), b"".join(rows), len(rows), sp, fp,
                                                      wp, wn, _stream_of(dev))
         else:
-            how = None if axes is None else ctypes.byref(_axes(tuple(axes), shape.rotary // 2))
+            how = None if axes is None else ctypes.byref(axes)
             rc = load_library().msa_norm_rope_axes_append(ctypes.byref(shape), b"".join(rows), len(rows), sp, pp,
                                                           fp, how, wp, wn, _stream_of(dev))
     if rc:
@@ -1194,22 +1210,21 @@ def msa_window_decode_q4(q, k_cache, v_cache, seq_len, window: int, sinks: int, 
     ptrs = (_ask(q, "q", torch.bfloat16, (B, Hq, D), dev), _q4(k_cache, "k_cache", (B, Hkv), dev),
             _ask(v_cache, "v_cache", torch.uint8, k_cache.shape, dev),
             _ask(seq_len, "seq_len", torch.int32, (B,), dev))
-    window, sinks, scale = _int32(window, "window"), _int32(sinks, "sinks"), float(scale)
-    shape = (B, blocks * 128, Hq, Hkv, D, window, sinks, scale)
     with _Guard(dev):
-        wp, wn, ws = _ws(ws, _window_bytes(OP_WINDOW_DECODE_Q4, *shape) if ws is None else 0, dev)
+        shape, need = _window_call(OP_WINDOW_DECODE_Q4, B, blocks * 128, Hq, Hkv, D, _int32(window, "window"),
+                                   _int32(sinks, "sinks"), float(scale))
+        wp, wn, ws = _ws(ws, need, dev)
         o = torch.empty_like(q)
         lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
-        rc = load_library().msa_window_decode_q4(ctypes.byref(WindowShape(*shape)), *ptrs, o.data_ptr(),
-                                                 lse.data_ptr(), wp, wn, _stream_of(dev))
+        rc = load_library().msa_window_decode_q4(shape, *ptrs, o.data_ptr(), lse.data_ptr(), wp, wn, _stream_of(dev))
     if rc:
         _check(rc, "msa_window_decode_q4")
     return o, lse
 
 
 @functools.lru_cache(maxsize=1024)
-def _decode_q4_bytes(*shape):
-    return msa_workspace_size(Shape(*shape), OP_DECODE_Q4)
+def _decode_q4_call(*shape):
+    return ctypes.byref(Shape(*shape)), msa_workspace_size(Shape(*shape), OP_DECODE_Q4)
 
 
 def msa_decode_q4(q, qp, k_cache, v_cache, kp_cache, seq_len, top_k: int, scale: float, ws=None):
@@ -1228,15 +1243,15 @@ def msa_decode_q4(q, qp, k_cache, v_cache, kp_cache, seq_len, top_k: int, scale:
             _q4(k_cache, "k_cache", (B, Hkv), dev), _ask(v_cache, "v_cache", torch.uint8, k_cache.shape, dev),
             _ask(kp_cache, "kp_cache", torch.bfloat16, (B, S, D) if kp_cache.dim() == 3 else (B, S, 1, D), dev),
             _ask(seq_len, "seq_len", torch.int32, (B,), dev))
-    shape = (B, S, Hq, Hkv, Hp, D, _int32(top_k, "top_k"), float(scale))
+    top_k = _int32(top_k, "top_k")
     with _Guard(dev):
-        need = _decode_q4_bytes(*shape)
+        shape, need = _decode_q4_call(B, S, Hq, Hkv, Hp, D, top_k, float(scale))
         wp, wn, ws = _ws(ws, need, dev)
         o = torch.empty_like(q)
         lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
-        idx = torch.empty((B, Hp, shape[6]), dtype=torch.int32, device=dev)
-        rc = load_library().msa_decode_q4(ctypes.byref(Shape(*shape)), *ptrs, idx.data_ptr(), o.data_ptr(),
-                                          lse.data_ptr(), wp, wn, _stream_of(dev))
+        idx = torch.empty((B, Hp, top_k), dtype=torch.int32, device=dev)
+        rc = load_library().msa_decode_q4(shape, *ptrs, idx.data_ptr(), o.data_ptr(), lse.data_ptr(), wp, wn,
+                                          _stream_of(dev))
     if rc:
         _check(rc, "msa_decode_q4")
     return o, lse, idx
