@@ -342,9 +342,11 @@ __global__ void __launch_bounds__(kQ4Threads, NT == 1 ? 3 : 2) q4_decode_kernel(
           float p[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float mb = !kFull && m[y][e & 1] == -INFINITY ? 0.f : m[y][e & 1];
-            l[y][e & 1] += exp2_ftz(x2[c][y][e] - mb);
-            p[e] = exp2_ftz(xv[c][y][e] - mb);
+            const bool none = !kFull && m[y][e & 1] == -INFINITY;
+            // (the row sum in units of 2^kSlack: weights of keys whose values are all zero, f = -100, reach 2^108, and
+            // 2^23 of them must not pass fp32's range)
+            l[y][e & 1] += exp2_ftz(x2[c][y][e] - (none ? 0.f : top[y][e & 1]));
+            p[e] = exp2_ftz(xv[c][y][e] - (none ? 0.f : m[y][e & 1]));
           }
           pb[y][0] = transpose8(pack_half(p[0], p[1]));
           pb[y][1] = transpose8(pack_half(p[2], p[3]));
@@ -431,8 +433,8 @@ __global__ void __launch_bounds__(kQ4Threads, NT == 1 ? 3 : 2) q4_decode_kernel(
         sum = fmaf(a, sh.l[k][h], sum);
         y = fmaf(a, sums[(k * NT * 8 + h) * kD + tid], y);
       }
-      y /= sum;
-      const float ls = mx + log2f(sum);
+      y /= sum * exp2f(kSlack);
+      const float ls = mx + kSlack + log2f(sum);
       if (A.nsplit == 1) {
         A.o[(row0 + h) * kD + tid] = __float2bfloat16_rn(y);
         if (tid == 0) A.lse[row0 + h] = ls * kLn2;

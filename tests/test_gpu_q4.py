@@ -177,6 +177,29 @@ def test_window_decode_uneven_rows():
     decode_check(q, kc, vc, [n], lambda b, m: torch.arange(m, device="cuda"), o, lse, 768)
 
 
+@pytest.mark.parametrize("zeros", ["all", "the heaviest", "all but one"])
+def test_window_decode_values_of_zero(zeros):
+    """Rows of zeros have the least exponent, which the weights of their keys are taken relative to."""
+    r = gen(12)
+    n, H = 5000, 2
+    k, v = r(1, n, H, 128, scale=0.5), r(1, n, H, 128)
+    if zeros == "all":
+        v.zero_()
+    elif zeros == "the heaviest":
+        k[:, 77] *= 8
+        v[:, 77] = 0
+    else:
+        v[:, :4999] = 0
+    caches = [msa.msa_q4_cache(1, H, 5120, "cuda") for _ in range(2)]
+    for c, x in zip(caches, (k, v)):
+        msa.msa_norm_rope_append([x], None, None, lens32(n), [c])
+    q = r(1, 8, 128) * 2
+    o, lse = msa.msa_window_decode_q4(q, *caches, lens32(n), n, 0, SCALE)
+    decode_check(q, *caches, [n], lambda b, m: torch.arange(m, device="cuda"), o, lse, 5120)
+    if zeros == "all":
+        assert (o == 0).all()
+
+
 def test_window_decode_lengths_out_of_range():
     r = gen(6)
     lens, cap = [0, 200, 257, -1, 256], 256
