@@ -979,7 +979,7 @@ int check_packed_shape(const msa_packed_shape_t* s, const int32_t* lengths, int 
   return MSA_OK;
 }
 // The plan that a caller hands back, with the sizes of the table that it stands for.
-int check_plan(const msa_packed_plan_t* p, const void* table, size_t table_bytes, float scale, PackedDims* out) {
+int check_plan(const msa_packed_plan_t* p, float scale, PackedDims* out) {
   if (!p) {
     set_err("plan is null");
     return MSA_ERR_INVALID_ARG;
@@ -1017,14 +1017,17 @@ int check_plan(const msa_packed_plan_t* p, const void* table, size_t table_bytes
     set_err("scale must be positive and finite");
     return MSA_ERR_INVALID_ARG;
   }
-  if (p->tokens) {
-    if ((rc = check_ptrs({table}))) return rc;
-    if (table_bytes < packed_table_bytes(x)) {
-      set_err("the plan's table is too small");
-      return MSA_ERR_INVALID_ARG;
-    }
-  }
   *out = x;
+  return MSA_OK;
+}
+int check_plan(const msa_packed_plan_t* p, const void* table, size_t table_bytes, float scale, PackedDims* out) {
+  int rc = check_plan(p, scale, out);
+  if (rc || !p->tokens) return rc;
+  if ((rc = check_ptrs({table}))) return rc;
+  if (table_bytes < packed_table_bytes(*out)) {
+    set_err("the plan's table is too small");
+    return MSA_ERR_INVALID_ARG;
+  }
   return MSA_OK;
 }
 struct PackedWs {
@@ -1569,8 +1572,7 @@ size_t msa_packed_workspace_size(const msa_packed_plan_t* plan, int op) {
     set_err("not a packed op");
     return 0;
   }
-  static const char none = 0;  // (the table is not looked at)
-  if (check_plan(plan, &none - (reinterpret_cast<uintptr_t>(&none) & 15), ~(size_t)0, 1.f, &x) != MSA_OK) return 0;
+  if (check_plan(plan, 1.f, &x) != MSA_OK) return 0;
   return packed_ws(x, op).bytes;
 }
 
