@@ -226,6 +226,67 @@ __global__ void __launch_bounds__(128)
   }
 }
 
+// The same selection where a row has at most 32 J blocks, J a lane: the K1-th largest score is found bit by bit (scores as
+// integers of their order, counted by ballots), then the blocks above it and the first of those equal to it are written in
+// order: 32 steps of J ballots, whatever K1, where the lists cost KMAX registers' worth of moves a block and a round a pick.
+// 256 rows, between events, the kernel above / this one, us: 64 blocks, top_k = 16 14.7 / 8.0, top_k = 64 86.9 / 8.1; 256
+// blocks, top_k = 4 12.2 / 9.1, 16 21.5 / 9.1, 64 104.4 / 8.8.  At 33 blocks and top_k = 4 it is 6.5 / 7.4: launch_decode_select
+// leaves rows of at most 64 blocks and 8 picks to the lists.
+template <int J>
+__global__ void __launch_bounds__(128)
+    decode_select_few_kernel(Dims d, const float* __restrict__ scores, const int32_t* __restrict__ seq_len,
+                             int32_t* __restrict__ block_idx) {
+  constexpr unsigned kAll = 0xffffffffu;
+  const int lane = threadIdx.x % 32;
+  const long long row = ((long long)blockIdx.x * blockDim.x + threadIdx.x) / 32;  // b * Hp + p
+  if (row >= (long long)d.B * d.Hp) return;
+  const int len = seq_len[row / d.Hp];
+  if (len < 1 || len > d.S) return;  // flagged by decode_scores_kernel
+  const int m = (len - 1) / kBlock;
+  const float* c = scores + row * d.nblk;
+  uint32_t key[J];  // 0: no block, or a NaN (never picked)
+  int valid = 0;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int n = lane + 32 * j;
+    const float x = n < m ? c[n] : __uint_as_float(0x7fffffffu);
+    const uint32_t u = x == 0.f ? 0u : __float_as_uint(x);  // the zeros are equal
+    key[j] = x != x ? 0u : u >> 31 ? ~u : u | 0x80000000u;
+    valid += __popc(__ballot_sync(kAll, key[j] != 0));
+  }
+  const int K1 = min(d.top_k - 1, m), pick = min(K1, valid);
+  uint32_t t = 0;  // the largest value that at least `pick` keys reach
+  if (pick > 0) {
+#pragma unroll 1
+    for (int bit = 31; bit >= 0; --bit) {
+      const uint32_t x = t | 1u << bit;
+      int n = 0;
+#pragma unroll
+      for (int j = 0; j < J; ++j) n += __popc(__ballot_sync(kAll, key[j] >= x));
+      if (n >= pick) t = x;
+    }
+  } else {
+    t = kAll;
+  }
+  int above = 0;
+#pragma unroll
+  for (int j = 0; j < J; ++j) above += __popc(__ballot_sync(kAll, key[j] > t));
+  int left = pick - above, at = 0;  // of those equal to t, the first ones
+  int32_t* out = block_idx + row * d.top_k;
+  const unsigned before = (1u << lane) - 1u;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const unsigned same = __ballot_sync(kAll, key[j] == t);
+    const bool take = key[j] > t || (key[j] == t && __popc(same & before) < left);
+    const unsigned taken = __ballot_sync(kAll, take);
+    if (take) out[at + __popc(taken & before)] = lane + 32 * j;
+    left -= min(left, __popc(same));
+    at += __popc(taken);
+  }
+  // the local block; places that only NaN were left for, as above; padding
+  for (int i = at + lane; i < d.top_k; i += 32) out[i] = i == at ? m : i <= K1 ? 0x7fffffff : -1;
+}
+
 // One block per (b, attention group a): the group's G <= 16 query heads against its selected
 // blocks of the caches, on the tensor core.  Per selected block n (K and V by TMA, two stages):
 //   S^T = K_n Q^T         (M = 128 keys, N = 16: the G heads, the rest zero)   -> tensor memory
@@ -483,7 +544,11 @@ void launch_decode_select(const Dims& d, const float* scores, const int32_t* seq
                           int32_t* block_idx, cudaStream_t st) {
   const long long rows = (long long)d.B * d.Hp;
   const int g2 = (int)((rows * 32 + 127) / 128);
-  if (d.top_k <= 8)
+  if (d.nblk <= 64 && d.top_k > 8)
+    decode_select_few_kernel<2><<<g2, 128, 0, st>>>(d, scores, seq_len, block_idx);
+  else if (d.nblk > 64 && d.nblk <= 256)
+    decode_select_few_kernel<8><<<g2, 128, 0, st>>>(d, scores, seq_len, block_idx);
+  else if (d.top_k <= 8)
     decode_select_kernel<8><<<g2, 128, 0, st>>>(d, scores, seq_len, block_idx);
   else if (d.top_k <= 16)
     decode_select_kernel<16><<<g2, 128, 0, st>>>(d, scores, seq_len, block_idx);

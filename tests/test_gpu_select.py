@@ -1,0 +1,61 @@
+"""The decode step's selection: rows of some blocks have a kernel of their own, which picks what the other one picks."""
+import pytest
+import torch
+
+from block_sparse_attention_qp_gb300 import binding as msa
+
+pytestmark = pytest.mark.gpu
+SCALE = 128 ** -0.5
+
+
+def select(qp, kp, n, top_k, cap):
+    B, Hp = qp.shape[:2]
+    pad = torch.zeros((B, cap - kp.shape[1], 1, 128), dtype=torch.bfloat16, device="cuda")
+    kp = torch.cat([kp, pad], 1)
+    kv = torch.zeros((B, cap, 1, 128), dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros((B, max(4, Hp), 128), dtype=torch.bfloat16, device="cuda")
+    return msa.msa_decode(q, qp, kv, kv, kp.contiguous(), n, top_k, SCALE)[2]
+
+
+def plain(qp, kp, n, top_k):
+    """Blocks by score, ties to the lower one, a sorted list each: quarters, so every order of summation is exact."""
+    out = []
+    for b, m in enumerate(n.tolist()):
+        last = (m - 1) // 128
+        z = (qp[b].double() @ kp[b, :, 0].double().T).view(qp.shape[1], -1, 128).amax(-1)
+        for p in range(qp.shape[1]):
+            best = sorted(range(last), key=lambda i: (-float(z[p, i]), i))[:top_k - 1]
+            row = sorted(best) + [last]
+            out.append(row + [-1] * (top_k - len(row)))
+    return torch.tensor(out, dtype=torch.int32).view(len(n), qp.shape[1], top_k)
+
+
+@pytest.mark.parametrize("blocks,top_k,Hp", [(1, 1, 1), (2, 2, 2), (33, 5, 4), (64, 16, 2), (64, 64, 1), (65, 16, 4), (200, 33, 2), (256, 7, 1)])
+@pytest.mark.parametrize("coarse", [False, True])
+def test_few_blocks_as_many(blocks, top_k, Hp, coarse):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(blocks + top_k)
+    B, cap = 3, 128 * blocks
+    quarter = lambda *s: (torch.randn(s, generator=g, device="cuda") * 4).round() / 4  # noqa: E731
+    qp, kp = quarter(B, Hp, 128), quarter(B, cap, 1, 128)
+    if coarse:  # few different scores: ties in every row, among them +0 and -0
+        qp[:] = 0
+        qp[..., 0] = -0.25
+        kp = kp.round().clamp(-1, 0)
+    qp, kp = qp.to(torch.bfloat16), kp.to(torch.bfloat16)
+    n = torch.tensor([cap, max(1, cap - 127), max(1, cap // 2)], dtype=torch.int32, device="cuda")
+    got = select(qp, kp, n, top_k, cap)
+    assert torch.equal(got.cpu(), plain(qp, kp, n, top_k))
+    assert torch.equal(got, select(qp, kp, n, top_k, 257 * 128))  # the kernel for more blocks
+
+
+def test_scores_that_are_not_finite():
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    kp = torch.randn((1, 128 * 9, 1, 128), generator=g, device="cuda").to(torch.bfloat16)
+    qp = torch.randn((1, 2, 128), generator=g, device="cuda").to(torch.bfloat16)
+    n = torch.tensor([128 * 9], dtype=torch.int32, device="cuda")
+    kp[0, 256:384] = float("nan")  # a whole block
+    kp[0, 700, 0, 3] = float("inf")
+    for top_k in (2, 4, 8, 9, 12):
+        assert torch.equal(select(qp, kp, n, top_k, 128 * 9), select(qp, kp, n, top_k, 257 * 128))
