@@ -21,19 +21,24 @@
 
 namespace msa {
 
-// grid (ceil(nblk / kScoreBlocks), B), 128 threads.  Per CTA: kScoreBlocks consecutive key blocks
-// of sequence b, loaded by TMA (the proxy-key cache rows of a block are contiguous: 32 KB), and one
-// tcgen05 product per block, S^T = Kp_block Qp^T (M = 128 keys, N = NP >= Hp proxy heads, the
-// rows beyond Hp zero), into tensor memory; thread = key then reads its NP scores and the warps
-// reduce each head's maximum over the block.  The products are exact bf16 x bf16 in fp32, summed
-// in the tensor core's order, as in the training selection kernel.
-constexpr int kScoreBlocks = 3;  // 3 x 32 KB of proxy keys in flight per CTA, two CTAs per SM
+// grid (nblk, B), 128 threads.  Per CTA one key block of sequence b, loaded by TMA (the proxy-key cache rows of a block are
+// contiguous: 32 KB), and one tcgen05 product, S^T = Kp_block Qp^T (M = 128 keys, N = NP >= Hp proxy heads, the rows beyond
+// Hp zero), into tensor memory; thread = key then reads its NP scores and the warps reduce each head's maximum over the
+// block.  The products are exact bf16 x bf16 in fp32, summed in the tensor core's order, as in the training selection kernel.
+// A CTA is a chain of latencies (length, keys, product, maxima), so its keys are asked for before anything else and five
+// CTAs an SM are in different places of it.  128 sequences of 256 blocks, 8 heads (1.07 GB), us: one block a CTA 174
+// (6.2 TB/s), two 174, two with maxima by five shuffles instead of one reduction 192, three 228, three and the keys
+// asked for behind the queries' staging 244; 64 blocks, 32 heads, in the same order 78, 88, 123, 152, 140.
 constexpr int kKpBlock = kBlock * kD * 2;
+__device__ __forceinline__ float warp_max(float x) {  // NaN only where all 32 are
+  asm volatile("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(x));
+  return x;
+}
 template <int NP>
 struct ScoreShared {
-  uint64_t kv_full[kScoreBlocks], s_full[kScoreBlocks], mma_done;
+  uint64_t kv_full, s_full;
   uint32_t tmem;
-  float wmax[kScoreBlocks][4][NP];  // per block, warp and head: the warp's maximum
+  float wmax[4][NP];  // per warp and head: the warp's maximum
 };
 template <int NP>
 __global__ void __launch_bounds__(128)
@@ -42,30 +47,29 @@ __global__ void __launch_bounds__(128)
                          unsigned* status) {
   using namespace sm100;
   extern __shared__ uint8_t smem_raw[];
+  constexpr int kColumns = NP < 32 ? 32 : NP;  // (the least that can be had)
   ScoreShared<NP>* sh = reinterpret_cast<ScoreShared<NP>*>(smem_raw);
-  uint8_t* sK = align1024(smem_raw + sizeof(ScoreShared<NP>));  // [kScoreBlocks][128 keys][128 d]
-  uint8_t* sQ = sK + kScoreBlocks * kKpBlock;                    // [NP rows][128 d], K-major
-  const int b = blockIdx.y, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  uint8_t* sK = align1024(smem_raw + sizeof(ScoreShared<NP>));  // [128 keys][128 d]
+  uint8_t* sQ = sK + kKpBlock;                                   // [NP rows][128 d], K-major
+  const int b = blockIdx.y, n = blockIdx.x, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int len = seq_len[b];
   if (len < 1 || len > d.S) {
     if (tid == 0) atomicOr(status, kStatusBadIndex);
     return;
   }
-  const int m = (len - 1) / kBlock;  // local block of the new token (forced, never scored)
-  const int n0 = blockIdx.x * kScoreBlocks;
-  const int nb = min(kScoreBlocks, m - n0);  // blocks of this CTA before the local one
-  if (nb <= 0) return;
+  if (n >= (len - 1) / kBlock) return;  // the new token's own block is forced, never scored
   if (tid == 0) {
-    for (int x = 0; x < kScoreBlocks; ++x) {
-      mbar_init(&sh->kv_full[x], 1);
-      mbar_init(&sh->s_full[x], 1);
-    }
-    mbar_init(&sh->mma_done, 1);
+    mbar_init(&sh->kv_full, 1);
+    mbar_init(&sh->s_full, 1);
     mbar_fence_init();
+    const int row = b * d.S + n * kBlock;
+    mbar_expect_tx(&sh->kv_full, kKpBlock);
+    tma_load_2d(sK, &tm_kp, 0, row, &sh->kv_full);
+    tma_load_2d(sK + kKpBlock / 2, &tm_kp, 64, row, &sh->kv_full);
   }
   if (warp == 0) {
     __syncwarp();  // lane 0 initialised the barriers alone; the allocation is warp-collective
-    tmem_alloc(&sh->tmem, 128);
+    tmem_alloc(&sh->tmem, kColumns);
     tmem_relinquish();
   }
   // the proxy queries as the B operand: SW128 K-major rows, rows Hp .. NP-1 zero
@@ -81,48 +85,31 @@ __global__ void __launch_bounds__(128)
   fence_after_sync();
   const uint32_t tmem = sh->tmem;
   if (tid == 0) {
-    tma_prefetch_desc(&tm_kp);
-    for (int x = 0; x < nb; ++x) {
-      const int row = b * d.S + (n0 + x) * kBlock;
-      mbar_expect_tx(&sh->kv_full[x], kKpBlock);
-      tma_load_2d(sK + x * kKpBlock, &tm_kp, 0, row, &sh->kv_full[x]);
-      tma_load_2d(sK + x * kKpBlock + kKpBlock / 2, &tm_kp, 64, row, &sh->kv_full[x]);
-    }
     constexpr uint32_t id = idesc_bf16(128, NP, false, false);
-    const uint32_t aQ = smem_u32(sQ);
-    for (int x = 0; x < nb; ++x) {
-      if (!mbar_wait(&sh->kv_full[x], 0, status)) break;
+    if (mbar_wait(&sh->kv_full, 0, status)) {
       fence_after_sync();
-      const uint32_t aK = smem_u32(sK + x * kKpBlock);
+      const uint32_t aK = smem_u32(sK), aQ = smem_u32(sQ);
 #pragma unroll
-      for (int ks = 0; ks < 8; ++ks)
-        mma_ss(tmem + x * NP, desc_kmajor(aK, 128, ks), desc_kmajor(aQ, NP, ks), id, ks > 0);
-      mma_commit(&sh->s_full[x]);
+      for (int ks = 0; ks < 8; ++ks) mma_ss(tmem, desc_kmajor(aK, 128, ks), desc_kmajor(aQ, NP, ks), id, ks > 0);
     }
-    mma_commit(&sh->mma_done);  // arrives once every product issued above has completed
+    mma_commit(&sh->s_full);  // arrives once every product issued above has completed
   }
   __syncwarp();
   // thread = key (tensor-memory lane 32 warp + lane): its NP head scores, then each head's
   // maximum over the warp's 32 keys
-  const uint32_t lrow = static_cast<uint32_t>(warp * 32) << 16;
-  bool ok = true;
-  for (int x = 0; x < nb; ++x) {
-    if (!mbar_wait_warp(&sh->s_full[x], 0, status)) {
-      ok = false;
-      break;
-    }
+  const bool ok = mbar_wait_warp(&sh->s_full, 0, status);
+  if (ok) {
     fence_after_sync();
+    const uint32_t lrow = static_cast<uint32_t>(warp * 32) << 16;
     uint32_t v[NP];
-    if constexpr (NP == 16) tmem_ld16(tmem + lrow + x * NP, v);
-    else tmem_ld32(tmem + lrow + x * NP, v);
+    if constexpr (NP == 16) tmem_ld16(tmem + lrow, v);
+    else tmem_ld32(tmem + lrow, v);
     tmem_wait_ld();
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
       if (p < d.Hp) {
-        float mx = __uint_as_float(v[p]);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-        if (lane == 0) sh->wmax[x][warp][p] = mx;
+        const float mx = warp_max(__uint_as_float(v[p]));
+        if (lane == 0) sh->wmax[warp][p] = mx;
       }
     }
   }
@@ -130,16 +117,12 @@ __global__ void __launch_bounds__(128)
   __syncthreads();
   fence_after_sync();
   if (ok && tid < d.Hp)
-    for (int x = 0; x < nb; ++x)
-      scores[((size_t)b * d.Hp + tid) * d.nblk + n0 + x] =
-          fmaxf(fmaxf(sh->wmax[x][0][tid], sh->wmax[x][1][tid]),
-                fmaxf(sh->wmax[x][2][tid], sh->wmax[x][3][tid]));
+    scores[((size_t)b * d.Hp + tid) * d.nblk + n] =
+        fmaxf(fmaxf(sh->wmax[0][tid], sh->wmax[1][tid]), fmaxf(sh->wmax[2][tid], sh->wmax[3][tid]));
   if (warp == 0) {
-    // no product may still write tensor memory, and no copy may still land in shared memory,
-    // when the block exits
-    mbar_wait_warp(&sh->mma_done, 0, status);
-    for (int x = 0; x < nb; ++x) mbar_wait_warp(&sh->kv_full[x], 0, status);
-    tmem_dealloc(tmem, 128);
+    // no copy may still land in shared memory when the block exits (of the product, s_full was waited for)
+    mbar_wait_warp(&sh->kv_full, 0, status);
+    tmem_dealloc(tmem, kColumns);
   }
 }
 
@@ -525,10 +508,10 @@ bool launch_decode_scores(const Dims& d, const void* qp, const void* kp_cache,
   const uint64_t kps[1] = {128 * 2};
   const uint32_t kpb[2] = {64, 128};
   if (!make_tmap_bf16(&mkp, kp_cache, 2, kpd, kps, kpb)) return false;
-  const dim3 g1((d.nblk + kScoreBlocks - 1) / kScoreBlocks, d.B);
+  const dim3 g1(d.nblk, d.B);
 #define MSA_SC(NP)                                                                               \
   {                                                                                              \
-    const size_t sm = sizeof(ScoreShared<NP>) + 1024 + kScoreBlocks * (size_t)kKpBlock + NP * 256; \
+    const size_t sm = sizeof(ScoreShared<NP>) + 1024 + (size_t)kKpBlock + NP * 256;                \
     cudaFuncSetAttribute(decode_scores_kernel<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,   \
                          (int)sm);                                                               \
     decode_scores_kernel<NP><<<g1, 128, sm, st>>>(mkp, d, (const bf16*)qp, seq_len, scores,      \
