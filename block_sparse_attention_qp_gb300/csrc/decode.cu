@@ -5,9 +5,10 @@
 //   1. decode_scores_kernel: c[b, p, n] = max over the 128 keys j of block n of qp[b, p] . kp[b, j]
 //      for every block n < t_b / 128 (the local block is forced and never scored): proxy-key
 //      blocks by TMA, one tcgen05 product per block (keys x proxy heads), block maxima by warps.
-//   2. decode_select_kernel: one warp per (b, p) keeps each lane's best top_k - 1 blocks sorted in
-//      registers, then merges the lanes by repeated warp arg-max (ties to the lower block), adds the
-//      local block and writes the selection ascending, padded with -1.
+//   2. decode_select_few_kernel: one warp per (b, p) finds the (top_k - 1)-th largest score (ties to
+//      the lower block), adds the local block and writes the selection ascending, padded with -1;
+//      beyond 1024 blocks decode_select_kernel, which keeps each lane's best top_k - 1 blocks sorted
+//      in registers and merges the lanes by repeated warp arg-max.
 //   3. decode_attn_kernel: one block per (b, attention group a): the selected K / V blocks by TMA
 //      (two stages), S^T and O^T of each block on the tensor core, online softmax across blocks.
 // The whole step reads the proxy-key cache once and the selected K / V blocks once: it is bound by
@@ -211,10 +212,10 @@ __global__ void __launch_bounds__(128)
 
 // The same selection where a row has at most 32 J blocks, J a lane: the K1-th largest score is found bit by bit (scores as
 // integers of their order, counted by ballots), then the blocks above it and the first of those equal to it are written in
-// order: 32 steps of J ballots, whatever K1, where the lists cost KMAX registers' worth of moves a block and a round a pick.
-// 256 rows, between events, the kernel above / this one, us: 64 blocks, top_k = 16 14.7 / 8.0, top_k = 64 86.9 / 8.1; 256
-// blocks, top_k = 4 12.2 / 9.1, 16 21.5 / 9.1, 64 104.4 / 8.8.  At 33 blocks and top_k = 4 it is 6.5 / 7.4: launch_decode_select
-// leaves rows of at most 64 blocks and 8 picks to the lists.
+// order: at most 32 steps of J ballots, whatever K1, where the lists cost KMAX registers' worth of moves a block and a round a
+// pick.  Between events, the kernel above / this one, us, at top_k 4, 16, 64: 256 rows of 64 blocks 7.9 / 6.6, 14.7 / 7.3,
+// 87 / 6.0; of 256 12.8 / 8.0, 22.9 / 8.1, 107 / 8.2; of 512 19.0 / 10.5, 33.6 / 10.7, 132 / 10.7; of 1024 31.4 / 12.9,
+// 55.0 / 12.9; never slower by more than 0.2 (one row, top_k = 2).  Longer rows are left to the lists.
 template <int J>
 __global__ void __launch_bounds__(128)
     decode_select_few_kernel(Dims d, const float* __restrict__ scores, const int32_t* __restrict__ seq_len,
@@ -238,7 +239,7 @@ __global__ void __launch_bounds__(128)
     valid += __popc(__ballot_sync(kAll, key[j] != 0));
   }
   const int K1 = min(d.top_k - 1, m), pick = min(K1, valid);
-  uint32_t t = 0;  // the largest value that at least `pick` keys reach
+  uint32_t t = 0;  // the largest value that at least `pick` keys reach, or one that exactly so many do
   if (pick > 0) {
 #pragma unroll 1
     for (int bit = 31; bit >= 0; --bit) {
@@ -247,6 +248,7 @@ __global__ void __launch_bounds__(128)
 #pragma unroll
       for (int j = 0; j < J; ++j) n += __popc(__ballot_sync(kAll, key[j] >= x));
       if (n >= pick) t = x;
+      if (n == pick) break;  // exactly those
     }
   } else {
     t = kAll;
@@ -527,10 +529,14 @@ void launch_decode_select(const Dims& d, const float* scores, const int32_t* seq
                           int32_t* block_idx, cudaStream_t st) {
   const long long rows = (long long)d.B * d.Hp;
   const int g2 = (int)((rows * 32 + 127) / 128);
-  if (d.nblk <= 64 && d.top_k > 8)
+  if (d.nblk <= 64)
     decode_select_few_kernel<2><<<g2, 128, 0, st>>>(d, scores, seq_len, block_idx);
-  else if (d.nblk > 64 && d.nblk <= 256)
+  else if (d.nblk <= 256)
     decode_select_few_kernel<8><<<g2, 128, 0, st>>>(d, scores, seq_len, block_idx);
+  else if (d.nblk <= 512)
+    decode_select_few_kernel<16><<<g2, 128, 0, st>>>(d, scores, seq_len, block_idx);
+  else if (d.nblk <= 1024)
+    decode_select_few_kernel<32><<<g2, 128, 0, st>>>(d, scores, seq_len, block_idx);
   else if (d.top_k <= 8)
     decode_select_kernel<8><<<g2, 128, 0, st>>>(d, scores, seq_len, block_idx);
   else if (d.top_k <= 16)

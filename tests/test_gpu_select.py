@@ -6,6 +6,7 @@ from block_sparse_attention_qp_gb300 import binding as msa
 
 pytestmark = pytest.mark.gpu
 SCALE = 128 ** -0.5
+MANY = 1025 * 128  # a capacity at which every row is merged from sorted lists
 
 
 def select(qp, kp, n, top_k, cap):
@@ -30,7 +31,7 @@ def plain(qp, kp, n, top_k):
     return torch.tensor(out, dtype=torch.int32).view(len(n), qp.shape[1], top_k)
 
 
-@pytest.mark.parametrize("blocks,top_k,Hp", [(1, 1, 1), (2, 2, 2), (33, 5, 4), (64, 16, 2), (64, 64, 1), (65, 16, 4), (200, 33, 2), (256, 7, 1)])
+@pytest.mark.parametrize("blocks,top_k,Hp", [(1, 1, 1), (2, 2, 2), (33, 5, 4), (64, 16, 2), (64, 64, 1), (65, 16, 4), (200, 33, 2), (256, 7, 1), (257, 16, 2), (1024, 64, 1)])
 @pytest.mark.parametrize("coarse", [False, True])
 def test_few_blocks_as_many(blocks, top_k, Hp, coarse):
     g = torch.Generator(device="cuda")
@@ -46,7 +47,7 @@ def test_few_blocks_as_many(blocks, top_k, Hp, coarse):
     n = torch.tensor([cap, max(1, cap - 127), max(1, cap // 2)], dtype=torch.int32, device="cuda")
     got = select(qp, kp, n, top_k, cap)
     assert torch.equal(got.cpu(), plain(qp, kp, n, top_k))
-    assert torch.equal(got, select(qp, kp, n, top_k, 257 * 128))  # the kernel for more blocks
+    assert torch.equal(got, select(qp, kp, n, top_k, MANY))  # the kernel for more blocks
 
 
 def test_scores_that_are_not_finite():
@@ -58,4 +59,4 @@ def test_scores_that_are_not_finite():
     kp[0, 256:384] = float("nan")  # a whole block
     kp[0, 700, 0, 3] = float("inf")
     for top_k in (2, 4, 8, 9, 12):
-        assert torch.equal(select(qp, kp, n, top_k, 128 * 9), select(qp, kp, n, top_k, 257 * 128))
+        assert torch.equal(select(qp, kp, n, top_k, 128 * 9), select(qp, kp, n, top_k, MANY))
