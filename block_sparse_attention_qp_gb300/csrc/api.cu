@@ -1417,8 +1417,7 @@ int msa_decode(const msa_shape_t* shape, const void* q, const void* qp, const vo
   if ((rc = check_ws(p, workspace, workspace_bytes))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaGetLastError();
-  unsigned* status = at<unsigned>(workspace, p.status);
-  cudaMemsetAsync(status, 0, 32 * sizeof(unsigned), st);  // status, counters, wait place
+  unsigned* status = at<unsigned>(workspace, p.status);  // written whole by the first kernel
   float* scores = at<float>(workspace, p.scores);
   bool ok = true;
   timed("decode_scores", st, [&] {
@@ -1663,8 +1662,7 @@ int msa_decode_q4(const msa_shape_t* shape, const void* q, const void* qp, const
   if ((rc = check_ws_bytes(p4.bytes, workspace, workspace_bytes))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaGetLastError();
-  unsigned* status = at<unsigned>(workspace, p.status);
-  cudaMemsetAsync(status, 0, 32 * sizeof(unsigned), st);  // status, counters, wait place
+  unsigned* status = at<unsigned>(workspace, p.status);  // written whole by the first kernel
   float* scores = at<float>(workspace, p.scores);
   bool ok = true;
   timed("decode_scores", st, [&] {

@@ -19,6 +19,7 @@
 #include "kernels.h"
 #include "sm100.cuh"
 #include "tmap.h"
+#include "window.cuh"
 
 namespace msa {
 
@@ -53,11 +54,14 @@ __global__ void __launch_bounds__(128)
   uint8_t* sK = align1024(smem_raw + sizeof(ScoreShared<NP>));  // [128 keys][128 d]
   uint8_t* sQ = sK + kKpBlock;                                   // [NP rows][128 d], K-major
   const int b = blockIdx.y, n = blockIdx.x, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  const int len = seq_len[b];
-  if (len < 1 || len > d.S) {
-    if (tid == 0) atomicOr(status, kStatusBadIndex);
-    return;
+  if (n == 0 && b == 0) {  // the status area whole (see clear_status): clear, or a length out of range
+    int bad = 0;
+    for (int x = tid; x < d.B; x += 128) bad |= seq_len[x] < 1 || seq_len[x] > d.S;
+    bad = __syncthreads_or(bad);
+    if (tid < 32) status[tid] = tid == 0 && bad ? kStatusBadIndex : 0u;
   }
+  const int len = seq_len[b];
+  if (len < 1 || len > d.S) return;
   if (n >= (len - 1) / kBlock) return;  // the new token's own block is forced, never scored
   if (tid == 0) {
     mbar_init(&sh->kv_full, 1);
@@ -514,8 +518,7 @@ bool launch_decode_scores(const Dims& d, const void* qp, const void* kp_cache,
 #define MSA_SC(NP)                                                                               \
   {                                                                                              \
     const size_t sm = sizeof(ScoreShared<NP>) + 1024 + (size_t)kKpBlock + NP * 256;                \
-    cudaFuncSetAttribute(decode_scores_kernel<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,   \
-                         (int)sm);                                                               \
+    allow_smem<decode_scores_kernel<NP>>(sm);                                                    \
     decode_scores_kernel<NP><<<g1, 128, sm, st>>>(mkp, d, (const bf16*)qp, seq_len, scores,      \
                                                   status);                                       \
   }
@@ -557,7 +560,7 @@ bool launch_decode_attn(const Dims& d, const void* q, const void* k_cache, const
   if (!make_tmap_bf16(&mk, k_cache, 3, kvd, kvs, kvb) || !make_tmap_bf16(&mv, v_cache, 3, kvd, kvs, kvb))
     return false;
   const size_t sm = sizeof(AttnShared) + 1024 + 4 * (size_t)kKVTile + 2 * (size_t)kNH * kD * 2;
-  cudaFuncSetAttribute(decode_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+  allow_smem<decode_attn_kernel>(sm);
   decode_attn_kernel<<<d.B * d.Hp * d.R, kAttnThreads, sm, st>>>(mk, mv, d, (const bf16*)q, seq_len,
                                                                  block_idx, (bf16*)o, lse, status);
   return true;

@@ -60,3 +60,18 @@ def test_scores_that_are_not_finite():
     kp[0, 700, 0, 3] = float("inf")
     for top_k in (2, 4, 8, 9, 12):
         assert torch.equal(select(qp, kp, n, top_k, 128 * 9), select(qp, kp, n, top_k, MANY))
+
+
+@pytest.mark.parametrize("at", [0, 199])
+def test_a_call_writes_its_own_status(at):
+    """A length out of range is flagged wherever it stands, and the next call on the same workspace starts clear."""
+    B, cap = 200, 256
+    qp = torch.zeros((B, 1, 128), dtype=torch.bfloat16, device="cuda")
+    kv = torch.zeros((B, cap, 1, 128), dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros((B, 4, 128), dtype=torch.bfloat16, device="cuda")
+    n = torch.full((B,), cap, dtype=torch.int32, device="cuda")
+    ws = torch.full((1 << 22,), 0xff, dtype=torch.uint8, device="cuda")
+    for length, flagged in ((cap, False), (cap + 1, True), (0, True), (1, False)):
+        n[at] = length
+        msa.msa_decode(q, qp, kv, kv, kv, n, 2, SCALE, ws=ws)
+        assert (msa.msa_device_status(ws) != 0) == flagged
