@@ -54,6 +54,7 @@ __global__ void __launch_bounds__(128)
   uint8_t* sK = align1024(smem_raw + sizeof(ScoreShared<NP>));  // [128 keys][128 d]
   uint8_t* sQ = sK + kKpBlock;                                   // [NP rows][128 d], K-major
   const int b = blockIdx.y, n = blockIdx.x, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  let_next();
   if (n == 0 && b == 0) {  // the status area whole (see clear_status): clear, or a length out of range
     int bad = 0;
     for (int x = tid; x < d.B; x += 128) bad |= seq_len[x] < 1 || seq_len[x] > d.S;
@@ -225,6 +226,8 @@ __global__ void __launch_bounds__(128)
     decode_select_few_kernel(Dims d, const float* __restrict__ scores, const int32_t* __restrict__ seq_len,
                              int32_t* __restrict__ block_idx) {
   constexpr unsigned kAll = 0xffffffffu;
+  wait_before();
+  let_next();
   const int lane = threadIdx.x % 32;
   const long long row = ((long long)blockIdx.x * blockDim.x + threadIdx.x) / 32;  // b * Hp + p
   if (row >= (long long)d.B * d.Hp) return;
@@ -237,7 +240,7 @@ __global__ void __launch_bounds__(128)
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     const int n = lane + 32 * j;
-    const float x = n < m ? c[n] : __uint_as_float(0x7fffffffu);
+    const float x = n < m ? __ldcg(c + n) : __uint_as_float(0x7fffffffu);
     const uint32_t u = x == 0.f ? 0u : __float_as_uint(x);  // the zeros are equal
     key[j] = x != x ? 0u : u >> 31 ? ~u : u | 0x80000000u;
     valid += __popc(__ballot_sync(kAll, key[j] != 0));
@@ -533,13 +536,13 @@ void launch_decode_select(const Dims& d, const float* scores, const int32_t* seq
   const long long rows = (long long)d.B * d.Hp;
   const int g2 = (int)((rows * 32 + 127) / 128);
   if (d.nblk <= 64)
-    decode_select_few_kernel<2><<<g2, 128, 0, st>>>(d, scores, seq_len, block_idx);
+    launch_behind(decode_select_few_kernel<2>, g2, 128, 0, st, d, scores, seq_len, block_idx);
   else if (d.nblk <= 256)
-    decode_select_few_kernel<8><<<g2, 128, 0, st>>>(d, scores, seq_len, block_idx);
+    launch_behind(decode_select_few_kernel<8>, g2, 128, 0, st, d, scores, seq_len, block_idx);
   else if (d.nblk <= 512)
-    decode_select_few_kernel<16><<<g2, 128, 0, st>>>(d, scores, seq_len, block_idx);
+    launch_behind(decode_select_few_kernel<16>, g2, 128, 0, st, d, scores, seq_len, block_idx);
   else if (d.nblk <= 1024)
-    decode_select_few_kernel<32><<<g2, 128, 0, st>>>(d, scores, seq_len, block_idx);
+    launch_behind(decode_select_few_kernel<32>, g2, 128, 0, st, d, scores, seq_len, block_idx);
   else if (d.top_k <= 8)
     decode_select_kernel<8><<<g2, 128, 0, st>>>(d, scores, seq_len, block_idx);
   else if (d.top_k <= 16)

@@ -154,6 +154,8 @@ __global__ void __launch_bounds__(kQ4Threads, NT == 1 ? 3 : 2) q4_decode_kernel(
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int split = blockIdx.x % A.nsplit, bg = blockIdx.x / A.nsplit;
   const int b = bg / A.groups, grp = bg % A.groups;
+  let_next();
+  if (tid / 32 == 4) wait_before();  // (the selected blocks; all else is older)
   if (A.own_status && blockIdx.x == 0) {  // the status word whole: clear, or a length out of range
     int bad = 0;
     for (int x = tid; x < A.B; x += kQ4Threads) bad |= A.seq_len[x] < 1 || A.seq_len[x] > A.cap;
@@ -184,7 +186,7 @@ __global__ void __launch_bounds__(kQ4Threads, NT == 1 ? 3 : 2) q4_decode_kernel(
     // ---------------------------------------------------------------- loads
     // (the selected blocks first, two a lane: read one by one they cost their latency at every tile)
     const int at0 = n0 + lane, at1 = at0 + 32;
-    const int e0 = list && at0 < w.count ? __ldg(list + at0) : -1, e1 = list && at1 < w.count ? __ldg(list + at1) : -1;
+    const int e0 = list && at0 < w.count ? __ldcg(list + at0) : -1, e1 = list && at1 < w.count ? __ldcg(list + at1) : -1;
     const long long head = ((long long)b * A.Hkv + (long long)grp * A.Hkv / A.groups) * A.blocks;
     int i = 0;
     for (; i < ntile; ++i) {
@@ -514,6 +516,10 @@ WinSplit q4_sparse_split(const Dims& d) {
   return q4_split((long long)d.B * d.Hp * d.R, d.top_k < blocks ? d.top_k : blocks, d.G);
 }
 
+static void q4_launch(void (*kernel)(Q4Args), int grid, size_t smem, const Q4Args& a, cudaStream_t st) {
+  if (a.list) launch_behind(kernel, grid, kQ4Threads, smem, st, a);
+  else kernel<<<grid, kQ4Threads, smem, st>>>(a);
+}
 static void launch_q4(Q4Args& a, const WinSplit& w, cudaStream_t st) {
   a.nsplit = w.nsplit;
   a.tiles = w.tiles;
@@ -521,10 +527,10 @@ static void launch_q4(Q4Args& a, const WinSplit& w, cudaStream_t st) {
   constexpr size_t smem = (size_t)kStages * kStageBytes;
   if (a.G > 8) {
     allow_smem<q4_decode_kernel<2>>(smem);
-    q4_decode_kernel<2><<<grid, kQ4Threads, smem, st>>>(a);
+    q4_launch(q4_decode_kernel<2>, grid, smem, a, st);
   } else {
     allow_smem<q4_decode_kernel<1>>(smem);
-    q4_decode_kernel<1><<<grid, kQ4Threads, smem, st>>>(a);
+    q4_launch(q4_decode_kernel<1>, grid, smem, a, st);
   }
   if (w.nsplit > 1) launch_decode_join(a.B, a.Hq, a.cap, w.nsplit, a.seq_len, a.opart, a.lpart, a.o, a.lse, st);
 }

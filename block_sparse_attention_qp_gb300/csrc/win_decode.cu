@@ -289,6 +289,7 @@ __global__ void __launch_bounds__(kJoinThreads) win_decode_join_kernel(int B, in
                                                                        const int32_t* seq_len, const float* opart,
                                                                        const float* lpart, bf16* o, float* lse) {
   extern __shared__ float w[];  // [nsplit] weights
+  wait_before();
   __shared__ float red[kJoinRuns];
   __shared__ float4 acc[kJoinRuns][32];
   const long long row = blockIdx.x, rows = (long long)B * Hq;
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(kJoinThreads) win_decode_join_kernel(int B, in
   if (len < 1 || len > S) return;  // flagged by win_decode_kernel
   float mx = -INFINITY;
   for (int s = threadIdx.x; s < nsplit; s += kJoinThreads) {
-    w[s] = __ldg(lpart + s * rows + row);
+    w[s] = __ldcg(lpart + s * rows + row);
     mx = fmaxf(mx, w[s]);
   }
   mx = warp_max(mx);
@@ -310,7 +311,7 @@ __global__ void __launch_bounds__(kJoinThreads) win_decode_join_kernel(int B, in
   for (int s = run; s < nsplit; s += kJoinRuns) {
     const float ls = w[s], p = exp2_ftz(ls - mx);
     if (ls == -INFINITY) continue;  // an empty split wrote no rows
-    const float4 v = __ldg(reinterpret_cast<const float4*>(opart + (s * rows + row) * kD) + lane);
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(opart + (s * rows + row) * kD) + lane);
     sum += p;
     a.x = fmaf(p, v.x, a.x);
     a.y = fmaf(p, v.y, a.y);
@@ -394,7 +395,7 @@ bool launch_win_decode(const WinDims& d, const void* q, const void* k_cache, con
 
 void launch_decode_join(int B, int Hq, int cap, int nsplit, const int32_t* seq_len, const float* opart,
                         const float* lpart, void* o, float* lse, cudaStream_t st) {
-  win_decode_join_kernel<<<B * Hq, kJoinThreads, nsplit * sizeof(float), st>>>(B, Hq, cap, nsplit, seq_len, opart, lpart, (bf16*)o, lse);
+  launch_behind(win_decode_join_kernel, B * Hq, kJoinThreads, nsplit * sizeof(float), st, B, Hq, cap, nsplit, seq_len, opart, lpart, (bf16*)o, lse);
 }
 
 }  // namespace msa
