@@ -59,7 +59,12 @@ def test_scores_that_are_not_finite():
     kp[0, 256:384] = float("nan")  # a whole block
     kp[0, 700, 0, 3] = float("inf")
     for top_k in (2, 4, 8, 9, 12):
-        assert torch.equal(select(qp, kp, n, top_k, 128 * 9), select(qp, kp, n, top_k, MANY))
+        got = select(qp, kp, n, top_k, 128 * 9)
+        assert torch.equal(got, select(qp, kp, n, top_k, MANY))
+        assert not (got == 2).any()  # seven blocks have a score
+    nan = torch.full_like(qp, float("nan"))
+    assert torch.equal(select(nan, kp, n, 4, 128 * 9), select(nan, kp, n, 4, MANY))
+    assert (select(nan, kp, n, 4, 128 * 9)[..., 0] == 8).all()  # the local block alone
 
 
 @pytest.mark.parametrize("at", [0, 199])
@@ -75,3 +80,36 @@ def test_a_call_writes_its_own_status(at):
         n[at] = length
         msa.msa_decode(q, qp, kv, kv, kv, n, 2, SCALE, ws=ws)
         assert (msa.msa_device_status(ws) != 0) == flagged
+
+
+def test_replays_of_a_captured_step_read_their_own_scores():
+    """Selection and attention start while the kernel in front ends: with other queries, keys and lengths in the same
+    memory every replay equals the eager step."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(7)
+    B, Hq, H, cap, top_k = 8, 32, 4, 128 * 40, 8
+    rand = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    q, qp, kp = rand(B, Hq, 128), rand(B, H, 128), rand(B, cap, 1, 128)
+    k4, v4 = (msa.msa_q4_cache(B, H, cap, "cuda") for _ in range(2))
+    kv = [rand(B, cap, H, 128) for _ in range(2)]
+    n = torch.full((B,), cap, dtype=torch.int32, device="cuda")
+    msa.msa_norm_rope_append(kv, None, None, n, [k4, v4])
+    k16, v16 = (msa.msa_q4_read(c, 0, cap) for c in (k4, v4))
+
+    def steps():
+        return msa.msa_decode_q4(q, qp, k4, v4, kp, n, top_k, SCALE) + msa.msa_decode(q, qp, k16, v16, kp, n, top_k, SCALE) \
+            + msa.msa_window_decode_q4(q, k4, v4, n, 3000, 4, SCALE)
+    steps()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = steps()
+    for i in range(20):
+        q.copy_(rand(B, Hq, 128))
+        qp.copy_(rand(B, H, 128))
+        kp.copy_(kp.roll(128 * 3 + i, 1))
+        n.copy_(torch.randint(1, cap + 1, (B,), generator=g, device="cuda", dtype=torch.int32))
+        graph.replay()
+        graph.replay()
+        got = [x.clone() for x in outs]
+        for x, y in zip(got, steps()):
+            assert torch.equal(x, y)
