@@ -44,6 +44,7 @@ namespace {
 constexpr int kStages = 4;
 constexpr int kStageBytes = 2 * kQ4Block;  // K, V
 constexpr int kQ4Threads = 160;            // warps 0-3 products, 4 loads
+constexpr int kSorted = 512, kSteps = 16;  // sequences that are sorted by length at most, and steps of it
 constexpr float kSlack = 8.f;              // log2 of the largest weight kept without moving the maximum
 
 struct Q4Args {
@@ -60,6 +61,7 @@ struct Q4Args {
   float scale;
   int nsplit, tiles;
   bool own_status;  // this kernel writes the status word
+  float steps;      // sorted by length: kSteps / tiles of the longest possible
 };
 struct Q4Tile {
   int block, r0, r1;  // rows r0 .. r1 - 1 of the block hold every visible key
@@ -105,6 +107,40 @@ __device__ __forceinline__ Q4Tile q4_tile(const Q4Args& A, const Q4Walk& w, int 
   x.full = x.r0 == 0 && x.r1 == kBlock && x.block * kBlock >= w.ws;
   return x;
 }
+// The sequence at place `at` when they are sorted by their tiles, most first, in kSteps steps and in order within one: every warp
+// finds it for itself, the step bit by bit by ballots.  (Loops of few instructions: unrolled they cost more than they do, in
+// fetching them.)
+__device__ __forceinline__ int q4_by_length(const Q4Args& A, int at, uint8_t* step) {
+  constexpr unsigned kAll = 0xffffffffu;
+  const int lane = threadIdx.x % 32, chunks = (A.B + 31) / 32;
+#pragma unroll 1
+  for (int b = threadIdx.x; b < 32 * chunks; b += kQ4Threads) {
+    const int n = b < A.B ? __ldg(A.seq_len + b) : 0;
+    const int tiles = n < 1 || n > A.cap ? 0 : q4_walk(A, n).count;
+    step[b] = b < A.B ? kSteps - 1 - min(kSteps - 1, (int)((float)tiles * A.steps)) : kSteps;
+  }
+  __syncthreads();
+  int t = 0, behind = at;
+#pragma unroll 1
+  for (int bit = kSteps / 2; bit > 0; bit >>= 1) {
+    int n = 0;  // in steps before t + bit
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c) n += __popc(__ballot_sync(kAll, step[32 * c + lane] < t + bit));
+    if (n <= at) {
+      t += bit;
+      behind = at - n;
+    }
+  }
+#pragma unroll 1
+  for (int c = 0; c < chunks; ++c) {
+    const bool here = step[32 * c + lane] == t;
+    const unsigned all = __ballot_sync(kAll, here);
+    const unsigned hit = __ballot_sync(kAll, here && __popc(all & ((1u << lane) - 1u)) == behind);
+    if (hit) return 32 * c + __ffs(hit) - 1;
+    behind -= __popc(all);
+  }
+  return 0;  // (not reached)
+}
 __device__ __forceinline__ bool q4_visible(const Q4Walk& w, int j) { return j <= w.t && (j >= w.ws || j < w.ns); }
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -146,14 +182,17 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
 }  // namespace
 
 // NT: runs of eight heads.
-template <int NT>
+template <int NT, bool kSort>
 __global__ void __launch_bounds__(kQ4Threads, NT == 1 ? 3 : 2) q4_decode_kernel(const __grid_constant__ Q4Args A) {
   using namespace sm100;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ Q4Shared sh;
+  __shared__ uint8_t step[kSort ? kSorted : 1];
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int split = blockIdx.x % A.nsplit, bg = blockIdx.x / A.nsplit;
-  const int b = bg / A.groups, grp = bg % A.groups;
+  const int grp = bg % A.groups;
+  int b = bg / A.groups;
+  if constexpr (kSort) b = __reduce_max_sync(0xffffffffu, q4_by_length(A, b, step));  // (a uniform register again)
   let_next();
   if (tid / 32 == 4) wait_before();  // (the selected blocks; all else is older)
   if (A.own_status && blockIdx.x == 0) {  // the status word whole: clear, or a length out of range
@@ -516,22 +555,27 @@ WinSplit q4_sparse_split(const Dims& d) {
   return q4_split((long long)d.B * d.Hp * d.R, d.top_k < blocks ? d.top_k : blocks, d.G);
 }
 
-static void q4_launch(void (*kernel)(Q4Args), int grid, size_t smem, const Q4Args& a, cudaStream_t st) {
-  if (a.list) launch_behind(kernel, grid, kQ4Threads, smem, st, a);
-  else kernel<<<grid, kQ4Threads, smem, st>>>(a);
+template <int NT, bool kSort>
+static void q4_launch(int grid, size_t smem, const Q4Args& a, cudaStream_t st) {
+  allow_smem<q4_decode_kernel<NT, kSort>>(smem);
+  if (a.list) launch_behind(q4_decode_kernel<NT, kSort>, grid, kQ4Threads, smem, st, a);
+  else q4_decode_kernel<NT, kSort><<<grid, kQ4Threads, smem, st>>>(a);
 }
 static void launch_q4(Q4Args& a, const WinSplit& w, cudaStream_t st) {
   a.nsplit = w.nsplit;
   a.tiles = w.tiles;
   const int grid = a.B * a.groups * w.nsplit;
   constexpr size_t smem = (size_t)kStages * kStageBytes;
-  if (a.G > 8) {
-    allow_smem<q4_decode_kernel<2>>(smem);
-    q4_launch(q4_decode_kernel<2>, grid, smem, a, st);
-  } else {
-    allow_smem<q4_decode_kernel<1>>(smem);
-    q4_launch(q4_decode_kernel<1>, grid, smem, a, st);
-  }
+  // Long sequences first, where blocks wait for a place: the last ones are then short.  Each block sorts for itself, which is
+  // worth it while B times the waves of blocks is a small multiple of a sequence's tiles.  Unsorted / sorted, us, warm, 64 / 8
+  // heads but for the last: 128 sequences of 4096 keys 125 / 129, of 2048 .. 4096 115 / 107, of 1 .. 4096 90 / 76, most
+  // of them short 66 / 49; 64 of 1 .. 8192 97 / 83; 512 of 1 .. 8192, 8 / 1 heads, 98 / 85 (all of 8192 140 / 148).  Outside the
+  // rule: 300 of 1 .. 2048, 32 / 4 heads, 67 / 67; 512 of 1 .. 1536, 32 / 8 heads, 128 / 166.
+  const long long room = (long long)num_sms() * (a.G > 8 ? 2 : 3);
+  const bool sort = w.nsplit == 1 && a.B > 1 && a.B <= kSorted && grid > room && (long long)grid * a.B <= 12 * room * w.tiles;
+  a.steps = (float)kSteps / w.tiles;
+  if (a.G > 8) sort ? q4_launch<2, true>(grid, smem, a, st) : q4_launch<2, false>(grid, smem, a, st);
+  else sort ? q4_launch<1, true>(grid, smem, a, st) : q4_launch<1, false>(grid, smem, a, st);
   if (w.nsplit > 1) launch_decode_join(a.B, a.Hq, a.cap, w.nsplit, a.seq_len, a.opart, a.lpart, a.o, a.lse, st);
 }
 

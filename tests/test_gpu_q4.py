@@ -1,5 +1,6 @@
 """Caches in 4 bits on the GPU: what is stored, bit for bit, and the decode steps that read them."""
 import ctypes
+import random
 
 import pytest
 import torch
@@ -328,3 +329,27 @@ def test_cache_past_32_bits():
     want = plain.attend(q[-1], kv, kv, SCALE)
     check("o", o[-1], want["o"])
     check("lse", lse[-1], want["lse"])
+
+
+@pytest.mark.parametrize("Hq,H,B,cap", [(8, 8, 64, 1024), (128, 8, 40, 896), (5, 5, 100, 1280), (64, 8, 58, 1024), (470, 470, 1, 128)])
+def test_window_decode_of_many_sequences(Hq, H, B, cap):
+    """More blocks than stay resident: the long sequences begin first, and each writes its own rows."""
+    R = random.Random(B)
+    lens = [R.choice([1, cap, cap // 2, R.randint(1, cap), R.randint(1, 200)]) for _ in range(B)]
+    test_window_decode(Hq, H, cap, lens, 2 ** 31 - 1, 0)
+
+
+def test_window_decode_of_many_sequences_with_wrong_lengths():
+    r, B, H, cap = gen(23), 64, 8, 1024
+    lens = [(i * 97) % cap + 1 for i in range(B)]
+    k, v = filled(r, B, H, cap, lens)
+    q = r(B, H, 128)
+    o, lse = msa.msa_window_decode_q4(q, k, v, lens32(*lens), 2 ** 31 - 1, 0, SCALE)
+    for wrong in (0, -1, cap + 1, 2 ** 31 - 1):
+        bad = list(lens)
+        bad[7] = bad[63] = wrong
+        ws = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+        o2, lse2 = msa.msa_window_decode_q4(q, k, v, lens32(*bad), 2 ** 31 - 1, 0, SCALE, ws=ws)
+        assert msa.msa_device_status(ws) == 1
+        good = [i for i in range(B) if i not in (7, 63)]
+        assert torch.equal(o[good], o2[good]) and torch.equal(lse[good], lse2[good])
