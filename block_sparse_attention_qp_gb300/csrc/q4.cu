@@ -23,7 +23,7 @@
 // loading.  Few (sequence, group) pairs: their tiles are split over blocks and joined by a second kernel.
 //
 // One wave of resident blocks over 16384 keys each (456 pairs): 5.7 TB/s, 0.84 of a copy; 128 sequences of 4096 keys, 8 KV heads
-// (2.25 waves): 121 us, 5.1 TB/s; the same with lengths from 1 to 4096: 105 us, 4.5 TB/s; one sequence of 65536 keys: 23 us
+// (2.25 waves): 126 us, 4.9 TB/s (121 in their order, launch_q4); the same with lengths of 2048 to 4096: 105 us, 4.4 TB/s (109 in their order); one sequence of 65536 keys: 23 us
 // and 8 of joining; 32 sequences with 16 of 64 blocks selected, 256 pairs on 152 SMs: 25 us, 2.8 TB/s.  16 heads a group
 // (twice the products and weights): 104 us for 64 sequences of 4096 keys.  340 instructions a run of 16 keys are issued in
 // 66 % of the cycles; the pipes are busy at half that or less.  Measured on the way (first line's 128 sequences): codes by
