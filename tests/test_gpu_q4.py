@@ -353,3 +353,9 @@ def test_window_decode_of_many_sequences_with_wrong_lengths():
         assert msa.msa_device_status(ws) == 1
         good = [i for i in range(B) if i not in (7, 63)]
         assert torch.equal(o[good], o2[good]) and torch.equal(lse[good], lse2[good])
+
+
+@pytest.mark.parametrize("Hq,H,Hp,B,cap,top_k", [(8, 8, 8, 64, 1024, 8), (64, 4, 8, 60, 2048, 6), (32, 4, 2, 116, 1664, 13)])
+def test_sparse_decode_of_many_sequences(Hq, H, Hp, B, cap, top_k):
+    R = random.Random(B)
+    test_sparse_decode(Hq, H, Hp, cap, [R.choice([1, cap, 129, R.randint(1, cap)]) for _ in range(B)], top_k)
