@@ -20,7 +20,7 @@
 //   V: a thread's 16 values of a row are one scale's dims, one 8-byte load; keys are dealt such that 32 lanes
 //      read consecutive bytes, and the score rows are dealt alike.
 // A tile's four warps take 32 keys each with sums of their own, joined at the end; a fifth keeps a ring of tiles
-// loading.  Few (sequence, group) pairs: their tiles are split over blocks and joined by a second kernel.
+// loading.  Few (sequence, group) pairs or long ones: their tiles are split over blocks and joined by a second kernel.
 //
 // One wave of resident blocks over 16384 keys each (456 pairs): 5.7 TB/s, 0.84 of a copy; 128 sequences of 4096 keys, 8 KV heads
 // (2.25 waves): 126 us, 4.9 TB/s (121 in their order, launch_q4); the same with lengths of 2048 to 4096: 105 us, 4.4 TB/s (109 in their order); one sequence of 65536 keys: 23 us
@@ -533,11 +533,20 @@ void launch_q4_read(const void* cache, int B, int H, int cap, int first, int cou
 }
 
 // Splits of a pair's tiles: as many as fill the resident blocks, of at least four tiles (a part's start, end and share of
-// the join cost about as much as three).
-WinSplit q4_split(long long pairs, int tiles, int G) {
+// the join cost about as much as three).  Where several sequences share the blocks, up to four times as many of 32 tiles:
+// one wave of parts as long as the longest sequence's leaves blocks idle beside it, and lengths are known on the device
+// only.  One wave / parts of 32, us, all of the capacity, of 1 .. capacity, most of them short, 64 / 8 heads: 40
+// sequences of 8192 103 / 101, 76 / 65, 54 / 51; of 16384 191 / 165, 125 / 108, 119 / 65; 16 of 65536 256 / 236,
+// 255 / 167, 189 / 91; 8 of 65536 121 / 131, 120 / 105, 90 / 62.  (Of 48 tiles the second line's last is 94, twice as
+// many at most the third's second 198; with more pairs than blocks 64 of 8192 85 / 106.)
+WinSplit q4_split(int B, long long groups, int tiles, int G) {
   WinSplit w;
-  const long long room = (long long)num_sms() * (G > 8 ? 2 : 3);
+  const long long pairs = B * groups, room = (long long)num_sms() * (G > 8 ? 2 : 3);
   long long n = room / pairs;
+  if (B > 1 && pairs < room) {
+    const long long more = tiles / 32 < 4 * room / pairs ? tiles / 32 : 4 * room / pairs;
+    if (n < more) n = more;
+  }
   if (n > (tiles + 3) / 4) n = (tiles + 3) / 4;
   if (n < 1) n = 1;
   w.tiles = (int)((tiles + n - 1) / n);
@@ -548,11 +557,11 @@ WinSplit q4_window_split(const WinDims& d) {
   // sinks, and a window that may begin inside a block
   const long long keys = (long long)(d.ns + kBlock - 1) / kBlock * kBlock + d.W + kBlock - 1;
   const long long most = (d.S + kBlock - 1) / kBlock, n = (keys + kBlock - 1) / kBlock;
-  return q4_split((long long)d.B * d.Hkv, (int)(n < most ? n : most), d.G);
+  return q4_split(d.B, d.Hkv, (int)(n < most ? n : most), d.G);
 }
 WinSplit q4_sparse_split(const Dims& d) {
   const int blocks = d.S / kBlock;
-  return q4_split((long long)d.B * d.Hp * d.R, d.top_k < blocks ? d.top_k : blocks, d.G);
+  return q4_split(d.B, d.Hp * d.R, d.top_k < blocks ? d.top_k : blocks, d.G);
 }
 
 template <int NT, bool kSort>
@@ -572,8 +581,8 @@ static void launch_q4(Q4Args& a, const WinSplit& w, cudaStream_t st) {
   // of them short 66 / 49; 64 of 1 .. 8192 97 / 83; 512 of 1 .. 8192, 8 / 1 heads, 98 / 85 (all of 8192 140 / 148).  Outside the
   // rule: 300 of 1 .. 2048, 32 / 4 heads, 67 / 67; 512 of 1 .. 1536, 32 / 8 heads, 128 / 166.
   const long long room = (long long)num_sms() * (a.G > 8 ? 2 : 3);
-  const bool sort = w.nsplit == 1 && a.B > 1 && a.B <= kSorted && grid > room && (long long)grid * a.B <= 12 * room * w.tiles;
-  a.steps = (float)kSteps / w.tiles;
+  const bool sort = a.B > 1 && a.B <= kSorted && grid > room && (long long)grid * a.B <= 12 * room * w.tiles;
+  a.steps = (float)kSteps / ((float)w.tiles * w.nsplit);
   if (a.G > 8) sort ? q4_launch<2, true>(grid, smem, a, st) : q4_launch<2, false>(grid, smem, a, st);
   else sort ? q4_launch<1, true>(grid, smem, a, st) : q4_launch<1, false>(grid, smem, a, st);
   if (w.nsplit > 1) launch_decode_join(a.B, a.Hq, a.cap, w.nsplit, a.seq_len, a.opart, a.lpart, a.o, a.lse, st);

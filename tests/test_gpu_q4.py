@@ -359,3 +359,11 @@ def test_window_decode_of_many_sequences_with_wrong_lengths():
 def test_sparse_decode_of_many_sequences(Hq, H, Hp, B, cap, top_k):
     R = random.Random(B)
     test_sparse_decode(Hq, H, Hp, cap, [R.choice([1, cap, 129, R.randint(1, cap)]) for _ in range(B)], top_k)
+
+
+@pytest.mark.parametrize("Hq,H,lens,cap,sinks", [(8, 8, [8192, 1, 8191, 4097, 130, 2000], 8192, 0), (32, 2, [12000, 16384, 4096, 5], 16384, 77),
+                                                 (4, 4, [1, 3, 100, 6000], 16384, 0)])
+def test_window_decode_in_parts(Hq, H, lens, cap, sinks):
+    """Several sequences of a large capacity: parts of equal length, most of them of short sequences empty."""
+    test_window_decode(Hq, H, cap, lens, 2 ** 31 - 1, sinks)
+    test_window_decode(Hq, H, cap, lens, cap - 1000, sinks)
