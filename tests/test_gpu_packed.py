@@ -278,3 +278,24 @@ def test_tensors_past_2_31_elements():
     o, lse = msa.msa_packed_forward(q, k, v, plan, SCALE)
     got = (o, lse) + msa.msa_packed_backward(q, k, v, o, lse, dout, plan, SCALE)
     against_plain(lengths, q, k, v, got, rows, which={0, 1, last // 2, last - 3, last - 2, last - 1}, dout=dout)
+
+
+def test_lengths_of_every_kind():
+    """Lengths as a list, a tuple, a range, a host tensor, an iterator, floats without a fraction: one plan."""
+    lens = [3, 0, 200, 17, 1]
+    want = run_forward(lens)
+    for kind in (tuple(lens), torch.tensor(lens), torch.tensor(lens, dtype=torch.int32), iter(lens), [float(n) for n in lens]):
+        for x, y in zip(want, run_forward(kind)):
+            assert torch.equal(x, y)
+    assert msa.msa_packed_plan(range(4), 2, 1, device="cuda").rows == 6
+    for bad in ([-1], [5, -2 ** 31], [2 ** 31], [2 ** 40, 1], [-2 ** 40], [1.0, -3.0]):
+        with pytest.raises(msa.MSAError, match="lengths must be in"):
+            msa.msa_packed_plan(bad, 2, 1, device="cuda")
+
+
+def run_forward(lengths):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    q = torch.randn((221, 4, 128), generator=g, device="cuda").to(torch.bfloat16)
+    k, v = torch.randn((2, 221, 2, 128), generator=g, device="cuda").to(torch.bfloat16)
+    return msa.msa_packed_forward(q, k, v, msa.msa_packed_plan(lengths, 4, 2, device="cuda"), 0.1)

@@ -132,3 +132,9 @@ def test_binding_refuses():
         msa._axes((0, 1), 3)
     with pytest.raises(msa.MSAError, match="axes"):
         msa._axes((0, -1, 1), 3)
+
+
+@pytest.mark.parametrize("bad", [[-1], (5, -2 ** 31), [2 ** 31], [2 ** 40, 1], [-2 ** 40], [1.0, -3.0], torch.tensor([4, -1])])
+def test_lengths_out_of_range(bad):
+    with pytest.raises(msa.MSAError, match="lengths must be in"):
+        msa.msa_packed_plan(bad, 2, 1, device="cuda:0")
