@@ -158,7 +158,7 @@ struct ProxyShared {
   int tokq[kQPB][kPG];  // per query-row buffer (read by the dQp-flush warps)
   int it_ring[kIR];  // item numbers taken by this block, in order (>= total: no more)
   uint64_t kp_full, kp_empty, qp_full[kQPB], qp_empty[kQPB], pb_full[kNPB], meta_free[kNPB], z_full[2],
-      dz_full, fl_full[2], fl_free, acc_free, it_full[kIR], it_empty[kIR];
+      dz_full[2], fl_full[2], fl_free, acc_free, it_full[kIR], it_empty[kIR];
   uint32_t tmem;
 };
 
@@ -1234,13 +1234,15 @@ __global__ void __launch_bounds__(384, 1)
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&sh->z_full[x], 1);
+      // (one for each dz^T buffer: z of the next group is there before this group's gradients, so a dz warp
+      // may be a group ahead of another; of one barrier its second arrival would stand for the other's first)
+      mbar_init(&sh->dz_full[x], 4);
       mbar_init(&sh->fl_full[x], 1);
     }
     for (int x = 0; x < kNPB; ++x) {
       mbar_init(&sh->pb_full[x], 64);   // the gather lanes (one with the bulk copy's expect-tx)
       mbar_init(&sh->meta_free[x], 4);  // the dz warps
     }
-    mbar_init(&sh->dz_full, 4);
     mbar_init(&sh->fl_free, 4);
     mbar_init(&sh->acc_free, 4);
     for (int x = 0; x < kIR; ++x) {
@@ -1320,7 +1322,7 @@ __global__ void __launch_bounds__(384, 1)
       // dKp += dz^T Qp and dQp^T = Kp^T dz^T for group j (gj-th of its item, gcount tokens)
       auto grads = [&](long long j, int gj, int gcount, bool last) -> bool {
         const int b = (int)(j & 1);
-        if (!mbar_wait(&sh->dz_full, par(j), A.status)) return false;
+        if (!mbar_wait(&sh->dz_full[b], par(j >> 1), A.status)) return false;
         if (gj == 0 && ni > 0 && !mbar_wait(&sh->acc_free, par(ni - 1), A.status)) return false;
         if (j > 0 && !mbar_wait(&sh->fl_free, par(j - 1), A.status)) return false;  // RQ read
         fence_async_smem();  // dz^T was written with st.shared by the dz warps
@@ -1548,7 +1550,7 @@ __global__ void __launch_bounds__(384, 1)
         fence_before_sync();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&sh->dz_full);        // also: RZ_bb read
+          mbar_arrive(&sh->dz_full[bb]);    // also: RZ_bb read
           mbar_arrive(&sh->meta_free[pbi]);  // tok / lpx2 / pbar rows of this buffer read
         }
         if (gi == ngroups - 1) {  // item end: dKp rows of this key, once its last product landed
