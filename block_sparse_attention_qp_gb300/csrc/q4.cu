@@ -364,10 +364,12 @@ __global__ void __launch_bounds__(kQ4Threads, NT == 1 ? 3 : 2) q4_decode_kernel(
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
             mx = fmaxf(mx, m[y][e]);
-            const float alpha = mx == m[y][e] ? 1.f : exp2_ftz(m[y][e] - mx);  // 0 at the first keys
+            // 2^(m - mx) as a square: V's exponents, -100 to 90, can move m by more than 126 at once, and the row sum,
+            // which leaves them out, may still be large by as much: taken in two steps it is not flushed.  (0 at the first keys)
+            const float root = mx == m[y][e] ? 1.f : exp2_ftz(0.5f * (m[y][e] - mx)), alpha = root * root;
             m[y][e] = mx;
             top[y][e] = mx + kSlack;
-            l[y][e] *= alpha;
+            l[y][e] = l[y][e] * root * root;
 #pragma unroll
             for (int mt = 0; mt < 8; ++mt) {
               acc[y][mt][e] *= alpha;
@@ -470,9 +472,9 @@ __global__ void __launch_bounds__(kQ4Threads, NT == 1 ? 3 : 2) q4_decode_kernel(
       float sum = 0.f, y = 0.f;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float a = sh.m[k][h] == -INFINITY ? 0.f : exp2_ftz(sh.m[k][h] - mx);
-        sum = fmaf(a, sh.l[k][h], sum);
-        y = fmaf(a, sums[(k * NT * 8 + h) * kD + tid], y);
+        const float root = sh.m[k][h] == -INFINITY ? 0.f : exp2_ftz(0.5f * (sh.m[k][h] - mx));  // (as above)
+        sum = fmaf(root * sh.l[k][h], root, sum);
+        y = fmaf(root * root, sums[(k * NT * 8 + h) * kD + tid], y);
       }
       y /= sum * exp2f(kSlack);
       const float ls = mx + kSlack + log2f(sum);
