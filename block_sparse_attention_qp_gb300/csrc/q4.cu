@@ -46,6 +46,11 @@ constexpr int kStageBytes = 2 * kQ4Block;  // K, V
 constexpr int kQ4Threads = 160;            // warps 0-3 products, 4 loads
 constexpr int kSorted = 512, kSteps = 16;  // sequences that are sorted by length at most, and steps of it
 constexpr float kSlack = 8.f;              // log2 of the largest weight kept without moving the maximum
+// The row sum is kept in units of 2^(m + kSlack + kShift), m the maximum of x + f.  A key of zero values adds 2^(100 + m) to it
+// (f = -100), one of a row that no call has written, zero bytes, 2^(127 + m), and 2^23 of them have to stay in range.  At the
+// other end, f = 90, the heaviest key adds 2^(m - 90), 2^-116 units: keys of a 2^10-th of its weight still count, and of a 2^24-th
+// where V's rows are below 2^83.  The shift is free: x is made by a multiply-add, and V's exponent has an offset as it is.
+constexpr float kShift = 18.f;
 
 struct Q4Args {
   const uint8_t *k, *v;
@@ -304,7 +309,7 @@ __global__ void __launch_bounds__(kQ4Threads, NT == 1 ? 3 : 2) q4_decode_kernel(
     auto keys32 = [&](auto full, const uint8_t* sk, int r0, int block) {
       constexpr bool kFull = decltype(full)::value;
       const uint8_t* sv = sk + kQ4Block;
-      float x2[2][NT][4], xv[2][NT][4];  // scores of two runs of 16 keys, with and without V's exponent
+      float x2[2][NT][4], xv[2][NT][4];  // scores of two runs of 16 keys, less kShift, and with V's exponent
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int ra = r0 + 16 * c + krow, rb = ra + 8;
@@ -336,14 +341,14 @@ __global__ void __launch_bounds__(kQ4Threads, NT == 1 ? 3 : 2) q4_decode_kernel(
             }
         }
         const float ea = __uint_as_float((uint32_t)sk[kQ4ExpAt + ra] << 23), eb = __uint_as_float((uint32_t)sk[kQ4ExpAt + rb] << 23);
-        const float va = (float)((int)sv[kQ4ExpAt + ra] - 127), vb = (float)((int)sv[kQ4ExpAt + rb] - 127);
+        const float va = (float)((int)sv[kQ4ExpAt + ra] - 127 + (int)kShift), vb = (float)((int)sv[kQ4ExpAt + rb] - 127 + (int)kShift);
         const bool vis_a = kFull || q4_visible(w, block * kBlock + ra), vis_b = kFull || q4_visible(w, block * kBlock + rb);
 #pragma unroll
         for (int y = 0; y < NT; ++y)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const bool vis = e < 2 ? vis_a : vis_b;
-            const float z = sc[y][e] * ((e < 2 ? ea : eb) * qs[y][e & 1]);
+            const float z = fmaf(sc[y][e], (e < 2 ? ea : eb) * qs[y][e & 1], -kShift);
             x2[c][y][e] = vis ? z : -INFINITY;
             xv[c][y][e] = vis ? z + (e < 2 ? va : vb) : -INFINITY;
           }
@@ -386,8 +391,6 @@ __global__ void __launch_bounds__(kQ4Threads, NT == 1 ? 3 : 2) q4_decode_kernel(
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const bool none = !kFull && m[y][e & 1] == -INFINITY;
-            // (the row sum in units of 2^kSlack: weights of keys whose values are all zero, f = -100, reach 2^108, and
-            // 2^23 of them must not pass fp32's range)
             l[y][e & 1] += exp2_ftz(x2[c][y][e] - (none ? 0.f : top[y][e & 1]));
             p[e] = exp2_ftz(xv[c][y][e] - (none ? 0.f : m[y][e & 1]));
           }
@@ -476,8 +479,8 @@ __global__ void __launch_bounds__(kQ4Threads, NT == 1 ? 3 : 2) q4_decode_kernel(
         sum = fmaf(root * sh.l[k][h], root, sum);
         y = fmaf(root * root, sums[(k * NT * 8 + h) * kD + tid], y);
       }
-      y /= sum * exp2f(kSlack);
-      const float ls = mx + kSlack + log2f(sum);
+      y = y * exp2f(-kSlack - kShift) / sum;  // (the sum itself may be too large for the factor)
+      const float ls = mx + kSlack + kShift + log2f(sum);
       if (A.nsplit == 1) {
         A.o[(row0 + h) * kD + tid] = __float2bfloat16_rn(y);
         if (tid == 0) A.lse[row0 + h] = ls * kLn2;

@@ -400,7 +400,7 @@ MSA_API int msa_norm_rope_axes_backward(const msa_rope_shape_t* shape, const msa
  * value is exact in bf16.  A row with an infinity or NaN is NaN throughout.
  * A cache is [B][heads][capacity / 128] blocks of 9344 bytes, 16-byte aligned, capacity a multiple of 128.  A block
  * is 128 rows of one head: [128][64] bytes of codes (low nibble first), [128][8] of scales, [128] of e + 127: 73
- * bytes a row, where bf16 takes 256.
+ * bytes a row, where bf16 takes 256.  Zero bytes, as in a new cache, are rows of zeros.
  * msa_norm_rope_append writes them (parts with MSA_ROPE_CACHE_Q4), new tokens as well as whole prompts.
  */
 /* Bytes of such a cache (0: a size that is not positive, or a capacity that is no multiple of 128). */

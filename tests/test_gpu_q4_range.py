@@ -1,9 +1,13 @@
 """Decode over caches in 4 bits where the sizes of rows lie far apart: exponents of V that move the running maximum by more
-than 2^126."""
+than 2^126, rows that no call has written."""
+import math
+
 import pytest
 import torch
 
 from block_sparse_attention_qp_gb300 import binding as msa
+from tests import plain_q4 as plain
+from tests.plain_local import F, check
 from tests.test_gpu_q4 import SCALE, decode_check, gen, lens32
 
 pytestmark = pytest.mark.gpu
@@ -30,3 +34,39 @@ def test_zero_values_beside_large_ones(n, zeros, power):
     q = r(1, 16, 128)
     o, lse = msa.msa_window_decode_q4(q, kc, vc, lens32(n), n, 0, SCALE)
     decode_check(q, kc, vc, [n], lambda b, m: torch.arange(m, device="cuda"), o, lse, n)
+
+
+@pytest.mark.parametrize("B, H, Hq, n", [(1, 1, 1, 300), (1, 2, 8, 5000), (64, 8, 64, 2048), (40, 8, 128, 3000)])
+@pytest.mark.parametrize("written", [0, 1, 700])
+def test_rows_never_written(B, H, Hq, n, written):
+    """A new cache holds zeros, and its rows stand for rows of zeros: they weigh 1 each (their scores are 0)."""
+    r = gen(B + n)
+    cap = (n + 127) // 128 * 128
+    kc, vc = (msa.msa_q4_cache(B, H, cap, "cuda") for _ in range(2))
+    w = min(written, n)
+    if w:  # the last ones, as a decoding program writes them
+        for c in (kc, vc):
+            msa.msa_norm_rope_append([r(B, w, H, 128, scale=0.5)], None, None, lens32(*[n] * B), [c])
+    q = r(B, Hq, 128)
+    o, lse = msa.msa_window_decode_q4(q, kc, vc, lens32(*[n] * B), n, 0, SCALE)
+    if w == 0:
+        assert (o == 0).all()
+        assert (lse - math.log(n)).abs().max() <= F
+        return
+    k, v = (plain.values(plain.unpack(c[[0, -1]])) for c in (kc, vc))
+    for i, b in ((0, 0), (1, B - 1)):
+        want = plain.attend(q[b], k[i, :n], v[i, :n], SCALE)
+        check(f"o[{b}]", o[b], want["o"])
+        check(f"lse[{b}]", lse[b], want["lse"])
+
+
+def test_sparse_rows_never_written():
+    B, cap = 2, 2048
+    kc, vc = (msa.msa_q4_cache(B, 8, cap, "cuda") for _ in range(2))
+    r = gen(3)
+    q, qp, kp = r(B, 64, 128), r(B, 8, 128), r(B, cap, 1, 128)
+    o, lse, idx = msa.msa_decode_q4(q, qp, kc, vc, kp, lens32(2048, 1500), 12, SCALE)
+    assert (o == 0).all()
+    assert (idx[1] == torch.arange(12, device="cuda", dtype=torch.int32)).all()  # all of the shorter sequence's blocks
+    for b, keys in ((0, 12 * 128), (1, 1500)):
+        assert (lse[b] - math.log(keys)).abs().max() <= F
