@@ -5,9 +5,11 @@
 // proxy selected.  With codes c, scales s and the rows' exponents e (K) and f (V):
 //   S[j, h] = 2^e_j sum_d (s c)[j, d] q[h, d]          x = scale log2(e) S,  masked keys -inf
 //   m_h >= max_j (x + f) - 8,  l_h = sum_j 2^(x - m),  O[h, :] = sum_j 2^(x + f - m) (s c)[j, :] / l_h
-// The exponents of V are folded into the weights, so every weight that enters a product is at most 2^8 and
-// the products' V operand s c is exact in fp16, as K's is; q is exact there after a power of two per head.  The only
-// roundings are those of the weights to fp16 (2^-11 relative) and of O.
+// The exponents of V are folded into the weights, and the products' V operand s c is exact in fp16, as K's is; q is exact there
+// after a power of two per head.  The only roundings are those of the weights to fp16 and of O.  m is a whole number and the
+// weights are taken 2^7 times as large: at most 2^15, the largest at least 2^6, so that they keep 11 bits down to 2^-20 of the
+// largest of their warp's keys and are off by at most 2^-31 of it below.  (With the largest kept as 1, 16384 keys of 2^-26 of the first
+// one's weight lost a quarter of what they add to O: all of those of the first one's warp.)
 //
 // Bound by memory, 73 bytes a key, head and tensor (bf16: 256), as long as the codes become operands with few
 // instructions: 47 values a cycle and SM at 7 TB/s.  So no operand passes through shared memory as 16-bit values:
@@ -45,7 +47,9 @@ constexpr int kStages = 4;
 constexpr int kStageBytes = 2 * kQ4Block;  // K, V
 constexpr int kQ4Threads = 160;            // warps 0-3 products, 4 loads
 constexpr int kSorted = 512, kSteps = 16;  // sequences that are sorted by length at most, and steps of it
-constexpr float kSlack = 8.f;              // log2 of the largest weight kept without moving the maximum
+// log2 of the largest weight when the maximum is moved, and of how much larger one may be without moving it: 2^15 in all,
+// within fp16.
+constexpr float kLift = 7.f, kSlack = 8.f;
 // The row sum is kept in units of 2^(m + kSlack + kShift), m the maximum of x + f.  A key of zero values adds 2^(100 + m) to it
 // (f = -100), one of a row that no call has written, zero bytes, 2^(127 + m), and 2^23 of them have to stay in range.  At the
 // other end, f = 90, the heaviest key adds 2^(m - 90), 2^-116 units: keys of a 2^10-th of its weight still count, and of a 2^24-th
@@ -263,7 +267,7 @@ __global__ void __launch_bounds__(kQ4Threads, NT == 1 ? 3 : 2) q4_decode_kernel(
     for (int x = i > kStages ? i - kStages : 0; x < i; ++x) mbar_wait_warp(&sh.full[x % kStages], phase_of(x / kStages), A.status);
   }
   const int g = lane >> 2, q4 = lane & 3;
-  float m[NT][2], top[NT][2], l[NT][2], acc[NT][8][4];  // top: m + kSlack
+  float m[NT][2], top[NT][2], l[NT][2], acc[NT][8][4];  // m: the maximum less kLift; top: the maximum and kSlack
   if (warp < 4) {
     // ---------------------------------------------------------------- queries: column g of run y, dims 32 q4 ..
     uint32_t qf[NT][8][2];
@@ -353,7 +357,7 @@ __global__ void __launch_bounds__(kQ4Threads, NT == 1 ? 3 : 2) q4_decode_kernel(
             xv[c][y][e] = vis ? z + (e < 2 ? va : vb) : -INFINITY;
           }
       }
-      // ---- the running maxima, moved only where a weight would pass 2^8
+      // ---- the running maxima, moved only where a weight would pass 2^15
       bool up = false;
 #pragma unroll
       for (int y = 0; y < NT; ++y)
@@ -368,12 +372,12 @@ __global__ void __launch_bounds__(kQ4Threads, NT == 1 ? 3 : 2) q4_decode_kernel(
             float mx = fmax3(xv[0][y][e], xv[0][y][e + 2], fmaxf(xv[1][y][e], xv[1][y][e + 2]));
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-            mx = fmaxf(mx, m[y][e]);
+            mx = fmaxf(ceilf(mx) - kLift, m[y][e]);
             // 2^(m - mx) as a square: V's exponents, -100 to 90, can move m by more than 126 at once, and the row sum,
             // which leaves them out, may still be large by as much: taken in two steps it is not flushed.  (0 at the first keys)
             const float root = mx == m[y][e] ? 1.f : exp2_ftz(0.5f * (m[y][e] - mx)), alpha = root * root;
             m[y][e] = mx;
-            top[y][e] = mx + kSlack;
+            top[y][e] = mx + kLift + kSlack;
             l[y][e] = l[y][e] * root * root;
 #pragma unroll
             for (int mt = 0; mt < 8; ++mt) {
@@ -479,8 +483,8 @@ __global__ void __launch_bounds__(kQ4Threads, NT == 1 ? 3 : 2) q4_decode_kernel(
         sum = fmaf(root * sh.l[k][h], root, sum);
         y = fmaf(root * root, sums[(k * NT * 8 + h) * kD + tid], y);
       }
-      y = y * exp2f(-kSlack - kShift) / sum;  // (the sum itself may be too large for the factor)
-      const float ls = mx + kSlack + kShift + log2f(sum);
+      y = y * exp2f(-kLift - kSlack - kShift) / sum;  // (the sum itself may be too large for the factor)
+      const float ls = mx + kLift + kSlack + kShift + log2f(sum);
       if (A.nsplit == 1) {
         A.o[(row0 + h) * kD + tid] = __float2bfloat16_rn(y);
         if (tid == 0) A.lse[row0 + h] = ls * kLn2;

@@ -1,5 +1,5 @@
 """Decode over caches in 4 bits where the sizes of rows lie far apart: exponents of V that move the running maximum by more
-than 2^126, rows that no call has written."""
+than 2^126, rows that no call has written, weights far below the largest."""
 import math
 
 import pytest
@@ -7,7 +7,7 @@ import torch
 
 from block_sparse_attention_qp_gb300 import binding as msa
 from tests import plain_q4 as plain
-from tests.plain_local import F, check
+from tests.plain_local import F, HALF, check
 from tests.test_gpu_q4 import SCALE, decode_check, gen, lens32
 
 pytestmark = pytest.mark.gpu
@@ -70,3 +70,25 @@ def test_sparse_rows_never_written():
     assert (idx[1] == torch.arange(12, device="cuda", dtype=torch.int32)).all()  # all of the shorter sequence's blocks
     for b, keys in ((0, 12 * 128), (1, 1500)):
         assert (lse[b] - math.log(keys)).abs().max() <= F
+
+
+@pytest.mark.parametrize("B, H, Hq, n", [(57, 8, 8, 16384), (38, 8, 128, 16384)])
+def test_one_heavy_key_among_many_light_ones(B, H, Hq, n):
+    """A first token 2^26 times as heavy as any of the 16383 others, whose values alone reach the upper 64 dims: their weights are
+    far below fp16's normal range.  Relative to a warp's largest weight they are off by at most 2^-31 (half a step of 2^-24 where the largest is
+    at least 2^6)."""
+    q = torch.full((B, Hq, 128), 1.0625, dtype=torch.bfloat16, device="cuda")
+    k = torch.zeros(1, n, H, 128, dtype=torch.bfloat16, device="cuda")
+    v = torch.ones_like(k)
+    k[:, 0] = 1.5
+    v[:, 0, :, 64:] = 0
+    kc, vc = caches(k.expand(B, n, H, 128), v.expand(B, n, H, 128), n)
+    o, lse = msa.msa_window_decode_q4(q, kc, vc, lens32(*[n] * B), n, 0, SCALE)
+    for b in (0, B - 1):
+        kb, vb = (plain.values(plain.unpack(c[b:b + 1]))[0] for c in (kc, vc))
+        want = plain.attend(q[b], kb, vb, SCALE)
+        ref = want["o"][0]
+        # (a row's largest kept value is between 1536 and half of that times its power of two: the factor 2)
+        bound = HALF * ref.abs() + (plain.HALF16 + F) * ref.abs() + n * 2.0 ** -31 * 2
+        check(f"o[{b}]", o[b], (ref, bound))
+        check(f"lse[{b}]", lse[b], want["lse"])
