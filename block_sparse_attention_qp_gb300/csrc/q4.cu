@@ -5,8 +5,9 @@
 // proxy selected.  With codes c, scales s and the rows' exponents e (K) and f (V):
 //   S[j, h] = 2^e_j sum_d (s c)[j, d] q[h, d]          x = scale log2(e) S,  masked keys -inf
 //   m_h >= max_j (x + f) - 8,  l_h = sum_j 2^(x - m),  O[h, :] = sum_j 2^(x + f - m) (s c)[j, :] / l_h
-// The exponents of V are folded into the weights, and the products' V operand s c is exact in fp16, as K's is; q is exact there
-// after a power of two per head.  The only roundings are those of the weights to fp16 and of O.  m is a whole number and the
+// The exponents of V are folded into the weights, and the products' V operand s c is exact in fp16, as K's is; q, its head's
+// largest element brought to 2^14 by a power of two, is exact there down to 2^-31 of that element, and off by at most 2^-39 of it
+// below (to 1 instead: 2^-17, 2^-25).  The other roundings are those of the weights to fp16 and of O.  m is a whole number and the
 // weights are taken 2^7 times as large: at most 2^15, the largest at least 2^6, so that they keep 11 bits down to 2^-20 of the
 // largest of their warp's keys and are off by at most 2^-31 of it below.  (With the largest kept as 1, 16384 keys of 2^-26 of the first
 // one's weight lost a quarter of what they add to O: all of those of the first one's warp.)
@@ -286,7 +287,8 @@ __global__ void __launch_bounds__(kQ4Threads, NT == 1 ? 3 : 2) q4_decode_kernel(
       big = max(big & 0xffffu, big >> 16);
       big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
       big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-      const int f = min(max((int)(big >> 7) - 127, -120), 120);
+      // the head's largest element to 2^14 .. 2^15 (pow2f: -126 .. 127)
+      const int f = max((int)(big >> 7) - 127 - 14, -126);
       const float down = pow2f(-f), up = A.scale * kLog2e * pow2f(f);
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks) {

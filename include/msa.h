@@ -415,8 +415,8 @@ MSA_API int msa_q4_read(const void* cache, int32_t B, int32_t heads, int32_t cap
  * msa_window_decode and msa_decode over K and V caches in 4 bits (kp_cache stays bf16, so the selection is that
  * of msa_decode).  Arguments, limits, status bits and the rows that are left as they were are those of the two;
  * S is the capacity.  The caches' values are used as they are kept; the softmax weights, V's powers of two in them, are
- * rounded to 11 bits for their product, those below 2^-20 of the largest to 2^-31 of it; q below 2^-17 of its head's largest
- * element to 2^-25 of that; everything else is fp32.  Workspace: MSA_OP_WINDOW_DECODE_Q4, MSA_OP_DECODE_Q4.
+ * rounded to 11 bits for their product, those below 2^-20 of the largest to 2^-31 of it; elements of q below 2^-31 of their
+ * head's largest to 2^-39 of that; everything else is fp32.  Workspace: MSA_OP_WINDOW_DECODE_Q4, MSA_OP_DECODE_Q4.
  */
 MSA_API int msa_window_decode_q4(const msa_window_shape_t* shape, const void* q, const void* k_cache,
                       const void* v_cache, const int32_t* seq_len, void* o, float* lse,

@@ -1,5 +1,6 @@
 """Decode over caches in 4 bits where the sizes of rows lie far apart: exponents of V that move the running maximum by more
-than 2^126, rows that no call has written, weights far below the largest."""
+than 2^126, rows that no call has written, weights far below the largest,
+elements of q far below their head's largest."""
 import math
 
 import pytest
@@ -92,3 +93,34 @@ def test_one_heavy_key_among_many_light_ones(B, H, Hq, n):
         bound = HALF * ref.abs() + (plain.HALF16 + F) * ref.abs() + n * 2.0 ** -31 * 2
         check(f"o[{b}]", o[b], (ref, bound))
         check(f"lse[{b}]", lse[b], want["lse"])
+
+
+def test_small_elements_of_q():
+    """All but one element of every head 2^-20 of the largest, whose keys are 0 there: the scores are theirs alone."""
+    r = gen(11)
+    n, H, Hq = 600, 2, 32
+    q = r(1, Hq, 128) * 2.0 ** -20
+    q[..., 5] = 1.0
+    k = r(1, n, H, 128) * 2.0 ** 20
+    k[..., 5] = 0
+    kc, vc = caches(k, r(1, n, H, 128), 640)
+    o, lse = msa.msa_window_decode_q4(q, kc, vc, lens32(n), n, 0, SCALE)
+    decode_check(q, kc, vc, [n], lambda b, m: torch.arange(m, device="cuda"), o, lse, 640)
+
+
+def test_a_head_of_infinities_or_of_the_smallest_numbers():
+    """q's power of two at its ends: a head of bf16's subnormal numbers scores 0, one with an infinity is NaN, one of
+    the largest numbers is what its scores make of it, and no head reaches another."""
+    r = gen(12)
+    kc, vc = caches(r(1, 200, 1, 128, scale=2.0 ** -100), r(1, 200, 1, 128), 256)
+    q = r(1, 8, 128)
+    q[0, 0] = 2.0 ** -133
+    q[0, 1] = 0
+    q[0, 2] = q[0, 2].abs().clamp(min=0.5) * 2.0 ** 97
+    q[0, 3, 7] = float("inf")
+    q[0, 4, 7] = float("nan")
+    q[0, 5] *= 2.0 ** 100
+    o, lse = msa.msa_window_decode_q4(q, kc, vc, lens32(200), 200, 0, SCALE)
+    fine = [0, 1, 2, 5, 6, 7]
+    assert torch.isnan(lse[0, [3, 4]]).all() and torch.isnan(o[0, [3, 4]]).any(-1).all()
+    decode_check(q[:, fine], kc, vc, [200], lambda b, m: torch.arange(m, device="cuda"), o[:, fine], lse[:, fine], 256)
