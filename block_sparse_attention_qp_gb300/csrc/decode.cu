@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(128)
       vals[KMAX - 2] = -INFINITY;
       ids[KMAX - 2] = 0x7fffffff;
     }
-    if (lane == 0) sel[picked++] = bi;
+    if (lane == 0 && bi != 0x7fffffff) sel[picked++] = bi;  // (no list has any left: the others are NaN)
   }
   if (lane == 0) {
     sel[picked++] = m;
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(128)
     key[j] = x != x ? 0u : u >> 31 ? ~u : u | 0x80000000u;
     valid += __popc(__ballot_sync(kAll, key[j] != 0));
   }
-  const int K1 = min(d.top_k - 1, m), pick = min(K1, valid);
+  const int pick = min(min(d.top_k - 1, m), valid);
   uint32_t t = 0;  // the largest value that at least `pick` keys reach, or one that exactly so many do
   if (pick > 0) {
 #pragma unroll 1
@@ -275,8 +275,7 @@ __global__ void __launch_bounds__(128)
     left -= min(left, __popc(same));
     at += __popc(taken);
   }
-  // the local block; places that only NaN were left for, as above; padding
-  for (int i = at + lane; i < d.top_k; i += 32) out[i] = i == at ? m : i <= K1 ? 0x7fffffff : -1;
+  for (int i = at + lane; i < d.top_k; i += 32) out[i] = i == at ? m : -1;  // the local block, padding
 }
 
 // One block per (b, attention group a): the group's G <= 16 query heads against its selected

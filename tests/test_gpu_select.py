@@ -67,6 +67,25 @@ def test_scores_that_are_not_finite():
     assert (select(nan, kp, n, 4, 128 * 9)[..., 0] == 8).all()  # the local block alone
 
 
+@pytest.mark.parametrize("cap", [128 * 40, 128 * 300, MANY])
+@pytest.mark.parametrize("top_k", [5, 16, 40])
+def test_blocks_without_a_score_are_padding(cap, top_k):
+    """Blocks of NaN are not picked, and the places that they leave are padded like any other: a row is ascending, ends with the
+    local block, and holds -1 behind it."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(top_k)
+    kp = torch.randn((3, 128 * 40, 1, 128), generator=g, device="cuda").to(torch.bfloat16)
+    qp = torch.randn((3, 2, 128), generator=g, device="cuda").to(torch.bfloat16)
+    kp[1, :128 * 30] = float("nan")
+    qp[2] = float("nan")
+    n = torch.tensor([128 * 40, 128 * 39 + 5, 128 * 40], dtype=torch.int32, device="cuda")
+    for b, (row, scored) in enumerate(zip(select(qp, kp, n, top_k, cap).tolist(), (39, 9, 0))):
+        for ids in row:
+            count = min(top_k - 1, scored) + 1
+            assert ids[count - 1] == 39 and ids[count:] == [-1] * (top_k - count)
+            assert ids[:count] == sorted(set(ids[:count])) and ids[0] >= (30 if b == 1 else 0)
+
+
 @pytest.mark.parametrize("at", [0, 199])
 def test_a_call_writes_its_own_status(at):
     """A length out of range is flagged wherever it stands, and the next call on the same workspace starts clear."""
