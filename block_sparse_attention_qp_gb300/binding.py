@@ -588,6 +588,17 @@ def _int32(x, name) -> int:
     return min(x, 2 ** 31 - 1)
 
 
+def _whole(x, name) -> int:
+    """x as an int, without dropping a fraction."""
+    try:
+        n = int(x)
+    except (TypeError, ValueError, OverflowError):  # nan, inf, no number
+        n = None
+    if n is None or n != x:
+        raise MSAError(f"{name} must be whole numbers, got {x}")
+    return n
+
+
 @functools.lru_cache(maxsize=4096)
 def _window_bytes(op, *shape):
     lib = load_library()
@@ -760,19 +771,20 @@ def msa_packed_plan(lengths, heads: int, kv_heads: int, rows: int | None = None,
     try:  # (0.04 us a sequence on the host, converted one by one 0.16)
         lengths = array.array("i", lengths)
     except (TypeError, OverflowError):
-        lengths = [int(n) for n in lengths]
+        lengths = [_whole(n, "lengths") for n in lengths]
         if not 0 <= min(lengths) <= max(lengths) < 2 ** 31:
             raise MSAError("lengths must be in 0 .. 2^31 - 1") from None
         lengths = array.array("i", lengths)
     if lengths and min(lengths) < 0:
         raise MSAError("lengths must be in 0 .. 2^31 - 1")
     total = sum(lengths)
-    rows = total if rows is None else int(rows)
+    rows = total if rows is None else _whole(rows, "rows")
     if not total <= rows < 2 ** 31:
         raise MSAError(f"{total} tokens in {rows} rows")
     n = len(lengths)
     arr = (ctypes.c_int32 * n).from_buffer(lengths) if n else (ctypes.c_int32 * 1)()
-    shape = PackedShape(rows, int(heads), int(kv_heads), 128, rows if window is None else _int32(window, "window"))
+    shape = PackedShape(rows, _int32(_whole(heads, "heads"), "heads"), _int32(_whole(kv_heads, "kv_heads"), "kv_heads"), 128,
+                        rows if window is None else _int32(window, "window"))
     dev = torch.device("cuda" if device is None else device)
     if dev.type != "cuda":
         raise MSAError(f"device must be a CUDA device, got {dev}")

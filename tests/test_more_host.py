@@ -138,3 +138,16 @@ def test_binding_refuses():
 def test_lengths_out_of_range(bad):
     with pytest.raises(msa.MSAError, match="lengths must be in"):
         msa.msa_packed_plan(bad, 2, 1, device="cuda:0")
+
+
+@pytest.mark.parametrize("bad", [[2.5], [2.7, 3.9], (4, 0.5), [float("nan")], [1, float("inf")], ["3"], [None], [[1, 2]],
+                                 torch.tensor([1.0, 2.5]), torch.tensor([[1, 2]])])
+def test_lengths_that_are_no_whole_numbers(bad):
+    with pytest.raises(msa.MSAError, match="lengths must be whole numbers"):
+        msa.msa_packed_plan(bad, 2, 1, device="cuda:0")
+
+
+@pytest.mark.parametrize("kw", [dict(heads=2.5), dict(kv_heads=0.5), dict(rows=9.5), dict(rows=float("nan"))])
+def test_sizes_that_are_no_whole_numbers(kw):
+    with pytest.raises(msa.MSAError, match=f"{list(kw)[0]} must be whole numbers"):
+        msa.msa_packed_plan(**{"lengths": [4, 5], "heads": 2, "kv_heads": 1, "device": "cuda:0", **kw})
