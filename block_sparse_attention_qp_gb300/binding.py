@@ -740,13 +740,20 @@ def msa_window_func(Q, K, V, window: int, sinks: int, scale: float):
 # ---------------------------------------------------------------- attention over packed sequences
 class PackedPlan:
     """What msa_packed_plan returns: the lengths' tables on the device, for the calls of one step (any number of
-    layers) over tensors of ``rows`` rows.  Made in the order of the stream that was current."""
-    __slots__ = ("counts", "table", "rows", "tokens", "Hq", "Hkv", "device", "_bytes")
+    layers) over tensors of ``rows`` rows.  Made in the order of the stream that was current: calls on another one have to
+    wait for it (an event).  The tables outlive the plan until the calls that use them are done, on whatever stream."""
+    __slots__ = ("counts", "table", "rows", "tokens", "Hq", "Hkv", "device", "_bytes", "_stream")
 
-    def __init__(self, counts, table):
-        self.counts, self.table, self.device = counts, table, table.device
+    def __init__(self, counts, table, stream):
+        self.counts, self.table, self.device, self._stream = counts, table, table.device, stream
         self.rows, self.tokens, self.Hq, self.Hkv = counts.rows, counts.tokens, counts.Hq, counts.Hkv
         self._bytes = {}
+
+    def used_on(self, stream: int) -> None:
+        """Called for every stream that reads the table: dropped, it goes back to its own stream's memory, which another
+        stream's kernels may still be reading."""
+        if stream != self._stream:
+            self.table.record_stream(torch.cuda.current_stream(self.device))
 
     def workspace_size(self, op: int) -> int:
         n = self._bytes.get(op)
@@ -795,12 +802,11 @@ def msa_packed_plan(lengths, heads: int, kv_heads: int, rows: int | None = None,
         need = int(lib.msa_packed_table_bytes(ctypes.byref(shape), arr, n))
         if need == 0:
             raise MSAError(f"msa_packed_plan: {lib.msa_last_error().decode()}")
-        table, counts = torch.empty(need, dtype=torch.uint8, device=dev), PackedCounts()
-        rc = lib.msa_packed_plan(ctypes.byref(shape), arr, n, ctypes.byref(counts), table.data_ptr(), need,
-                                 _stream_of(dev))
+        table, counts, stream = torch.empty(need, dtype=torch.uint8, device=dev), PackedCounts(), _stream_of(dev)
+        rc = lib.msa_packed_plan(ctypes.byref(shape), arr, n, ctypes.byref(counts), table.data_ptr(), need, stream)
     if rc:
         _check(rc, "msa_packed_plan")
-    return PackedPlan(counts, table)
+    return PackedPlan(counts, table, stream)
 
 
 def _packed_args(q, k, v, plan):
@@ -827,8 +833,10 @@ def msa_packed_forward(q, k, v, plan: PackedPlan, scale: float, ws=None):
         wp, wn, ws = _ws(ws, plan.workspace_size(OP_PACKED_FORWARD) if ws is None else 0, dev)
         o = torch.empty_like(q)
         lse = torch.empty((plan.Hq, plan.rows), dtype=torch.float32, device=dev)
+        stream = _stream_of(dev)
+        plan.used_on(stream)
         rc = load_library().msa_packed_forward(ctypes.byref(plan.counts), plan.table.data_ptr(), plan.table.numel(), *ptrs,
-                                               float(scale), o.data_ptr(), lse.data_ptr(), wp, wn, _stream_of(dev))
+                                               float(scale), o.data_ptr(), lse.data_ptr(), wp, wn, stream)
     if rc:
         _check(rc, "msa_packed_forward")
     return o, lse
@@ -845,9 +853,11 @@ def msa_packed_backward(q, k, v, o, lse, dout, plan: PackedPlan, scale: float, w
     with _Guard(dev):
         wp, wn, ws = _ws(ws, plan.workspace_size(OP_PACKED_BACKWARD) if ws is None else 0, dev)
         grads = dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        stream = _stream_of(dev)
+        plan.used_on(stream)
         rc = load_library().msa_packed_backward(ctypes.byref(plan.counts), plan.table.data_ptr(), plan.table.numel(), *ptrs, op,
                                                 lp, dp, float(scale), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), wp, wn,
-                                                _stream_of(dev))
+                                                stream)
     if rc:
         _check(rc, "msa_packed_backward")
     return grads

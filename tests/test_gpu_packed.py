@@ -299,3 +299,34 @@ def run_forward(lengths):
     q = torch.randn((221, 4, 128), generator=g, device="cuda").to(torch.bfloat16)
     k, v = torch.randn((2, 221, 2, 128), generator=g, device="cuda").to(torch.bfloat16)
     return msa.msa_packed_forward(q, k, v, msa.msa_packed_plan(lengths, 4, 2, device="cuda"), 0.1)
+
+
+@pytest.mark.parametrize("train", [False, True])
+def test_a_plan_dropped_while_another_stream_reads_its_table(train):
+    """Planned on one stream, used on another, dropped before that one has come to it: the table's memory is given to nobody
+    until it has."""
+    lengths, Hq, Hkv = [700, 3, 1500, 90], 8, 2
+    q, k, v, dout = make(11, sum(lengths), Hq, Hkv)
+    plan = msa.msa_packed_plan(lengths, Hq, Hkv, device="cuda")
+    o, lse = msa.msa_packed_forward(q, k, v, plan, SCALE)
+    want = (o, lse) + (msa.msa_packed_backward(q, k, v, o, lse, dout, plan, SCALE) if train else ())
+    torch.cuda.synchronize()
+    plan = msa.msa_packed_plan(lengths, Hq, Hkv, device="cuda")
+    at, size = plan.table.data_ptr(), plan.table.numel()
+    compute = torch.cuda.Stream()
+    compute.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(compute):
+        torch.cuda._sleep(200_000_000)  # a tenth of a second
+        if train:
+            got = (o, lse) + msa.msa_packed_backward(q, k, v, o, lse, dout, plan, SCALE)
+        else:
+            got = msa.msa_packed_forward(q, k, v, plan, SCALE)
+    del plan
+    held = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(50)]
+    busy = not compute.query()
+    assert busy and all(t.data_ptr() != at for t in held)
+    for t in held:
+        t.fill_(255)
+    compute.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
