@@ -4,7 +4,9 @@ import torch
 
 from block_sparse_attention_qp_gb300 import binding as msa
 from tests import plain_local as plain
+from tests import plain_q4
 from tests.plain_local import check
+from tests.test_gpu_q4 import same_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -137,3 +139,30 @@ def test_more_positions_than_axes_used():
     a = msa.msa_norm_rope_forward([x], ws, freq, positions=pos, axes=axes)
     b = msa.msa_norm_rope_forward([x], ws, freq, positions=pos[:2].contiguous(), axes=axes)
     assert torch.equal(a[0], b[0])
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("axes,A", [(None, 1), ([0] * 16 + [1] * 24 + [2] * 24, 3), ([i % 4 for i in range(16)], 4)])
+@pytest.mark.parametrize("N,lens", [(1, [1, 77, 128]), (5, [5, 200, 256])])
+def test_append_with_positions_of_its_own_in_4_bits(axes, A, interleaved, N, lens):
+    """A cache in 4 bits takes what a bf16 output of the same call holds for the same rows: normed, turned by the given positions
+    and rounded; at the rows that the lengths say, and no others."""
+    B, cap, H = 3, 256, 3
+    rot = 2 * len(axes) if axes else 128
+    x, ws, freq, pos, _ = make(9 + N, B, N, [H, H], rot, A)
+    k, k2 = x.split([H, H], 2)
+    k2.copy_(k)
+    ws = [ws[0], ws[0]]
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    cache = msa.msa_q4_cache(B, H, cap, "cuda")
+    p = pos if axes else pos[0].contiguous()
+    state = torch.empty(256, dtype=torch.uint8, device="cuda")
+    _, y = msa.msa_norm_rope_append([k, k2], ws, freq, n, [cache, None], positions=p, axes=axes, interleaved=interleaved, ws=state)
+    assert msa.msa_device_status(state) == 0
+    check("k", y, plain_axes(k, ws[0], pos, freq, axes or [0] * (rot // 2), interleaved)["y"])
+    rows = [torch.arange(m - N, m, device="cuda") for m in lens]
+    same_rows(cache, rows, y)
+    for part in plain_q4.unpack(cache):
+        for b in range(B):
+            part[b, rows[b]] = 0
+        assert not part.any()
