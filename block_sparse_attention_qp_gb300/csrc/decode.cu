@@ -23,14 +23,17 @@
 
 namespace msa {
 
-// grid (nblk, B), 128 threads.  Per CTA one key block of sequence b, loaded by TMA (the proxy-key cache rows of a block are
+// grid (score_ctas, B), 128 threads.  A CTA takes every gridDim.x-th key block of sequence b, one after the other, each loaded by TMA (the proxy-key cache rows of a block are
 // contiguous: 32 KB), and one tcgen05 product, S^T = Kp_block Qp^T (M = 128 keys, N = NP >= Hp proxy heads, the rows beyond
 // Hp zero), into tensor memory; thread = key then reads its NP scores and the warps reduce each head's maximum over the
 // block.  The products are exact bf16 x bf16 in fp32, summed in the tensor core's order, as in the training selection kernel.
-// A CTA is a chain of latencies (length, keys, product, maxima), so its keys are asked for before anything else and five
-// CTAs an SM are in different places of it.  128 sequences of 256 blocks, 8 heads (1.07 GB), us: one block a CTA 174
-// (6.2 TB/s), two 174, two with maxima by five shuffles instead of one reduction 192, three 228, three and the keys
-// asked for behind the queries' staging 244; 64 blocks, 32 heads, in the same order 78, 88, 123, 152, 140.
+// A CTA is a chain of latencies (length, keys, product, maxima), so its keys are asked for before anything else, the next block's as
+// soon as the product has read these, and five CTAs an SM are in different places of it.  CTAs are dealt out by the capacity,
+// and one that finds its sequence short costs 4 ns all the same: up to three waves of them have a block each, beyond that they
+// share (score_ctas).  Between events, us, of 64 / 256 / 1024 blocks of capacity (128, 128, 64 sequences, 4 heads), full and of one
+// token: a CTA a block 47 / 161 / 311 and 37 / 123 / 238; two waves 46 / 162 / 326 and 12 / 13 / 13; three 45 / 157 / 309 and
+// 18 / 16 / 15; four 44 / 153 / 302 and 22 / 19 / 18; eight 49 / 151 / 294 and 37 / 31 / 30.  (Three full waves: 1.07 GB at
+// 6.8 TB/s.)  Maxima by five shuffles instead of one reduction: 192 for 174.
 constexpr int kKpBlock = kBlock * kD * 2;
 __device__ __forceinline__ float warp_max(float x) {  // NaN only where all 32 are
   asm volatile("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(x));
@@ -40,7 +43,7 @@ template <int NP>
 struct ScoreShared {
   uint64_t kv_full, s_full;
   uint32_t tmem;
-  float wmax[4][NP];  // per warp and head: the warp's maximum
+  float wmax[2][4][NP];  // per block in turn, warp and head: the warp's maximum
 };
 template <int NP>
 __global__ void __launch_bounds__(128)
@@ -53,9 +56,9 @@ __global__ void __launch_bounds__(128)
   ScoreShared<NP>* sh = reinterpret_cast<ScoreShared<NP>*>(smem_raw);
   uint8_t* sK = align1024(smem_raw + sizeof(ScoreShared<NP>));  // [128 keys][128 d]
   uint8_t* sQ = sK + kKpBlock;                                   // [NP rows][128 d], K-major
-  const int b = blockIdx.y, n = blockIdx.x, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int b = blockIdx.y, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   let_next();
-  if (n == 0 && b == 0) {  // the status area whole (see clear_status): clear, or a length out of range
+  if (blockIdx.x == 0 && b == 0) {  // the status area whole (see clear_status): clear, or a length out of range
     int bad = 0;
     for (int x = tid; x < d.B; x += 128) bad |= seq_len[x] < 1 || seq_len[x] > d.S;
     bad = __syncthreads_or(bad);
@@ -63,15 +66,19 @@ __global__ void __launch_bounds__(128)
   }
   const int len = seq_len[b];
   if (len < 1 || len > d.S) return;
-  if (n >= (len - 1) / kBlock) return;  // the new token's own block is forced, never scored
-  if (tid == 0) {
-    mbar_init(&sh->kv_full, 1);
-    mbar_init(&sh->s_full, 1);
-    mbar_fence_init();
+  const int blocks = (len - 1) / kBlock;  // the new token's own block is forced, never scored
+  if ((int)blockIdx.x >= blocks) return;
+  auto load = [&](int n) {  // by one thread
     const int row = b * d.S + n * kBlock;
     mbar_expect_tx(&sh->kv_full, kKpBlock);
     tma_load_2d(sK, &tm_kp, 0, row, &sh->kv_full);
     tma_load_2d(sK + kKpBlock / 2, &tm_kp, 64, row, &sh->kv_full);
+  };
+  if (tid == 0) {
+    mbar_init(&sh->kv_full, 1);
+    mbar_init(&sh->s_full, 1);
+    mbar_fence_init();
+    load(blockIdx.x);
   }
   if (warp == 0) {
     __syncwarp();  // lane 0 initialised the barriers alone; the allocation is warp-collective
@@ -90,44 +97,55 @@ __global__ void __launch_bounds__(128)
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = sh->tmem;
-  if (tid == 0) {
-    constexpr uint32_t id = idesc_bf16(128, NP, false, false);
-    if (mbar_wait(&sh->kv_full, 0, status)) {
-      fence_after_sync();
-      const uint32_t aK = smem_u32(sK), aQ = smem_u32(sQ);
+  int asked = 1;  // blocks asked for (by thread 0)
+  for (int n = blockIdx.x, i = 0; n < blocks; n += (int)gridDim.x, ++i) {
+    bool landed = true;
+    if (tid == 0) {
+      constexpr uint32_t id = idesc_bf16(128, NP, false, false);
+      if ((landed = mbar_wait(&sh->kv_full, i & 1, status))) {
+        fence_after_sync();
+        const uint32_t aK = smem_u32(sK), aQ = smem_u32(sQ);
 #pragma unroll
-      for (int ks = 0; ks < 8; ++ks) mma_ss(tmem, desc_kmajor(aK, 128, ks), desc_kmajor(aQ, NP, ks), id, ks > 0);
+        for (int ks = 0; ks < 8; ++ks) mma_ss(tmem, desc_kmajor(aK, 128, ks), desc_kmajor(aQ, NP, ks), id, ks > 0);
+      }
+      mma_commit(&sh->s_full);  // arrives once every product issued above has completed
     }
-    mma_commit(&sh->s_full);  // arrives once every product issued above has completed
-  }
-  __syncwarp();
-  // thread = key (tensor-memory lane 32 warp + lane): its NP head scores, then each head's
-  // maximum over the warp's 32 keys
-  const bool ok = mbar_wait_warp(&sh->s_full, 0, status);
-  if (ok) {
-    fence_after_sync();
-    const uint32_t lrow = static_cast<uint32_t>(warp * 32) << 16;
-    uint32_t v[NP];
-    if constexpr (NP == 16) tmem_ld16(tmem + lrow, v);
-    else tmem_ld32(tmem + lrow, v);
-    tmem_wait_ld();
+    __syncwarp();
+    const bool done = mbar_wait_warp(&sh->s_full, i & 1, status);
+    if (done) {
+      fence_after_sync();
+      // the product has read these keys: the next ones are asked for before its result is looked at
+      if (tid == 0 && landed && n + (int)gridDim.x < blocks) {
+        load(n + gridDim.x);
+        ++asked;
+      }
+      __syncwarp();
+      // thread = key (tensor-memory lane 32 warp + lane): its NP head scores, then each head's
+      // maximum over the warp's 32 keys
+      const uint32_t lrow = static_cast<uint32_t>(warp * 32) << 16;
+      uint32_t v[NP];
+      if constexpr (NP == 16) tmem_ld16(tmem + lrow, v);
+      else tmem_ld32(tmem + lrow, v);
+      tmem_wait_ld();
 #pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      if (p < d.Hp) {
-        const float mx = warp_max(__uint_as_float(v[p]));
-        if (lane == 0) sh->wmax[warp][p] = mx;
+      for (int p = 0; p < NP; ++p) {
+        if (p < d.Hp) {
+          const float mx = warp_max(__uint_as_float(v[p]));
+          if (lane == 0) sh->wmax[i & 1][warp][p] = mx;
+        }
       }
     }
+    fence_before_sync();
+    if (!__syncthreads_and(done && landed)) break;  // a wait gave up
+    fence_after_sync();
+    const float(&m)[4][NP] = sh->wmax[i & 1];
+    if (tid < d.Hp)
+      scores[((size_t)b * d.Hp + tid) * d.nblk + n] = fmaxf(fmaxf(m[0][tid], m[1][tid]), fmaxf(m[2][tid], m[3][tid]));
   }
-  fence_before_sync();
-  __syncthreads();
-  fence_after_sync();
-  if (ok && tid < d.Hp)
-    scores[((size_t)b * d.Hp + tid) * d.nblk + n] =
-        fmaxf(fmaxf(sh->wmax[0][tid], sh->wmax[1][tid]), fmaxf(sh->wmax[2][tid], sh->wmax[3][tid]));
   if (warp == 0) {
     // no copy may still land in shared memory when the block exits (of the product, s_full was waited for)
-    mbar_wait_warp(&sh->kv_full, 0, status);
+    if (lane == 0) mbar_wait(&sh->kv_full, (asked - 1) & 1, status);
+    __syncwarp();
     tmem_dealloc(tmem, kColumns);
   }
 }
@@ -508,6 +526,10 @@ __global__ void __launch_bounds__(kAttnThreads)
   }
 }
 
+static int score_ctas(const Dims& d) {  // of a sequence (see decode_scores_kernel)
+  const long long most = 3ll * 5 * num_sms(), each = (long long)d.nblk * d.B / most;
+  return (int)(each > 1 ? (d.nblk + each - 1) / each : d.nblk);
+}
 bool launch_decode_scores(const Dims& d, const void* qp, const void* kp_cache,
                           const int32_t* seq_len, float* scores, unsigned* status,
                           cudaStream_t st) {
@@ -516,7 +538,7 @@ bool launch_decode_scores(const Dims& d, const void* qp, const void* kp_cache,
   const uint64_t kps[1] = {128 * 2};
   const uint32_t kpb[2] = {64, 128};
   if (!make_tmap_bf16(&mkp, kp_cache, 2, kpd, kps, kpb)) return false;
-  const dim3 g1(d.nblk, d.B);
+  const dim3 g1(score_ctas(d), d.B);
 #define MSA_SC(NP)                                                                               \
   {                                                                                              \
     const size_t sm = sizeof(ScoreShared<NP>) + 1024 + (size_t)kKpBlock + NP * 256;                \

@@ -67,6 +67,26 @@ def test_scores_that_are_not_finite():
     assert (select(nan, kp, n, 4, 128 * 9)[..., 0] == 8).all()  # the local block alone
 
 
+@pytest.mark.parametrize("B,blocks,Hp", [(24, 300, 2), (64, 96, 1), (130, 47, 4), (2, 6000, 1)])
+def test_large_capacities_of_many_sequences(B, blocks, Hp):
+    """More blocks of capacity than CTAs: each takes several, of sequences of every length (the last a whole number of
+    rounds, one block less and one more among them)."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(B)
+    cap, top_k = 128 * blocks, 9
+    quarter = lambda *s: (torch.randn(s, generator=g, device="cuda") * 4).round() / 4  # noqa: E731
+    qp, kp = quarter(B, Hp, 128).to(torch.bfloat16), quarter(B, cap, 1, 128).to(torch.bfloat16)
+    n = torch.randint(1, cap + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
+    n[0], n[1] = cap, 1
+    for i, m in enumerate((128, 129, 256, 257, cap - 128, cap - 127, cap // 2, 5, 0, cap + 1)):
+        if 2 + i < B:
+            n[2 + i] = m
+    kp[:, -1] = 100  # no score of the last block's keys reaches those of the others
+    ok = [b for b, m in enumerate(n.tolist()) if 1 <= m <= cap]
+    got = select(qp, kp, n, top_k, cap)[ok]
+    assert torch.equal(got.cpu(), plain(qp[ok], kp[ok], n[ok], top_k))
+
+
 @pytest.mark.parametrize("cap", [128 * 40, 128 * 300, MANY])
 @pytest.mark.parametrize("top_k", [5, 16, 40])
 def test_blocks_without_a_score_are_padding(cap, top_k):
