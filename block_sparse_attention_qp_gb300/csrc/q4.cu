@@ -25,11 +25,12 @@
 // A tile's four warps take 32 keys each with sums of their own, joined at the end; a fifth keeps a ring of tiles
 // loading.  Few (sequence, group) pairs or long ones: their tiles are split over blocks and joined by a second kernel.
 //
-// One wave of resident blocks over 16384 keys each (456 pairs): 5.7 TB/s, 0.84 of a copy; 128 sequences of 4096 keys, 8 KV heads
-// (2.25 waves): 126 us, 4.9 TB/s (121 in their order, launch_q4); the same with lengths of 2048 to 4096: 105 us, 4.4 TB/s (109 in their order); one sequence of 65536 keys: 23 us
-// and 8 of joining; 32 sequences with 16 of 64 blocks selected, 256 pairs on 152 SMs: 25 us, 2.8 TB/s.  16 heads a group
-// (twice the products and weights): 104 us for 64 sequences of 4096 keys.  340 instructions a run of 16 keys are issued in
-// 66 % of the cycles; the pipes are busy at half that or less.  Measured on the way (first line's 128 sequences): codes by
+// A call of a replayed graph of 20, 64 / 8 heads, us.  One wave of resident blocks over 16384 keys each (456 pairs): 188, 5.8 TB/s,
+// 0.85 of a copy; 128 sequences of 4096 keys (2.25 waves): 122, 5.0 TB/s (118 in their order, launch_q4); the same with
+// lengths of 2048 to 4096: 98, 4.8 TB/s (110 in their order); one sequence of 65536 keys: 23 with its join (alone, caches cold, 23
+// and 8); 64 sequences of 4096 keys and 16 heads a group (twice the products and weights): 105; 32 sequences with 16 of 64
+// blocks selected, 256 pairs on 152 SMs: 25, 2.8 TB/s (alone, cold).  340 instructions a run of 16 keys are issued in
+// 66 % of the cycles; the pipes are busy at half that or less.  Measured on the way (128 sequences of 4096, among single calls): codes by
 // shifts and masks and keys paired by byte permutations 260 us (660 instructions); both as below 149; tile data by the
 // loading warp, full tiles without masks 123.  Tried and not kept: four blocks an SM with three stages (123) or with more
 // (156, spills); the P of even and odd dims as two halves of the 16 rows, half of the multiplications and 24 instead of 16
@@ -546,10 +547,11 @@ void launch_q4_read(const void* cache, int B, int H, int cap, int first, int cou
 // Splits of a pair's tiles: as many as fill the resident blocks, of at least four tiles (a part's start, end and share of
 // the join cost about as much as three).  Where several sequences share the blocks, up to four times as many of 32 tiles:
 // one wave of parts as long as the longest sequence's leaves blocks idle beside it, and lengths are known on the device
-// only.  One wave / parts of 32, us, all of the capacity, of 1 .. capacity, most of them short, 64 / 8 heads: 40
-// sequences of 8192 103 / 101, 76 / 65, 54 / 51; of 16384 191 / 165, 125 / 108, 119 / 65; 16 of 65536 256 / 236,
-// 255 / 167, 189 / 91; 8 of 65536 121 / 131, 120 / 105, 90 / 62.  (Of 48 tiles the second line's last is 94, twice as
-// many at most the third's second 198; with more pairs than blocks 64 of 8192 85 / 106.)
+// only.  One wave / parts of 32, us (as above), all of the capacity, of 1 .. capacity, most of them short, 64 / 8 heads: 40
+// sequences of 8192 97 / 93, 66 / 58, 54 / 37; of 16384 188 / 157, 145 / 103, 99 / 63; 16 of 65536 251 / 228,
+// 245 / 148, 201 / 110; 8 of 65536 116 / 123, 115 / 97, 101 / 58: what it loses is 7 % where a few sequences are all full.
+// (Among single calls, of 48 tiles the second line's last is 94 for 65, twice as many parts at most the third's second 198 for
+// 167; with more pairs than blocks 64 of 8192 106 for 85.)
 WinSplit q4_split(int B, long long groups, int tiles, int G) {
   WinSplit w;
   const long long pairs = B * groups, room = (long long)num_sms() * (G > 8 ? 2 : 3);
@@ -587,10 +589,10 @@ static void launch_q4(Q4Args& a, const WinSplit& w, cudaStream_t st) {
   const int grid = a.B * a.groups * w.nsplit;
   constexpr size_t smem = (size_t)kStages * kStageBytes;
   // Long sequences first, where blocks wait for a place: the last ones are then short.  Each block sorts for itself, which is
-  // worth it while B times the waves of blocks is a small multiple of a sequence's tiles.  Unsorted / sorted, us, warm, 64 / 8
-  // heads but for the last: 128 sequences of 4096 keys 125 / 129, of 2048 .. 4096 115 / 107, of 1 .. 4096 90 / 76, most
-  // of them short 66 / 49; 64 of 1 .. 8192 97 / 83; 512 of 1 .. 8192, 8 / 1 heads, 98 / 85 (all of 8192 140 / 148).  Outside the
-  // rule: 300 of 1 .. 2048, 32 / 4 heads, 67 / 67; 512 of 1 .. 1536, 32 / 8 heads, 128 / 166.
+  // worth it while B times the waves of blocks is a small multiple of a sequence's tiles.  Unsorted / sorted, us (as above), 64 / 8
+  // heads but for the last: 128 sequences of 4096 keys 118 / 122, of 2048 .. 4096 110 / 98, of 1 .. 4096 81 / 67, most
+  // of them short 57 / 40; 64 of 1 .. 8192 83 / 79; 512 of 1 .. 8192, 8 / 1 heads, 92 / 78 (all of 8192 135 / 142: equal lengths
+  // lose 3 to 6 %).  Outside the rule: 300 of 1 .. 2048, 32 / 4 heads, 58 / 58; 512 of 1 .. 1536, 32 / 8 heads, 121 / 159.
   const long long room = (long long)num_sms() * (a.G > 8 ? 2 : 3);
   const bool sort = a.B > 1 && a.B <= kSorted && grid > room && (long long)grid * a.B <= 12 * room * w.tiles;
   a.steps = (float)kSteps / ((float)w.tiles * w.nsplit);

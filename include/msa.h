@@ -396,8 +396,8 @@ MSA_API int msa_norm_rope_axes_backward(const msa_rope_shape_t* shape, const msa
  * (sign, four exponent bits, three of mantissa), e one byte:
  *     a = max |x| / 6,  e = floor(log2 a) - 7, at least -100 and at most 90
  *     s[g] = 2^-e max |x[16 g .. 16 g + 15]| / 6,  c[i] = 2^-e x[i] / s[i / 16],
- * each rounded to nearest, ties to even (c: at most 6; s = 0: c = 0).  x is first rounded to bf16.  Every kept
- * value is exact in bf16.  A row with an infinity or NaN is NaN throughout.
+ * each rounded to nearest, ties to even (c: at most 6; s: at most 448, so that kept values end at 2688 2^90; s = 0:
+ * c = 0).  x is first rounded to bf16.  Every kept value is exact in bf16.  A row with an infinity or NaN is NaN throughout.
  * A cache is [B][heads][capacity / 128] blocks of 9344 bytes, 16-byte aligned, capacity a multiple of 128.  A block
  * is 128 rows of one head: [128][64] bytes of codes (low nibble first), [128][8] of scales, [128] of e + 127: 73
  * bytes a row, where bf16 takes 256.  Zero bytes, as in a new cache, are rows of zeros.
