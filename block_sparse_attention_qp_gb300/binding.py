@@ -260,8 +260,12 @@ def cached_workspace(shape: Shape, op: int, device) -> torch.Tensor:
     """Workspace kept per (device, current stream) and reused by later calls on that stream: the
     stream orders each call after the previous one, and no call leaves state in it that a later
     call reads.  Grows (never shrinks) to the largest size asked for; clear_workspace_cache()
-    releases it."""
+    releases it.  A call that is being captured gets memory of its graph's own instead: graphs captured on
+    one stream may be replayed on several, and outlive the cache."""
     device = torch.device(device)
+    with torch.cuda.device(device):
+        if torch.cuda.is_current_stream_capturing():
+            return workspace(shape, op, device)
     key = (device.index if device.index is not None else torch.cuda.current_device(),
            torch.cuda.current_stream(device).cuda_stream)
     need = msa_workspace_size(shape, op)
